@@ -85,6 +85,7 @@ typedef enum {
 #define DSA_DEVERR_INDEX 0x4   /* a Top-K entry outside [-1, p] reached the attention kernel */
 #define DSA_DEVERR_TIMEOUT 0x8 /* a pipeline wait exceeded its limit (one second unless
                                   dsa_set_wait_limit_ns() says otherwise) */
+#define DSA_DEVERR_ROPE 0x10   /* a position beyond the rotation table was needed */
 
 typedef struct {
     int32_t batch;             /* B >= 1 sequences */
@@ -104,6 +105,28 @@ typedef struct {
     int32_t kv_dtype;          /* dsa_dtype_t of the latent-KV cache: DSA_BF16 rows of D values, or
                                   DSA_FP8_E4M3 rows in the FP8 row layout above */
 } dsa_dims_t;
+
+/*
+ * Position rotation (rotary embedding) of 64 dims by 32 angles per position.  The table holds, for every
+ * position, the 32 cosines and then the 32 sines in fp32 (a scaling of the angles or of the magnitude is
+ * the table's business).  Pair i of the rotated dims, (x1, x2), becomes
+ *     y1 = x1 * cos_i - x2 * sin_i,   y2 = x1 * sin_i + x2 * cos_i
+ * in fp32, each product rounded before the sum.  Latent-KV rows and attention queries rotate their last
+ * 64 dims (512..575); indexer rows rotate the 64 dims from idx_begin.
+ */
+typedef enum {
+    DSA_ROPE_HALVES = 0,     /* pair i is dims (i, i + 32) of the 64 */
+    DSA_ROPE_INTERLEAVED = 1 /* pair i is dims (2i, 2i + 1) */
+} dsa_rope_pairing_t;
+
+typedef struct {
+    const float* table;  /* DEVICE [table_len, 64] fp32, 16-byte aligned */
+    int32_t table_len;   /* positions in the table, >= 1 */
+    int32_t kv_pairing;  /* dsa_rope_pairing_t of latent-KV rows and attention queries */
+    int32_t idx_pairing; /* dsa_rope_pairing_t of indexer keys and queries */
+    int32_t idx_begin;   /* first rotated dim of an indexer row (a multiple of 8, idx_begin + 64 <= Di), or -1
+                            to leave indexer rows unrotated */
+} dsa_rope_t;
 
 /* ABI version of the loaded library (DSA_ABI_VERSION). */
 int32_t dsa_abi_version(void);
@@ -305,6 +328,85 @@ dsa_status_t dsa_get_device_error(const void* workspace, void* stream, int32_t* 
 dsa_status_t dsa_append_rows(const dsa_dims_t* dims, const void* k_new, const void* kv_new,
                              const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_q_lens,
                              void* k_cache, void* k_scale, void* kv_cache, void* workspace, void* stream);
+
+/*
+ * dsa_append_rows with the position rotation applied on the way ([A4] 3.3): for every query token t, its
+ * latent-KV row, with dims 512..575 rotated by the angles of p_t, goes to the latent-KV cache row of p_t,
+ * and its indexer key, with 64 dims from rope->idx_begin rotated, to the indexer cache row of p_t.
+ * Rotated values are rounded once, to the cache's type; FP8 caches are quantised as in dsa_append_rows
+ * (from the fp32 rotated values), and MXFP8 keys per group of 32: shared exponent
+ * floor(log2(absmax)) - 8 clamped to [-127, 127] (0 for an all-zero group), codes saturated at 448.
+ *   k_new      [T, Di] bf16 new indexer keys, or NULL; row t starts k_stride elements after row t - 1
+ *   kv_new     [T, D] bf16 new latent-KV rows, or NULL; row stride kv_stride elements
+ *   k_stride, kv_stride   0 (dense: Di, D) or a multiple of 8 that is at least the row's width
+ *   k_cache, k_scale, kv_cache, workspace   as for dsa_append_rows, k_scale [num_pages, 64, Di/32] E8M0
+ *              bytes for DSA_MXFP8_E4M3.  (256 bytes of workspace are enough here.)
+ * A token that no sequence owns or whose position is inconsistent (DSA_DEVERR_SEQ), whose page is out of
+ * range (DSA_DEVERR_PAGE) or whose position has no table row (DSA_DEVERR_ROPE) writes nothing.  No two
+ * tokens may share a cache row.
+ * Supported: Di a multiple of 8 (MXFP8: of 32) up to 128; D = 576, Dv = 512.
+ */
+dsa_status_t dsa_rope_append(const dsa_dims_t* dims, const dsa_rope_t* rope, const void* k_new, int64_t k_stride,
+                             const void* kv_new, int64_t kv_stride, const int32_t* page_table,
+                             const int32_t* seq_lens, const int32_t* cu_q_lens, void* k_cache, void* k_scale,
+                             void* kv_cache, void* workspace, void* stream);
+
+/*
+ * The rotation of one step's queries, and the quantisation of the indexer's ([A4] 3.3; [A3] 3.1): for
+ * every query token t and attention head h, q[t,h,512:576] = the 64 rotary values q_pe[t,h] rotated by the
+ * angles of p_t (the other dims of q are left as they are); for every indexer head, q_idx[t,h] =
+ * q_idx_in[t,h] with 64 dims from rope->idx_begin rotated, as bf16 or quantised: one scale per row
+ * (DSA_FP8_E4M3) or per group of 32 (DSA_MXFP8_E4M3), by the rules of dsa_rope_append.
+ *   q_pe       [T, Hq, 64] bf16, or NULL to leave q alone; head h of token t starts
+ *              t * q_pe_token_stride + h * q_pe_head_stride elements in (both 0: dense; else both multiples
+ *              of 8, q_pe_head_stride >= 64).  It may be q's own last 64 dims (q + 512, strides Hq * 576 and
+ *              576): in place.
+ *   q          [T, Hq, D] bf16, written in dims 512..575
+ *   q_idx_in   [T, Hi, Di] bf16, or NULL to leave the indexer's queries alone; token stride q_idx_stride
+ *              elements (0: dense; else a multiple of 8, at least Hi * Di).  With bf16 output it may be
+ *              q_idx itself (dense).
+ *   q_idx      [T, Hi, Di] of dims->idx_dtype, output;  q_scale as for dsa_indexer_topk, output (NULL for bf16)
+ *   workspace  as for dsa_rope_append
+ * No page is looked up: num_pages and max_pages_per_seq play no part.  A token that no sequence owns or
+ * whose sequence has n_b > L_b (DSA_DEVERR_SEQ), or whose position has no table row (DSA_DEVERR_ROPE),
+ * writes nothing.
+ * Supported: Hi, Hq <= 128, D = 576, Dv = 512, Di as for dsa_rope_append.
+ */
+dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, const void* q_pe,
+                              int64_t q_pe_token_stride, int64_t q_pe_head_stride, void* q, const void* q_idx_in,
+                              int64_t q_idx_stride, void* q_idx, void* q_scale, const int32_t* seq_lens,
+                              const int32_t* cu_q_lens, void* workspace, void* stream);
+
+/*
+ * Dense attention over the latent-KV cache for a batch whose sequences share a prefix ([A2] step 2 without
+ * the selection; [A1] 3.2): for every query token t of sequence b and head h,
+ *     z_s = softmax_scale * q[t,h,:] . kv[s,:]  for every visible position s = 0..p_t,
+ *     out[t,h,:] = sum_s softmax(z)_s * kv[s, 0:v_dim],   lse[t,h] = log sum_s exp(z_s)
+ * where positions below prefix_len are the same rows for every sequence: they are read through the page
+ * table of sequence 0, once for all the sequences that share a matrix tile.  Every sequence's table still
+ * maps all its positions (as a page pool with shared prefix pages leaves it); where prefix_len is not a
+ * multiple of 64, the page in which it ends may be each sequence's own copy.  prefix_len = 0 is plain
+ * attention of each sequence over its own context.
+ *   prefix_len >= 0, at most L_b - n_b for every sequence with queries (every query is behind the prefix)
+ *   q, kv_cache, page_table, seq_lens, cu_q_lens, out, lse   as for dsa_sparse_attn
+ *   workspace  dsa_prefix_attn_workspace_size(dims, prefix_len) bytes, first 256 zero-filled once
+ * dims->idx_* and top_k are not looked at.  Positions beyond p_t and rows behind L_b are never part of the
+ * result, whatever they hold.  A score of -inf has weight 0; a NaN in a visible row, or in q, makes
+ * the rows that see it NaN; with every score -inf, out = 0 and lse = -inf.
+ * A sequence with n_b > L_b - prefix_len or a context beyond its page table (DSA_DEVERR_SEQ) and a token that
+ * no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were; rows of a page that is out of range
+ * (DSA_DEVERR_PAGE) are skipped.
+ * Supported: D = 576, Dv = 512, Hq <= 128.
+ */
+dsa_status_t dsa_prefix_attn(const dsa_dims_t* dims, int32_t prefix_len, const void* q, const void* kv_cache,
+                             const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_q_lens, void* out,
+                             float* lse, void* workspace, void* stream);
+
+/*
+ * Bytes of workspace dsa_prefix_attn needs: the 256-byte error word area, then partial results where the
+ * context is split over several CTAs.  0 when dims is NULL or prefix_len negative.  Host-only.
+ */
+size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len);
 
 /* Zeroes the device error word (asynchronously on `stream`). */
 dsa_status_t dsa_clear_device_error(void* workspace, void* stream);

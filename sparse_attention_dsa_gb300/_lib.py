@@ -17,7 +17,8 @@ LIB_PATH = os.path.join(_PKG, "libdsa_gb300.so")
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE, DSA_ERR_TIMEOUT = range(6)
 DSA_BF16, DSA_FP8_E4M3, DSA_MXFP8_E4M3 = 0, 1, 2
 DSA_KV_FP8_ROW_BYTES = 656
-DSA_DEVERR_PAGE, DSA_DEVERR_SEQ, DSA_DEVERR_INDEX, DSA_DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DSA_DEVERR_PAGE, DSA_DEVERR_SEQ, DSA_DEVERR_INDEX, DSA_DEVERR_TIMEOUT, DSA_DEVERR_ROPE = 0x1, 0x2, 0x4, 0x8, 0x10
+DSA_ROPE_HALVES, DSA_ROPE_INTERLEAVED = 0, 1
 
 EXPORTED = (
     "dsa_abi_version",
@@ -37,6 +38,10 @@ EXPORTED = (
     "dsa_topk_merge",
     "dsa_attn_combine",
     "dsa_set_wait_limit_ns",
+    "dsa_rope_append",
+    "dsa_rope_queries",
+    "dsa_prefix_attn",
+    "dsa_prefix_attn_workspace_size",
 )
 
 
@@ -63,6 +68,21 @@ class DsaDims(ctypes.Structure):
 
     def __repr__(self):
         return "DsaDims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class DsaRope(ctypes.Structure):
+    """Mirror of dsa_rope_t.  ``table`` is a device address (``tensor.data_ptr()``): keep the tensor alive."""
+
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("table_len", ctypes.c_int32),
+        ("kv_pairing", ctypes.c_int32),
+        ("idx_pairing", ctypes.c_int32),
+        ("idx_begin", ctypes.c_int32),
+    ]
+
+    def __repr__(self):
+        return "DsaRope(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
 class DsaError(RuntimeError):
@@ -121,6 +141,16 @@ def lib() -> ctypes.CDLL:
             L.dsa_indexer_topk_static.argtypes = [ctypes.POINTER(DsaDims)] + [vp] * 12
             L.dsa_append_rows.restype = st
             L.dsa_append_rows.argtypes = [ctypes.POINTER(DsaDims)] + [vp] * 10
+            i64 = ctypes.c_int64
+            L.dsa_rope_append.restype = st
+            L.dsa_rope_append.argtypes = [ctypes.POINTER(DsaDims), ctypes.POINTER(DsaRope), vp, i64, vp, i64] + [vp] * 8
+            L.dsa_rope_queries.restype = st
+            L.dsa_rope_queries.argtypes = ([ctypes.POINTER(DsaDims), ctypes.POINTER(DsaRope), vp, i64, i64, vp, vp, i64] +
+                                           [vp] * 6)
+            L.dsa_prefix_attn.restype = st
+            L.dsa_prefix_attn.argtypes = [ctypes.POINTER(DsaDims), ctypes.c_int32] + [vp] * 9
+            L.dsa_prefix_attn_workspace_size.restype = ctypes.c_size_t
+            L.dsa_prefix_attn_workspace_size.argtypes = [ctypes.POINTER(DsaDims), ctypes.c_int32]
             _lib = L
     return _lib
 
@@ -251,4 +281,32 @@ def append_rows(dims, k_new, kv_new, page_table, seq_lens, cu_q_lens, k_cache, k
     """dsa_append_rows: write every query token's new indexer key / latent-KV row at its position."""
     _check(lib().dsa_append_rows(ctypes.byref(dims), _ptr(k_new), _ptr(kv_new), _ptr(page_table), _ptr(seq_lens),
                                  _ptr(cu_q_lens), _ptr(k_cache), _ptr(k_scale), _ptr(kv_cache), _ptr(workspace),
+                                 _stream(stream)))
+
+
+def rope_append(dims, rope, k_new, kv_new, page_table, seq_lens, cu_q_lens, k_cache, k_scale, kv_cache, workspace,
+                stream=None, k_stride=0, kv_stride=0):
+    """dsa_rope_append: append_rows with the position rotation applied on the way (row strides in elements, 0 = dense)."""
+    _check(lib().dsa_rope_append(ctypes.byref(dims), ctypes.byref(rope), _ptr(k_new), int(k_stride), _ptr(kv_new),
+                                 int(kv_stride), _ptr(page_table), _ptr(seq_lens), _ptr(cu_q_lens), _ptr(k_cache),
+                                 _ptr(k_scale), _ptr(kv_cache), _ptr(workspace), _stream(stream)))
+
+
+def rope_queries(dims, rope, q_pe, q, q_idx_in, q_idx, q_scale, seq_lens, cu_q_lens, workspace, stream=None,
+                 q_pe_strides=(0, 0), q_idx_stride=0):
+    """dsa_rope_queries: rotate the step's queries and quantise the indexer's.  q_pe_strides: (token, head) in
+    elements; q_idx_stride: token stride of q_idx_in (0 = dense)."""
+    _check(lib().dsa_rope_queries(ctypes.byref(dims), ctypes.byref(rope), _ptr(q_pe), int(q_pe_strides[0]),
+                                  int(q_pe_strides[1]), _ptr(q), _ptr(q_idx_in), int(q_idx_stride), _ptr(q_idx),
+                                  _ptr(q_scale), _ptr(seq_lens), _ptr(cu_q_lens), _ptr(workspace), _stream(stream)))
+
+
+def prefix_attn_workspace_size(dims: DsaDims, prefix_len: int) -> int:
+    return int(lib().dsa_prefix_attn_workspace_size(ctypes.byref(dims), int(prefix_len)))
+
+
+def prefix_attn(dims, prefix_len, q, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace, stream=None):
+    """dsa_prefix_attn: dense attention of a batch whose first prefix_len positions are the same rows."""
+    _check(lib().dsa_prefix_attn(ctypes.byref(dims), int(prefix_len), _ptr(q), _ptr(kv_cache), _ptr(page_table),
+                                 _ptr(seq_lens), _ptr(cu_q_lens), _ptr(out), _ptr(lse), _ptr(workspace),
                                  _stream(stream)))

@@ -101,7 +101,8 @@ dsa_status_t check_ptr(const void* p, const char* name, bool required = true) {
     return DSA_OK;
 }
 
-dsa_status_t check_common(const dsa_dims_t* d) {
+// batch, query and paging sizes (every call's); top_k is checked apart by the calls that select
+dsa_status_t check_paging(const dsa_dims_t* d) {
     if (!d) return fail(DSA_ERR_INVALID_ARG, "dims is NULL");
     if (d->batch < 1) return fail(DSA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", d->batch);
     if (d->total_q < 0) return fail(DSA_ERR_INVALID_ARG, "total_q must be >= 0 (got %d)", d->total_q);
@@ -113,9 +114,92 @@ dsa_status_t check_common(const dsa_dims_t* d) {
         return fail(DSA_ERR_INVALID_ARG, "max_pages_per_seq must be >= 1 (got %d)", d->max_pages_per_seq);
     if ((int64_t)d->max_pages_per_seq * 64 > (int64_t)INT32_MAX)
         return fail(DSA_ERR_UNSUPPORTED, "max_pages_per_seq * 64 exceeds int32");
+    return DSA_OK;
+}
+
+dsa_status_t check_common(const dsa_dims_t* d) {
+    dsa_status_t st = check_paging(d);
+    if (st) return st;
     if (d->top_k < 1) return fail(DSA_ERR_INVALID_ARG, "top_k must be >= 1 (got %d)", d->top_k);
     if (d->top_k > 16384) return fail(DSA_ERR_UNSUPPORTED, "top_k must be <= 16384 (got %d)", d->top_k);
     return DSA_OK;
+}
+
+// Heads, row widths, cache type and scale of attention over the latent-KV cache.
+dsa_status_t check_latent_attention(const dsa_dims_t* d) {
+    if (d->attn_heads < 1) return fail(DSA_ERR_INVALID_ARG, "attn_heads must be >= 1 (got %d)", d->attn_heads);
+    if (d->kv_dim < 1 || d->v_dim < 1 || d->v_dim > d->kv_dim)
+        return fail(DSA_ERR_INVALID_ARG, "need 1 <= v_dim <= kv_dim (got %d, %d)", d->v_dim, d->kv_dim);
+    if (d->kv_dim != 576 || d->v_dim != 512)
+        return fail(DSA_ERR_UNSUPPORTED, "attention supports kv_dim 576 / v_dim 512 (got %d / %d)", d->kv_dim,
+                    d->v_dim);
+    if (d->attn_heads > 128) return fail(DSA_ERR_UNSUPPORTED, "attn_heads must be <= 128 (got %d)", d->attn_heads);
+    if (d->kv_dtype != DSA_BF16 && d->kv_dtype != DSA_FP8_E4M3)
+        return fail(DSA_ERR_INVALID_ARG, "kv_dtype %d is not a dsa_dtype_t", d->kv_dtype);
+    if ((int64_t)d->num_pages * 64 > (int64_t)INT32_MAX)
+        return fail(DSA_ERR_UNSUPPORTED, "num_pages * 64 must fit in int32 (got %d pages)", d->num_pages);
+    if (!(d->softmax_scale > 0.f) || d->softmax_scale > 1e30f)
+        return fail(DSA_ERR_INVALID_ARG, "softmax_scale must be a positive finite number");
+    return DSA_OK;
+}
+
+// The rotation's table and, where indexer rows take part, their width, type and rotated dims.
+dsa_status_t check_rope(const dsa_dims_t* d, const dsa_rope_t* r, bool kv, bool idx) {
+    if (!r) return fail(DSA_ERR_INVALID_ARG, "rope is NULL");
+    dsa_status_t st = check_ptr(r->table, "rope table");
+    if (st) return st;
+    if (r->table_len < 1) return fail(DSA_ERR_INVALID_ARG, "rope table_len must be >= 1 (got %d)", r->table_len);
+    if (kv) {
+        if (r->kv_pairing != DSA_ROPE_HALVES && r->kv_pairing != DSA_ROPE_INTERLEAVED)
+            return fail(DSA_ERR_INVALID_ARG, "kv_pairing %d is not a dsa_rope_pairing_t", r->kv_pairing);
+        if (d->kv_dim != 576 || d->v_dim != 512)
+            return fail(DSA_ERR_UNSUPPORTED, "rotation supports kv_dim 576 / v_dim 512 (got %d / %d)", d->kv_dim, d->v_dim);
+    }
+    if (idx) {
+        if (d->idx_dtype != DSA_BF16 && d->idx_dtype != DSA_FP8_E4M3 && d->idx_dtype != DSA_MXFP8_E4M3)
+            return fail(DSA_ERR_INVALID_ARG, "idx_dtype %d is not a dsa_dtype_t", d->idx_dtype);
+        const int unit = d->idx_dtype == DSA_MXFP8_E4M3 ? 32 : 8;
+        if (d->idx_dim < unit || d->idx_dim > 128 || d->idx_dim % unit)
+            return fail(DSA_ERR_UNSUPPORTED, "rotation supports an idx_dim that is a multiple of %d up to 128 (got %d)",
+                        unit, d->idx_dim);
+        if (r->idx_pairing != DSA_ROPE_HALVES && r->idx_pairing != DSA_ROPE_INTERLEAVED)
+            return fail(DSA_ERR_INVALID_ARG, "idx_pairing %d is not a dsa_rope_pairing_t", r->idx_pairing);
+        if (r->idx_begin != -1 && (r->idx_begin < 0 || r->idx_begin % 8 || r->idx_begin > d->idx_dim - 64))
+            return fail(DSA_ERR_INVALID_ARG, "idx_begin must be -1 or a multiple of 8 with idx_begin + 64 <= idx_dim "
+                        "(got %d of %d dims)", r->idx_begin, d->idx_dim);
+    }
+    return DSA_OK;
+}
+
+// A row stride in elements: 0 stands for `dense`.
+dsa_status_t check_stride(int64_t* stride, int64_t dense, const char* name) {
+    if (*stride == 0) *stride = dense;
+    if (*stride < dense || *stride % 8)
+        return fail(DSA_ERR_INVALID_ARG, "%s must be 0 or a multiple of 8 of at least %lld elements (got %lld)", name,
+                    (long long)dense, (long long)*stride);
+    return DSA_OK;
+}
+
+dsa::RopeParams rope_params(const dsa_dims_t* d, const dsa_rope_t* r, const int32_t* page_table,
+                            const int32_t* seq_lens, const int32_t* cu_q_lens, void* workspace) {
+    dsa::RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.table = r->table;
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.cu_q_lens = cu_q_lens;
+    p.err = static_cast<int32_t*>(workspace);
+    p.table_len = r->table_len;
+    p.kv_interleaved = r->kv_pairing == DSA_ROPE_INTERLEAVED;
+    p.idx_interleaved = r->idx_pairing == DSA_ROPE_INTERLEAVED;
+    p.idx_begin = r->idx_begin;
+    p.batch = d->batch;
+    p.total_q = d->total_q;
+    p.num_pages = d->num_pages;
+    p.max_pages = d->max_pages_per_seq;
+    p.idx_dim = d->idx_dim;
+    p.idx_dtype = d->idx_dtype;
+    return p;
 }
 
 constexpr int kMaxClusterSize = 16;
@@ -309,19 +393,7 @@ dsa_status_t prepare_sfa(const dsa_dims_t* d, const void* q, const void* kv_cach
     *launch = false;
     dsa_status_t st = check_common(d);
     if (st) return st;
-    if (d->attn_heads < 1) return fail(DSA_ERR_INVALID_ARG, "attn_heads must be >= 1 (got %d)", d->attn_heads);
-    if (d->kv_dim < 1 || d->v_dim < 1 || d->v_dim > d->kv_dim)
-        return fail(DSA_ERR_INVALID_ARG, "need 1 <= v_dim <= kv_dim (got %d, %d)", d->v_dim, d->kv_dim);
-    if (d->kv_dim != 576 || d->v_dim != 512)
-        return fail(DSA_ERR_UNSUPPORTED, "sparse attention supports kv_dim 576 / v_dim 512 (got %d / %d)", d->kv_dim,
-                    d->v_dim);
-    if (d->attn_heads > 128) return fail(DSA_ERR_UNSUPPORTED, "attn_heads must be <= 128 (got %d)", d->attn_heads);
-    if (d->kv_dtype != DSA_BF16 && d->kv_dtype != DSA_FP8_E4M3)
-        return fail(DSA_ERR_INVALID_ARG, "kv_dtype %d is not a dsa_dtype_t", d->kv_dtype);
-    if ((int64_t)d->num_pages * 64 > (int64_t)INT32_MAX)
-        return fail(DSA_ERR_UNSUPPORTED, "num_pages * 64 must fit in int32 (got %d pages)", d->num_pages);
-    if (!(d->softmax_scale > 0.f) || d->softmax_scale > 1e30f)
-        return fail(DSA_ERR_INVALID_ARG, "softmax_scale must be a positive finite number");
+    if ((st = check_latent_attention(d))) return st;
     if ((st = check_ptr(q, "q")) || (st = check_ptr(kv_cache, "kv_cache")) ||
         (st = check_ptr(page_table, "page_table")) || (st = check_ptr(seq_lens, "seq_lens")) ||
         (st = check_ptr(cu_q_lens, "cu_q_lens")) || (st = check_ptr(topk_idx, "topk_idx")) ||
@@ -593,6 +665,143 @@ dsa_status_t dsa_append_rows(const dsa_dims_t* d, const void* k_new, const void*
     p.kv_fp8 = kv_fp8 ? 1 : 0;
     cudaError_t e = dsa::launch_append(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "append launch");
+    return DSA_OK;
+}
+
+dsa_status_t dsa_rope_append(const dsa_dims_t* d, const dsa_rope_t* rope, const void* k_new, int64_t k_stride,
+                             const void* kv_new, int64_t kv_stride, const int32_t* page_table,
+                             const int32_t* seq_lens, const int32_t* cu_q_lens, void* k_cache, void* k_scale,
+                             void* kv_cache, void* workspace, void* stream) {
+    g_last_error.clear();
+    dsa_status_t st = check_paging(d);
+    if (st || (st = check_rope(d, rope, kv_new != nullptr, k_new != nullptr))) return st;
+    if ((st = check_ptr(k_new, "k_new", false)) || (st = check_ptr(kv_new, "kv_new", false)) ||
+        (st = check_ptr(page_table, "page_table")) || (st = check_ptr(seq_lens, "seq_lens")) ||
+        (st = check_ptr(cu_q_lens, "cu_q_lens")) || (st = check_ptr(workspace, "workspace")))
+        return st;
+    if (k_new && ((st = check_stride(&k_stride, d->idx_dim, "k_stride")) || (st = check_ptr(k_cache, "k_cache")) ||
+                  (st = check_ptr(k_scale, "k_scale", d->idx_dtype != DSA_BF16))))
+        return st;
+    if (kv_new) {
+        if (d->kv_dtype != DSA_BF16 && d->kv_dtype != DSA_FP8_E4M3)
+            return fail(DSA_ERR_INVALID_ARG, "kv_dtype %d is not a latent-KV cache type", d->kv_dtype);
+        if ((st = check_stride(&kv_stride, d->kv_dim, "kv_stride")) || (st = check_ptr(kv_cache, "kv_cache"))) return st;
+    }
+    if ((int64_t)d->num_pages * 64 > (int64_t)INT32_MAX)
+        return fail(DSA_ERR_UNSUPPORTED, "num_pages * 64 must fit in int32 (got %d pages)", d->num_pages);
+    if (d->total_q == 0 || (!k_new && !kv_new)) return DSA_OK;
+    DeviceInfo dev;
+    if ((st = device_info(&dev))) return st;
+    dsa::RopeAppendParams p;
+    memset(&p, 0, sizeof p);
+    p.r = rope_params(d, rope, page_table, seq_lens, cu_q_lens, workspace);
+    p.k_new = static_cast<const uint16_t*>(k_new);
+    p.kv_new = static_cast<const uint16_t*>(kv_new);
+    p.k_stride = k_stride;
+    p.kv_stride = kv_stride;
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.k_scale = k_scale;
+    p.kv_cache = static_cast<uint8_t*>(kv_cache);
+    p.kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
+    cudaError_t e = dsa::launch_rope_append(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rotating append launch");
+    return DSA_OK;
+}
+
+dsa_status_t dsa_rope_queries(const dsa_dims_t* d, const dsa_rope_t* rope, const void* q_pe,
+                              int64_t q_pe_token_stride, int64_t q_pe_head_stride, void* q, const void* q_idx_in,
+                              int64_t q_idx_stride, void* q_idx, void* q_scale, const int32_t* seq_lens,
+                              const int32_t* cu_q_lens, void* workspace, void* stream) {
+    g_last_error.clear();
+    dsa_status_t st = check_paging(d);
+    if (st || (st = check_rope(d, rope, q_pe != nullptr, q_idx_in != nullptr))) return st;
+    if ((st = check_ptr(q_pe, "q_pe", false)) || (st = check_ptr(q_idx_in, "q_idx_in", false)) ||
+        (st = check_ptr(seq_lens, "seq_lens")) || (st = check_ptr(cu_q_lens, "cu_q_lens")) ||
+        (st = check_ptr(workspace, "workspace")))
+        return st;
+    if (q_pe) {
+        if (d->attn_heads < 1) return fail(DSA_ERR_INVALID_ARG, "attn_heads must be >= 1 (got %d)", d->attn_heads);
+        if (d->attn_heads > 128) return fail(DSA_ERR_UNSUPPORTED, "attn_heads must be <= 128 (got %d)", d->attn_heads);
+        if ((q_pe_token_stride == 0) != (q_pe_head_stride == 0) || q_pe_token_stride < 0 || q_pe_token_stride % 8)
+            return fail(DSA_ERR_INVALID_ARG, "q_pe strides must both be 0 or both positive multiples of 8 (got %lld, %lld)",
+                        (long long)q_pe_token_stride, (long long)q_pe_head_stride);
+        if ((st = check_stride(&q_pe_head_stride, 64, "q_pe_head_stride")) || (st = check_ptr(q, "q"))) return st;
+        if (q_pe_token_stride == 0) q_pe_token_stride = (int64_t)64 * d->attn_heads;
+    }
+    if (q_idx_in) {
+        if (d->idx_heads < 1) return fail(DSA_ERR_INVALID_ARG, "idx_heads must be >= 1 (got %d)", d->idx_heads);
+        if (d->idx_heads > 128) return fail(DSA_ERR_UNSUPPORTED, "idx_heads must be <= 128 (got %d)", d->idx_heads);
+        if ((st = check_stride(&q_idx_stride, (int64_t)d->idx_heads * d->idx_dim, "q_idx_stride")) ||
+            (st = check_ptr(q_idx, "q_idx")) || (st = check_ptr(q_scale, "q_scale", d->idx_dtype != DSA_BF16)))
+            return st;
+    }
+    if (d->total_q == 0 || (!q_pe && !q_idx_in)) return DSA_OK;
+    DeviceInfo dev;
+    if ((st = device_info(&dev))) return st;
+    dsa::RopeQueriesParams p;
+    memset(&p, 0, sizeof p);
+    p.r = rope_params(d, rope, nullptr, seq_lens, cu_q_lens, workspace);
+    p.r.max_pages = INT32_MAX / 64;  // no page table here, so no limit from one
+    p.q_pe = static_cast<const uint16_t*>(q_pe);
+    p.q_pe_token_stride = q_pe_token_stride;
+    p.q_pe_head_stride = q_pe_head_stride;
+    p.q = static_cast<uint16_t*>(q);
+    p.q_idx_in = static_cast<const uint16_t*>(q_idx_in);
+    p.q_idx_stride = q_idx_stride;
+    p.q_idx = static_cast<uint8_t*>(q_idx);
+    p.q_scale = q_scale;
+    p.heads = d->attn_heads;
+    p.idx_heads = d->idx_heads;
+    p.num_sms = dev.num_sms;
+    cudaError_t e = dsa::launch_rope_queries(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "query rotation launch");
+    return DSA_OK;
+}
+
+size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len) {
+    if (!dims || prefix_len < 0) return 0;
+    return dsa::kErrorWordArea;
+}
+
+dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void* q, const void* kv_cache,
+                             const int32_t* page_table, const int32_t* seq_lens, const int32_t* cu_q_lens, void* out,
+                             float* lse, void* workspace, void* stream) {
+    g_last_error.clear();
+    dsa_status_t st = check_paging(d);
+    if (st || (st = check_latent_attention(d))) return st;
+    if (prefix_len < 0) return fail(DSA_ERR_INVALID_ARG, "prefix_len must be >= 0 (got %d)", prefix_len);
+    if ((int64_t)prefix_len > (int64_t)d->max_pages_per_seq * 64)
+        return fail(DSA_ERR_INVALID_ARG, "prefix_len %d exceeds the page table's %d pages", prefix_len, d->max_pages_per_seq);
+    if ((st = check_ptr(q, "q")) || (st = check_ptr(kv_cache, "kv_cache")) ||
+        (st = check_ptr(page_table, "page_table")) || (st = check_ptr(seq_lens, "seq_lens")) ||
+        (st = check_ptr(cu_q_lens, "cu_q_lens")) || (st = check_ptr(out, "out")) ||
+        (st = check_ptr(lse, "lse", false)) || (st = check_ptr(workspace, "workspace")))
+        return st;
+    if (d->total_q == 0) return DSA_OK;
+    DeviceInfo dev;
+    if ((st = device_info(&dev))) return st;
+    dsa::PrefixLaunch L;
+    memset(&L, 0, sizeof L);
+    dsa::PrefixParams& p = L.params;
+    p.q = static_cast<const uint16_t*>(q);
+    p.kv_cache = static_cast<const uint8_t*>(kv_cache);
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.cu_q_lens = cu_q_lens;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.err = static_cast<int32_t*>(workspace);
+    p.batch = d->batch;
+    p.total_q = d->total_q;
+    p.num_pages = d->num_pages;
+    p.max_pages = d->max_pages_per_seq;
+    p.heads = d->attn_heads;
+    p.prefix_len = prefix_len;
+    p.kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
+    p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
+    p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    cudaError_t e = dsa::launch_prefix(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
     return DSA_OK;
 }
 

@@ -172,6 +172,77 @@ struct CombineParams {
 };
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 
+// ---- position rotation: appending rotated rows, rotating a step's queries -------------------------------
+struct RopeParams {
+    const float* table;  // [table_len, 64] fp32: 32 cosines, 32 sines
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* cu_q_lens;
+    int32_t* err;
+    int32_t table_len;
+    int32_t kv_interleaved;
+    int32_t idx_interleaved;
+    int32_t idx_begin;  // first rotated dim of an indexer row, or -1
+    int32_t batch;
+    int32_t total_q;
+    int32_t num_pages;
+    int32_t max_pages;
+    int32_t idx_dim;
+    int32_t idx_dtype;  // dsa_dtype_t
+};
+struct RopeAppendParams {
+    RopeParams r;
+    const uint16_t* k_new;   // bf16 bits, rows k_stride elements apart, or null
+    const uint16_t* kv_new;  // bf16 bits, rows kv_stride elements apart, or null
+    int64_t k_stride;
+    int64_t kv_stride;
+    uint8_t* k_cache;
+    void* k_scale;  // fp32 [num_pages * 64], or E8M0 bytes [num_pages * 64, Di / 32]
+    uint8_t* kv_cache;
+    int32_t kv_fp8;
+};
+struct RopeQueriesParams {
+    RopeParams r;
+    const uint16_t* q_pe;  // bf16 bits or null; may alias q
+    int64_t q_pe_token_stride;
+    int64_t q_pe_head_stride;
+    uint16_t* q;               // [T, Hq, 576] bf16 bits
+    const uint16_t* q_idx_in;  // bf16 bits or null; may be q_idx (bf16)
+    int64_t q_idx_stride;
+    uint8_t* q_idx;  // [T, Hi, Di]
+    void* q_scale;   // fp32 [T, Hi], or E8M0 bytes [T, Hi, Di / 32]
+    int32_t heads;
+    int32_t idx_heads;
+    int32_t num_sms;
+};
+cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream);
+cudaError_t launch_rope_queries(const RopeQueriesParams& p, cudaStream_t stream);
+
+// ---- dense attention over the latent-KV cache with a shared prefix --------------------------------------
+struct PrefixParams {
+    const uint16_t* q;        // [T, Hq, 576] bf16 bits
+    const uint8_t* kv_cache;  // bf16 rows, or FP8 rows of kKvFp8RowBytes
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* cu_q_lens;
+    uint16_t* out;  // [T, Hq, 512] bf16 bits
+    float* lse;     // [T, Hq] or null
+    int32_t* err;
+    int32_t batch;
+    int32_t total_q;
+    int32_t num_pages;
+    int32_t max_pages;
+    int32_t heads;
+    int32_t prefix_len;
+    int32_t kv_fp8;
+    float scale_log2;  // softmax_scale * log2(e)
+    uint64_t wait_ns;
+};
+struct PrefixLaunch {
+    PrefixParams params;
+};
+cudaError_t launch_prefix(const PrefixLaunch& launch, cudaStream_t stream);
+
 // Sets the message returned by dsa_last_error_message() on this host thread.
 void set_last_error(const char* message);
 
