@@ -202,6 +202,22 @@ dsa::RopeParams rope_params(const dsa_dims_t* d, const dsa_rope_t* r, const int3
     return p;
 }
 
+// The sizes of a shared-prefix attention call and their plan; false when they are empty or out of range.
+bool prefix_sizes(const dsa_dims_t* d, int32_t prefix_len, dsa::PrefixParams* p) {
+    memset(p, 0, sizeof *p);
+    if (d->batch < 1 || d->total_q < 1 || d->max_q_len < 1 || d->attn_heads < 1 || d->attn_heads > 128) return false;
+    if ((int64_t)d->total_q * d->attn_heads > (int64_t)INT32_MAX - 128) return false;
+    const int64_t tiles = ((int64_t)d->max_q_len * d->attn_heads + 127) / 128;
+    if ((int64_t)d->batch * tiles > (int64_t)INT32_MAX / 2) return false;
+    p->batch = d->batch;
+    p->total_q = d->total_q;
+    p->max_q_len = d->max_q_len;
+    p->heads = d->attn_heads;
+    p->prefix_len = prefix_len;
+    dsa::plan_prefix(p);
+    return true;
+}
+
 constexpr int kMaxClusterSize = 16;
 
 // Candidate positions of an indexer call: [pos_begin, pos_end) (the whole context by default).
@@ -760,7 +776,9 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* d, const dsa_rope_t* rope, const
 
 size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len) {
     if (!dims || prefix_len < 0) return 0;
-    return dsa::kErrorWordArea;
+    dsa::PrefixParams p;
+    if (!prefix_sizes(dims, prefix_len, &p)) return dsa::kErrorWordArea;
+    return dsa::kErrorWordArea + dsa::prefix_workspace_bytes(p);
 }
 
 dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void* q, const void* kv_cache,
@@ -783,6 +801,9 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
     dsa::PrefixLaunch L;
     memset(&L, 0, sizeof L);
     dsa::PrefixParams& p = L.params;
+    if (!prefix_sizes(d, prefix_len, &p))
+        return fail(DSA_ERR_UNSUPPORTED, "total_q * attn_heads (%d * %d) or batch * max_q_len (%d * %d) is too large",
+                    d->total_q, d->attn_heads, d->batch, d->max_q_len);
     p.q = static_cast<const uint16_t*>(q);
     p.kv_cache = static_cast<const uint8_t*>(kv_cache);
     p.page_table = page_table;
@@ -791,15 +812,29 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
     p.err = static_cast<int32_t*>(workspace);
-    p.batch = d->batch;
-    p.total_q = d->total_q;
     p.num_pages = d->num_pages;
     p.max_pages = d->max_pages_per_seq;
-    p.heads = d->attn_heads;
-    p.prefix_len = prefix_len;
     p.kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
     p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
     p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.plan = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea);
+    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea + dsa::prefix_plan_bytes(p));
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    auto atoms_map = [&](CUtensorMap* map, const void* base, int rank, uint64_t rows, uint32_t box_atoms, const char* name) {
+        // rows of 576 values seen as nine 64-value atoms (one 128-byte swizzle line of a row each)
+        const cuuint64_t gdim[4] = {64, (cuuint64_t)rows, 9, (cuuint64_t)d->num_pages};
+        const cuuint64_t gstride[3] = {576 * 2, 64 * 2, 64 * 576 * 2};
+        const cuuint32_t box[4] = {64, 64, box_atoms, 1}, es[4] = {1, 1, 1, 1};
+        CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), gdim, gstride, box,
+                         es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        return r == CUDA_SUCCESS ? DSA_OK : fail(DSA_ERR_CUDA, "tensor map for %s: CUresult %d", name, (int)r);
+    };
+    if ((st = atoms_map(&L.qmap, q, 3, (uint64_t)d->total_q * d->attn_heads, 9, "q"))) return st;
+    if (!p.kv_fp8 && ((st = atoms_map(&L.kmap, kv_cache, 4, 64, 3, "kv_cache")) ||
+                      (st = atoms_map(&L.vmap, kv_cache, 4, 64, 4, "kv_cache"))))
+        return st;
     cudaError_t e = dsa::launch_prefix(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
     return DSA_OK;

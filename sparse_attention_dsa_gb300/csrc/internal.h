@@ -237,8 +237,30 @@ struct PrefixParams {
     int32_t kv_fp8;
     float scale_log2;  // softmax_scale * log2(e)
     uint64_t wait_ns;
+    int32_t max_q_len;
+    // filled in by plan_prefix()
+    int32_t packed;         // rows of different sequences share tiles over the prefix
+    int32_t packed_tiles;   // 128-row tiles of all the batch's rows
+    int32_t tiles_per_seq;  // 128-row tiles of the longest sequence's rows
+    int32_t prefix_tiles;   // 128-position tiles of the prefix
+    int32_t n_items;
+    int32_t planned;  // the items' tiles are divided evenly among the CTA pairs (else: whole items in turn)
+    // workspace (planned)
+    int32_t* plan;   // [0] tiles in all, [1] parts, [4 + i] tiles before item i, i = 0..n_items
+    float* partial;  // slots of kPartialFloats
 };
+constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs
+constexpr int kPlanItems = 2048;     // most items that are divided evenly
+constexpr int kPackGain = 2;         // tiles that packing must save per pair
+// A partial result: O [128][512] fp32 (unnormalised), then (maximum in log2 units, sum) per row.
+constexpr int kPartialFloats = 128 * 512 + 2 * 128;
+void plan_prefix(PrefixParams* p);  // from the sizes alone
+size_t prefix_plan_bytes(const PrefixParams& p);
+size_t prefix_workspace_bytes(const PrefixParams& p);  // beyond the error word area
 struct PrefixLaunch {
+    CUtensorMap qmap;  // 3-D view [9][T*Hq][64] of q: 64-dim atoms of 64 rows, nine at a time
+    CUtensorMap kmap;  // 4-D view [num_pages][9][64][64] of the bf16 cache: atoms of a page, three at a time
+    CUtensorMap vmap;  // the same view, four atoms (256 dims) at a time
     PrefixParams params;
 };
 cudaError_t launch_prefix(const PrefixLaunch& launch, cudaStream_t stream);

@@ -1,11 +1,34 @@
-// Dense attention over the paged latent-KV cache for a batch whose sequences share a prefix.
+// Dense attention over the paged latent-KV cache for a batch whose sequences share a prefix, for sm_103a.
 //
 // For query token t of sequence b at position p and head h: z_s = scale * q[t,h,:] . kv[s,:] for s = 0..p,
 // out[t,h,:] = softmax(z) . kv[:, :512], lse[t,h] = logsumexp(z) ("Optimizing Inference for Hybrid Attention
 // Architectures: From Operator Fusion to Sequence Sharding", section "Breaking Down the Computational Path of
 // Hybrid Attention", step 2, without the selection).  Positions below prefix_len are read through sequence 0.
 //
-// One warp per (token, head) and a running maximum and sum over its keys.
+// Rows.  A query row is one (token, head); the latent rows are the keys and values of every head, so a
+// product tile takes 128 rows whatever tokens and heads they are.  An item is such a tile with the positions
+// it attends to, in tiles of 128:
+//   * merged: the tile's rows belong to one sequence and its positions are the prefix and then the sequence's
+//     own; with all its tiles in one place the result is written directly;
+//   * packed: an item of 128 rows of any sequences over the prefix, and for each sequence items over its own
+//     positions; the partial results of a row are combined by a second kernel.  Taken when the heads are so
+//     few that packing saves whole tiles (plan()).
+// The tiles of all items form one line that is cut into equal parts, one for each CTA pair, so that the work
+// is even whatever the lengths are; an item cut in two or more is combined from its parts.
+//
+// One CTA pair (a cluster of two, cta_group::2) works on 128 rows, 64 in each CTA, because a 128 x 512 fp32
+// accumulator would fill the tensor memory of one: the pair's products of 128 rows put the first half of the
+// columns into lanes 0-63 and the second half into lanes 64-127, so O takes 256 columns, two S tiles 64 each.
+//   S (128 x 128) = Q K^T: CTA c holds Q of its rows and K of page c of the tile (64 rows x 576 dims);
+//   O (128 x 512) += P V: CTA c holds P of its rows and V of both pages for dims 256c .. 256c + 255.
+// K and V are rings of shared-memory slots filled by TMA straight from the pages, K 192 dims and V 64 positions
+// x 256 dims at a time (a copy takes some 270 cycles to issue, whatever its size), each freed by the commit of
+// the products that read it.  A tile's P V is
+// issued behind the next tile's Q K^T, so the softmax of one tile runs under the products of the other.
+//   softmax: thread (row, column half), 64 scores each; the two halves of a row exchange their maxima through
+// shared memory.  The running maximum is raised only when it grows by more than 2^8.
+//   Tiles that some row does not see whole (the prefix's or a context's end, the causal edge) take their V
+// through registers, where infinities and NaN become 0: 0 x inf would reach rows that do not see them.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -16,6 +39,795 @@
 namespace dsa {
 namespace {
 
+constexpr uint32_t kAllLanes = 0xFFFFFFFFu;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// ---------------------------------------------------------------------------------------------------------
+// Items and their division among the CTA pairs (used by both kernels)
+// ---------------------------------------------------------------------------------------------------------
+struct Item {
+    int row0, nrows;    // rows of [T * Hq]
+    int b;              // sequence, or -1: packed rows over the prefix
+    int tiles_a;        // tiles of the prefix, then
+    int tiles_b;        // tiles of the sequence's own positions, from position base_b
+    int base_b;
+    int hi_all, hi_max;  // positions below hi_all are seen by every row, those from hi_max on by none
+    int pos0, lrow0;    // position of the sequence's first query; first row within the sequence's rows
+};
+
+// Offsets and length of sequence b; false when they are inconsistent.
+__device__ __forceinline__ bool sequence(const PrefixParams& p, int b, int* c0, int* n, int* L) {
+    const int a = __ldg(p.cu_q_lens + b), e = __ldg(p.cu_q_lens + b + 1);
+    *L = __ldg(p.seq_lens + b);
+    *c0 = a;
+    *n = e - a;
+    if (a < 0 || e < a || e > p.total_q || *n > p.max_q_len) return false;
+    if (*n == 0) return true;
+    return (int64_t)*n <= (int64_t)*L - p.prefix_len && (int64_t)*L <= (int64_t)p.max_pages * 64;
+}
+
+__device__ __forceinline__ Item decode_item(const PrefixParams& p, int i) {
+    Item it;
+    it.b = -1;
+    it.tiles_a = p.prefix_tiles;
+    it.tiles_b = it.base_b = it.pos0 = it.lrow0 = 0;
+    it.hi_all = it.hi_max = p.prefix_len;
+    const int nt = p.packed ? p.packed_tiles : 0;
+    if (i < nt) {
+        it.row0 = 128 * i;
+        it.nrows = min(128, p.total_q * p.heads - it.row0);
+        return it;
+    }
+    const int j = i - nt;
+    it.b = j / p.tiles_per_seq;
+    const int r = j - it.b * p.tiles_per_seq;
+    int c0, n, L;
+    const bool ok = sequence(p, it.b, &c0, &n, &L);
+    it.lrow0 = 128 * r;
+    it.row0 = ok ? c0 * p.heads + it.lrow0 : 0;
+    it.nrows = ok ? min(128, n * p.heads - it.lrow0) : 0;
+    if (it.nrows <= 0) {
+        it.nrows = it.tiles_a = 0;
+        return it;
+    }
+    if (p.packed) it.tiles_a = 0;
+    it.pos0 = L - n;
+    it.hi_all = it.pos0 + it.lrow0 / p.heads + 1;
+    it.hi_max = it.pos0 + (it.lrow0 + it.nrows - 1) / p.heads + 1;
+    it.base_b = p.prefix_len & ~63;
+    it.tiles_b = (it.hi_max - it.base_b + 127) / 128;
+    return it;
+}
+
+// Part k of a line of W tiles cut in G parts starts at floor(k W / G); the part that holds tile w.
+__device__ __forceinline__ int part_begin(int k, int W, int G) { return (int)((int64_t)k * W / G); }
+__device__ __forceinline__ int part_of(int w, int W, int G) { return (int)((((int64_t)w + 1) * G - 1) / W); }
+
+// Where pair k leaves its partial result of an item.  Merged: only a pair's first and last segment can be cut,
+// and a segment with the item's first tile is the last one.  Packed: every segment has a result to combine,
+// and there are at most item + pair of them before this one.
+__device__ __forceinline__ int64_t partial_slot(const PrefixParams& p, int item, int k, bool has_first_tile) {
+    return p.packed ? item + k : 2 * k + (has_first_tile ? 1 : 0);
+}
+
+// Parts of the line: no shorter than kMinTiles on average (a part has a set-up and a result to write).
+constexpr int kMinTiles = 2;
+__device__ __forceinline__ int parts_for(int W, int pairs) { return max(1, min(pairs, W / kMinTiles)); }
+
+// ---------------------------------------------------------------------------------------------------------
+// The attention kernel
+// ---------------------------------------------------------------------------------------------------------
+constexpr int kSoftmaxWarp = 4;  // warp 0: TMA, 1: products, 4-7: softmax, 8-11: V of edge tiles
+constexpr int kFillWarp = 8;
+constexpr int kFillWarps = 4;
+constexpr int kThreads = 32 * (kFillWarp + kFillWarps);
+constexpr int kQAtoms = 9;                  // 64-dim pieces of a row
+constexpr int kAtom = 64 * 128;             // 64 rows x 128 bytes, 128-byte swizzle
+constexpr int kKAtoms = 3, kKSlots = 3;     // K ring: slots of three atoms (one copy each)
+constexpr int kKSlot = kKAtoms * kAtom;
+constexpr int kVSlots = 2;                  // V ring: slots of 64 positions x 256 dims
+constexpr int kVSlot = 4 * kAtom;
+constexpr int kPBytes = 2 * kAtom;          // 64 rows x 128 positions
+constexpr int kSCol = 256;                  // tensor memory: O in columns 0-255, S tiles at 256 and 320
+constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
+constexpr uint32_t kIdescPV = make_idesc(128, 256, 1, 1, 0, 1);
+constexpr float kRaise = 8.f;  // raise the running maximum (log2) only when it grows by more than this
+
+struct Ctrl {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[kKSlots], k_empty[kKSlots];
+    uint64_t v_full[kVSlots], v_empty[kVSlots];
+    uint64_t s_full[2], s_empty[2];
+    uint64_t p_full, pv_done, o_free, edge_full, drained, exchanged;
+    uint32_t tmem_base;
+    int32_t failed;
+    int32_t total, parts, first_item, first_tile;  // this pair's place on the line
+    int32_t scan[kThreads / 32];
+    float exchange[2][128];
+};
+constexpr int kSmem = 1024 + kQAtoms * kAtom + kKSlots * kKSlot + kVSlots * kVSlot + kPBytes + (int)sizeof(Ctrl);
+static_assert(kSmem <= 232448, "shared memory of one CTA");
+static_assert(kQAtoms % kKAtoms == 0, "whole slots");
+static_assert(kPlanItems * 4 <= kKSlots * kKSlot, "the plan's scan is done in the K ring's memory");
+
+// Where a role stands in its pair's list of segments.
+struct Walk {
+    int item, tile, left;  // next item and tile, tiles left (planned) or the stride (whole items)
+};
+struct Segment {
+    Item it;
+    int index;   // item number
+    int u0, u1;  // tiles of the item
+};
+
+__device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Segment& s) {
+    if (p.planned) {
+        while (w.left > 0 && w.item < p.n_items) {
+            s.it = decode_item(p, w.item);
+            const int tiles = s.it.tiles_a + s.it.tiles_b;
+            if (w.tile < tiles) {
+                s.index = w.item;
+                s.u0 = w.tile;
+                s.u1 = min(tiles, w.tile + w.left);
+                w.left -= s.u1 - s.u0;
+                w.tile = s.u1;
+                if (s.u1 == tiles) {
+                    ++w.item;
+                    w.tile = 0;
+                }
+                return true;
+            }
+            ++w.item;
+            w.tile = 0;
+        }
+        return false;
+    }
+    while (w.item >= 0) {  // whole items, the ones with the most positions (the last of each sequence) first
+        s.it = decode_item(p, w.item);
+        s.index = w.item;
+        s.u0 = 0;
+        s.u1 = s.it.tiles_a + s.it.tiles_b;
+        w.item -= w.left;
+        if (s.u1 > 0) return true;
+    }
+    return false;
+}
+
+// Tile u of an item: its first position, the range that exists, its page-table row, whether every row sees it whole.
+struct Tile {
+    int base, lo, hi;
+    const int32_t* pages;
+    bool edge;
+};
+__device__ __forceinline__ Tile tile_of(const PrefixParams& p, const Item& it, int u) {
+    Tile t;
+    if (u < it.tiles_a) {
+        t.base = 128 * u;
+        t.lo = 0;
+        t.hi = p.prefix_len;
+        t.pages = p.page_table;
+        t.edge = t.base + 128 > t.hi;
+    } else {
+        t.base = it.base_b + 128 * (u - it.tiles_a);
+        t.lo = p.prefix_len;
+        t.hi = it.hi_max;
+        t.pages = p.page_table + (int64_t)it.b * p.max_pages;
+        t.edge = t.base < t.lo || t.base + 128 > it.hi_all;
+    }
+    return t;
+}
+// Table entry of half h (64 positions) of a tile; kNoPage where it has no position that exists.  The entry is
+// checked where it is used, a tile later, so that nothing waits for its load here.
+constexpr int kNoPage = INT32_MIN;
+__device__ __forceinline__ int page_of(const Tile& t, int h) {
+    const int first = t.base + 64 * h;
+    return first < t.hi ? __ldg(t.pages + (first >> 6)) : kNoPage;
+}
+
+// Infinities and NaN of a bf16 pair become 0.
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+    return v;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2^-22; exp2(-inf) = +0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefix_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const PrefixParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* q_s = smem;
+    uint8_t* k_s = q_s + kQAtoms * kAtom;
+    uint8_t* v_s = k_s + kKSlots * kKSlot;
+    uint8_t* p_s = v_s + kVSlots * kVSlot;
+    Ctrl* ctl = reinterpret_cast<Ctrl*>(p_s + kPBytes);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    allow_dependent_launch();  // the combining kernel waits for this one's end before it reads anything
+
+    // ---- the division of the work ----
+    if (pair == 0 && rank == 0) {  // inconsistent sequences and tokens of no sequence are reported once
+        for (int b = tid; b < p.batch; b += kThreads) {
+            int c0, n, L;
+            if (!sequence(p, b, &c0, &n, &L)) raise_error(p.err, DSA_DEVERR_SEQ);
+        }
+        if (tid == 0 && (__ldg(p.cu_q_lens) != 0 || __ldg(p.cu_q_lens + p.batch) != p.total_q))
+            raise_error(p.err, DSA_DEVERR_SEQ);
+    }
+    Walk start;
+    if (p.planned) {
+        // tiles before each item: every thread a run of items, then a scan of the threads' sums
+        int32_t* cum = reinterpret_cast<int32_t*>(k_s);
+        const int run = (p.n_items + kThreads - 1) / kThreads;
+        const int i0 = min(p.n_items, tid * run), i1 = min(p.n_items, i0 + run);
+        int sum = 0;
+        for (int i = i0; i < i1; ++i) {
+            const Item it = decode_item(p, i);
+            cum[i] = it.tiles_a + it.tiles_b;
+            sum += cum[i];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(kAllLanes, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (lane == 31) ctl->scan[warp] = incl;
+        __syncthreads();
+        int before = incl - sum, W = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += ctl->scan[w];
+            W += ctl->scan[w];
+        }
+        const int G = parts_for(W, pairs);
+        if (pair == 0 && rank == 0 && tid == 0) {
+            p.plan[0] = W;
+            p.plan[1] = G;
+            p.plan[4 + p.n_items] = W;
+        }
+        if (pair >= G || W == 0) {
+            if (pair != 0 || rank != 0) return;  // uniform over the pair but for the plan's writer, below
+        }
+        const int w0 = W > 0 ? part_begin(pair, W, G) : 0;
+        for (int i = i0; i < i1; ++i) {
+            const int tiles = cum[i];
+            if (pair == 0 && rank == 0) p.plan[4 + i] = before;
+            if (w0 >= before && w0 < before + tiles) {
+                ctl->first_item = i;
+                ctl->first_tile = w0 - before;
+            }
+            before += tiles;
+        }
+        if (W == 0) return;  // (the writer of the plan's pair: its partner has returned too)
+        fence_proxy_async_smem();  // the scan's memory is the K ring's, which the async proxy writes next
+        __syncthreads();
+        start.item = ctl->first_item;
+        start.tile = ctl->first_tile;
+        start.left = part_begin(pair + 1, W, G) - w0;
+    } else {
+        start.item = p.n_items - 1 - pair;
+        start.tile = 0;
+        start.left = pairs;
+        if (start.item < 0) return;  // uniform over the pair
+    }
+
+    // ---- set-up ----
+    if (tid == 0) {
+        prefetch_tensormap(&qmap);
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+        mbar_init(&ctl->q_full, 1);
+        mbar_init(&ctl->q_empty, 1);
+        for (int i = 0; i < kKSlots; ++i) {
+            mbar_init(&ctl->k_full[i], 1);
+            mbar_init(&ctl->k_empty[i], 1);
+        }
+        for (int i = 0; i < kVSlots; ++i) {
+            mbar_init(&ctl->v_full[i], 1);
+            mbar_init(&ctl->v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->s_empty[i], 8);  // the softmax warps of both CTAs
+        }
+        mbar_init(&ctl->p_full, 8);
+        mbar_init(&ctl->pv_done, 1);
+        mbar_init(&ctl->o_free, 8);
+        mbar_init(&ctl->edge_full, 2 * kFillWarps);
+        mbar_init(&ctl->drained, 1);
+        mbar_init(&ctl->exchanged, 4);
+        ctl->failed = 0;
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tmem_pair_alloc(&ctl->tmem_base, 512);
+        tmem_pair_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers exist before anything arrives on them
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    auto leader = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(kAllLanes, mbar_wait(bar, parity, p.err, p.wait_ns)) != 0;
+    };
+    bool ok = true;
+
+    if (warp == 0) {
+        // ---------------- loads: Q of a segment, then K(u) and V(u - 1) in the order of their use ----------------
+        Walk w = start;
+        Segment s;
+        uint32_t seg = 0, kslot = 0, kphase = 1, vslot = 0, vphase = 1;
+        const uint32_t q_full = leader(&ctl->q_full), k_full = leader(&ctl->k_full[0]), v_full = leader(&ctl->v_full[0]);
+        while (ok && next_segment(p, w, s)) {
+            if (seg > 0 && !(ok = wait(&ctl->q_empty, (seg - 1) & 1u))) break;
+            if (elect_one_sync()) {
+                if (rank == 0) mbar_arrive_expect_tx(&ctl->q_full, 2 * kQAtoms * kAtom);
+                tma_pair_load_3d(q_s, &qmap, q_full, 0, s.it.row0 + 64 * rank, 0);
+            }
+            ++seg;
+            Tile t = tile_of(p, s.it, s.u0), tv = t;
+            int page0 = page_of(t, 0), page1 = page_of(t, 1), vpage0 = 0, vpage1 = 0;
+            for (int u = s.u0; ok && u <= s.u1; ++u) {
+                Tile tn = t;
+                int next0 = kNoPage, next1 = kNoPage;
+                if (u + 1 < s.u1) {
+                    tn = tile_of(p, s.it, u + 1);
+                    next0 = page_of(tn, 0);
+                    next1 = page_of(tn, 1);
+                }
+                if (u < s.u1) {
+                    // entries out of range are reported; behind the last page the copy writes zeros
+                    const bool in0 = page0 >= 0 && page0 < p.num_pages, in1 = page1 >= 0 && page1 < p.num_pages;
+                    if (((!in0 && page0 != kNoPage) || (!in1 && page1 != kNoPage)) && rank == 0 && lane == 0)
+                        raise_error(p.err, DSA_DEVERR_PAGE);
+                    if (!in0) page0 = p.num_pages;
+                    if (!in1) page1 = p.num_pages;
+                    const int page = rank == 0 ? page0 : page1;
+#pragma unroll 1
+                    for (int a = 0; a < kQAtoms; a += kKAtoms) {
+                        if (!(ok = wait(&ctl->k_empty[kslot], kphase))) break;
+                        if (elect_one_sync()) {
+                            if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[kslot], 2 * kKSlot);
+                            tma_pair_load_4d(k_s + kslot * kKSlot, &kmap, k_full + 8 * kslot, 0, 0, a, page);
+                        }
+                        if (++kslot == kKSlots) {
+                            kslot = 0;
+                            kphase ^= 1u;
+                        }
+                    }
+                }
+                if (ok && u > s.u0) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        if (!(ok = wait(&ctl->v_empty[vslot], vphase))) break;
+                        if (elect_one_sync()) {
+                            if (tv.edge) {  // filled by the warps below, which have a barrier of their own
+                                if (rank == 0) mbar_arrive(&ctl->v_full[vslot]);
+                            } else {
+                                if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[vslot], 2 * kVSlot);
+                                tma_pair_load_4d(v_s + vslot * kVSlot, &vmap, v_full + 8 * vslot, 0, 0, 4 * rank,
+                                                 h == 0 ? vpage0 : vpage1);
+                            }
+                        }
+                        if (++vslot == kVSlots) {
+                            vslot = 0;
+                            vphase ^= 1u;
+                        }
+                    }
+                }
+                vpage0 = page0;
+                vpage1 = page1;
+                tv = t;
+                page0 = next0;
+                page1 = next1;
+                t = tn;
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---------------- products: S(u) = Q K(u)^T, then O += P(u - 1) V(u - 1) ----------------
+        Walk w = start;
+        Segment s;
+        uint32_t seg = 0, tile = 0, edges = 0, kslot = 0, kphase = 0, vslot = 0, vphase = 0;
+        const uint64_t qd = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
+        const uint64_t kd = smem_desc(smem_u32(k_s), 16, 1024, kSwizzle128B);
+        const uint64_t pd = smem_desc(smem_u32(p_s), 16, 1024, kSwizzle128B);
+        const uint64_t vd = smem_desc(smem_u32(v_s), kAtom, 1024, kSwizzle128B);  // MN-major, atoms kAtom apart
+        auto pv = [&](uint32_t n, bool first, bool edge) {  // n: number of the tile among all of this pair's
+            if (!wait(&ctl->p_full, n & 1u)) return false;
+            if (edge && !wait(&ctl->edge_full, edges++ & 1u)) return false;
+            if (first && seg > 1 && !wait(&ctl->o_free, seg & 1u)) return false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!wait(&ctl->v_full[vslot], vphase)) return false;
+                tc_fence_after();
+                if (elect_one_sync()) {
+                    const uint64_t b = vd + vslot * (kVSlot / 16);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            umma_pair_f16_ss(tmem + 128 * j, pd + (uint64_t)(h * (kAtom / 16) + 2 * kk),
+                                             b + (uint64_t)(j * (2 * kAtom / 16) + 128 * kk), kIdescPV,
+                                             first && h == 0 && kk == 0 ? 0u : 1u);
+                    umma_pair_commit(&ctl->v_empty[vslot], 3);
+                    if (h == 1) umma_pair_commit(&ctl->pv_done, 3);
+                }
+                if (++vslot == kVSlots) {
+                    vslot = 0;
+                    vphase ^= 1u;
+                }
+            }
+            return true;
+        };
+        while (ok && next_segment(p, w, s)) {
+            if (!(ok = wait(&ctl->q_full, seg & 1u))) break;
+            ++seg;
+            bool edge = false;
+            for (int u = s.u0; ok && u < s.u1; ++u, ++tile) {
+                const uint32_t buf = tile & 1u;
+                const bool last = u == s.u1 - 1;
+                if (!(ok = wait(&ctl->s_empty[buf], ((tile >> 1) & 1u) ^ 1u))) break;
+#pragma unroll
+                for (int a = 0; a < kQAtoms; a += kKAtoms) {
+                    if (!(ok = wait(&ctl->k_full[kslot], kphase))) break;
+                    tc_fence_after();
+                    if (elect_one_sync()) {
+                        const uint64_t b = kd + kslot * (kKSlot / 16);
+                        const uint32_t d = tmem + kSCol + 64 * buf;
+#pragma unroll
+                        for (int kk = 0; kk < 4 * kKAtoms; ++kk)
+                            umma_pair_f16_ss(d, qd + (uint64_t)((a + kk / 4) * (kAtom / 16) + 2 * (kk & 3)),
+                                             b + (uint64_t)((kk / 4) * (kAtom / 16) + 2 * (kk & 3)), kIdescQK,
+                                             a == 0 && kk == 0 ? 0u : 1u);
+                        umma_pair_commit(&ctl->k_empty[kslot], 3);
+                        if (a == kQAtoms - kKAtoms) {
+                            umma_pair_commit(&ctl->s_full[buf], 3);
+                            if (last) umma_pair_commit(&ctl->q_empty, 3);
+                        }
+                    }
+                    if (++kslot == kKSlots) {
+                        kslot = 0;
+                        kphase ^= 1u;
+                    }
+                }
+                if (ok && u > s.u0) ok = pv(tile - 1, u == s.u0 + 1, edge);
+                edge = tile_of(p, s.it, u).edge;
+            }
+            if (ok) ok = pv(tile - 1, s.u1 == s.u0 + 1, edge);
+        }
+        // drain (default limit): every product of the pair is done before its memory is given back
+        if (elect_one_sync()) {
+            umma_pair_commit(&ctl->drained, 1);
+            mbar_wait(&ctl->drained, 0, p.err);
+        }
+        __syncwarp();
+    } else if (warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4) {
+        // ---------------- softmax: thread (row, half of the positions) ----------------
+        Walk w = start;
+        Segment s;
+        const int st = tid - 32 * kSoftmaxWarp;  // lane of tensor memory
+        const int half = st >> 6, r = st & 63;
+        const uint32_t trow = tmem + ((uint32_t)(st & ~31) << 16);
+        const uint32_t s_empty = leader(&ctl->s_empty[0]), p_full = leader(&ctl->p_full), o_free = leader(&ctl->o_free);
+        const uint32_t p_row = smem_u32(p_s) + half * kAtom + r * 128;
+        uint32_t tile = 0, swaps = 0;
+        // A value of the row's other half (tensor-memory lane st ^ 64).  Two buffers, and a bounded wait instead
+        // of a block barrier, so that a warp that has given up stops no other.
+        auto swap = [&](float mine, float* other) {
+            ctl->exchange[swaps & 1u][st] = mine;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->exchanged);
+            if (!wait(&ctl->exchanged, swaps & 1u)) return false;
+            *other = ctl->exchange[swaps & 1u][st ^ 64];
+            ++swaps;
+            return true;
+        };
+        while (ok && next_segment(p, w, s)) {
+            const int tr = 64 * rank + r;  // row of the tile
+            // positions this row sees: below `limit`
+            const int limit = s.it.b < 0 ? p.prefix_len : s.it.pos0 + (s.it.lrow0 + tr) / p.heads + 1;
+            float m_used = -INFINITY, l_sum = 0.f;
+            Tile t = tile_of(p, s.it, s.u0);
+            int pg = page_of(t, half);
+            for (int u = s.u0; u < s.u1; ++u, ++tile) {
+                const uint32_t buf = tile & 1u;
+                const Tile cur = t;
+                const bool bad_page = pg < 0 || pg >= p.num_pages;
+                if (u + 1 < s.u1) {
+                    t = tile_of(p, s.it, u + 1);
+                    pg = page_of(t, half);
+                }
+                if (!(ok = wait(&ctl->s_full[buf], (tile >> 1) & 1u))) break;
+                tc_fence_after();
+                float sv[64];
+                {
+                    float a0[16], a1[16], a2[16], a3[16];
+                    const uint32_t col = trow + kSCol + 64 * buf;
+                    tmem_ld16(col, a0);
+                    tmem_ld16(col + 16, a1);
+                    tmem_ld16(col + 32, a2);
+                    tmem_ld16(col + 48, a3);
+                    tmem_ld_wait();
+                    tmem_regs_ready(a0);
+                    tmem_regs_ready(a1);
+                    tmem_regs_ready(a2);
+                    tmem_regs_ready(a3);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        sv[j] = a0[j];
+                        sv[16 + j] = a1[j];
+                        sv[32 + j] = a2[j];
+                        sv[48 + j] = a3[j];
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(s_empty + 8 * buf);
+                if (cur.edge || bad_page) {
+                    const int first = cur.base + 64 * half;
+                    const int lo = bad_page ? 64 : cur.lo - first, hi = min(cur.hi, limit) - first;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (j < lo || j >= hi) sv[j] = -INFINITY;
+                }
+                float mx[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) mx[k] = fmaxf(fmaxf(sv[k], sv[k + 16]), fmaxf(sv[k + 32], sv[k + 48]));
+#pragma unroll
+                for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+                    for (int k = 0; k < n; ++k) mx[k] = fmaxf(mx[k], mx[k + n]);
+                float other;
+                if (!(ok = swap(mx[0], &other))) break;
+                const float mt = fmaxf(mx[0], other) * p.scale_log2;
+                const bool raise = mt > m_used + kRaise;
+                const float m_new = raise ? mt : m_used;
+                const float alpha = (raise && m_used != -INFINITY) ? exp2f(m_used - m_new) : 1.f;
+                const float mu = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf) = 0
+                // weights: the sum takes the fp32 values, the products their bf16 rounding (at most 2^-9 each
+                // way, unbiased), so that lse keeps fp32 accuracy
+                uint32_t packed[32];
+                float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) {
+                    const float e0 = exp2_fast(fmaf(sv[j], p.scale_log2, -mu));
+                    const float e1 = exp2_fast(fmaf(sv[j + 1], p.scale_log2, -mu));
+                    packed[j / 2] = f2_to_bf2(e0, e1);
+                    ps[(j / 2) & 7] += e0 + e1;
+                }
+                const float rs = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+                // the previous tile's P V is done: P may be overwritten, O is still
+                if (tile > 0 && !(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
+                tc_fence_after();
+                if (u > s.u0 && __any_sync(kAllLanes, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int c = 0; c < 256; c += 16) {
+                        float o[16];
+                        tmem_ld16(trow + c, o);
+                        tmem_ld_wait();
+                        tmem_regs_ready(o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] *= alpha;
+                        tmem_st16(trow + c, o);
+                    }
+                    tmem_st_wait();
+                }
+                l_sum = l_sum * alpha + rs;
+                m_used = m_new;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    st_shared_v4(p_row + ((c ^ (r & 7)) << 4),
+                                 make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]));
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(p_full);
+            }
+            if (!ok) break;
+            // ---- the segment's result: O / l and lse, or O, m and l for the combining kernel ----
+            if (!(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
+            tc_fence_after();
+            float other;
+            if (!(ok = swap(l_sum, &other))) break;
+            const float l = half == 0 ? l_sum + other : other + l_sum;  // the same sum in both halves
+            const bool whole = s.u0 == 0 && s.u1 == s.it.tiles_a + s.it.tiles_b && !p.packed;
+            const bool mine = tr < s.it.nrows;
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t row = (int64_t)s.it.row0 + tr;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 16) {
+                    float o[16];
+                    tmem_ld16(trow + c, o);
+                    tmem_ld_wait();
+                    tmem_regs_ready(o);
+                    if (mine) {
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) pk[j] = f2_to_bf2(o[2 * j] * inv, o[2 * j + 1] * inv);
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + row * 512 + 256 * half + c);
+                        dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    }
+                }
+                if (mine && half == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+            } else {
+                float* slot = p.partial + partial_slot(p, s.index, pair, s.u0 == 0) * kPartialFloats;
+#pragma unroll 1
+                for (int c = 0; c < 256; c += 16) {
+                    float o[16];
+                    tmem_ld16(trow + c, o);
+                    tmem_ld_wait();
+                    tmem_regs_ready(o);
+                    if (mine) {
+                        float4* dst = reinterpret_cast<float4*>(slot + tr * 512 + 256 * half + c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                }
+                if (mine && half == 0) reinterpret_cast<float2*>(slot + 128 * 512)[tr] = make_float2(m_used, l);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(o_free);
+        }
+    } else if (warp >= kFillWarp) {
+        // ---------------- V of edge tiles, through registers ----------------
+        Walk w = start;
+        Segment s;
+        const int fw = warp - kFillWarp;
+        static_assert(kFillWarps == 4, "16 rows of a page each");
+        const uint32_t edge_full = leader(&ctl->edge_full);
+        uint32_t vphase = 1;  // a tile takes every slot of the V ring once
+        static_assert(kVSlots == 2, "one slot for each page of a tile");
+        while (ok && next_segment(p, w, s)) {
+            for (int u = s.u0; ok && u < s.u1; ++u, vphase ^= 1u) {
+                const Tile t = tile_of(p, s.it, u);
+                if (!t.edge) {
+                    // keep step with the ring (a parity names one of two phases: never run further ahead)
+                    ok = wait(&ctl->v_empty[0], vphase);
+                    continue;
+                }
+                for (int h = 0; ok && h < 2; ++h) {
+                    const int pg = page_of(t, h);
+                    const bool in = pg >= 0 && pg < p.num_pages;
+                    // a row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 are this warp's
+                    const int row0 = 16 * fw, pos0 = t.base + 64 * h + row0;
+                    const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * 1152 + 512 * rank + 16 * lane;
+                    uint4 v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        v[k] = in && pos0 + k >= t.lo && pos0 + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
+                                                                         : make_uint4(0, 0, 0, 0);
+                    if (!(ok = wait(&ctl->v_empty[h], vphase))) break;
+                    const uint32_t dst = smem_u32(v_s + h * kVSlot + (lane >> 3) * kAtom);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        st_shared_v4(dst + (row0 + k) * 128 + (((lane & 7) ^ (k & 7)) << 4),
+                                     make_uint4(finite2(v[k].x), finite2(v[k].y), finite2(v[k].z), finite2(v[k].w)));
+                }
+                if (!ok) break;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(edge_full);
+            }
+        }
+    }
+    if (!ok && lane == 0) ctl->failed = 1;
+    tc_fence_before();
+    __syncthreads();
+    if (ctl->failed && tid == 0) {
+        // a wait gave up: nobody consumed the copies still in flight, so leave them time to land (they take
+        // microseconds) before this shared memory is given back
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+    }
+    cluster_sync();  // neither CTA leaves before the other's products, copies and arrivals are done
+    tc_fence_after();
+    if (warp == 2) tmem_pair_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// Combination of partial results: one warp per row.
+//   M = max m_k, L = sum_k l_k 2^(m_k - M), out = sum_k 2^(m_k - M) O_k / L, lse = (M + log2 L) ln 2
+// ---------------------------------------------------------------------------------------------------------
+constexpr int kCombineWarps = 4;
+
+__global__ void __launch_bounds__(32 * kCombineWarps) prefix_combine_kernel(const PrefixParams p) {
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+    const int rows = p.total_q * p.heads;
+    if (row >= rows) return;
+    grid_dependency_wait();
+    const int t = row / p.heads;
+    int b = -1;
+    for (int j0 = 0; j0 < p.batch && b < 0; j0 += 32) {
+        const int j = j0 + lane;
+        const bool hit = j < p.batch && __ldg(p.cu_q_lens + j) <= t && t < __ldg(p.cu_q_lens + j + 1);
+        const uint32_t bal = __ballot_sync(kAllLanes, hit);
+        if (bal) b = j0 + __ffs(bal) - 1;
+    }
+    if (b < 0) return;
+    int c0, n, L;
+    if (!sequence(p, b, &c0, &n, &L)) return;  // reported by the attention kernel
+    const int W = __ldcg(p.plan), G = __ldcg(p.plan + 1);
+    const int local = row - c0 * p.heads;
+    // up to two items hold this row: packed rows over the prefix, and the sequence's own
+    int k_first[2], count[2], in_tile[2];
+    const int nt = p.packed ? p.packed_tiles : 0;
+    const int items[2] = {nt + b * p.tiles_per_seq + local / 128, p.packed && p.prefix_tiles > 0 ? row / 128 : -1};
+    in_tile[0] = local & 127;
+    in_tile[1] = row & 127;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        k_first[k] = count[k] = 0;
+        if (items[k] < 0) continue;
+        const int a = __ldcg(p.plan + 4 + items[k]), e = __ldcg(p.plan + 5 + items[k]);
+        if (e <= a) continue;
+        const int k0 = part_of(a, W, G), k1 = part_of(e - 1, W, G);
+        k_first[k] = k0;
+        count[k] = k1 - k0 + 1;
+    }
+    if (!p.packed && count[0] == 1) return;  // written by the attention kernel
+    const int parts = count[0] + count[1];
+    auto part = [&](int i) -> const float* {
+        const int k = i < count[0] ? 0 : 1, j = k ? i - count[0] : i;
+        return p.partial + partial_slot(p, items[k], k_first[k] + j, j == 0) * kPartialFloats;
+    };
+    auto tile_row = [&](int i) { return i < count[0] ? in_tile[0] : in_tile[1]; };
+    auto stats = [&](int i) {
+        return i < parts ? __ldcg(reinterpret_cast<const float2*>(part(i) + 128 * 512) + tile_row(i)) : make_float2(-INFINITY, 0.f);
+    };
+    float M = -INFINITY;
+    for (int i0 = 0; i0 < parts; i0 += 32) M = fmaxf(M, stats(i0 + lane).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kAllLanes, M, off));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float Ls = 0.f, acc[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        const float2 ml = stats(i0 + lane);
+        const float wl = exp2f(ml.x - mu);  // 0 for a part without a score; NaN stays NaN
+        float lw = ml.y * wl;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(kAllLanes, lw, off);
+        Ls += lw;
+        for (int i = i0; i < min(parts, i0 + 32); ++i) {
+            const float wgt = __shfl_sync(kAllLanes, wl, i - i0);
+            if (wgt == 0.f) continue;
+            const float4* o = reinterpret_cast<const float4*>(part(i) + tile_row(i) * 512);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 v = __ldcg(o + 32 * k + lane);
+                acc[4 * k] += wgt * v.x;
+                acc[4 * k + 1] += wgt * v.y;
+                acc[4 * k + 2] += wgt * v.z;
+                acc[4 * k + 3] += wgt * v.w;
+            }
+        }
+    }
+    const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        reinterpret_cast<uint2*>(p.out + (int64_t)row * 512)[32 * k + lane] =
+            make_uint2(f2_to_bf2(acc[4 * k] * inv, acc[4 * k + 1] * inv), f2_to_bf2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+    if (lane == 0 && p.lse) p.lse[row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// FP8 rows: one warp per (token, head), a running maximum and sum over its positions
+// ---------------------------------------------------------------------------------------------------------
 constexpr int kWarps = 4;
 
 // Values 2*lane + 64*i, +1 (i = 0..8) of a cache row.
@@ -110,15 +922,53 @@ __global__ void __launch_bounds__(32 * kWarps) prefix_simple_kernel(const Prefix
 
 }  // namespace
 
+// Whether rows of different sequences share tiles over the prefix, and how many items there are.
+void plan_prefix(PrefixParams* p) {
+    const int64_t rows = (int64_t)p->total_q * p->heads;
+    p->prefix_tiles = (p->prefix_len + 127) / 128;
+    p->packed_tiles = (int)((rows + 127) / 128);
+    p->tiles_per_seq = (int)(((int64_t)p->max_q_len * p->heads + 127) / 128);
+    const int64_t merged = (int64_t)p->batch * p->tiles_per_seq;
+    // Packing saves (merged - packed_tiles) passes over the prefix, spread over the pairs, and costs a second
+    // launch and a result per sequence written and read once more.
+    p->packed = merged + p->packed_tiles <= kPlanItems &&
+                (merged - p->packed_tiles) * p->prefix_tiles > kPackGain * (int64_t)kPrefixPairs;
+    const int64_t items = merged + (p->packed ? p->packed_tiles : 0);
+    p->n_items = (int)items;
+    // Many items: each pair takes whole ones in turn; no cuts, so nothing to combine.
+    p->planned = items <= kPlanItems;
+}
+
+size_t prefix_workspace_bytes(const PrefixParams& p) {
+    if (!p.planned) return 0;
+    const int64_t slots = p.packed ? p.n_items + kPrefixPairs : 2 * kPrefixPairs;
+    return (size_t)slots * kPartialFloats * sizeof(float) + prefix_plan_bytes(p);
+}
+size_t prefix_plan_bytes(const PrefixParams& p) { return ((size_t)(p.n_items + 5) * sizeof(int32_t) + 255) / 256 * 256; }
+
 cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     const PrefixParams& p = L.params;
-    const int64_t rows = (int64_t)p.total_q * p.heads;
-    const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
-    if (p.kv_fp8)
-        prefix_simple_kernel<true><<<blocks, 32 * kWarps, 0, stream>>>(p);
-    else
-        prefix_simple_kernel<false><<<blocks, 32 * kWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (p.kv_fp8) {
+        const int64_t rows = (int64_t)p.total_q * p.heads;
+        prefix_simple_kernel<true><<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    cudaError_t e = cudaFuncSetAttribute(prefix_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const int pairs = (int)(p.planned ? kPrefixPairs : (p.n_items < kPrefixPairs ? p.n_items : kPrefixPairs));
+    prefix_pair_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(L.qmap, L.kmap, L.vmap, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !p.planned) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)((p.total_q * p.heads + kCombineWarps - 1) / kCombineWarps));
+    cfg.blockDim = dim3(32 * kCombineWarps);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefix_combine_kernel, p);
 }
 
 }  // namespace dsa
