@@ -214,7 +214,7 @@ bool prefix_sizes(const dsa_dims_t* d, int32_t prefix_len, dsa::PrefixParams* p)
     p->max_q_len = d->max_q_len;
     p->heads = d->attn_heads;
     p->prefix_len = prefix_len;
-    dsa::plan_prefix(p);
+    dsa::plan_prefix(p, d->max_pages_per_seq);
     return true;
 }
 

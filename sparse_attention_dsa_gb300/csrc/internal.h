@@ -246,15 +246,16 @@ struct PrefixParams {
     int32_t n_items;
     int32_t planned;  // the items' tiles are divided evenly among the CTA pairs (else: whole items in turn)
     // workspace (planned)
-    int32_t* plan;   // [0] tiles in all, [1] parts, [4 + i] tiles before item i, i = 0..n_items
+    int32_t* plan;   // [0] places on the line, [1] parts, [4 + i] places before item i, i = 0..n_items
     float* partial;  // slots of kPartialFloats
 };
 constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs
 constexpr int kPlanItems = 2048;     // most items that are divided evenly
-constexpr int kPackGain = 2;         // tiles that packing must save per pair
+constexpr int kPackCost = 5;         // what a partial result costs, in tiles
+constexpr int kWholeTiles = 6;       // contexts of no more tiles are not divided
 // A partial result: O [128][512] fp32 (unnormalised), then (maximum in log2 units, sum) per row.
 constexpr int kPartialFloats = 128 * 512 + 2 * 128;
-void plan_prefix(PrefixParams* p);  // from the sizes alone
+void plan_prefix(PrefixParams* p, int max_pages);  // from the sizes alone
 size_t prefix_plan_bytes(const PrefixParams& p);
 size_t prefix_workspace_bytes(const PrefixParams& p);  // beyond the error word area
 struct PrefixLaunch {

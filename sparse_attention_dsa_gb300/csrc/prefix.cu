@@ -13,8 +13,9 @@
 //   * packed: an item of 128 rows of any sequences over the prefix, and for each sequence items over its own
 //     positions; the partial results of a row are combined by a second kernel.  Taken when the heads are so
 //     few that packing saves whole tiles (plan()).
-// The tiles of all items form one line that is cut into equal parts, one for each CTA pair, so that the work
-// is even whatever the lengths are; an item cut in two or more is combined from its parts.
+// The tiles of all items form one line (each item with a few places for what it costs beside its tiles) that is
+// cut into equal parts, one for each CTA pair, so that the work is even whatever the lengths are; an item cut in
+// two or more is combined from its parts.
 //
 // One CTA pair (a cluster of two, cta_group::2) works on 128 rows, 64 in each CTA, because a 128 x 512 fp32
 // accumulator would fill the tensor memory of one: the pair's products of 128 rows put the first half of the
@@ -110,9 +111,15 @@ __device__ __forceinline__ int64_t partial_slot(const PrefixParams& p, int item,
     return p.packed ? item + k : 2 * k + (has_first_tile ? 1 : 0);
 }
 
-// Parts of the line: no shorter than kMinTiles on average (a part has a set-up and a result to write).
-constexpr int kMinTiles = 2;
-__device__ __forceinline__ int parts_for(int W, int pairs) { return max(1, min(pairs, W / kMinTiles)); }
+// On the line an item is kItemCost places longer than its tiles, in front of them: what its queries' load, its
+// first tile's latency and its result cost in tiles.  Parts are no shorter than kMinPlaces on average.
+constexpr int kItemCost = 2;
+constexpr int kMinPlaces = 2 + kItemCost;
+__device__ __forceinline__ int parts_for(int W, int pairs) { return max(1, min(pairs, W / kMinPlaces)); }
+__device__ __forceinline__ int places(const Item& it) {
+    const int tiles = it.tiles_a + it.tiles_b;
+    return tiles > 0 ? tiles + kItemCost : 0;
+}
 
 // ---------------------------------------------------------------------------------------------------------
 // The attention kernel
@@ -152,7 +159,7 @@ static_assert(kPlanItems * 4 <= kKSlots * kKSlot, "the plan's scan is done in th
 
 // Where a role stands in its pair's list of segments.
 struct Walk {
-    int item, tile, left;  // next item and tile, tiles left (planned) or the stride (whole items)
+    int item, tile, left;  // next item, place in it, places left (planned) or the stride (whole items)
 };
 struct Segment {
     Item it;
@@ -165,20 +172,15 @@ __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Seg
         while (w.left > 0 && w.item < p.n_items) {
             s.it = decode_item(p, w.item);
             const int tiles = s.it.tiles_a + s.it.tiles_b;
-            if (w.tile < tiles) {
+            if (tiles > 0) {  // w.tile counts places: the first kItemCost stand for no tile
                 s.index = w.item;
-                s.u0 = w.tile;
-                s.u1 = min(tiles, w.tile + w.left);
-                w.left -= s.u1 - s.u0;
-                w.tile = s.u1;
-                if (s.u1 == tiles) {
-                    ++w.item;
-                    w.tile = 0;
-                }
-                return true;
+                s.u0 = max(0, w.tile - kItemCost);
+                s.u1 = min(tiles, w.tile + w.left - kItemCost);
+                w.left -= tiles + kItemCost - w.tile;
             }
             ++w.item;
             w.tile = 0;
+            if (tiles > 0 && s.u1 > s.u0) return true;
         }
         return false;
     }
@@ -252,73 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     allow_dependent_launch();  // the combining kernel waits for this one's end before it reads anything
 
-    // ---- the division of the work ----
-    if (pair == 0 && rank == 0) {  // inconsistent sequences and tokens of no sequence are reported once
-        for (int b = tid; b < p.batch; b += kThreads) {
-            int c0, n, L;
-            if (!sequence(p, b, &c0, &n, &L)) raise_error(p.err, DSA_DEVERR_SEQ);
-        }
-        if (tid == 0 && (__ldg(p.cu_q_lens) != 0 || __ldg(p.cu_q_lens + p.batch) != p.total_q))
-            raise_error(p.err, DSA_DEVERR_SEQ);
-    }
-    Walk start;
-    if (p.planned) {
-        // tiles before each item: every thread a run of items, then a scan of the threads' sums
-        int32_t* cum = reinterpret_cast<int32_t*>(k_s);
-        const int run = (p.n_items + kThreads - 1) / kThreads;
-        const int i0 = min(p.n_items, tid * run), i1 = min(p.n_items, i0 + run);
-        int sum = 0;
-        for (int i = i0; i < i1; ++i) {
-            const Item it = decode_item(p, i);
-            cum[i] = it.tiles_a + it.tiles_b;
-            sum += cum[i];
-        }
-        int incl = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(kAllLanes, incl, off);
-            if (lane >= off) incl += o;
-        }
-        if (lane == 31) ctl->scan[warp] = incl;
-        __syncthreads();
-        int before = incl - sum, W = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += ctl->scan[w];
-            W += ctl->scan[w];
-        }
-        const int G = parts_for(W, pairs);
-        if (pair == 0 && rank == 0 && tid == 0) {
-            p.plan[0] = W;
-            p.plan[1] = G;
-            p.plan[4 + p.n_items] = W;
-        }
-        if (pair >= G || W == 0) {
-            if (pair != 0 || rank != 0) return;  // uniform over the pair but for the plan's writer, below
-        }
-        const int w0 = W > 0 ? part_begin(pair, W, G) : 0;
-        for (int i = i0; i < i1; ++i) {
-            const int tiles = cum[i];
-            if (pair == 0 && rank == 0) p.plan[4 + i] = before;
-            if (w0 >= before && w0 < before + tiles) {
-                ctl->first_item = i;
-                ctl->first_tile = w0 - before;
-            }
-            before += tiles;
-        }
-        if (W == 0) return;  // (the writer of the plan's pair: its partner has returned too)
-        fence_proxy_async_smem();  // the scan's memory is the K ring's, which the async proxy writes next
-        __syncthreads();
-        start.item = ctl->first_item;
-        start.tile = ctl->first_tile;
-        start.left = part_begin(pair + 1, W, G) - w0;
-    } else {
-        start.item = p.n_items - 1 - pair;
-        start.tile = 0;
-        start.left = pairs;
-        if (start.item < 0) return;  // uniform over the pair
-    }
-
-    // ---- set-up ----
+    // ---- set-up (before the division of the work: its loads hide it) ----
     if (tid == 0) {
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kmap);
@@ -350,6 +286,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_pair_alloc(&ctl->tmem_base, 512);
         tmem_pair_relinquish();
     }
+    // ---- the division of the work ----
+    if (pair == 0 && rank == 0) {  // inconsistent sequences and tokens of no sequence are reported once
+        for (int b = tid; b < p.batch; b += kThreads) {
+            int c0, n, L;
+            if (!sequence(p, b, &c0, &n, &L)) raise_error(p.err, DSA_DEVERR_SEQ);
+        }
+        if (tid == 0 && (__ldg(p.cu_q_lens) != 0 || __ldg(p.cu_q_lens + p.batch) != p.total_q))
+            raise_error(p.err, DSA_DEVERR_SEQ);
+    }
+    Walk start;
+    bool idle = false;
+    if (p.planned) {
+        // places before each item: every thread a run of items, then a scan of the threads' sums
+        int32_t* cum = reinterpret_cast<int32_t*>(k_s);
+        const int run = (p.n_items + kThreads - 1) / kThreads;
+        const int i0 = min(p.n_items, tid * run), i1 = min(p.n_items, i0 + run);
+        int sum = 0;
+        for (int i = i0; i < i1; ++i) {
+            const Item it = decode_item(p, i);
+            cum[i] = places(it);
+            sum += cum[i];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(kAllLanes, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (lane == 31) ctl->scan[warp] = incl;
+        __syncthreads();
+        int before = incl - sum, W = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += ctl->scan[w];
+            W += ctl->scan[w];
+        }
+        const int G = parts_for(W, pairs);
+        if (pair == 0 && rank == 0 && tid == 0) {
+            p.plan[0] = W;
+            p.plan[1] = G;
+            p.plan[4 + p.n_items] = W;
+        }
+        idle = pair >= G || W == 0;
+        const int w0 = idle ? 0 : part_begin(pair, W, G);
+        for (int i = i0; i < i1; ++i) {
+            const int tiles = cum[i];
+            if (pair == 0 && rank == 0) p.plan[4 + i] = before;
+            if (w0 >= before && w0 < before + tiles) {
+                ctl->first_item = i;
+                ctl->first_tile = w0 - before;
+            }
+            before += tiles;
+        }
+        fence_proxy_async_smem();  // the scan's memory is the K ring's, which the async proxy writes next
+        __syncthreads();
+        start.item = ctl->first_item;
+        start.tile = ctl->first_tile;
+        start.left = idle ? 0 : part_begin(pair + 1, W, G) - w0;
+    } else {
+        start.item = p.n_items - 1 - pair;
+        start.tile = 0;
+        start.left = pairs;
+    }
+
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers exist before anything arrives on them
@@ -640,41 +639,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!(ok = swap(l_sum, &other))) break;
             const float l = half == 0 ? l_sum + other : other + l_sum;  // the same sum in both halves
             const bool whole = s.u0 == 0 && s.u1 == s.it.tiles_a + s.it.tiles_b && !p.packed;
-            const bool mine = tr < s.it.nrows;
+            float* slot = p.partial + partial_slot(p, s.index, pair, s.u0 == 0) * kPartialFloats;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            // A thread holds 256 values of its row.  They pass through this warp's part of the P memory, 128 bytes
+            // a row at a time, so that a store instruction writes four whole 128-byte lines (row by row it touched
+            // 32, and took 6400 cycles a segment).
+            const uint32_t stage = smem_u32(p_s) + half * kAtom + (r & 32) * 128;
+            const int sub = lane >> 3, piece = lane & 7, row_first = 64 * rank + (r & 32);
+            auto write_lines = [&](uint8_t* dst, int64_t pitch) {  // dst: this warp's first row, its 128 bytes
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int lr = 4 * k + sub;
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(stage + lr * 128 + ((piece ^ (lr & 7)) << 4))
+                                 : "memory");
+                    if (row_first + lr < s.it.nrows) *reinterpret_cast<uint4*>(dst + lr * pitch + 16 * piece) = v;
+                }
+                __syncwarp();
+            };
             if (whole) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                const int64_t row = (int64_t)s.it.row0 + tr;
+                uint8_t* dst = reinterpret_cast<uint8_t*>(p.out + ((int64_t)s.it.row0 + row_first) * 512 + 256 * half);
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 16) {
-                    float o[16];
-                    tmem_ld16(trow + c, o);
-                    tmem_ld_wait();
-                    tmem_regs_ready(o);
-                    if (mine) {
-                        uint32_t pk[8];
+                for (int c = 0; c < 256; c += 64) {
+                    float o[4][16];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) pk[j] = f2_to_bf2(o[2 * j] * inv, o[2 * j + 1] * inv);
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + row * 512 + 256 * half + c);
-                        dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                        dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                    for (int k = 0; k < 4; ++k) tmem_ld16(trow + c + 16 * k, o[k]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_regs_ready(o[k]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float* v = &o[k >> 1][8 * (k & 1)];
+                        st_shared_v4(p_row + ((k ^ (r & 7)) << 4),
+                                     make_uint4(f2_to_bf2(v[0] * inv, v[1] * inv), f2_to_bf2(v[2] * inv, v[3] * inv),
+                                                f2_to_bf2(v[4] * inv, v[5] * inv), f2_to_bf2(v[6] * inv, v[7] * inv)));
                     }
+                    write_lines(dst + 2 * c, 1024);
                 }
-                if (mine && half == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+                if (tr < s.it.nrows && half == 0 && p.lse)
+                    p.lse[(int64_t)s.it.row0 + tr] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
             } else {
-                float* slot = p.partial + partial_slot(p, s.index, pair, s.u0 == 0) * kPartialFloats;
+                uint8_t* dst = reinterpret_cast<uint8_t*>(slot + row_first * 512 + 256 * half);
 #pragma unroll 1
-                for (int c = 0; c < 256; c += 16) {
-                    float o[16];
-                    tmem_ld16(trow + c, o);
+                for (int c = 0; c < 256; c += 32) {
+                    float o[2][16];
+                    tmem_ld16(trow + c, o[0]);
+                    tmem_ld16(trow + c + 16, o[1]);
                     tmem_ld_wait();
-                    tmem_regs_ready(o);
-                    if (mine) {
-                        float4* dst = reinterpret_cast<float4*>(slot + tr * 512 + 256 * half + c);
+                    tmem_regs_ready(o[0]);
+                    tmem_regs_ready(o[1]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    for (int k = 0; k < 8; ++k) {
+                        const float* v = &o[k >> 2][4 * (k & 3)];
+                        st_shared_v4(p_row + ((k ^ (r & 7)) << 4),
+                                     make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                __float_as_uint(v[3])));
                     }
+                    write_lines(dst + 4 * c, 2048);
                 }
-                if (mine && half == 0) reinterpret_cast<float2*>(slot + 128 * 512)[tr] = make_float2(m_used, l);
+                if (tr < s.it.nrows && half == 0) reinterpret_cast<float2*>(slot + 128 * 512)[tr] = make_float2(m_used, l);
             }
             tc_fence_before();
             __syncwarp();
@@ -697,23 +723,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = wait(&ctl->v_empty[0], vphase);
                     continue;
                 }
-                for (int h = 0; ok && h < 2; ++h) {
-                    const int pg = page_of(t, h);
+                // a row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's
+                const int row0 = 16 * fw, pg0 = page_of(t, 0), pg1 = page_of(t, 1);
+                uint4 v[2][16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int pg = h == 0 ? pg0 : pg1, pos0 = t.base + 64 * h + row0;
                     const bool in = pg >= 0 && pg < p.num_pages;
-                    // a row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 are this warp's
-                    const int row0 = 16 * fw, pos0 = t.base + 64 * h + row0;
                     const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * 1152 + 512 * rank + 16 * lane;
-                    uint4 v[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        v[k] = in && pos0 + k >= t.lo && pos0 + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
-                                                                         : make_uint4(0, 0, 0, 0);
+                        v[h][k] = in && pos0 + k >= t.lo && pos0 + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
+                                                                            : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     if (!(ok = wait(&ctl->v_empty[h], vphase))) break;
                     const uint32_t dst = smem_u32(v_s + h * kVSlot + (lane >> 3) * kAtom);
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
                         st_shared_v4(dst + (row0 + k) * 128 + (((lane & 7) ^ (k & 7)) << 4),
-                                     make_uint4(finite2(v[k].x), finite2(v[k].y), finite2(v[k].z), finite2(v[k].w)));
+                                     make_uint4(finite2(v[h][k].x), finite2(v[h][k].y), finite2(v[h][k].z), finite2(v[h][k].w)));
                 }
                 if (!ok) break;
                 fence_proxy_async_smem();
@@ -774,7 +804,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) prefix_combine_kernel(cons
         if (items[k] < 0) continue;
         const int a = __ldcg(p.plan + 4 + items[k]), e = __ldcg(p.plan + 5 + items[k]);
         if (e <= a) continue;
-        const int k0 = part_of(a, W, G), k1 = part_of(e - 1, W, G);
+        const int k0 = part_of(a + kItemCost, W, G), k1 = part_of(e - 1, W, G);  // of its first and last tile
         k_first[k] = k0;
         count[k] = k1 - k0 + 1;
     }
@@ -923,20 +953,27 @@ __global__ void __launch_bounds__(32 * kWarps) prefix_simple_kernel(const Prefix
 }  // namespace
 
 // Whether rows of different sequences share tiles over the prefix, and how many items there are.
-void plan_prefix(PrefixParams* p) {
+void plan_prefix(PrefixParams* p, int max_pages) {
     const int64_t rows = (int64_t)p->total_q * p->heads;
     p->prefix_tiles = (p->prefix_len + 127) / 128;
     p->packed_tiles = (int)((rows + 127) / 128);
     p->tiles_per_seq = (int)(((int64_t)p->max_q_len * p->heads + 127) / 128);
     const int64_t merged = (int64_t)p->batch * p->tiles_per_seq;
-    // Packing saves (merged - packed_tiles) passes over the prefix, spread over the pairs, and costs a second
-    // launch and a result per sequence written and read once more.
+    // Packing saves passes over the prefix and costs a second launch and the writing and reading of two results a
+    // row, of which one tile's takes about as long as kPackCost tiles of one pair's products.
+    const int64_t most = p->packed_tiles + p->batch;  // tiles of the sequences' rows, whatever their lengths
+    const int64_t alone = merged < most ? merged : most;
     p->packed = merged + p->packed_tiles <= kPlanItems &&
-                (merged - p->packed_tiles) * p->prefix_tiles > kPackGain * (int64_t)kPrefixPairs;
+                (alone - p->packed_tiles) * p->prefix_tiles > kPackCost * (alone + p->packed_tiles);
     const int64_t items = merged + (p->packed ? p->packed_tiles : 0);
-    p->n_items = (int)items;
-    // Many items: each pair takes whole ones in turn; no cuts, so nothing to combine.
-    p->planned = items <= kPlanItems;
+    // Many items, or none long enough to be worth a combination: each pair takes whole ones in turn.
+    const int64_t own = (int64_t)max_pages * 64 - (p->prefix_len & ~63);
+    const int64_t longest = p->prefix_tiles + (own + 127) / 128;
+    // (The places on the line are counted in 32 bits.)
+    const bool fits = items * (longest + 2) <= INT32_MAX;
+    if (!fits) p->packed = 0;
+    p->n_items = (int)(merged + (p->packed ? p->packed_tiles : 0));
+    p->planned = p->packed || (fits && items <= kPlanItems && longest > kWholeTiles);
 }
 
 size_t prefix_workspace_bytes(const PrefixParams& p) {
