@@ -246,7 +246,7 @@ struct PrefixParams {
     int32_t n_items;
     int32_t planned;  // the items' tiles are divided evenly among the CTA pairs (else: whole items in turn)
     // workspace (planned)
-    int32_t* plan;   // [0] places on the line, [1] parts, [4 + i] places before item i, i = 0..n_items
+    int32_t* plan;  // merged: an int4 for each part; packed: behind those, an int2 for each item (see the kernels)
     float* partial;  // slots of kPartialFloats
 };
 constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs

@@ -140,6 +140,12 @@ constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
 constexpr uint32_t kIdescPV = make_idesc(128, 256, 1, 1, 0, 1);
 constexpr float kRaise = 8.f;  // raise the running maximum (log2) only when it grows by more than this
 
+struct Segment {
+    Item it;
+    int index;   // item number
+    int u0, u1;  // tiles of the item
+};
+
 struct Ctrl {
     uint64_t q_full, q_empty;
     uint64_t k_full[kKSlots], k_empty[kKSlots];
@@ -148,7 +154,8 @@ struct Ctrl {
     uint64_t p_full, pv_done, o_free, edge_full, drained, exchanged;
     uint32_t tmem_base;
     int32_t failed;
-    int32_t total, parts, first_item, first_tile;  // this pair's place on the line
+    int32_t first_place;  // this pair's first item (in `first`) and its place in it
+    Segment first;
     int32_t scan[kThreads / 32];
     float exchange[2][128];
 };
@@ -160,17 +167,14 @@ static_assert(kPlanItems * 4 <= kKSlots * kKSlot, "the plan's scan is done in th
 // Where a role stands in its pair's list of segments.
 struct Walk {
     int item, tile, left;  // next item, place in it, places left (planned) or the stride (whole items)
-};
-struct Segment {
-    Item it;
-    int index;   // item number
-    int u0, u1;  // tiles of the item
+    bool decoded;          // the segment passed in holds the next item already
 };
 
 __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Segment& s) {
     if (p.planned) {
         while (w.left > 0 && w.item < p.n_items) {
-            s.it = decode_item(p, w.item);
+            if (!w.decoded) s.it = decode_item(p, w.item);
+            w.decoded = false;
             const int tiles = s.it.tiles_a + s.it.tiles_b;
             if (tiles > 0) {  // w.tile counts places: the first kItemCost stand for no tile
                 s.index = w.item;
@@ -185,7 +189,8 @@ __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Seg
         return false;
     }
     while (w.item >= 0) {  // whole items, the ones with the most positions (the last of each sequence) first
-        s.it = decode_item(p, w.item);
+        if (!w.decoded) s.it = decode_item(p, w.item);
+        w.decoded = false;
         s.index = w.item;
         s.u0 = 0;
         s.u1 = s.it.tiles_a + s.it.tiles_b;
@@ -252,7 +257,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    allow_dependent_launch();  // the combining kernel waits for this one's end before it reads anything
 
     // ---- set-up (before the division of the work: its loads hide it) ----
     if (tid == 0) {
@@ -282,10 +286,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ctl->failed = 0;
         fence_mbar_init();
     }
+    __syncwarp();
+    cluster_arrive();
     if (warp == 2) {
         tmem_pair_alloc(&ctl->tmem_base, 512);
         tmem_pair_relinquish();
     }
+    // everything above may run before the previous kernel of the stream has ended, nothing below may; the
+    // combining kernel, launched behind this one in the same way, does likewise
+    grid_dependency_wait();
+    allow_dependent_launch();
+
     // ---- the division of the work ----
     if (pair == 0 && rank == 0) {  // inconsistent sequences and tokens of no sequence are reported once
         for (int b = tid; b < p.batch; b += kThreads) {
@@ -303,9 +314,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int run = (p.n_items + kThreads - 1) / kThreads;
         const int i0 = min(p.n_items, tid * run), i1 = min(p.n_items, i0 + run);
         int sum = 0;
+        Item mine;  // the last of the run, the only one as a rule
         for (int i = i0; i < i1; ++i) {
-            const Item it = decode_item(p, i);
-            cum[i] = places(it);
+            mine = decode_item(p, i);
+            cum[i] = places(mine);
             sum += cum[i];
         }
         int incl = sum;
@@ -322,36 +334,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             W += ctl->scan[w];
         }
         const int G = parts_for(W, pairs);
-        if (pair == 0 && rank == 0 && tid == 0) {
-            p.plan[0] = W;
-            p.plan[1] = G;
-            p.plan[4 + p.n_items] = W;
-        }
         idle = pair >= G || W == 0;
         const int w0 = idle ? 0 : part_begin(pair, W, G);
+        if (idle && rank == 0 && tid == 0) reinterpret_cast<int4*>(p.plan)[pair] = make_int4(0, 0, 0, 0);
         for (int i = i0; i < i1; ++i) {
             const int tiles = cum[i];
-            if (pair == 0 && rank == 0) p.plan[4 + i] = before;
-            if (w0 >= before && w0 < before + tiles) {
-                ctl->first_item = i;
-                ctl->first_tile = w0 - before;
+            if (run > 1) mine = decode_item(p, i);
+            // for the combining kernel: packed, the parts of every item; merged, for each part that begins inside an
+            // item, as the second of that item's parts, the item's rows and parts
+            const bool here = w0 >= before && w0 < before + tiles;
+            if (rank == 0 && (p.packed ? pair == 0 : here && !idle)) {
+                int k0 = 0, count = 0;
+                if (tiles > 0) {
+                    k0 = part_of(before + kItemCost, W, G);  // of its first and last tile
+                    count = part_of(before + tiles - 1, W, G) - k0 + 1;
+                }
+                if (p.packed)
+                    reinterpret_cast<int2*>(p.plan + 4 * kPrefixPairs)[i] = make_int2(k0, count);
+                else
+                    reinterpret_cast<int4*>(p.plan)[pair] =
+                        make_int4(mine.row0, count > 1 && k0 == pair - 1 ? mine.nrows : 0, k0, count);
+            }
+            if (here) {
+                ctl->first.index = i;
+                ctl->first.it = mine;
+                ctl->first_place = w0 - before;
             }
             before += tiles;
         }
         fence_proxy_async_smem();  // the scan's memory is the K ring's, which the async proxy writes next
-        __syncthreads();
-        start.item = ctl->first_item;
-        start.tile = ctl->first_tile;
         start.left = idle ? 0 : part_begin(pair + 1, W, G) - w0;
     } else {
-        start.item = p.n_items - 1 - pair;
-        start.tile = 0;
+        if (tid == 0) {
+            ctl->first.index = p.n_items - 1 - pair;
+            ctl->first.it = decode_item(p, p.n_items - 1 - pair);  // no more pairs than items
+            ctl->first_place = 0;
+        }
         start.left = pairs;
     }
-
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // the peer's barriers exist before anything arrives on them
+    start.item = ctl->first.index;
+    start.tile = ctl->first_place;
+    start.decoded = true;
+    cluster_wait();  // the peer's barriers exist before anything arrives on them
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     auto leader = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
@@ -363,18 +389,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ---------------- loads: Q of a segment, then K(u) and V(u - 1) in the order of their use ----------------
         Walk w = start;
-        Segment s;
+        Segment s = ctl->first;
         uint32_t seg = 0, kslot = 0, kphase = 1, vslot = 0, vphase = 1;
         const uint32_t q_full = leader(&ctl->q_full), k_full = leader(&ctl->k_full[0]), v_full = leader(&ctl->v_full[0]);
         while (ok && next_segment(p, w, s)) {
+            Tile t = tile_of(p, s.it, s.u0), tv = t;
+            int page0 = page_of(t, 0), page1 = page_of(t, 1), vpage0 = 0, vpage1 = 0;
             if (seg > 0 && !(ok = wait(&ctl->q_empty, (seg - 1) & 1u))) break;
             if (elect_one_sync()) {
                 if (rank == 0) mbar_arrive_expect_tx(&ctl->q_full, 2 * kQAtoms * kAtom);
                 tma_pair_load_3d(q_s, &qmap, q_full, 0, s.it.row0 + 64 * rank, 0);
             }
             ++seg;
-            Tile t = tile_of(p, s.it, s.u0), tv = t;
-            int page0 = page_of(t, 0), page1 = page_of(t, 1), vpage0 = 0, vpage1 = 0;
             for (int u = s.u0; ok && u <= s.u1; ++u) {
                 Tile tn = t;
                 int next0 = kNoPage, next1 = kNoPage;
@@ -434,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && rank == 0) {
         // ---------------- products: S(u) = Q K(u)^T, then O += P(u - 1) V(u - 1) ----------------
         Walk w = start;
-        Segment s;
+        Segment s = ctl->first;
         uint32_t seg = 0, tile = 0, edges = 0, kslot = 0, kphase = 0, vslot = 0, vphase = 0;
         const uint64_t qd = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
         const uint64_t kd = smem_desc(smem_u32(k_s), 16, 1024, kSwizzle128B);
@@ -449,12 +475,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!wait(&ctl->v_full[vslot], vphase)) return false;
                 tc_fence_after();
                 if (elect_one_sync()) {
-                    const uint64_t b = vd + vslot * (kVSlot / 16);
+                    const uint64_t pa = pd + (uint64_t)(h * (kAtom / 16)), b = vd + vslot * (kVSlot / 16);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            umma_pair_f16_ss(tmem + 128 * j, pd + (uint64_t)(h * (kAtom / 16) + 2 * kk),
+                            umma_pair_f16_ss(tmem + 128 * j, pa + (uint64_t)(2 * kk),
                                              b + (uint64_t)(j * (2 * kAtom / 16) + 128 * kk), kIdescPV,
                                              first && h == 0 && kk == 0 ? 0u : 1u);
                     umma_pair_commit(&ctl->v_empty[vslot], 3);
@@ -480,11 +506,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!(ok = wait(&ctl->k_full[kslot], kphase))) break;
                     tc_fence_after();
                     if (elect_one_sync()) {
-                        const uint64_t b = kd + kslot * (kKSlot / 16);
+                        const uint64_t q = qd + (uint64_t)(a * (kAtom / 16)), b = kd + kslot * (kKSlot / 16);
                         const uint32_t d = tmem + kSCol + 64 * buf;
 #pragma unroll
                         for (int kk = 0; kk < 4 * kKAtoms; ++kk)
-                            umma_pair_f16_ss(d, qd + (uint64_t)((a + kk / 4) * (kAtom / 16) + 2 * (kk & 3)),
+                            umma_pair_f16_ss(d, q + (uint64_t)((kk / 4) * (kAtom / 16) + 2 * (kk & 3)),
                                              b + (uint64_t)((kk / 4) * (kAtom / 16) + 2 * (kk & 3)), kIdescQK,
                                              a == 0 && kk == 0 ? 0u : 1u);
                         umma_pair_commit(&ctl->k_empty[kslot], 3);
@@ -512,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4) {
         // ---------------- softmax: thread (row, half of the positions) ----------------
         Walk w = start;
-        Segment s;
+        Segment s = ctl->first;
         const int st = tid - 32 * kSoftmaxWarp;  // lane of tensor memory
         const int half = st >> 6, r = st & 63;
         const uint32_t trow = tmem + ((uint32_t)(st & ~31) << 16);
@@ -530,22 +556,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++swaps;
             return true;
         };
-        while (ok && next_segment(p, w, s)) {
+        // First a dry pass over one tile (no waits or arrivals) while the first copies are in flight: it fetches this
+        // loop's code, edge masks included, which the first real passes would wait for (some 3 us a call).  The
+        // flag is opaque to the compiler, which would otherwise give the dry pass code of its own.
+        int dry = idle ? 0 : 1;
+        while (true) {
+            asm volatile("" : "+r"(dry));
+            if (dry == 0 && !(ok && next_segment(p, w, s))) break;
+            const int u0 = dry ? 0 : s.u0, u1 = dry ? 1 : s.u1;
             const int tr = 64 * rank + r;  // row of the tile
             // positions this row sees: below `limit`
             const int limit = s.it.b < 0 ? p.prefix_len : s.it.pos0 + (s.it.lrow0 + tr) / p.heads + 1;
             float m_used = -INFINITY, l_sum = 0.f;
-            Tile t = tile_of(p, s.it, s.u0);
-            int pg = page_of(t, half);
-            for (int u = s.u0; u < s.u1; ++u, ++tile) {
+            Tile t = tile_of(p, s.it, u0);
+            int pg = dry ? kNoPage : page_of(t, half);
+#pragma unroll 1
+            for (int u = u0; u < u1; ++u) {
                 const uint32_t buf = tile & 1u;
                 const Tile cur = t;
                 const bool bad_page = pg < 0 || pg >= p.num_pages;
-                if (u + 1 < s.u1) {
+                if (u + 1 < u1) {
                     t = tile_of(p, s.it, u + 1);
                     pg = page_of(t, half);
                 }
-                if (!(ok = wait(&ctl->s_full[buf], (tile >> 1) & 1u))) break;
+                if (!dry && !(ok = wait(&ctl->s_full[buf], (tile >> 1) & 1u))) break;
                 tc_fence_after();
                 float sv[64];
                 {
@@ -570,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(s_empty + 8 * buf);
+                if (!dry && lane == 0) mbar_arrive_cluster(s_empty + 8 * buf);
                 if (cur.edge || bad_page) {
                     const int first = cur.base + 64 * half;
                     const int lo = bad_page ? 64 : cur.lo - first, hi = min(cur.hi, limit) - first;
@@ -585,8 +619,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int n = 8; n > 0; n >>= 1)
 #pragma unroll
                     for (int k = 0; k < n; ++k) mx[k] = fmaxf(mx[k], mx[k + n]);
-                float other;
-                if (!(ok = swap(mx[0], &other))) break;
+                float other = mx[0];
+                if (!dry && !(ok = swap(mx[0], &other))) break;
                 const float mt = fmaxf(mx[0], other) * p.scale_log2;
                 const bool raise = mt > m_used + kRaise;
                 const float m_new = raise ? mt : m_used;
@@ -605,9 +639,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 const float rs = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
                 // the previous tile's P V is done: P may be overwritten, O is still
-                if (tile > 0 && !(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
+                if (!dry && tile > 0 && !(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
                 tc_fence_after();
-                if (u > s.u0 && __any_sync(kAllLanes, alpha != 1.f)) {
+                if (u > u0 && __any_sync(kAllLanes, alpha != 1.f)) {
 #pragma unroll 1
                     for (int c = 0; c < 256; c += 16) {
                         float o[16];
@@ -629,9 +663,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(p_full);
+                if (!dry) {
+                    if (lane == 0) mbar_arrive_cluster(p_full);
+                    ++tile;
+                }
             }
             if (!ok) break;
+            if (dry) {
+                dry = 0;
+                continue;
+            }
             // ---- the segment's result: O / l and lse, or O, m and l for the combining kernel ----
             if (!(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
             tc_fence_after();
@@ -709,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= kFillWarp) {
         // ---------------- V of edge tiles, through registers ----------------
         Walk w = start;
-        Segment s;
+        Segment s = ctl->first;
         const int fw = warp - kFillWarp;
         static_assert(kFillWarps == 4, "16 rows of a page each");
         const uint32_t edge_full = leader(&ctl->edge_full);
@@ -723,27 +764,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = wait(&ctl->v_empty[0], vphase);
                     continue;
                 }
-                // a row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's
+                // A row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's, eight
+                // at a time (kept short: this code runs once or twice a call, at the speed of its fetching).
                 const int row0 = 16 * fw, pg0 = page_of(t, 0), pg1 = page_of(t, 1);
-                uint4 v[2][16];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int pg = h == 0 ? pg0 : pg1, pos0 = t.base + 64 * h + row0;
+                auto load = [&](int i, uint4 (&v)[8]) {
+                    const int pg = i < 2 ? pg0 : pg1, row = row0 + 8 * (i & 1), pos = t.base + 64 * (i >> 1) + row;
                     const bool in = pg >= 0 && pg < p.num_pages;
-                    const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * 1152 + 512 * rank + 16 * lane;
+                    const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row) * 1152 + 512 * rank + 16 * lane;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        v[h][k] = in && pos0 + k >= t.lo && pos0 + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
-                                                                            : make_uint4(0, 0, 0, 0);
-                }
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = in && pos + k >= t.lo && pos + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
+                                                                       : make_uint4(0, 0, 0, 0);
+                };
+                uint4 v[8], next[8];
+                load(0, v);
+#pragma unroll 1
+                for (int i = 0; ok && i < 4; ++i) {
+                    if (i < 3) load(i + 1, next);
+                    if ((i & 1) == 0 && !(ok = wait(&ctl->v_empty[i >> 1], vphase))) break;
+                    // an exponent of all ones carries into the sign bit's place
+                    uint32_t found = 0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!(ok = wait(&ctl->v_empty[h], vphase))) break;
-                    const uint32_t dst = smem_u32(v_s + h * kVSlot + (lane >> 3) * kAtom);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t c = 0x7F807F80u, one = 0x00800080u;
+                        found |= (((v[k].x & c) + one) | ((v[k].y & c) + one) | ((v[k].z & c) + one) | ((v[k].w & c) + one));
+                    }
+                    if (__any_sync(kAllLanes, (found & 0x80008000u) != 0)) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        st_shared_v4(dst + (row0 + k) * 128 + (((lane & 7) ^ (k & 7)) << 4),
-                                     make_uint4(finite2(v[h][k].x), finite2(v[h][k].y), finite2(v[h][k].z), finite2(v[h][k].w)));
+                        for (int k = 0; k < 8; ++k)
+                            v[k] = make_uint4(finite2(v[k].x), finite2(v[k].y), finite2(v[k].z), finite2(v[k].w));
+                    }
+                    const uint32_t dst = smem_u32(v_s + (i >> 1) * kVSlot + (lane >> 3) * kAtom) + (row0 + 8 * (i & 1)) * 128;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        st_shared_v4(dst + k * 128 + (((lane & 7) ^ k) << 4), v[k]);
+                        v[k] = next[k];
+                    }
                 }
                 if (!ok) break;
                 fence_proxy_async_smem();
@@ -771,88 +827,191 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Combination of partial results: one warp per row.
 //   M = max m_k, L = sum_k l_k 2^(m_k - M), out = sum_k 2^(m_k - M) O_k / L, lse = (M + log2 L) ln 2
 // ---------------------------------------------------------------------------------------------------------
-constexpr int kCombineWarps = 4;
+// The units of work are four rows, a warp each, or one row of an item in many parts, which the block's warps share.
+constexpr int kCombineThreads = 128;
+constexpr int kCombineBlocks = 1216;  // eight blocks on each of 152 SMs
+constexpr int kManyParts = 8;
 
-__global__ void __launch_bounds__(32 * kCombineWarps) prefix_combine_kernel(const PrefixParams p) {
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-    const int rows = p.total_q * p.heads;
-    if (row >= rows) return;
-    grid_dependency_wait();
-    const int t = row / p.heads;
-    int b = -1;
-    for (int j0 = 0; j0 < p.batch && b < 0; j0 += 32) {
-        const int j = j0 + lane;
-        const bool hit = j < p.batch && __ldg(p.cu_q_lens + j) <= t && t < __ldg(p.cu_q_lens + j + 1);
-        const uint32_t bal = __ballot_sync(kAllLanes, hit);
-        if (bal) b = j0 + __ffs(bal) - 1;
-    }
-    if (b < 0) return;
-    int c0, n, L;
-    if (!sequence(p, b, &c0, &n, &L)) return;  // reported by the attention kernel
-    const int W = __ldcg(p.plan), G = __ldcg(p.plan + 1);
-    const int local = row - c0 * p.heads;
-    // up to two items hold this row: packed rows over the prefix, and the sequence's own
-    int k_first[2], count[2], in_tile[2];
-    const int nt = p.packed ? p.packed_tiles : 0;
-    const int items[2] = {nt + b * p.tiles_per_seq + local / 128, p.packed && p.prefix_tiles > 0 ? row / 128 : -1};
-    in_tile[0] = local & 127;
-    in_tile[1] = row & 127;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        k_first[k] = count[k] = 0;
-        if (items[k] < 0) continue;
-        const int a = __ldcg(p.plan + 4 + items[k]), e = __ldcg(p.plan + 5 + items[k]);
-        if (e <= a) continue;
-        const int k0 = part_of(a + kItemCost, W, G), k1 = part_of(e - 1, W, G);  // of its first and last tile
-        k_first[k] = k0;
-        count[k] = k1 - k0 + 1;
-    }
-    if (!p.packed && count[0] == 1) return;  // written by the attention kernel
-    const int parts = count[0] + count[1];
-    auto part = [&](int i) -> const float* {
-        const int k = i < count[0] ? 0 : 1, j = k ? i - count[0] : i;
-        return p.partial + partial_slot(p, items[k], k_first[k] + j, j == 0) * kPartialFloats;
-    };
-    auto tile_row = [&](int i) { return i < count[0] ? in_tile[0] : in_tile[1]; };
-    auto stats = [&](int i) {
-        return i < parts ? __ldcg(reinterpret_cast<const float2*>(part(i) + 128 * 512) + tile_row(i)) : make_float2(-INFINITY, 0.f);
-    };
+// One row's parts: those of its own item, then of the packed item over the prefix.
+struct RowParts {
+    int item0, k0, count0, tr0;
+    int item1, k1, count1, tr1;
+};
+
+__device__ __forceinline__ const float* part_of_row(const PrefixParams& p, const RowParts& r, int i, int* tr) {
+    const bool own = i < r.count0;
+    const int j = own ? i : i - r.count0;
+    *tr = own ? r.tr0 : r.tr1;
+    return p.partial + partial_slot(p, own ? r.item0 : r.item1, (own ? r.k0 : r.k1) + j, j == 0) * kPartialFloats;
+}
+
+// Parts sub, sub + step, ... of a row: acc = sum 2^(m - M) O (lane: float4 number 32 k + lane), returns the weighted
+// sum of the l.  M: the maximum over all of the row's parts.
+__device__ __forceinline__ float add_parts(const PrefixParams& p, const RowParts& r, int sub, int step, float (&acc)[16],
+                                           float* M_out, int lane) {
+    const int parts = r.count0 + r.count1;
+    int tr;
     float M = -INFINITY;
-    for (int i0 = 0; i0 < parts; i0 += 32) M = fmaxf(M, stats(i0 + lane).x);
+    for (int i = lane; i < parts; i += 32) {
+        const float* slot = part_of_row(p, r, i, &tr);
+        M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(slot + 128 * 512) + tr).x);
+    }
+    float Ls = 0.f, mu = 0.f;
+    bool first = true;
+    for (int i = sub; i < parts; i += 2 * step) {  // two parts in flight
+        const bool two = i + step < parts;
+        const float* slot0 = part_of_row(p, r, i, &tr);
+        const float2 s0 = __ldcg(reinterpret_cast<const float2*>(slot0 + 128 * 512) + tr);
+        const float4* o0 = reinterpret_cast<const float4*>(slot0 + tr * 512) + lane;
+        const float* slot1 = part_of_row(p, r, two ? i + step : i, &tr);
+        const float2 s1 = __ldcg(reinterpret_cast<const float2*>(slot1 + 128 * 512) + tr);
+        const float4* o1 = reinterpret_cast<const float4*>(slot1 + tr * 512) + lane;
+        float4 a[4], b[4];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kAllLanes, M, off));
-    const float mu = M == -INFINITY ? 0.f : M;
-    float Ls = 0.f, acc[16];
+        for (int k = 0; k < 4; ++k) {
+            a[k] = __ldcg(o0 + 32 * k);
+            b[k] = __ldcg(o1 + 32 * k);
+        }
+        if (first) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        const float2 ml = stats(i0 + lane);
-        const float wl = exp2f(ml.x - mu);  // 0 for a part without a score; NaN stays NaN
-        float lw = ml.y * wl;
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kAllLanes, M, off));
+            mu = M == -INFINITY ? 0.f : M;
+            first = false;
+        }
+        const float w0 = exp2f(s0.x - mu), w1 = two ? exp2f(s1.x - mu) : 0.f;  // 0 for a part without a score
+        Ls += s0.y * w0 + (two ? s1.y * w1 : 0.f);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(kAllLanes, lw, off);
-        Ls += lw;
-        for (int i = i0; i < min(parts, i0 + 32); ++i) {
-            const float wgt = __shfl_sync(kAllLanes, wl, i - i0);
-            if (wgt == 0.f) continue;
-            const float4* o = reinterpret_cast<const float4*>(part(i) + tile_row(i) * 512);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 v = __ldcg(o + 32 * k + lane);
-                acc[4 * k] += wgt * v.x;
-                acc[4 * k + 1] += wgt * v.y;
-                acc[4 * k + 2] += wgt * v.z;
-                acc[4 * k + 3] += wgt * v.w;
+        for (int k = 0; k < 4; ++k) {
+            acc[4 * k] += w0 * a[k].x;
+            acc[4 * k + 1] += w0 * a[k].y;
+            acc[4 * k + 2] += w0 * a[k].z;
+            acc[4 * k + 3] += w0 * a[k].w;
+            if (two) {
+                acc[4 * k] += w1 * b[k].x;
+                acc[4 * k + 1] += w1 * b[k].y;
+                acc[4 * k + 2] += w1 * b[k].z;
+                acc[4 * k + 3] += w1 * b[k].w;
             }
         }
     }
+    *M_out = M;
+    return Ls;
+}
+
+__device__ __forceinline__ void write_row(const PrefixParams& p, int row, const float (&acc)[16], float M, float Ls, int lane) {
     const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         reinterpret_cast<uint2*>(p.out + (int64_t)row * 512)[32 * k + lane] =
             make_uint2(f2_to_bf2(acc[4 * k] * inv, acc[4 * k + 1] * inv), f2_to_bf2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
     if (lane == 0 && p.lse) p.lse[row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
+}
+
+// Packed: every row has parts in two items.
+__global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(const PrefixParams p) {
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5);
+    if (row >= p.total_q * p.heads) return;
+    grid_dependency_wait();
+    const int t = row / p.heads;
+    int b = -1, c0 = 0, n = 0, L = 0;
+    for (int j0 = 0; j0 < p.batch && b < 0; j0 += 32) {
+        const int j = j0 + lane;
+        const bool hit = j < p.batch && __ldg(p.cu_q_lens + j) <= t && t < __ldg(p.cu_q_lens + j + 1);
+        const uint32_t bal = __ballot_sync(kAllLanes, hit);
+        if (bal) b = j0 + __ffs(bal) - 1;
+    }
+    if (b < 0 || !sequence(p, b, &c0, &n, &L)) return;  // reported by the attention kernel
+    const int local = row - c0 * p.heads;
+    const int2* parts = reinterpret_cast<const int2*>(p.plan + 4 * kPrefixPairs);
+    RowParts r;
+    r.item0 = p.packed_tiles + b * p.tiles_per_seq + local / 128;
+    r.item1 = row / 128;
+    const int2 own = __ldcg(parts + r.item0), shared = __ldcg(parts + r.item1);
+    r.k0 = own.x;
+    r.count0 = own.y;
+    r.tr0 = local & 127;
+    r.k1 = shared.x;
+    r.count1 = shared.y;
+    r.tr1 = row & 127;
+    float acc[16], M;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+    const float Ls = add_parts(p, r, 0, 1, acc, &M, lane);
+    write_row(p, row, acc, M, Ls, lane);
+}
+
+// Merged: only items in several parts, each described by the part that begins inside it first.
+__global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(const PrefixParams p) {
+    __shared__ int4 cut[kCombineThreads];
+    __shared__ int first_unit[kCombineThreads + 1];
+    __shared__ __align__(16) float sums[kCombineThreads / 32][512];
+    __shared__ float norms[kCombineThreads / 32];
+    static_assert(kPrefixPairs <= kCombineThreads, "one thread for each part");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dependency_wait();
+    const int4 d = tid > 0 && tid < kPrefixPairs ? __ldcg(reinterpret_cast<const int4*>(p.plan) + tid) : make_int4(0, 0, 0, 0);
+    cut[tid] = d;
+    const int units = d.w > kManyParts ? d.y : (d.y + 3) / 4;
+    int incl = units;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kAllLanes, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) norms[warp] = __int_as_float(incl);
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += __float_as_int(norms[w]);
+    first_unit[tid + 1] = incl;
+    if (tid == 0) first_unit[0] = 0;
+    __syncthreads();
+    const int total = first_unit[kCombineThreads];
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        int lo = 0, hi = kCombineThreads;  // first_unit[lo] <= u < first_unit[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (first_unit[mid] <= u) lo = mid;
+            else hi = mid;
+        }
+        const int4 c = cut[lo];
+        const bool many = c.w > kManyParts;
+        const int tr = many ? u - first_unit[lo] : 4 * (u - first_unit[lo]) + warp;
+        RowParts r = {};
+        r.k0 = c.z;
+        r.count0 = tr < c.y ? c.w : 0;
+        r.tr0 = tr;
+        float acc[16], M;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+        float Ls = add_parts(p, r, many ? warp : 0, many ? kCombineThreads / 32 : 1, acc, &M, lane);
+        if (!many) {
+            if (tr < c.y) write_row(p, c.x + tr, acc, M, Ls, lane);
+            continue;
+        }
+        // the warps' sums, in their order
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            reinterpret_cast<float4*>(sums[warp])[32 * k + lane] =
+                make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+        if (lane == 0) norms[warp] = Ls;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int w = 1; w < kCombineThreads / 32; ++w) {
+                Ls += norms[w];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 v = reinterpret_cast<const float4*>(sums[w])[32 * k + lane];
+                    acc[4 * k] += v.x;
+                    acc[4 * k + 1] += v.y;
+                    acc[4 * k + 2] += v.z;
+                    acc[4 * k + 3] += v.w;
+                }
+            }
+            write_row(p, c.x + tr, acc, M, Ls, lane);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -981,7 +1140,7 @@ size_t prefix_workspace_bytes(const PrefixParams& p) {
     const int64_t slots = p.packed ? p.n_items + kPrefixPairs : 2 * kPrefixPairs;
     return (size_t)slots * kPartialFloats * sizeof(float) + prefix_plan_bytes(p);
 }
-size_t prefix_plan_bytes(const PrefixParams& p) { return ((size_t)(p.n_items + 5) * sizeof(int32_t) + 255) / 256 * 256; }
+size_t prefix_plan_bytes(const PrefixParams& p) { return ((size_t)(2 * p.n_items + 4 * kPrefixPairs) * sizeof(int32_t) + 255) / 256 * 256; }
 
 cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     const PrefixParams& p = L.params;
@@ -993,19 +1152,27 @@ cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(prefix_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(p.planned ? kPrefixPairs : (p.n_items < kPrefixPairs ? p.n_items : kPrefixPairs));
-    prefix_pair_kernel<<<2 * pairs, kThreads, kSmem, stream>>>(L.qmap, L.kmap, L.vmap, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !p.planned) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)((p.total_q * p.heads + kCombineWarps - 1) / kCombineWarps));
-    cfg.blockDim = dim3(32 * kCombineWarps);
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_combine_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, prefix_pair_kernel, L.qmap, L.kmap, L.vmap, p);
+    if (e != cudaSuccess || !p.planned) return e;
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.dynamicSmemBytes = 0;
+    constexpr int kRows = kCombineThreads / 32;
+    if (p.packed) {
+        cfg.gridDim = dim3((unsigned)(((int64_t)p.total_q * p.heads + kRows - 1) / kRows));
+        return cudaLaunchKernelEx(&cfg, prefix_combine_packed_kernel, p);
+    }
+    cfg.gridDim = dim3(kCombineBlocks);
+    return cudaLaunchKernelEx(&cfg, prefix_combine_merged_kernel, p);
 }
 
 }  // namespace dsa
