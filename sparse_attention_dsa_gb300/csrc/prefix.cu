@@ -124,10 +124,13 @@ __device__ __forceinline__ int places(const Item& it) {
 // ---------------------------------------------------------------------------------------------------------
 // The attention kernel
 // ---------------------------------------------------------------------------------------------------------
-constexpr int kSoftmaxWarp = 4;  // warp 0: TMA, 1: products, 4-7: softmax, 8-11: V of edge tiles
+// warp 0: TMA, 1: products, 4-7: softmax; bf16: 8-11 V of edge tiles; FP8: 2, 3, 8, 9 convert K, 10-13 V
+constexpr int kSoftmaxWarp = 4;
 constexpr int kFillWarp = 8;
-constexpr int kFillWarps = 4;
-constexpr int kThreads = 32 * (kFillWarp + kFillWarps);
+constexpr int kFillWarps = 4;  // of each kind
+constexpr int kMaxWarps = 14;
+template <bool KVFP8>
+constexpr int kThreads = 32 * (KVFP8 ? kMaxWarps : kFillWarp + kFillWarps);
 constexpr int kQAtoms = 9;                  // 64-dim pieces of a row
 constexpr int kAtom = 64 * 128;             // 64 rows x 128 bytes, 128-byte swizzle
 constexpr int kKAtoms = 3, kKSlots = 3;     // K ring: slots of three atoms (one copy each)
@@ -156,7 +159,7 @@ struct Ctrl {
     int32_t failed;
     int32_t first_place;  // this pair's first item (in `first`) and its place in it
     Segment first;
-    int32_t scan[kThreads / 32];
+    int32_t scan[kMaxWarps];
     float exchange[2][128];
 };
 constexpr int kSmem = 1024 + kQAtoms * kAtom + kKSlots * kKSlot + kVSlots * kVSlot + kPBytes + (int)sizeof(Ctrl);
@@ -244,9 +247,11 @@ __device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2
     return y;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool KVFP8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     prefix_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const PrefixParams p) {
+    constexpr int kThreads = dsa::kThreads<KVFP8>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_s = smem;
@@ -261,16 +266,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---- set-up (before the division of the work: its loads hide it) ----
     if (tid == 0) {
         prefetch_tensormap(&qmap);
-        prefetch_tensormap(&kmap);
-        prefetch_tensormap(&vmap);
+        if (!KVFP8) {
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+        }
         mbar_init(&ctl->q_full, 1);
         mbar_init(&ctl->q_empty, 1);
         for (int i = 0; i < kKSlots; ++i) {
-            mbar_init(&ctl->k_full[i], 1);
+            mbar_init(&ctl->k_full[i], KVFP8 ? 2 * kFillWarps : 1);
             mbar_init(&ctl->k_empty[i], 1);
         }
         for (int i = 0; i < kVSlots; ++i) {
-            mbar_init(&ctl->v_full[i], 1);
+            mbar_init(&ctl->v_full[i], KVFP8 ? 2 * kFillWarps : 1);
             mbar_init(&ctl->v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -401,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tma_pair_load_3d(q_s, &qmap, q_full, 0, s.it.row0 + 64 * rank, 0);
             }
             ++seg;
-            for (int u = s.u0; ok && u <= s.u1; ++u) {
+            for (int u = s.u0; !KVFP8 && ok && u <= s.u1; ++u) {
                 Tile tn = t;
                 int next0 = kNoPage, next1 = kNoPage;
                 if (u + 1 < s.u1) {
@@ -468,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t vd = smem_desc(smem_u32(v_s), kAtom, 1024, kSwizzle128B);  // MN-major, atoms kAtom apart
         auto pv = [&](uint32_t n, bool first, bool edge) {  // n: number of the tile among all of this pair's
             if (!wait(&ctl->p_full, n & 1u)) return false;
-            if (edge && !wait(&ctl->edge_full, edges++ & 1u)) return false;
+            if (!KVFP8 && edge && !wait(&ctl->edge_full, edges++ & 1u)) return false;
             if (first && seg > 1 && !wait(&ctl->o_free, seg & 1u)) return false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -747,7 +754,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(o_free);
         }
-    } else if (warp >= kFillWarp) {
+    } else if (!KVFP8 && warp >= kFillWarp) {
         // ---------------- V of edge tiles, through registers ----------------
         Walk w = start;
         Segment s = ctl->first;
@@ -805,6 +812,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(edge_full);
+            }
+        }
+    }
+    if constexpr (KVFP8) {
+        // ---------------- FP8 rows: codes times scales, rounded to bf16, into the K and V rings ----------------
+        // Every unit (a ring slot) is loaded into registers one unit ahead of its conversion.  A lane's chunks are 16
+        // codes (16 bytes); each CTA converts K of its page and V of both pages for its 256 dims.
+        const int cw = warp < kSoftmaxWarp ? warp - 2 : warp - kFillWarp + 2;  // 0-3: K, 4-7: V
+        if (cw >= 0 && warp != 1 && !(warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4)) {
+            const bool v_side = cw >= kFillWarps;
+            const int cl = 32 * (cw & 3) + lane;  // lane among the 128 of this side
+            Walk w = start;
+            Segment s = ctl->first;
+            // the tile ahead: its table entries are loaded a tile before its rows
+            int u = 0, u1 = 0;
+            auto advance = [&](Tile& t) {
+                if (++u >= u1) {
+                    if (!next_segment(p, w, s)) return false;
+                    u = s.u0;
+                    u1 = s.u1;
+                }
+                t = tile_of(p, s.it, u);
+                return true;
+            };
+            auto usable = [&](int pg) { return pg >= 0 && pg < p.num_pages; };
+            auto store16 = [&](uint32_t row_base, int r, int dim, uint4 codes, float scale, bool clean) {
+                uint4 lo = e4m3x8_to_bf16x8(make_uint2(codes.x, codes.y), scale);
+                uint4 hi = e4m3x8_to_bf16x8(make_uint2(codes.z, codes.w), scale);
+                if (clean) {
+                    lo = make_uint4(finite2(lo.x), finite2(lo.y), finite2(lo.z), finite2(lo.w));
+                    hi = make_uint4(finite2(hi.x), finite2(hi.y), finite2(hi.z), finite2(hi.w));
+                }
+                const uint32_t base = row_base + (dim >> 6) * kAtom + r * 128;
+                const int c8 = (dim & 63) >> 3;
+                st_shared_v4(base + ((c8 ^ (r & 7)) << 4), lo);
+                st_shared_v4(base + (((c8 + 1) ^ (r & 7)) << 4), hi);
+            };
+            Tile t, tn;
+            bool more = advance(t);
+            if (!v_side) {
+                const uint32_t k_full = leader(&ctl->k_full[0]);
+                uint32_t phase = 1;  // a tile takes every slot of the K ring once
+                static_assert(kKSlots * kKAtoms == kQAtoms && kKAtoms == 3, "three slots a tile");
+                // slot j holds dims 192 j ..: 12 chunks a row, the last slot 8 and the rotary part's eight 16-byte pieces
+                auto load = [&](int j, int pg, uint4 (&c)[8], float (&sc)[6]) {
+                    const bool in = usable(pg);
+                    const uint8_t* page = p.kv_cache + (int64_t)(in ? pg : 0) * 64 * kKvFp8RowBytes;
+                    const int per = j < 2 ? 12 : 8;
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) {
+                        if (j == 2 && i >= 4) break;
+                        const int idx = cl + 128 * i, r = idx / per, dim = 192 * j + 16 * (idx - r * per);
+                        const uint8_t* src = page + r * kKvFp8RowBytes;
+                        c[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + dim)) : make_uint4(0, 0, 0, 0);
+                        sc[i] = in ? __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (dim >> 7)) : 0.f;
+                    }
+                    if (j == 2) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int idx = cl + 128 * i;
+                            c[4 + i] = in ? __ldg(reinterpret_cast<const uint4*>(page + (idx >> 3) * kKvFp8RowBytes + kKvFp8RopeOff) +
+                                                  (idx & 7))
+                                          : make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                };
+                auto put = [&](int j, const uint4 (&c)[8], const float (&sc)[6]) {
+                    if (!(ok = wait(&ctl->k_empty[j], phase))) return;
+                    const uint32_t slot = smem_u32(k_s + j * kKSlot);
+                    const int per = j < 2 ? 12 : 8;
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) {
+                        if (j == 2 && i >= 4) break;
+                        const int idx = cl + 128 * i, r = idx / per;
+                        store16(slot, r, 16 * (idx - r * per), c[i], sc[i], false);
+                    }
+                    if (j == 2) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int idx = cl + 128 * i, r = idx >> 3;
+                            st_shared_v4(slot + 2 * kAtom + r * 128 + (((idx & 7) ^ (r & 7)) << 4), c[4 + i]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(k_full + 8 * j);
+                };
+                uint4 a[8], b[8];
+                float sa[6], sb[6];
+                int pg = more ? page_of(t, rank) : kNoPage;
+                if (more) load(0, pg, a, sa);
+                while (ok && more) {
+                    if (pg != kNoPage && !usable(pg) && cl == 0) raise_error(p.err, DSA_DEVERR_PAGE);
+                    more = advance(tn);
+                    const int pn = more ? page_of(tn, rank) : kNoPage;
+                    load(1, pg, b, sb);
+                    put(0, a, sa);
+                    if (!ok) break;
+                    load(2, pg, a, sa);
+                    put(1, b, sb);
+                    if (!ok) break;
+                    if (more) load(0, pn, b, sb);
+                    put(2, a, sa);
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) {
+                        a[i] = b[i];
+                        sa[i] = sb[i];
+                    }
+                    pg = pn;
+                    phase ^= 1u;
+                }
+            } else {
+                const uint32_t v_full = leader(&ctl->v_full[0]);
+                uint32_t phase = 1;
+                static_assert(kVSlots == 2, "one slot for each page of a tile");
+                auto load = [&](const Tile& tt, int h, int pg, uint4 (&c)[8], float (&sc)[8]) {
+                    const bool in = usable(pg);
+                    const uint8_t* page = p.kv_cache + (int64_t)(in ? pg : 0) * 64 * kKvFp8RowBytes;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int idx = cl + 128 * i, r = idx >> 4, dim = 256 * rank + 16 * (idx & 15);
+                        const int pos = tt.base + 64 * h + r;
+                        const bool on = in && pos >= tt.lo && pos < tt.hi;
+                        const uint8_t* src = page + r * kKvFp8RowBytes;
+                        c[i] = on ? __ldg(reinterpret_cast<const uint4*>(src + dim)) : make_uint4(0, 0, 0, 0);
+                        sc[i] = on ? __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (dim >> 7)) : 0.f;
+                    }
+                };
+                auto put = [&](const Tile& tt, int h, const uint4 (&c)[8], const float (&sc)[8]) {
+                    if (!(ok = wait(&ctl->v_empty[h], phase))) return;
+                    const uint32_t slot = smem_u32(v_s + h * kVSlot);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int idx = cl + 128 * i;
+                        store16(slot, idx >> 4, 16 * (idx & 15), c[i], sc[i], tt.edge);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(v_full + 8 * h);
+                };
+                uint4 a[8], b[8];
+                float sa[8], sb[8];
+                int pg0 = more ? page_of(t, 0) : kNoPage, pg1 = more ? page_of(t, 1) : kNoPage;
+                if (more) load(t, 0, pg0, a, sa);
+                while (ok && more) {
+                    more = advance(tn);
+                    const int pn0 = more ? page_of(tn, 0) : kNoPage, pn1 = more ? page_of(tn, 1) : kNoPage;
+                    load(t, 1, pg1, b, sb);
+                    put(t, 0, a, sa);
+                    if (!ok) break;
+                    if (more) load(tn, 0, pn0, a, sa);
+                    put(t, 1, b, sb);
+                    t = tn;
+                    pg0 = pn0;
+                    pg1 = pn1;
+                    phase ^= 1u;
+                }
             }
         }
     }
@@ -1014,101 +1178,6 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(
     }
 }
 
-// ---------------------------------------------------------------------------------------------------------
-// FP8 rows: one warp per (token, head), a running maximum and sum over its positions
-// ---------------------------------------------------------------------------------------------------------
-constexpr int kWarps = 4;
-
-// Values 2*lane + 64*i, +1 (i = 0..8) of a cache row.
-template <bool KVFP8>
-__device__ __forceinline__ void load_row(const uint8_t* cache, int64_t row, int lane, float (&x)[18]) {
-    if constexpr (KVFP8) {
-        const uint8_t* src = cache + row * kKvFp8RowBytes;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint16_t c = __ldg(reinterpret_cast<const uint16_t*>(src + 64 * i) + lane);
-            const float s = __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + i / 2);
-            uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
-            float lo, hi;
-            asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-                : "=f"(lo), "=f"(hi)
-                : "r"(h2));
-            x[2 * i] = lo * s;
-            x[2 * i + 1] = hi * s;
-        }
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(src + kKvFp8RopeOff) + lane);
-        x[16] = __uint_as_float(v << 16);
-        x[17] = __uint_as_float(v & 0xFFFF0000u);
-    } else {
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(cache + row * 1152);
-#pragma unroll
-        for (int i = 0; i < 9; ++i) {
-            const uint32_t v = __ldg(src + 32 * i + lane);
-            x[2 * i] = __uint_as_float(v << 16);
-            x[2 * i + 1] = __uint_as_float(v & 0xFFFF0000u);
-        }
-    }
-}
-
-template <bool KVFP8>
-__global__ void __launch_bounds__(32 * kWarps) prefix_simple_kernel(const PrefixParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (r >= (int64_t)p.total_q * p.heads) return;
-    const int t = (int)(r / p.heads);
-    int b = -1, c0 = 0, c1 = 0;
-    for (int j = 0; j < p.batch; ++j) {
-        c0 = __ldg(p.cu_q_lens + j);
-        c1 = __ldg(p.cu_q_lens + j + 1);
-        if (c0 <= t && t < c1) {
-            b = j;
-            break;
-        }
-    }
-    const int L = b < 0 ? 0 : __ldg(p.seq_lens + b);
-    if (b < 0 || (int64_t)c1 - c0 > (int64_t)L - p.prefix_len || (int64_t)L > (int64_t)p.max_pages * 64) {
-        if (lane == 0) raise_error(p.err, DSA_DEVERR_SEQ);
-        return;
-    }
-    const int pos = L - (c1 - t);
-    float q[18];
-#pragma unroll
-    for (int i = 0; i < 9; ++i) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p.q + r * 576) + 32 * i + lane);
-        q[2 * i] = __uint_as_float(v << 16);
-        q[2 * i + 1] = __uint_as_float(v & 0xFFFF0000u);
-    }
-    float m = -INFINITY, l = 0.f, acc[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int s = 0; s <= pos; ++s) {
-        const int32_t pg = __ldg(p.page_table + (int64_t)(s < p.prefix_len ? 0 : b) * p.max_pages + s / 64);
-        if (pg < 0 || pg >= p.num_pages) {
-            if (lane == 0) raise_error(p.err, DSA_DEVERR_PAGE);
-            continue;
-        }
-        float x[18], z = 0.f;
-        load_row<KVFP8>(p.kv_cache, (int64_t)pg * 64 + (s & 63), lane, x);
-#pragma unroll
-        for (int i = 0; i < 18; ++i) z = fmaf(q[i], x[i], z);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
-        z *= p.scale_log2;
-        if (z == -INFINITY) continue;  // weight 0
-        const float mn = fmaxf(m, z), a = exp2f(m - mn), e = exp2f(z - mn);
-        l = l * a + e;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = acc[i] * a + e * x[i];
-        m = mn;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        reinterpret_cast<uint32_t*>(p.out + r * 512)[32 * i + lane] = f2_to_bf2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-}
-
 }  // namespace
 
 // Whether rows of different sequences share tiles over the prefix, and how many items there are.
@@ -1144,12 +1213,8 @@ size_t prefix_plan_bytes(const PrefixParams& p) { return ((size_t)(2 * p.n_items
 
 cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     const PrefixParams& p = L.params;
-    if (p.kv_fp8) {
-        const int64_t rows = (int64_t)p.total_q * p.heads;
-        prefix_simple_kernel<true><<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, stream>>>(p);
-        return cudaGetLastError();
-    }
-    cudaError_t e = cudaFuncSetAttribute(prefix_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    auto kernel = p.kv_fp8 ? prefix_pair_kernel<true> : prefix_pair_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(p.planned ? kPrefixPairs : (p.n_items < kPrefixPairs ? p.n_items : kPrefixPairs));
     cudaLaunchConfig_t cfg = {};
@@ -1157,12 +1222,12 @@ cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)(p.kv_fp8 ? kThreads<true> : kThreads<false>));
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, prefix_pair_kernel, L.qmap, L.kmap, L.vmap, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, L.qmap, L.kmap, L.vmap, p);
     if (e != cudaSuccess || !p.planned) return e;
     cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = 0;
