@@ -214,6 +214,7 @@ bool prefix_sizes(const dsa_dims_t* d, int32_t prefix_len, dsa::PrefixParams* p)
     p->max_q_len = d->max_q_len;
     p->heads = d->attn_heads;
     p->prefix_len = prefix_len;
+    p->kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
     dsa::plan_prefix(p, d->max_pages_per_seq);
     return true;
 }
@@ -778,7 +779,7 @@ size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len
     if (!dims || prefix_len < 0) return 0;
     dsa::PrefixParams p;
     if (!prefix_sizes(dims, prefix_len, &p)) return dsa::kErrorWordArea;
-    return dsa::kErrorWordArea + dsa::prefix_workspace_bytes(p);
+    return dsa::kErrorWordArea + dsa::prefix_plan_bytes(p) + dsa::prefix_partial_bytes(p) + dsa::prefix_ahead_bytes(p);
 }
 
 dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void* q, const void* kv_cache,
@@ -814,16 +815,18 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
     p.err = static_cast<int32_t*>(workspace);
     p.num_pages = d->num_pages;
     p.max_pages = d->max_pages_per_seq;
-    p.kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
     p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
     p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-    p.plan = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea);
-    p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea + dsa::prefix_plan_bytes(p));
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea;
+    p.plan = reinterpret_cast<int32_t*>(ws);
+    p.partial = reinterpret_cast<float*>(ws + dsa::prefix_plan_bytes(p));
+    p.ahead = p.convert_ahead ? ws + dsa::prefix_plan_bytes(p) + dsa::prefix_partial_bytes(p) : nullptr;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    auto atoms_map = [&](CUtensorMap* map, const void* base, int rank, uint64_t rows, uint32_t box_atoms, const char* name) {
+    auto atoms_map = [&](CUtensorMap* map, const void* base, int rank, uint64_t rows, uint64_t pages, uint32_t box_atoms,
+                         const char* name) {
         // rows of 576 values seen as nine 64-value atoms (one 128-byte swizzle line of a row each)
-        const cuuint64_t gdim[4] = {64, (cuuint64_t)rows, 9, (cuuint64_t)d->num_pages};
+        const cuuint64_t gdim[4] = {64, (cuuint64_t)rows, 9, (cuuint64_t)pages};
         const cuuint64_t gstride[3] = {576 * 2, 64 * 2, 64 * 576 * 2};
         const cuuint32_t box[4] = {64, 64, box_atoms, 1}, es[4] = {1, 1, 1, 1};
         CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), gdim, gstride, box,
@@ -831,9 +834,11 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         return r == CUDA_SUCCESS ? DSA_OK : fail(DSA_ERR_CUDA, "tensor map for %s: CUresult %d", name, (int)r);
     };
-    if ((st = atoms_map(&L.qmap, q, 3, (uint64_t)d->total_q * d->attn_heads, 9, "q"))) return st;
-    if (!p.kv_fp8 && ((st = atoms_map(&L.kmap, kv_cache, 4, 64, 3, "kv_cache")) ||
-                      (st = atoms_map(&L.vmap, kv_cache, 4, 64, 4, "kv_cache"))))
+    const void* rows = p.kv_fp8 ? (p.ahead ? p.ahead : q) : kv_cache;  // (no FP8 row converted ahead: never read)
+    const uint64_t pages = p.kv_fp8 ? (p.ahead ? (uint64_t)(prefix_len + 63) / 64 : 1) : (uint64_t)d->num_pages;
+    if ((st = atoms_map(&L.qmap, q, 3, (uint64_t)d->total_q * d->attn_heads, 1, 9, "q")) ||
+        (st = atoms_map(&L.kmap, rows, 4, 64, pages, p.kv_fp8 ? 1 : 3, "kv_cache")) ||
+        (st = atoms_map(&L.vmap, rows, 4, 64, pages, 4, "kv_cache")))
         return st;
     cudaError_t e = dsa::launch_prefix(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");

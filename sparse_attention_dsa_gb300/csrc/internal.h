@@ -248,20 +248,25 @@ struct PrefixParams {
     // workspace (planned)
     int32_t* plan;  // merged: an int4 for each part; packed: behind those, an int2 for each item (see the kernels)
     float* partial;  // slots of kPartialFloats
+    int32_t convert_ahead;  // plan_prefix(): the prefix's FP8 rows are converted to bf16 first
+    uint8_t* ahead;         // those rows [ceil(prefix_len / 64) * 64][576] bf16, or null
 };
 constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs
 constexpr int kPlanItems = 2048;     // most items that are divided evenly
 constexpr int kPackCost = 5;         // what a partial result costs, in tiles
 constexpr int kWholeTiles = 6;       // contexts of no more tiles are not divided
+constexpr int kAheadGain = 100;      // tiles that converting ahead must save
 // A partial result: O [128][512] fp32 (unnormalised), then (maximum in log2 units, sum) per row.
 constexpr int kPartialFloats = 128 * 512 + 2 * 128;
 void plan_prefix(PrefixParams* p, int max_pages);  // from the sizes alone
 size_t prefix_plan_bytes(const PrefixParams& p);
-size_t prefix_workspace_bytes(const PrefixParams& p);  // beyond the error word area
+size_t prefix_partial_bytes(const PrefixParams& p);
+size_t prefix_ahead_bytes(const PrefixParams& p);
 struct PrefixLaunch {
     CUtensorMap qmap;  // 3-D view [9][T*Hq][64] of q: 64-dim atoms of 64 rows, nine at a time
-    CUtensorMap kmap;  // 4-D view [num_pages][9][64][64] of the bf16 cache: atoms of a page, three at a time
-    CUtensorMap vmap;  // the same view, four atoms (256 dims) at a time
+    // 4-D views [pages][9][64][64] of bf16 rows (the cache, or the prefix's FP8 rows converted ahead)
+    CUtensorMap kmap;  // atoms of a page three at a time (converted rows: one)
+    CUtensorMap vmap;  // four atoms (256 dims) at a time
     PrefixParams params;
 };
 cudaError_t launch_prefix(const PrefixLaunch& launch, cudaStream_t stream);

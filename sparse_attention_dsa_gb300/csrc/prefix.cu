@@ -133,8 +133,13 @@ template <bool KVFP8>
 constexpr int kThreads = 32 * (KVFP8 ? kMaxWarps : kFillWarp + kFillWarps);
 constexpr int kQAtoms = 9;                  // 64-dim pieces of a row
 constexpr int kAtom = 64 * 128;             // 64 rows x 128 bytes, 128-byte swizzle
-constexpr int kKAtoms = 3, kKSlots = 3;     // K ring: slots of three atoms (one copy each)
-constexpr int kKSlot = kKAtoms * kAtom;
+// K ring: the nine atoms of a tile, handed over in three units: bf16 three atoms each (one copy each), FP8 four, four
+// and the rotary atom
+constexpr int kKUnits = 3;
+template <bool KVFP8>
+__host__ __device__ constexpr int unit_atom(int j) { return (KVFP8 ? 4 : 3) * j; }
+template <bool KVFP8>
+__host__ __device__ constexpr int unit_atoms(int j) { return KVFP8 ? (j < 2 ? 4 : 1) : 3; }
 constexpr int kVSlots = 2;                  // V ring: slots of 64 positions x 256 dims
 constexpr int kVSlot = 4 * kAtom;
 constexpr int kPBytes = 2 * kAtom;          // 64 rows x 128 positions
@@ -151,7 +156,7 @@ struct Segment {
 
 struct Ctrl {
     uint64_t q_full, q_empty;
-    uint64_t k_full[kKSlots], k_empty[kKSlots];
+    uint64_t k_full[kKUnits], k_empty[kKUnits];
     uint64_t v_full[kVSlots], v_empty[kVSlots];
     uint64_t s_full[2], s_empty[2];
     uint64_t p_full, pv_done, o_free, edge_full, drained, exchanged;
@@ -162,10 +167,9 @@ struct Ctrl {
     int32_t scan[kMaxWarps];
     float exchange[2][128];
 };
-constexpr int kSmem = 1024 + kQAtoms * kAtom + kKSlots * kKSlot + kVSlots * kVSlot + kPBytes + (int)sizeof(Ctrl);
+constexpr int kSmem = 1024 + 2 * kQAtoms * kAtom + kVSlots * kVSlot + kPBytes + (int)sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
-static_assert(kQAtoms % kKAtoms == 0, "whole slots");
-static_assert(kPlanItems * 4 <= kKSlots * kKSlot, "the plan's scan is done in the K ring's memory");
+static_assert(kPlanItems * 4 <= kQAtoms * kAtom, "the plan's scan is done in the K ring's memory");
 
 // Where a role stands in its pair's list of segments.
 struct Walk {
@@ -208,6 +212,7 @@ struct Tile {
     int base, lo, hi;
     const int32_t* pages;
     bool edge;
+    bool copied;  // FP8: its rows have been converted ahead
 };
 __device__ __forceinline__ Tile tile_of(const PrefixParams& p, const Item& it, int u) {
     Tile t;
@@ -217,12 +222,14 @@ __device__ __forceinline__ Tile tile_of(const PrefixParams& p, const Item& it, i
         t.hi = p.prefix_len;
         t.pages = p.page_table;
         t.edge = t.base + 128 > t.hi;
+        t.copied = p.ahead != nullptr;
     } else {
         t.base = it.base_b + 128 * (u - it.tiles_a);
         t.lo = p.prefix_len;
         t.hi = it.hi_max;
         t.pages = p.page_table + (int64_t)it.b * p.max_pages;
         t.edge = t.base < t.lo || t.base + 128 > it.hi_all;
+        t.copied = false;
     }
     return t;
 }
@@ -256,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* q_s = smem;
     uint8_t* k_s = q_s + kQAtoms * kAtom;
-    uint8_t* v_s = k_s + kKSlots * kKSlot;
+    uint8_t* v_s = k_s + kQAtoms * kAtom;
     uint8_t* p_s = v_s + kVSlots * kVSlot;
     Ctrl* ctl = reinterpret_cast<Ctrl*>(p_s + kPBytes);
 
@@ -266,18 +273,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     // ---- set-up (before the division of the work: its loads hide it) ----
     if (tid == 0) {
         prefetch_tensormap(&qmap);
-        if (!KVFP8) {
-            prefetch_tensormap(&kmap);
-            prefetch_tensormap(&vmap);
-        }
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
         mbar_init(&ctl->q_full, 1);
         mbar_init(&ctl->q_empty, 1);
-        for (int i = 0; i < kKSlots; ++i) {
-            mbar_init(&ctl->k_full[i], KVFP8 ? 2 * kFillWarps : 1);
+        for (int i = 0; i < kKUnits; ++i) {
+            mbar_init(&ctl->k_full[i], KVFP8 ? 1 + 2 * kFillWarps : 1);
             mbar_init(&ctl->k_empty[i], 1);
         }
         for (int i = 0; i < kVSlots; ++i) {
-            mbar_init(&ctl->v_full[i], KVFP8 ? 2 * kFillWarps : 1);
+            mbar_init(&ctl->v_full[i], KVFP8 ? 1 + 2 * kFillWarps : 1);
             mbar_init(&ctl->v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -397,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         // ---------------- loads: Q of a segment, then K(u) and V(u - 1) in the order of their use ----------------
         Walk w = start;
         Segment s = ctl->first;
-        uint32_t seg = 0, kslot = 0, kphase = 1, vslot = 0, vphase = 1;
+        uint32_t seg = 0, kphase = 1, vphase = 1;  // a tile takes every slot of both rings once
         const uint32_t q_full = leader(&ctl->q_full), k_full = leader(&ctl->k_full[0]), v_full = leader(&ctl->v_full[0]);
         while (ok && next_segment(p, w, s)) {
             Tile t = tile_of(p, s.it, s.u0), tv = t;
@@ -408,7 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 tma_pair_load_3d(q_s, &qmap, q_full, 0, s.it.row0 + 64 * rank, 0);
             }
             ++seg;
-            for (int u = s.u0; !KVFP8 && ok && u <= s.u1; ++u) {
+            for (int u = s.u0; ok && u <= s.u1; ++u) {
                 Tile tn = t;
                 int next0 = kNoPage, next1 = kNoPage;
                 if (u + 1 < s.u1) {
@@ -417,44 +422,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     next1 = page_of(tn, 1);
                 }
                 if (u < s.u1) {
-                    // entries out of range are reported; behind the last page the copy writes zeros
-                    const bool in0 = page0 >= 0 && page0 < p.num_pages, in1 = page1 >= 0 && page1 < p.num_pages;
-                    if (((!in0 && page0 != kNoPage) || (!in1 && page1 != kNoPage)) && rank == 0 && lane == 0)
-                        raise_error(p.err, DSA_DEVERR_PAGE);
-                    if (!in0) page0 = p.num_pages;
-                    if (!in1) page1 = p.num_pages;
+                    if (KVFP8) {  // rows converted ahead lie in the order of their positions
+                        page0 = t.base >> 6;
+                        page1 = page0 + 1;
+                    } else {
+                        // entries out of range are reported; behind the last page the copy writes zeros
+                        const bool in0 = page0 >= 0 && page0 < p.num_pages, in1 = page1 >= 0 && page1 < p.num_pages;
+                        if (((!in0 && page0 != kNoPage) || (!in1 && page1 != kNoPage)) && rank == 0 && lane == 0)
+                            raise_error(p.err, DSA_DEVERR_PAGE);
+                        if (!in0) page0 = p.num_pages;
+                        if (!in1) page1 = p.num_pages;
+                    }
                     const int page = rank == 0 ? page0 : page1;
-#pragma unroll 1
-                    for (int a = 0; a < kQAtoms; a += kKAtoms) {
-                        if (!(ok = wait(&ctl->k_empty[kslot], kphase))) break;
+                    const bool copied = !KVFP8 || t.copied;
+#pragma unroll
+                    for (int j = 0; j < kKUnits; ++j) {
+                        if (!(ok = wait(&ctl->k_empty[j], kphase))) break;
                         if (elect_one_sync()) {
-                            if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[kslot], 2 * kKSlot);
-                            tma_pair_load_4d(k_s + kslot * kKSlot, &kmap, k_full + 8 * kslot, 0, 0, a, page);
-                        }
-                        if (++kslot == kKSlots) {
-                            kslot = 0;
-                            kphase ^= 1u;
+                            constexpr int kBytes = unit_atoms<KVFP8>(0) * kAtom;  // the rotary atom: kmap's
+                            const bool tail = KVFP8 && j == 2;
+                            if (!copied) {
+                                if (rank == 0) mbar_arrive(&ctl->k_full[j]);
+                            } else {
+                                if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[j], 2 * (tail ? kAtom : kBytes));
+                                tma_pair_load_4d(k_s + j * kBytes, KVFP8 && !tail ? &vmap : &kmap, k_full + 8 * j, 0, 0,
+                                                 unit_atom<KVFP8>(j), page);
+                            }
                         }
                     }
+                    kphase ^= 1u;
                 }
                 if (ok && u > s.u0) {
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        if (!(ok = wait(&ctl->v_empty[vslot], vphase))) break;
+                    for (int h = 0; h < kVSlots; ++h) {
+                        if (!(ok = wait(&ctl->v_empty[h], vphase))) break;
                         if (elect_one_sync()) {
-                            if (tv.edge) {  // filled by the warps below, which have a barrier of their own
-                                if (rank == 0) mbar_arrive(&ctl->v_full[vslot]);
+                            // bf16 edge tiles are filled by the warps below, which have a barrier of their own
+                            if (KVFP8 ? !tv.copied : tv.edge) {
+                                if (rank == 0) mbar_arrive(&ctl->v_full[h]);
                             } else {
-                                if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[vslot], 2 * kVSlot);
-                                tma_pair_load_4d(v_s + vslot * kVSlot, &vmap, v_full + 8 * vslot, 0, 0, 4 * rank,
+                                if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[h], 2 * kVSlot);
+                                tma_pair_load_4d(v_s + h * kVSlot, &vmap, v_full + 8 * h, 0, 0, 4 * rank,
                                                  h == 0 ? vpage0 : vpage1);
                             }
                         }
-                        if (++vslot == kVSlots) {
-                            vslot = 0;
-                            vphase ^= 1u;
-                        }
                     }
+                    vphase ^= 1u;
                 }
                 vpage0 = page0;
                 vpage1 = page1;
@@ -468,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         // ---------------- products: S(u) = Q K(u)^T, then O += P(u - 1) V(u - 1) ----------------
         Walk w = start;
         Segment s = ctl->first;
-        uint32_t seg = 0, tile = 0, edges = 0, kslot = 0, kphase = 0, vslot = 0, vphase = 0;
+        uint32_t seg = 0, tile = 0, edges = 0;
         const uint64_t qd = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
         const uint64_t kd = smem_desc(smem_u32(k_s), 16, 1024, kSwizzle128B);
         const uint64_t pd = smem_desc(smem_u32(p_s), 16, 1024, kSwizzle128B);
@@ -478,11 +491,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             if (!KVFP8 && edge && !wait(&ctl->edge_full, edges++ & 1u)) return false;
             if (first && seg > 1 && !wait(&ctl->o_free, seg & 1u)) return false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!wait(&ctl->v_full[vslot], vphase)) return false;
+            for (int h = 0; h < kVSlots; ++h) {
+                if (!wait(&ctl->v_full[h], n & 1u)) return false;
                 tc_fence_after();
                 if (elect_one_sync()) {
-                    const uint64_t pa = pd + (uint64_t)(h * (kAtom / 16)), b = vd + vslot * (kVSlot / 16);
+                    const uint64_t pa = pd + (uint64_t)(h * (kAtom / 16)), b = vd + (uint64_t)(h * (kVSlot / 16));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -490,12 +503,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                             umma_pair_f16_ss(tmem + 128 * j, pa + (uint64_t)(2 * kk),
                                              b + (uint64_t)(j * (2 * kAtom / 16) + 128 * kk), kIdescPV,
                                              first && h == 0 && kk == 0 ? 0u : 1u);
-                    umma_pair_commit(&ctl->v_empty[vslot], 3);
+                    umma_pair_commit(&ctl->v_empty[h], 3);
                     if (h == 1) umma_pair_commit(&ctl->pv_done, 3);
-                }
-                if (++vslot == kVSlots) {
-                    vslot = 0;
-                    vphase ^= 1u;
                 }
             }
             return true;
@@ -509,26 +518,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 const bool last = u == s.u1 - 1;
                 if (!(ok = wait(&ctl->s_empty[buf], ((tile >> 1) & 1u) ^ 1u))) break;
 #pragma unroll
-                for (int a = 0; a < kQAtoms; a += kKAtoms) {
-                    if (!(ok = wait(&ctl->k_full[kslot], kphase))) break;
+                for (int j = 0; j < kKUnits; ++j) {
+                    if (!(ok = wait(&ctl->k_full[j], tile & 1u))) break;
                     tc_fence_after();
                     if (elect_one_sync()) {
-                        const uint64_t q = qd + (uint64_t)(a * (kAtom / 16)), b = kd + kslot * (kKSlot / 16);
+                        constexpr uint32_t kStep = kAtom / 16;
                         const uint32_t d = tmem + kSCol + 64 * buf;
 #pragma unroll
-                        for (int kk = 0; kk < 4 * kKAtoms; ++kk)
-                            umma_pair_f16_ss(d, q + (uint64_t)((kk / 4) * (kAtom / 16) + 2 * (kk & 3)),
-                                             b + (uint64_t)((kk / 4) * (kAtom / 16) + 2 * (kk & 3)), kIdescQK,
-                                             a == 0 && kk == 0 ? 0u : 1u);
-                        umma_pair_commit(&ctl->k_empty[kslot], 3);
-                        if (a == kQAtoms - kKAtoms) {
+                        for (int kk = 0; kk < 4 * unit_atoms<KVFP8>(j); ++kk) {
+                            const uint32_t at = (unit_atom<KVFP8>(j) + kk / 4) * kStep + 2 * (kk & 3);
+                            umma_pair_f16_ss(d, qd + at, kd + at, kIdescQK, j == 0 && kk == 0 ? 0u : 1u);
+                        }
+                        umma_pair_commit(&ctl->k_empty[j], 3);
+                        if (j == kKUnits - 1) {
                             umma_pair_commit(&ctl->s_full[buf], 3);
                             if (last) umma_pair_commit(&ctl->q_empty, 3);
                         }
-                    }
-                    if (++kslot == kKSlots) {
-                        kslot = 0;
-                        kphase ^= 1u;
                     }
                 }
                 if (ok && u > s.u0) ok = pv(tile - 1, u == s.u0 + 1, edge);
@@ -817,158 +822,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     }
     if constexpr (KVFP8) {
         // ---------------- FP8 rows: codes times scales, rounded to bf16, into the K and V rings ----------------
-        // Every unit (a ring slot) is loaded into registers one unit ahead of its conversion.  A lane's chunks are 16
-        // codes (16 bytes); each CTA converts K of its page and V of both pages for its 256 dims.
+        // Four warps convert K (this CTA's page: four scale tiles of 128 dims and the rotary part), four V (both
+        // pages, this CTA's two scale tiles), by the same code.  A unit is 64 rows x 128 dims: lane c of eight takes 16
+        // codes of a row, four rows a lane, loaded while the unit before is converted.  (One copy of this code: with
+        // three buffers in turn and three copies it ran slower, short of instructions.)  Tiles that were converted
+        // ahead are only waved through.
         const int cw = warp < kSoftmaxWarp ? warp - 2 : warp - kFillWarp + 2;  // 0-3: K, 4-7: V
-        if (cw >= 0 && warp != 1 && !(warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4)) {
+        if (cw >= 0 && !(warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4)) {
             const bool v_side = cw >= kFillWarps;
-            const int cl = 32 * (cw & 3) + lane;  // lane among the 128 of this side
+            const int units = v_side ? 4 : 5;
+            const int row0 = 4 * (cw & 3) + (lane >> 3), c = lane & 7;  // rows row0 + 16 i
+            const uint32_t full = leader(v_side ? &ctl->v_full[0] : &ctl->k_full[0]);
+            uint64_t* empty = v_side ? ctl->v_empty : ctl->k_empty;
+            // the tile being loaded and the one behind it, whose table entries are already on their way
             Walk w = start;
             Segment s = ctl->first;
-            // the tile ahead: its table entries are loaded a tile before its rows
             int u = 0, u1 = 0;
-            auto advance = [&](Tile& t) {
+            auto advance = [&](Tile& t, int& pg0, int& pg1) {
                 if (++u >= u1) {
                     if (!next_segment(p, w, s)) return false;
                     u = s.u0;
                     u1 = s.u1;
                 }
                 t = tile_of(p, s.it, u);
+                pg0 = page_of(t, v_side ? 0 : rank);
+                pg1 = page_of(t, 1);
                 return true;
             };
-            auto usable = [&](int pg) { return pg >= 0 && pg < p.num_pages; };
-            auto store16 = [&](uint32_t row_base, int r, int dim, uint4 codes, float scale, bool clean) {
-                uint4 lo = e4m3x8_to_bf16x8(make_uint2(codes.x, codes.y), scale);
-                uint4 hi = e4m3x8_to_bf16x8(make_uint2(codes.z, codes.w), scale);
-                if (clean) {
-                    lo = make_uint4(finite2(lo.x), finite2(lo.y), finite2(lo.z), finite2(lo.w));
-                    hi = make_uint4(finite2(hi.x), finite2(hi.y), finite2(hi.z), finite2(hi.w));
-                }
-                const uint32_t base = row_base + (dim >> 6) * kAtom + r * 128;
-                const int c8 = (dim & 63) >> 3;
-                st_shared_v4(base + ((c8 ^ (r & 7)) << 4), lo);
-                st_shared_v4(base + (((c8 + 1) ^ (r & 7)) << 4), hi);
-            };
             Tile t, tn;
-            bool more = advance(t);
-            if (!v_side) {
-                const uint32_t k_full = leader(&ctl->k_full[0]);
-                uint32_t phase = 1;  // a tile takes every slot of the K ring once
-                static_assert(kKSlots * kKAtoms == kQAtoms && kKAtoms == 3, "three slots a tile");
-                // slot j holds dims 192 j ..: 12 chunks a row, the last slot 8 and the rotary part's eight 16-byte pieces
-                auto load = [&](int j, int pg, uint4 (&c)[8], float (&sc)[6]) {
-                    const bool in = usable(pg);
-                    const uint8_t* page = p.kv_cache + (int64_t)(in ? pg : 0) * 64 * kKvFp8RowBytes;
-                    const int per = j < 2 ? 12 : 8;
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) {
-                        if (j == 2 && i >= 4) break;
-                        const int idx = cl + 128 * i, r = idx / per, dim = 192 * j + 16 * (idx - r * per);
-                        const uint8_t* src = page + r * kKvFp8RowBytes;
-                        c[i] = in ? __ldg(reinterpret_cast<const uint4*>(src + dim)) : make_uint4(0, 0, 0, 0);
-                        sc[i] = in ? __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (dim >> 7)) : 0.f;
-                    }
-                    if (j == 2) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int idx = cl + 128 * i;
-                            c[4 + i] = in ? __ldg(reinterpret_cast<const uint4*>(page + (idx >> 3) * kKvFp8RowBytes + kKvFp8RopeOff) +
-                                                  (idx & 7))
-                                          : make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                };
-                auto put = [&](int j, const uint4 (&c)[8], const float (&sc)[6]) {
-                    if (!(ok = wait(&ctl->k_empty[j], phase))) return;
-                    const uint32_t slot = smem_u32(k_s + j * kKSlot);
-                    const int per = j < 2 ? 12 : 8;
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) {
-                        if (j == 2 && i >= 4) break;
-                        const int idx = cl + 128 * i, r = idx / per;
-                        store16(slot, r, 16 * (idx - r * per), c[i], sc[i], false);
-                    }
-                    if (j == 2) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int idx = cl + 128 * i, r = idx >> 3;
-                            st_shared_v4(slot + 2 * kAtom + r * 128 + (((idx & 7) ^ (r & 7)) << 4), c[4 + i]);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(k_full + 8 * j);
-                };
-                uint4 a[8], b[8];
-                float sa[6], sb[6];
-                int pg = more ? page_of(t, rank) : kNoPage;
-                if (more) load(0, pg, a, sa);
-                while (ok && more) {
-                    if (pg != kNoPage && !usable(pg) && cl == 0) raise_error(p.err, DSA_DEVERR_PAGE);
-                    more = advance(tn);
-                    const int pn = more ? page_of(tn, rank) : kNoPage;
-                    load(1, pg, b, sb);
-                    put(0, a, sa);
-                    if (!ok) break;
-                    load(2, pg, a, sa);
-                    put(1, b, sb);
-                    if (!ok) break;
-                    if (more) load(0, pn, b, sb);
-                    put(2, a, sa);
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) {
-                        a[i] = b[i];
-                        sa[i] = sb[i];
-                    }
-                    pg = pn;
-                    phase ^= 1u;
-                }
-            } else {
-                const uint32_t v_full = leader(&ctl->v_full[0]);
-                uint32_t phase = 1;
-                static_assert(kVSlots == 2, "one slot for each page of a tile");
-                auto load = [&](const Tile& tt, int h, int pg, uint4 (&c)[8], float (&sc)[8]) {
-                    const bool in = usable(pg);
-                    const uint8_t* page = p.kv_cache + (int64_t)(in ? pg : 0) * 64 * kKvFp8RowBytes;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int idx = cl + 128 * i, r = idx >> 4, dim = 256 * rank + 16 * (idx & 15);
-                        const int pos = tt.base + 64 * h + r;
-                        const bool on = in && pos >= tt.lo && pos < tt.hi;
-                        const uint8_t* src = page + r * kKvFp8RowBytes;
-                        c[i] = on ? __ldg(reinterpret_cast<const uint4*>(src + dim)) : make_uint4(0, 0, 0, 0);
-                        sc[i] = on ? __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (dim >> 7)) : 0.f;
-                    }
-                };
-                auto put = [&](const Tile& tt, int h, const uint4 (&c)[8], const float (&sc)[8]) {
-                    if (!(ok = wait(&ctl->v_empty[h], phase))) return;
-                    const uint32_t slot = smem_u32(v_s + h * kVSlot);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int idx = cl + 128 * i;
-                        store16(slot, idx >> 4, 16 * (idx & 15), c[i], sc[i], tt.edge);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(v_full + 8 * h);
-                };
-                uint4 a[8], b[8];
-                float sa[8], sb[8];
-                int pg0 = more ? page_of(t, 0) : kNoPage, pg1 = more ? page_of(t, 1) : kNoPage;
-                if (more) load(t, 0, pg0, a, sa);
-                while (ok && more) {
-                    more = advance(tn);
-                    const int pn0 = more ? page_of(tn, 0) : kNoPage, pn1 = more ? page_of(tn, 1) : kNoPage;
-                    load(t, 1, pg1, b, sb);
-                    put(t, 0, a, sa);
-                    if (!ok) break;
-                    if (more) load(tn, 0, pn0, a, sa);
-                    put(t, 1, b, sb);
+            int pg0 = kNoPage, pg1 = kNoPage, pn0 = kNoPage, pn1 = kNoPage, q = 0;
+            bool have = advance(t, pg0, pg1), have_next = have && advance(tn, pn0, pn1);
+            struct Unit {
+                uint4 code[4];
+                float scale[4];
+                bool valid, edge, copied;
+            };
+            auto load = [&](Unit& x) {
+                if (q == units) {
+                    q = 0;
                     t = tn;
                     pg0 = pn0;
                     pg1 = pn1;
+                    have = have_next;
+                    have_next = have && advance(tn, pn0, pn1);
+                }
+                x.valid = have;
+                x.copied = t.copied;
+                x.edge = v_side && t.edge;
+                const int h = v_side ? q >> 1 : 0;
+                const int pg = h == 0 ? pg0 : pg1;
+                const bool in = pg >= 0 && pg < p.num_pages;
+                const int tile128 = v_side ? 2 * rank + (q & 1) : q;
+                ++q;
+                if (!have || x.copied) return;
+                if (!in && pg != kNoPage && lane == 0) raise_error(p.err, DSA_DEVERR_PAGE);
+                const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * kKvFp8RowBytes;
+                const int at = (tile128 < 4 ? 128 * tile128 : kKvFp8RopeOff) + 16 * c;
+                const int pos = t.base + 64 * h + row0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // V of positions that do not exist is 0; K of such positions is masked by the softmax
+                    const bool on = in && (!x.edge || (pos + 16 * i >= t.lo && pos + 16 * i < t.hi));
+                    const uint8_t* r = src + 16 * i * kKvFp8RowBytes;
+                    x.code[i] = on ? __ldg(reinterpret_cast<const uint4*>(r + at)) : make_uint4(0, 0, 0, 0);
+                    x.scale[i] = on ? __ldg(reinterpret_cast<const float*>(r + kKvFp8ScaleOff) + (tile128 & 3)) : 0.f;
+                }
+            };
+            Unit x0, x1;
+            load(x0);
+            int unit = 0;
+            uint32_t phase = 1;
+#pragma unroll 1
+            while (x0.valid) {
+                load(x1);
+                if (!(ok = wait(empty + (unit >> 1), phase))) break;
+                const uint32_t dst = (v_side ? smem_u32(v_s) : smem_u32(k_s)) + 2 * unit * kAtom + row0 * 128;
+                if (x0.copied) {
+                } else if (!v_side && unit == 4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        st_shared_v4(dst + 16 * i * 128 + ((c ^ (row0 & 7)) << 4), x0.code[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 lo = e4m3x8_to_bf16x8(make_uint2(x0.code[i].x, x0.code[i].y), x0.scale[i]);
+                        uint4 hi = e4m3x8_to_bf16x8(make_uint2(x0.code[i].z, x0.code[i].w), x0.scale[i]);
+                        if (x0.edge) {
+                            lo = make_uint4(finite2(lo.x), finite2(lo.y), finite2(lo.z), finite2(lo.w));
+                            hi = make_uint4(finite2(hi.x), finite2(hi.y), finite2(hi.z), finite2(hi.w));
+                        }
+                        const uint32_t to = dst + (c >> 2) * kAtom + 16 * i * 128;  // (row & 7) is row0 & 7
+                        st_shared_v4(to + (((2 * (c & 3)) ^ (row0 & 7)) << 4), lo);
+                        st_shared_v4(to + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4), hi);
+                    }
+                }
+                if ((unit & 1) || unit == 4) {  // both halves of a barrier's part, or the rotary atom
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(full + 8 * (unit >> 1));
+                }
+                if (++unit == units) {
+                    unit = 0;
                     phase ^= 1u;
                 }
+                x0 = x1;
             }
         }
     }
@@ -985,6 +942,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     cluster_sync();  // neither CTA leaves before the other's products, copies and arrivals are done
     tc_fence_after();
     if (warp == 2) tmem_pair_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// FP8 rows of the prefix to bf16, once for all the tiles of rows that attend to them: a warp per position, in the
+// order of the positions (rows behind the prefix in its last page are zeros).  Bound by L2 and HBM: 656 bytes read,
+// 1152 written a row.
+// ---------------------------------------------------------------------------------------------------------
+constexpr int kAheadWarps = 8;
+
+__global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const PrefixParams p) {
+    const int lane = threadIdx.x & 31;
+    const int pos = blockIdx.x * kAheadWarps + (threadIdx.x >> 5);
+    if (pos >= (p.prefix_len + 63) / 64 * 64) return;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    uint4* dst = reinterpret_cast<uint4*>(p.ahead + (int64_t)pos * 1152);
+    const int pg = pos < p.prefix_len ? __ldg(p.page_table + (pos >> 6)) : -1;
+    const bool in = pg >= 0 && pg < p.num_pages;
+    if (!in && pos < p.prefix_len && lane == 0) raise_error(p.err, DSA_DEVERR_PAGE);
+    uint4 code = make_uint4(0, 0, 0, 0), rot = code;
+    float scale = 0.f;
+    if (in) {
+        const uint8_t* src = p.kv_cache + ((int64_t)pg * 64 + (pos & 63)) * kKvFp8RowBytes;
+        code = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+        scale = __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (lane >> 3));
+        if (lane < 8) rot = __ldg(reinterpret_cast<const uint4*>(src + kKvFp8RopeOff) + lane);
+    }
+    dst[2 * lane] = e4m3x8_to_bf16x8(make_uint2(code.x, code.y), scale);
+    dst[2 * lane + 1] = e4m3x8_to_bf16x8(make_uint2(code.z, code.w), scale);
+    if (lane < 8) dst[64 + lane] = rot;
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -1201,13 +1188,20 @@ void plan_prefix(PrefixParams* p, int max_pages) {
     const bool fits = items * (longest + 2) <= INT32_MAX;
     if (!fits) p->packed = 0;
     p->n_items = (int)(merged + (p->packed ? p->packed_tiles : 0));
+    // FP8: a tile converted in passing takes about three times as long as one of bf16 rows, for every tile of rows
+    // again; converting the prefix ahead takes a launch and about as long as a twentieth of a tile a tile.
+    const int64_t row_tiles = p->packed ? p->packed_tiles : alone;
+    p->convert_ahead = p->kv_fp8 && (row_tiles - 2) * p->prefix_tiles > kAheadGain;
     p->planned = p->packed || (fits && items <= kPlanItems && longest > kWholeTiles);
 }
 
-size_t prefix_workspace_bytes(const PrefixParams& p) {
+size_t prefix_partial_bytes(const PrefixParams& p) {
     if (!p.planned) return 0;
     const int64_t slots = p.packed ? p.n_items + kPrefixPairs : 2 * kPrefixPairs;
-    return (size_t)slots * kPartialFloats * sizeof(float) + prefix_plan_bytes(p);
+    return (size_t)slots * kPartialFloats * sizeof(float);
+}
+size_t prefix_ahead_bytes(const PrefixParams& p) {
+    return p.convert_ahead ? (size_t)((p.prefix_len + 63) / 64) * 64 * 1152 : 0;
 }
 size_t prefix_plan_bytes(const PrefixParams& p) { return ((size_t)(2 * p.n_items + 4 * kPrefixPairs) * sizeof(int32_t) + 255) / 256 * 256; }
 
@@ -1218,15 +1212,21 @@ cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int pairs = (int)(p.planned ? kPrefixPairs : (p.n_items < kPrefixPairs ? p.n_items : kPrefixPairs));
     cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.convert_ahead) {
+        cfg.gridDim = dim3((unsigned)((p.prefix_len + 63) / 64 * 64 / kAheadWarps));
+        cfg.blockDim = dim3(32 * kAheadWarps);
+        e = cudaLaunchKernelEx(&cfg, prefix_ahead_kernel, p);
+        if (e != cudaSuccess) return e;
+    }
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3((unsigned)(p.kv_fp8 ? kThreads<true> : kThreads<false>));
     cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, L.qmap, L.kmap, L.vmap, p);
     if (e != cudaSuccess || !p.planned) return e;
     cfg.blockDim = dim3(kCombineThreads);
