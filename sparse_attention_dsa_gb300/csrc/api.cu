@@ -840,6 +840,24 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
         (st = atoms_map(&L.kmap, rows, 4, 64, pages, p.kv_fp8 ? 1 : 3, "kv_cache")) ||
         (st = atoms_map(&L.vmap, rows, 4, 64, pages, 4, "kv_cache")))
         return st;
+    if (p.kv_fp8) {
+        auto bytes_map = [&](CUtensorMap* map, int rank, const cuuint64_t* gdim, const cuuint64_t* gstride,
+                             const cuuint32_t* box) {
+            const cuuint32_t es[4] = {1, 1, 1, 1};
+            CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(kv_cache), gdim, gstride,
+                             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            return r == CUDA_SUCCESS ? DSA_OK : fail(DSA_ERR_CUDA, "tensor map for kv_cache: CUresult %d", (int)r);
+        };
+        const cuuint64_t n = (cuuint64_t)d->num_pages, row = dsa::kKvFp8RowBytes;
+        const cuuint64_t code_dim[4] = {128, 64, 4, n}, code_stride[3] = {row, 128, 64 * row};
+        const cuuint32_t code_box[4] = {128, 64, 2, 1};
+        const cuuint64_t rot_dim[3] = {row, 64, n}, rot_stride[2] = {row, 64 * row};
+        const cuuint32_t rot_box[3] = {128, 64, 1};
+        if ((st = bytes_map(&L.codemap, 4, code_dim, code_stride, code_box)) ||
+            (st = bytes_map(&L.rotmap, 3, rot_dim, rot_stride, rot_box)))
+            return st;
+    }
     cudaError_t e = dsa::launch_prefix(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
     return DSA_OK;

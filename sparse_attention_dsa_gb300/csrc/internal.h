@@ -267,6 +267,8 @@ struct PrefixLaunch {
     // 4-D views [pages][9][64][64] of bf16 rows (the cache, or the prefix's FP8 rows converted ahead)
     CUtensorMap kmap;  // atoms of a page three at a time (converted rows: one)
     CUtensorMap vmap;  // four atoms (256 dims) at a time
+    CUtensorMap codemap;  // FP8 rows, 4-D view [num_pages][4][64][128] of their codes: two scale tiles at a time
+    CUtensorMap rotmap;   // FP8 rows, 3-D view [num_pages][64][656] bytes: the rotary part of a page
     PrefixParams params;
 };
 cudaError_t launch_prefix(const PrefixLaunch& launch, cudaStream_t stream);

@@ -113,12 +113,26 @@ __device__ __forceinline__ int64_t partial_slot(const PrefixParams& p, int item,
 
 // On the line an item is kItemCost places longer than its tiles, in front of them: what its queries' load, its
 // first tile's latency and its result cost in tiles.  Parts are no shorter than kMinPlaces on average.
+// A tile of FP8 rows that are converted in passing takes two places.  A cut gives the tiles that begin before it to
+// the part before it.
 constexpr int kItemCost = 2;
 constexpr int kMinPlaces = 2 + kItemCost;
 __device__ __forceinline__ int parts_for(int W, int pairs) { return max(1, min(pairs, W / kMinPlaces)); }
-__device__ __forceinline__ int places(const Item& it) {
-    const int tiles = it.tiles_a + it.tiles_b;
-    return tiles > 0 ? tiles + kItemCost : 0;
+__device__ __forceinline__ int cost_a(const PrefixParams& p) { return p.kv_fp8 && p.ahead == nullptr ? 2 : 1; }
+__device__ __forceinline__ int cost_b(const PrefixParams& p) { return p.kv_fp8 ? 2 : 1; }
+__device__ __forceinline__ int places(const PrefixParams& p, const Item& it) {
+    return it.tiles_a + it.tiles_b > 0 ? kItemCost + it.tiles_a * cost_a(p) + it.tiles_b * cost_b(p) : 0;
+}
+// Tiles of an item that begin before its place o.
+__device__ __forceinline__ int tiles_before(const PrefixParams& p, const Item& it, int o) {
+    const int ca = cost_a(p), cb = cost_b(p), x = max(0, o - kItemCost), a = it.tiles_a * ca;
+    return x <= a ? (x + ca - 1) / ca : min(it.tiles_a + it.tiles_b, it.tiles_a + (x - a + cb - 1) / cb);
+}
+// First and last part of an item of `n` places from place `before` of the line.
+__device__ __forceinline__ void parts_of_item(const PrefixParams& p, const Item& it, int before, int n, int W, int G, int* k0,
+                                              int* k1) {
+    *k0 = part_of(before + kItemCost, W, G);  // the part of its first tile's first place, and of its last tile's
+    *k1 = part_of(before + n - (it.tiles_b > 0 ? cost_b(p) : cost_a(p)), W, G);
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -160,6 +174,7 @@ struct Ctrl {
     uint64_t v_full[kVSlots], v_empty[kVSlots];
     uint64_t s_full[2], s_empty[2];
     uint64_t p_full, pv_done, o_free, edge_full, drained, exchanged;
+    uint64_t k_raw[2], v_raw[2], k_conv[2], v_conv[2];  // FP8 tiles: the codes are here, are converted
     uint32_t tmem_base;
     int32_t failed;
     int32_t first_place;  // this pair's first item (in `first`) and its place in it
@@ -183,11 +198,12 @@ __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Seg
             if (!w.decoded) s.it = decode_item(p, w.item);
             w.decoded = false;
             const int tiles = s.it.tiles_a + s.it.tiles_b;
-            if (tiles > 0) {  // w.tile counts places: the first kItemCost stand for no tile
+            if (tiles > 0) {  // w.tile counts places
                 s.index = w.item;
-                s.u0 = max(0, w.tile - kItemCost);
-                s.u1 = min(tiles, w.tile + w.left - kItemCost);
-                w.left -= tiles + kItemCost - w.tile;
+                const int n = places(p, s.it);
+                s.u0 = tiles_before(p, s.it, w.tile);
+                s.u1 = w.tile + w.left >= n ? tiles : tiles_before(p, s.it, w.tile + w.left);
+                w.left -= n - w.tile;
             }
             ++w.item;
             w.tile = 0;
@@ -257,7 +273,8 @@ __device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2
 template <bool KVFP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     prefix_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap, const PrefixParams p) {
+                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap codemap,
+                       const __grid_constant__ CUtensorMap rotmap, const PrefixParams p) {
     constexpr int kThreads = dsa::kThreads<KVFP8>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -275,14 +292,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
+        if (KVFP8) {
+            prefetch_tensormap(&codemap);
+            prefetch_tensormap(&rotmap);
+        }
         mbar_init(&ctl->q_full, 1);
         mbar_init(&ctl->q_empty, 1);
         for (int i = 0; i < kKUnits; ++i) {
-            mbar_init(&ctl->k_full[i], KVFP8 ? 1 + 2 * kFillWarps : 1);
+            mbar_init(&ctl->k_full[i], 1);
             mbar_init(&ctl->k_empty[i], 1);
         }
         for (int i = 0; i < kVSlots; ++i) {
-            mbar_init(&ctl->v_full[i], KVFP8 ? 1 + 2 * kFillWarps : 1);
+            mbar_init(&ctl->v_full[i], 1);
             mbar_init(&ctl->v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -294,6 +315,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         mbar_init(&ctl->o_free, 8);
         mbar_init(&ctl->edge_full, 2 * kFillWarps);
         mbar_init(&ctl->drained, 1);
+        if (KVFP8) {
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&ctl->k_raw[i], 1);
+                mbar_init(&ctl->v_raw[i], 1);
+                mbar_init(&ctl->k_conv[i], 2 * kFillWarps);
+                mbar_init(&ctl->v_conv[i], 2 * kFillWarps);
+            }
+        }
         mbar_init(&ctl->exchanged, 4);
         ctl->failed = 0;
         fence_mbar_init();
@@ -329,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         Item mine;  // the last of the run, the only one as a rule
         for (int i = i0; i < i1; ++i) {
             mine = decode_item(p, i);
-            cum[i] = places(mine);
+            cum[i] = places(p, mine);
             sum += cum[i];
         }
         int incl = sum;
@@ -358,8 +387,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             if (rank == 0 && (p.packed ? pair == 0 : here && !idle)) {
                 int k0 = 0, count = 0;
                 if (tiles > 0) {
-                    k0 = part_of(before + kItemCost, W, G);  // of its first and last tile
-                    count = part_of(before + tiles - 1, W, G) - k0 + 1;
+                    int k1;
+                    parts_of_item(p, mine, before, tiles, W, G, &k0, &k1);
+                    count = k1 - k0 + 1;
                 }
                 if (p.packed)
                     reinterpret_cast<int2*>(p.plan + 4 * kPrefixPairs)[i] = make_int2(k0, count);
@@ -422,31 +452,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     next1 = page_of(tn, 1);
                 }
                 if (u < s.u1) {
-                    if (KVFP8) {  // rows converted ahead lie in the order of their positions
+                    // entries out of range are reported; behind the last page the copy writes zeros
+                    const bool in0 = page0 >= 0 && page0 < p.num_pages, in1 = page1 >= 0 && page1 < p.num_pages;
+                    if (((!in0 && page0 != kNoPage) || (!in1 && page1 != kNoPage)) && rank == 0 && lane == 0)
+                        raise_error(p.err, DSA_DEVERR_PAGE);
+                    if (!in0) page0 = p.num_pages;
+                    if (!in1) page1 = p.num_pages;
+                    if (KVFP8 && t.copied) {  // rows converted ahead lie in the order of their positions
                         page0 = t.base >> 6;
                         page1 = page0 + 1;
-                    } else {
-                        // entries out of range are reported; behind the last page the copy writes zeros
-                        const bool in0 = page0 >= 0 && page0 < p.num_pages, in1 = page1 >= 0 && page1 < p.num_pages;
-                        if (((!in0 && page0 != kNoPage) || (!in1 && page1 != kNoPage)) && rank == 0 && lane == 0)
-                            raise_error(p.err, DSA_DEVERR_PAGE);
-                        if (!in0) page0 = p.num_pages;
-                        if (!in1) page1 = p.num_pages;
                     }
                     const int page = rank == 0 ? page0 : page1;
-                    const bool copied = !KVFP8 || t.copied;
 #pragma unroll
                     for (int j = 0; j < kKUnits; ++j) {
                         if (!(ok = wait(&ctl->k_empty[j], kphase))) break;
                         if (elect_one_sync()) {
-                            constexpr int kBytes = unit_atoms<KVFP8>(0) * kAtom;  // the rotary atom: kmap's
-                            const bool tail = KVFP8 && j == 2;
-                            if (!copied) {
+                            constexpr int kBytes = unit_atoms<KVFP8>(0) * kAtom;
+                            uint8_t* dst = k_s + j * kBytes;
+                            const uint32_t bar = k_full + 8 * j;
+                            if (KVFP8 && j < 2 && !t.copied) {
+                                // the codes of four atoms into the middle two (see the conversion below)
                                 if (rank == 0) mbar_arrive(&ctl->k_full[j]);
+                                mbar_arrive_expect_tx(&ctl->k_raw[j], 2 * kAtom);
+                                tma_load_4d(dst + kAtom, &codemap, &ctl->k_raw[j], 0, 0, 2 * j, page);
                             } else {
-                                if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[j], 2 * (tail ? kAtom : kBytes));
-                                tma_pair_load_4d(k_s + j * kBytes, KVFP8 && !tail ? &vmap : &kmap, k_full + 8 * j, 0, 0,
-                                                 unit_atom<KVFP8>(j), page);
+                                if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[j], 2 * unit_atoms<KVFP8>(j) * kAtom);
+                                if (!KVFP8)
+                                    tma_pair_load_4d(dst, &kmap, bar, 0, 0, unit_atom<KVFP8>(j), page);
+                                else if (j < 2)
+                                    tma_pair_load_4d(dst, &vmap, bar, 0, 0, unit_atom<KVFP8>(j), page);
+                                else if (t.copied)
+                                    tma_pair_load_4d(dst, &kmap, bar, 0, 0, unit_atom<KVFP8>(j), page);
+                                else
+                                    tma_pair_load_3d(dst, &rotmap, bar, kKvFp8RopeOff, 0, page);
                             }
                         }
                     }
@@ -457,13 +495,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     for (int h = 0; h < kVSlots; ++h) {
                         if (!(ok = wait(&ctl->v_empty[h], vphase))) break;
                         if (elect_one_sync()) {
-                            // bf16 edge tiles are filled by the warps below, which have a barrier of their own
-                            if (KVFP8 ? !tv.copied : tv.edge) {
+                            const int page = h == 0 ? vpage0 : vpage1;
+                            uint8_t* dst = v_s + h * kVSlot;
+                            if (KVFP8 && !tv.copied) {
+                                if (rank == 0) mbar_arrive(&ctl->v_full[h]);
+                                mbar_arrive_expect_tx(&ctl->v_raw[h], 2 * kAtom);
+                                tma_load_4d(dst + kAtom, &codemap, &ctl->v_raw[h], 0, 0, 2 * rank, page);
+                            } else if (!KVFP8 && tv.edge) {
+                                // filled by the warps below, which have a barrier of their own
                                 if (rank == 0) mbar_arrive(&ctl->v_full[h]);
                             } else {
                                 if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[h], 2 * kVSlot);
-                                tma_pair_load_4d(v_s + h * kVSlot, &vmap, v_full + 8 * h, 0, 0, 4 * rank,
-                                                 h == 0 ? vpage0 : vpage1);
+                                tma_pair_load_4d(dst, &vmap, v_full + 8 * h, 0, 0, 4 * rank, page);
                             }
                         }
                     }
@@ -481,18 +524,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         // ---------------- products: S(u) = Q K(u)^T, then O += P(u - 1) V(u - 1) ----------------
         Walk w = start;
         Segment s = ctl->first;
-        uint32_t seg = 0, tile = 0, edges = 0;
+        uint32_t seg = 0, tile = 0, edges = 0, k_raws = 0, v_raws = 0;
         const uint64_t qd = smem_desc(smem_u32(q_s), 16, 1024, kSwizzle128B);
         const uint64_t kd = smem_desc(smem_u32(k_s), 16, 1024, kSwizzle128B);
         const uint64_t pd = smem_desc(smem_u32(p_s), 16, 1024, kSwizzle128B);
         const uint64_t vd = smem_desc(smem_u32(v_s), kAtom, 1024, kSwizzle128B);  // MN-major, atoms kAtom apart
-        auto pv = [&](uint32_t n, bool first, bool edge) {  // n: number of the tile among all of this pair's
+        auto pv = [&](uint32_t n, bool first, bool edge, bool raw) {  // n: the tile's number among all of this pair's
             if (!wait(&ctl->p_full, n & 1u)) return false;
             if (!KVFP8 && edge && !wait(&ctl->edge_full, edges++ & 1u)) return false;
             if (first && seg > 1 && !wait(&ctl->o_free, seg & 1u)) return false;
 #pragma unroll
             for (int h = 0; h < kVSlots; ++h) {
                 if (!wait(&ctl->v_full[h], n & 1u)) return false;
+                if (KVFP8 && raw && !wait(&ctl->v_conv[h], v_raws & 1u)) return false;
                 tc_fence_after();
                 if (elect_one_sync()) {
                     const uint64_t pa = pd + (uint64_t)(h * (kAtom / 16)), b = vd + (uint64_t)(h * (kVSlot / 16));
@@ -507,19 +551,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     if (h == 1) umma_pair_commit(&ctl->pv_done, 3);
                 }
             }
+            if (raw) ++v_raws;
             return true;
         };
         while (ok && next_segment(p, w, s)) {
             if (!(ok = wait(&ctl->q_full, seg & 1u))) break;
             ++seg;
-            bool edge = false;
+            bool edge = false, raw = false;
             for (int u = s.u0; ok && u < s.u1; ++u, ++tile) {
                 const uint32_t buf = tile & 1u;
                 const bool last = u == s.u1 - 1;
+                const Tile cur = tile_of(p, s.it, u);
+                const bool cur_raw = KVFP8 && !cur.copied;
                 if (!(ok = wait(&ctl->s_empty[buf], ((tile >> 1) & 1u) ^ 1u))) break;
 #pragma unroll
                 for (int j = 0; j < kKUnits; ++j) {
                     if (!(ok = wait(&ctl->k_full[j], tile & 1u))) break;
+                    if (KVFP8 && j < 2 && cur_raw && !(ok = wait(&ctl->k_conv[j], k_raws & 1u))) break;
                     tc_fence_after();
                     if (elect_one_sync()) {
                         constexpr uint32_t kStep = kAtom / 16;
@@ -536,10 +584,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                         }
                     }
                 }
-                if (ok && u > s.u0) ok = pv(tile - 1, u == s.u0 + 1, edge);
-                edge = tile_of(p, s.it, u).edge;
+                if (cur_raw) ++k_raws;
+                if (ok && u > s.u0) ok = pv(tile - 1, u == s.u0 + 1, edge, raw);
+                edge = cur.edge;
+                raw = cur_raw;
             }
-            if (ok) ok = pv(tile - 1, s.u1 == s.u0 + 1, edge);
+            if (ok) ok = pv(tile - 1, s.u1 == s.u0 + 1, edge, raw);
         }
         // drain (default limit): every product of the pair is done before its memory is given back
         if (elect_one_sync()) {
@@ -822,110 +872,99 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     }
     if constexpr (KVFP8) {
         // ---------------- FP8 rows: codes times scales, rounded to bf16, into the K and V rings ----------------
-        // Four warps convert K (this CTA's page: four scale tiles of 128 dims and the rotary part), four V (both
-        // pages, this CTA's two scale tiles), by the same code.  A unit is 64 rows x 128 dims: lane c of eight takes 16
-        // codes of a row, four rows a lane, loaded while the unit before is converted.  (One copy of this code: with
-        // three buffers in turn and three copies it ran slower, short of instructions.)  Tiles that were converted
-        // ahead are only waved through.
+        // The codes of a row of two atoms (128 dims, one scale) come by TMA into that row's place in one of the two, so
+        // that a row is expanded inside what it will fill: of four atoms, codes 0-127 lie in atom 1, 128-255 in atom
+        // 2.  Eight lanes of a warp take a row, 16 codes each; they read, meet, and write.  Four warps expand K (this
+        // CTA's page), four V (both pages, this CTA's 256 dims), a row of every 16 each.  Tiles converted ahead pass by.
         const int cw = warp < kSoftmaxWarp ? warp - 2 : warp - kFillWarp + 2;  // 0-3: K, 4-7: V
         if (cw >= 0 && !(warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4)) {
             const bool v_side = cw >= kFillWarps;
-            const int units = v_side ? 4 : 5;
             const int row0 = 4 * (cw & 3) + (lane >> 3), c = lane & 7;  // rows row0 + 16 i
-            const uint32_t full = leader(v_side ? &ctl->v_full[0] : &ctl->k_full[0]);
-            uint64_t* empty = v_side ? ctl->v_empty : ctl->k_empty;
-            // the tile being loaded and the one behind it, whose table entries are already on their way
+            const uint32_t done = leader(v_side ? &ctl->v_conv[0] : &ctl->k_conv[0]);
+            uint64_t* raw = v_side ? ctl->v_raw : ctl->k_raw;
+            const uint32_t ring = smem_u32(v_side ? v_s : k_s) + row0 * 128;
             Walk w = start;
             Segment s = ctl->first;
             int u = 0, u1 = 0;
-            auto advance = [&](Tile& t, int& pg0, int& pg1) {
-                if (++u >= u1) {
-                    if (!next_segment(p, w, s)) return false;
-                    u = s.u0;
-                    u1 = s.u1;
-                }
-                t = tile_of(p, s.it, u);
-                pg0 = page_of(t, v_side ? 0 : rank);
-                pg1 = page_of(t, 1);
+            auto advance = [&](Tile& t) {  // the next tile that is to be converted
+                do {
+                    if (++u >= u1) {
+                        if (!next_segment(p, w, s)) return false;
+                        u = s.u0;
+                        u1 = s.u1;
+                    }
+                    t = tile_of(p, s.it, u);
+                } while (t.copied);
                 return true;
             };
-            Tile t, tn;
-            int pg0 = kNoPage, pg1 = kNoPage, pn0 = kNoPage, pn1 = kNoPage, q = 0;
-            bool have = advance(t, pg0, pg1), have_next = have && advance(tn, pn0, pn1);
-            struct Unit {
-                uint4 code[4];
-                float scale[4];
-                bool valid, edge, copied;
-            };
-            auto load = [&](Unit& x) {
-                if (q == units) {
-                    q = 0;
-                    t = tn;
-                    pg0 = pn0;
-                    pg1 = pn1;
-                    have = have_next;
-                    have_next = have && advance(tn, pn0, pn1);
-                }
-                x.valid = have;
-                x.copied = t.copied;
-                x.edge = v_side && t.edge;
-                const int h = v_side ? q >> 1 : 0;
-                const int pg = h == 0 ? pg0 : pg1;
-                const bool in = pg >= 0 && pg < p.num_pages;
-                const int tile128 = v_side ? 2 * rank + (q & 1) : q;
-                ++q;
-                if (!have || x.copied) return;
-                if (!in && pg != kNoPage && lane == 0) raise_error(p.err, DSA_DEVERR_PAGE);
-                const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * kKvFp8RowBytes;
-                const int at = (tile128 < 4 ? 128 * tile128 : kKvFp8RopeOff) + 16 * c;
-                const int pos = t.base + 64 * h + row0;
+            // scales of this lane's rows in the order of use: K the four scale tiles of a row, V two of each page
+            auto load_scales = [&](const Tile& t, float (&sc)[4][4]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // V of positions that do not exist is 0; K of such positions is masked by the softmax
-                    const bool on = in && (!x.edge || (pos + 16 * i >= t.lo && pos + 16 * i < t.hi));
-                    const uint8_t* r = src + 16 * i * kKvFp8RowBytes;
-                    x.code[i] = on ? __ldg(reinterpret_cast<const uint4*>(r + at)) : make_uint4(0, 0, 0, 0);
-                    x.scale[i] = on ? __ldg(reinterpret_cast<const float*>(r + kKvFp8ScaleOff) + (tile128 & 3)) : 0.f;
-                }
-            };
-            Unit x0, x1;
-            load(x0);
-            int unit = 0;
-            uint32_t phase = 1;
-#pragma unroll 1
-            while (x0.valid) {
-                load(x1);
-                if (!(ok = wait(empty + (unit >> 1), phase))) break;
-                const uint32_t dst = (v_side ? smem_u32(v_s) : smem_u32(k_s)) + 2 * unit * kAtom + row0 * 128;
-                if (x0.copied) {
-                } else if (!v_side && unit == 4) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        st_shared_v4(dst + 16 * i * 128 + ((c ^ (row0 & 7)) << 4), x0.code[i]);
-                } else {
+                for (int h = 0; h < 2; ++h) {
+                    const int pg = page_of(t, v_side ? h : rank);
+                    const bool in = pg >= 0 && pg < p.num_pages;
+                    const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * kKvFp8RowBytes + kKvFp8ScaleOff +
+                                         (v_side ? 8 * rank : 8 * h);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint4 lo = e4m3x8_to_bf16x8(make_uint2(x0.code[i].x, x0.code[i].y), x0.scale[i]);
-                        uint4 hi = e4m3x8_to_bf16x8(make_uint2(x0.code[i].z, x0.code[i].w), x0.scale[i]);
-                        if (x0.edge) {
-                            lo = make_uint4(finite2(lo.x), finite2(lo.y), finite2(lo.z), finite2(lo.w));
-                            hi = make_uint4(finite2(hi.x), finite2(hi.y), finite2(hi.z), finite2(hi.w));
-                        }
-                        const uint32_t to = dst + (c >> 2) * kAtom + 16 * i * 128;  // (row & 7) is row0 & 7
-                        st_shared_v4(to + (((2 * (c & 3)) ^ (row0 & 7)) << 4), lo);
-                        st_shared_v4(to + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4), hi);
+                        const float2 v = in ? __ldg(reinterpret_cast<const float2*>(src + 16 * i * kKvFp8RowBytes))
+                                            : make_float2(0.f, 0.f);
+                        sc[2 * h][i] = v.x;
+                        sc[2 * h + 1][i] = v.y;
                     }
                 }
-                if ((unit & 1) || unit == 4) {  // both halves of a barrier's part, or the rotary atom
-                    fence_proxy_async_smem();
+            };
+            Tile t, tn;
+            float sc[4][4], next[4][4];
+            bool have = advance(t);
+            if (have) load_scales(t, sc);
+            uint32_t phase = 0;
+            while (ok && have) {
+                const bool have_next = advance(tn);
+                if (have_next) load_scales(tn, next);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {  // two atoms each
+                    if (!(q & 1) && !(ok = wait(&raw[q >> 1], phase))) break;
+                    const uint32_t at = ring + (4 * (q >> 1)) * kAtom;
+                    const uint32_t from = at + ((q & 1) ? 2 : 1) * kAtom, to = at + ((q & 1) ? 2 : 0) * kAtom + (c >> 2) * kAtom;
+                    uint4 code[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
+                                     : "r"(from + 16 * i * 128 + ((c ^ (row0 & 7)) << 4))
+                                     : "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full + 8 * (unit >> 1));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 lo = e4m3x8_to_bf16x8(make_uint2(code[i].x, code[i].y), sc[0][i]);
+                        uint4 hi = e4m3x8_to_bf16x8(make_uint2(code[i].z, code[i].w), sc[0][i]);
+                        if (v_side && t.edge) {  // V of positions that do not exist is 0, and infinities and NaN are
+                            const int pos = t.base + 64 * (q >> 1) + row0 + 16 * i;
+                            const uint32_t keep = pos >= t.lo && pos < t.hi ? 0xFFFFFFFFu : 0u;
+                            lo = make_uint4(finite2(lo.x) & keep, finite2(lo.y) & keep, finite2(lo.z) & keep, finite2(lo.w) & keep);
+                            hi = make_uint4(finite2(hi.x) & keep, finite2(hi.y) & keep, finite2(hi.z) & keep, finite2(hi.w) & keep);
+                        }
+                        // (row & 7) is row0 & 7
+                        st_shared_v4(to + 16 * i * 128 + (((2 * (c & 3)) ^ (row0 & 7)) << 4), lo);
+                        st_shared_v4(to + 16 * i * 128 + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4), hi);
+                        sc[0][i] = sc[1][i];
+                        sc[1][i] = sc[2][i];
+                        sc[2][i] = sc[3][i];
+                    }
+                    if (q & 1) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(done + 8 * (q >> 1));
+                    }
                 }
-                if (++unit == units) {
-                    unit = 0;
-                    phase ^= 1u;
-                }
-                x0 = x1;
+                phase ^= 1u;
+                have = have_next;
+                t = tn;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[j][i] = next[j][i];
             }
         }
     }
@@ -1185,10 +1224,10 @@ void plan_prefix(PrefixParams* p, int max_pages) {
     const int64_t own = (int64_t)max_pages * 64 - (p->prefix_len & ~63);
     const int64_t longest = p->prefix_tiles + (own + 127) / 128;
     // (The places on the line are counted in 32 bits.)
-    const bool fits = items * (longest + 2) <= INT32_MAX;
+    const bool fits = items * (2 * longest + 2) <= INT32_MAX;
     if (!fits) p->packed = 0;
     p->n_items = (int)(merged + (p->packed ? p->packed_tiles : 0));
-    // FP8: a tile converted in passing takes about three times as long as one of bf16 rows, for every tile of rows
+    // FP8: a tile converted in passing takes about half as long again as one of bf16 rows, for every tile of rows
     // again; converting the prefix ahead takes a launch and about as long as a twentieth of a tile a tile.
     const int64_t row_tiles = p->packed ? p->packed_tiles : alone;
     p->convert_ahead = p->kv_fp8 && (row_tiles - 2) * p->prefix_tiles > kAheadGain;
@@ -1227,7 +1266,7 @@ cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3((unsigned)(p.kv_fp8 ? kThreads<true> : kThreads<false>));
     cfg.dynamicSmemBytes = kSmem;
-    e = cudaLaunchKernelEx(&cfg, kernel, L.qmap, L.kmap, L.vmap, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, L.qmap, L.kmap, L.vmap, L.codemap, L.rotmap, p);
     if (e != cudaSuccess || !p.planned) return e;
     cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = 0;
