@@ -622,9 +622,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         // loop's code, edge masks included, which the first real passes would wait for (some 3 us a call).  The
         // flag is opaque to the compiler, which would otherwise give the dry pass code of its own.
         int dry = idle ? 0 : 1;
+        bool have = next_segment(p, w, s);
         while (true) {
             asm volatile("" : "+r"(dry));
-            if (dry == 0 && !(ok && next_segment(p, w, s))) break;
+            if (dry == 0 && !have) break;
             const int u0 = dry ? 0 : s.u0, u1 = dry ? 1 : s.u1;
             const int tr = 64 * rank + r;  // row of the tile
             // positions this row sees: below `limit`
@@ -735,6 +736,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 dry = 0;
                 continue;
             }
+            // the next segment, looked up while this one's last products run
+            Segment ahead = s;
+            have = next_segment(p, w, ahead);
             // ---- the segment's result: O / l and lse, or O, m and l for the combining kernel ----
             if (!(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
             tc_fence_after();
@@ -751,19 +755,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             const int sub = lane >> 3, piece = lane & 7, row_first = 64 * rank + (r & 32);
             auto write_lines = [&](uint8_t* dst, int64_t pitch) {  // dst: this warp's first row, its 128 bytes
                 __syncwarp();
+                uint4 v[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int lr = 4 * k + sub;
-                    uint4 v;
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
                                  : "r"(stage + lr * 128 + ((piece ^ (lr & 7)) << 4))
                                  : "memory");
-                    if (row_first + lr < s.it.nrows) *reinterpret_cast<uint4*>(dst + lr * pitch + 16 * piece) = v;
                 }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (row_first + 4 * k + sub < s.it.nrows)
+                        *reinterpret_cast<uint4*>(dst + (4 * k + sub) * pitch + 16 * piece) = v[k];
                 __syncwarp();
             };
-            if (whole) {
+            if (row_first >= s.it.nrows) {
+                // none of this warp's rows exists
+            } else if (whole) {
                 uint8_t* dst = reinterpret_cast<uint8_t*>(p.out + ((int64_t)s.it.row0 + row_first) * 512 + 256 * half);
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 64) {
@@ -808,6 +817,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(o_free);
+            s = ahead;
         }
     } else if (!KVFP8 && warp >= kFillWarp) {
         // ---------------- V of edge tiles, through registers ----------------
