@@ -623,6 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         // flag is opaque to the compiler, which would otherwise give the dry pass code of its own.
         int dry = idle ? 0 : 1;
         bool have = next_segment(p, w, s);
+        int first_pg = have ? page_of(tile_of(p, s.it, s.u0), half) : kNoPage;
         while (true) {
             asm volatile("" : "+r"(dry));
             if (dry == 0 && !have) break;
@@ -632,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             const int limit = s.it.b < 0 ? p.prefix_len : s.it.pos0 + (s.it.lrow0 + tr) / p.heads + 1;
             float m_used = -INFINITY, l_sum = 0.f;
             Tile t = tile_of(p, s.it, u0);
-            int pg = dry ? kNoPage : page_of(t, half);
+            int pg = dry ? kNoPage : first_pg;
 #pragma unroll 1
             for (int u = u0; u < u1; ++u) {
                 const uint32_t buf = tile & 1u;
@@ -739,6 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             // the next segment, looked up while this one's last products run
             Segment ahead = s;
             have = next_segment(p, w, ahead);
+            if (have) first_pg = page_of(tile_of(p, ahead.it, ahead.u0), half);
             // ---- the segment's result: O / l and lse, or O, m and l for the combining kernel ----
             if (!(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
             tc_fence_after();
@@ -795,11 +797,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     p.lse[(int64_t)s.it.row0 + tr] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
             } else {
                 uint8_t* dst = reinterpret_cast<uint8_t*>(slot + row_first * 512 + 256 * half);
+                float o[2][16];
+                tmem_ld16(trow, o[0]);
+                tmem_ld16(trow + 16, o[1]);
 #pragma unroll 1
                 for (int c = 0; c < 256; c += 32) {
-                    float o[2][16];
-                    tmem_ld16(trow + c, o[0]);
-                    tmem_ld16(trow + c + 16, o[1]);
                     tmem_ld_wait();
                     tmem_regs_ready(o[0]);
                     tmem_regs_ready(o[1]);
@@ -809,6 +811,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                         st_shared_v4(p_row + ((k ^ (r & 7)) << 4),
                                      make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                                                 __float_as_uint(v[3])));
+                    }
+                    if (c + 32 < 256) {  // the next ones come while these are written
+                        tmem_ld16(trow + c + 32, o[0]);
+                        tmem_ld16(trow + c + 48, o[1]);
                     }
                     write_lines(dst + 4 * c, 2048);
                 }
@@ -836,42 +842,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     ok = wait(&ctl->v_empty[0], vphase);
                     continue;
                 }
-                // A row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's, eight
-                // at a time (kept short: this code runs once or twice a call, at the speed of its fetching).
-                const int row0 = 16 * fw, pg0 = page_of(t, 0), pg1 = page_of(t, 1);
-                auto load = [&](int i, uint4 (&v)[8]) {
-                    const int pg = i < 2 ? pg0 : pg1, row = row0 + 8 * (i & 1), pos = t.base + 64 * (i >> 1) + row;
+                // A row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's.  All is
+                // loaded and looked at before the slots are waited for: only the stores are on the way to the products.
+                const int row0 = 16 * fw;
+                uint4 v[2][16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int pg = page_of(t, h), pos = t.base + 64 * h + row0;
                     const bool in = pg >= 0 && pg < p.num_pages;
-                    const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row) * 1152 + 512 * rank + 16 * lane;
+                    const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * 1152 + 512 * rank + 16 * lane;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = in && pos + k >= t.lo && pos + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
-                                                                       : make_uint4(0, 0, 0, 0);
-                };
-                uint4 v[8], next[8];
-                load(0, v);
-#pragma unroll 1
-                for (int i = 0; ok && i < 4; ++i) {
-                    if (i < 3) load(i + 1, next);
-                    if ((i & 1) == 0 && !(ok = wait(&ctl->v_empty[i >> 1], vphase))) break;
-                    // an exponent of all ones carries into the sign bit's place
-                    uint32_t found = 0;
+                    for (int k = 0; k < 16; ++k)
+                        v[h][k] = in && pos + k >= t.lo && pos + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
+                                                                          : make_uint4(0, 0, 0, 0);
+                }
+                uint32_t found = 0;  // an exponent of all ones carries into the sign bit's place
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
                         const uint32_t c = 0x7F807F80u, one = 0x00800080u;
-                        found |= (((v[k].x & c) + one) | ((v[k].y & c) + one) | ((v[k].z & c) + one) | ((v[k].w & c) + one));
+                        found |= ((v[h][k].x & c) + one) | ((v[h][k].y & c) + one) | ((v[h][k].z & c) + one) |
+                                 ((v[h][k].w & c) + one);
                     }
-                    if (__any_sync(kAllLanes, (found & 0x80008000u) != 0)) {
+                if (__any_sync(kAllLanes, (found & 0x80008000u) != 0)) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            v[k] = make_uint4(finite2(v[k].x), finite2(v[k].y), finite2(v[k].z), finite2(v[k].w));
-                    }
-                    const uint32_t dst = smem_u32(v_s + (i >> 1) * kVSlot + (lane >> 3) * kAtom) + (row0 + 8 * (i & 1)) * 128;
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        st_shared_v4(dst + k * 128 + (((lane & 7) ^ k) << 4), v[k]);
-                        v[k] = next[k];
-                    }
+                        for (int k = 0; k < 16; ++k)
+                            v[h][k] = make_uint4(finite2(v[h][k].x), finite2(v[h][k].y), finite2(v[h][k].z), finite2(v[h][k].w));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!(ok = wait(&ctl->v_empty[h], vphase))) break;
+                    const uint32_t dst = smem_u32(v_s + h * kVSlot + (lane >> 3) * kAtom) + row0 * 128;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) st_shared_v4(dst + k * 128 + (((lane & 7) ^ (k & 7)) << 4), v[h][k]);
                 }
                 if (!ok) break;
                 fence_proxy_async_smem();
