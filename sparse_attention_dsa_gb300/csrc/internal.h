@@ -243,6 +243,7 @@ struct PrefixParams {
     int32_t packed_tiles;   // 128-row tiles of all the batch's rows
     int32_t tiles_per_seq;  // 128-row tiles of the longest sequence's rows
     int32_t prefix_tiles;   // 128-position tiles of the prefix
+    int32_t row_tiles;      // 128-row tiles that attend to the prefix
     int32_t n_items;
     int32_t planned;  // the items' tiles are divided evenly among the CTA pairs (else: whole items in turn)
     // workspace (planned)

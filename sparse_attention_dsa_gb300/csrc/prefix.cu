@@ -113,13 +113,13 @@ __device__ __forceinline__ int64_t partial_slot(const PrefixParams& p, int item,
 
 // On the line an item is kItemCost places longer than its tiles, in front of them: what its queries' load, its
 // first tile's latency and its result cost in tiles.  Parts are no shorter than kMinPlaces on average.
-// A tile of FP8 rows that are converted in passing takes two places.  A cut gives the tiles that begin before it to
+// A tile of FP8 rows that are converted in passing takes three places.  A cut gives the tiles that begin before it to
 // the part before it.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 3;
 constexpr int kMinPlaces = 2 + kItemCost;
 __device__ __forceinline__ int parts_for(int W, int pairs) { return max(1, min(pairs, W / kMinPlaces)); }
-__device__ __forceinline__ int cost_a(const PrefixParams& p) { return p.kv_fp8 && p.ahead == nullptr ? 2 : 1; }
-__device__ __forceinline__ int cost_b(const PrefixParams& p) { return p.kv_fp8 ? 2 : 1; }
+__device__ __forceinline__ int cost_a(const PrefixParams& p) { return p.kv_fp8 && p.ahead == nullptr ? 3 : 1; }
+__device__ __forceinline__ int cost_b(const PrefixParams& p) { return p.kv_fp8 ? 3 : 1; }
 __device__ __forceinline__ int places(const PrefixParams& p, const Item& it) {
     return it.tiles_a + it.tiles_b > 0 ? kItemCost + it.tiles_a * cost_a(p) + it.tiles_b * cost_b(p) : 0;
 }
@@ -445,11 +445,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             ++seg;
             for (int u = s.u0; ok && u <= s.u1; ++u) {
                 Tile tn = t;
-                int next0 = kNoPage, next1 = kNoPage;
+                int next0 = kNoPage, next1 = kNoPage, later = kNoPage;
                 if (u + 1 < s.u1) {
                     tn = tile_of(p, s.it, u + 1);
                     next0 = page_of(tn, 0);
                     next1 = page_of(tn, 1);
+                }
+                if (u + 2 < s.u1 && (u + 2 >= s.it.tiles_a || p.row_tiles <= 2)) {
+                    const Tile t2 = tile_of(p, s.it, u + 2);
+                    if (!t2.copied) later = page_of(t2, rank);
                 }
                 if (u < s.u1) {
                     // entries out of range are reported; behind the last page the copy writes zeros
@@ -511,6 +515,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                         }
                     }
                     vphase ^= 1u;
+                }
+                // A ring holds one tile, so a copy is asked for about one tile before its use: less than HBM's latency.
+                // The tile after the next is brought to L2, unless it is the prefix's and so in L2 for the other pairs.
+                if (later >= 0 && later < p.num_pages && elect_one_sync()) {
+                    const uint32_t bytes = 64 * (KVFP8 ? kKvFp8RowBytes : 1152);
+                    l2_prefetch(p.kv_cache + (int64_t)later * bytes, bytes);
                 }
                 vpage0 = page0;
                 vpage1 = page1;
@@ -1240,13 +1250,13 @@ void plan_prefix(PrefixParams* p, int max_pages) {
     const int64_t own = (int64_t)max_pages * 64 - (p->prefix_len & ~63);
     const int64_t longest = p->prefix_tiles + (own + 127) / 128;
     // (The places on the line are counted in 32 bits.)
-    const bool fits = items * (2 * longest + 2) <= INT32_MAX;
+    const bool fits = items * (3 * longest + 3) <= INT32_MAX;
     if (!fits) p->packed = 0;
     p->n_items = (int)(merged + (p->packed ? p->packed_tiles : 0));
     // FP8: a tile converted in passing takes about half as long again as one of bf16 rows, for every tile of rows
     // again; converting the prefix ahead takes a launch and about as long as a twentieth of a tile a tile.
-    const int64_t row_tiles = p->packed ? p->packed_tiles : alone;
-    p->convert_ahead = p->kv_fp8 && (row_tiles - 2) * p->prefix_tiles > kAheadGain;
+    p->row_tiles = (int)(p->packed ? p->packed_tiles : alone);
+    p->convert_ahead = p->kv_fp8 && (int64_t)(p->row_tiles - 2) * p->prefix_tiles > kAheadGain;
     p->planned = p->packed || (fits && items <= kPlanItems && longest > kWholeTiles);
 }
 
