@@ -98,6 +98,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libdsa_gb300.so (built by ``sparse_attention_dsa_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -163,11 +165,18 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_torch = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        global _torch
+        if _torch is None:
+            import torch
 
-        return torch.cuda.current_stream().cuda_stream
+            _torch = torch
+        # the handle alone: building a Stream object for it takes 3 us, as long as the rest of a call
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -628,32 +628,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             ++swaps;
             return true;
         };
-        // First a dry pass over one tile (no waits or arrivals) while the first copies are in flight: it fetches this
-        // loop's code, edge masks included, which the first real passes would wait for (some 3 us a call).  The
-        // flag is opaque to the compiler, which would otherwise give the dry pass code of its own.
-        int dry = idle ? 0 : 1;
         bool have = next_segment(p, w, s);
         int first_pg = have ? page_of(tile_of(p, s.it, s.u0), half) : kNoPage;
-        while (true) {
-            asm volatile("" : "+r"(dry));
-            if (dry == 0 && !have) break;
-            const int u0 = dry ? 0 : s.u0, u1 = dry ? 1 : s.u1;
+        while (have) {
             const int tr = 64 * rank + r;  // row of the tile
             // positions this row sees: below `limit`
             const int limit = s.it.b < 0 ? p.prefix_len : s.it.pos0 + (s.it.lrow0 + tr) / p.heads + 1;
             float m_used = -INFINITY, l_sum = 0.f;
-            Tile t = tile_of(p, s.it, u0);
-            int pg = dry ? kNoPage : first_pg;
+            Tile t = tile_of(p, s.it, s.u0);
+            int pg = first_pg;
 #pragma unroll 1
-            for (int u = u0; u < u1; ++u) {
+            for (int u = s.u0; u < s.u1; ++u, ++tile) {
                 const uint32_t buf = tile & 1u;
                 const Tile cur = t;
                 const bool bad_page = pg < 0 || pg >= p.num_pages;
-                if (u + 1 < u1) {
+                if (u + 1 < s.u1) {
                     t = tile_of(p, s.it, u + 1);
                     pg = page_of(t, half);
                 }
-                if (!dry && !(ok = wait(&ctl->s_full[buf], (tile >> 1) & 1u))) break;
+                if (!(ok = wait(&ctl->s_full[buf], (tile >> 1) & 1u))) break;
                 tc_fence_after();
                 float sv[64];
                 {
@@ -678,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (!dry && lane == 0) mbar_arrive_cluster(s_empty + 8 * buf);
+                if (lane == 0) mbar_arrive_cluster(s_empty + 8 * buf);
                 if (cur.edge || bad_page) {
                     const int first = cur.base + 64 * half;
                     const int lo = bad_page ? 64 : cur.lo - first, hi = min(cur.hi, limit) - first;
@@ -693,8 +686,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 for (int n = 8; n > 0; n >>= 1)
 #pragma unroll
                     for (int k = 0; k < n; ++k) mx[k] = fmaxf(mx[k], mx[k + n]);
-                float other = mx[0];
-                if (!dry && !(ok = swap(mx[0], &other))) break;
+                float other;
+                if (!(ok = swap(mx[0], &other))) break;
                 const float mt = fmaxf(mx[0], other) * p.scale_log2;
                 const bool raise = mt > m_used + kRaise;
                 const float m_new = raise ? mt : m_used;
@@ -713,9 +706,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 }
                 const float rs = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
                 // the previous tile's P V is done: P may be overwritten, O is still
-                if (!dry && tile > 0 && !(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
+                if (tile > 0 && !(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
                 tc_fence_after();
-                if (u > u0 && __any_sync(kAllLanes, alpha != 1.f)) {
+                if (u > s.u0 && __any_sync(kAllLanes, alpha != 1.f)) {
 #pragma unroll 1
                     for (int c = 0; c < 256; c += 16) {
                         float o[16];
@@ -737,16 +730,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (!dry) {
-                    if (lane == 0) mbar_arrive_cluster(p_full);
-                    ++tile;
-                }
+                if (lane == 0) mbar_arrive_cluster(p_full);
             }
             if (!ok) break;
-            if (dry) {
-                dry = 0;
-                continue;
-            }
             // the next segment, looked up while this one's last products run
             Segment ahead = s;
             have = next_segment(p, w, ahead);
