@@ -396,6 +396,9 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  * A sequence with n_b > L_b - prefix_len or a context beyond its page table (DSA_DEVERR_SEQ) and a token that
  * no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were; rows of a page that is out of range
  * (DSA_DEVERR_PAGE) are skipped.
+ * FP8 rows are multiplied as f16, with q as f16: an element code * scale, or a rotary value, of more than
+ * 16376, or a q of more than 262016, becomes infinite (and its row NaN); below 2^-16 elements lose
+ * relative precision.
  * Supported: D = 576, Dv = 512, Hq <= 128.
  */
 dsa_status_t dsa_prefix_attn(const dsa_dims_t* dims, int32_t prefix_len, const void* q, const void* kv_cache,

@@ -249,8 +249,8 @@ struct PrefixParams {
     // workspace (planned)
     int32_t* plan;  // merged: an int4 for each part; packed: behind those, an int2 for each item (see the kernels)
     float* partial;  // slots of kPartialFloats
-    int32_t convert_ahead;  // plan_prefix(): the prefix's FP8 rows are converted to bf16 first
-    uint8_t* ahead;         // those rows [ceil(prefix_len / 64) * 64][576] bf16, or null
+    int32_t convert_ahead;  // plan_prefix(): the prefix's FP8 rows are converted to f16 first
+    uint8_t* ahead;         // those rows [ceil(prefix_len / 64) * 64][576] f16, or null
 };
 constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs
 constexpr int kPlanItems = 2048;     // most items that are divided evenly
@@ -265,7 +265,7 @@ size_t prefix_partial_bytes(const PrefixParams& p);
 size_t prefix_ahead_bytes(const PrefixParams& p);
 struct PrefixLaunch {
     CUtensorMap qmap;  // 3-D view [9][T*Hq][64] of q: 64-dim atoms of 64 rows, nine at a time
-    // 4-D views [pages][9][64][64] of bf16 rows (the cache, or the prefix's FP8 rows converted ahead)
+    // 4-D views [pages][9][64][64] of 16-bit rows (the bf16 cache, or the prefix's FP8 rows converted ahead)
     CUtensorMap kmap;  // atoms of a page three at a time (converted rows: one)
     CUtensorMap vmap;  // four atoms (256 dims) at a time
     CUtensorMap codemap;  // FP8 rows, 4-D view [num_pages][4][64][128] of their codes: two scale tiles at a time

@@ -158,8 +158,10 @@ constexpr int kVSlots = 2;                  // V ring: slots of 64 positions x 2
 constexpr int kVSlot = 4 * kAtom;
 constexpr int kPBytes = 2 * kAtom;          // 64 rows x 128 positions
 constexpr int kSCol = 256;                  // tensor memory: O in columns 0-255, S tiles at 256 and 320
-constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
-constexpr uint32_t kIdescPV = make_idesc(128, 256, 1, 1, 0, 1);
+template <bool KVFP8>
+constexpr uint32_t kIdescQK = make_idesc(128, 128, KVFP8 ? 0 : 1, KVFP8 ? 0 : 1, 0, 0);
+template <bool KVFP8>
+constexpr uint32_t kIdescPV = make_idesc(128, 256, KVFP8 ? 0 : 1, KVFP8 ? 0 : 1, 0, 1);
 constexpr float kRaise = 8.f;  // raise the running maximum (log2) only when it grows by more than this
 
 struct Segment {
@@ -174,7 +176,8 @@ struct Ctrl {
     uint64_t v_full[kVSlots], v_empty[kVSlots];
     uint64_t s_full[2], s_empty[2];
     uint64_t p_full, pv_done, o_free, edge_full, drained, exchanged;
-    uint64_t k_raw[2], v_raw[2], k_conv[2], v_conv[2];  // FP8 tiles: the codes are here, are converted
+    // FP8: bf16 queries, codes and rotary parts are here; are converted
+    uint64_t q_raw, q_conv, k_raw[3], k_conv[3], v_raw[2], v_conv[2];
     uint32_t tmem_base;
     int32_t failed;
     int32_t first_place;  // this pair's first item (in `first`) and its place in it
@@ -257,10 +260,45 @@ __device__ __forceinline__ int page_of(const Tile& t, int h) {
     return first < t.hi ? __ldg(t.pages + (first >> 6)) : kNoPage;
 }
 
-// Infinities and NaN of a bf16 pair become 0.
+// Infinities and NaN of a pair (bf16, or f16) become 0.
+template <uint32_t kExponent = 0x7F80u>
 __device__ __forceinline__ uint32_t finite2(uint32_t v) {
-    if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
-    if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+    if ((v & kExponent) == kExponent) v &= 0xFFFF0000u;
+    if ((v & (kExponent << 16)) == kExponent << 16) v &= 0x0000FFFFu;
+    return v;
+}
+
+// FP8 rows are multiplied as f16, q and the weights with them: a code's four significant bits times a scale of eleven
+// lose three bits less than in bf16 (errors of 2^-11 against 2^-8), and a pair of codes takes two instructions rather
+// than six.  Rows are kept times kF16Gain, which cancels in the scores (q is divided by it) and is taken out of the
+// result, so that a row whose largest value is 0.007 still has a scale of full precision; the largest values are
+// 65504 / kF16Gain.
+constexpr float kF16Gain = 4.f;
+__device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the low half
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// Eight E4M3 codes times a scale given as a f16 pair.
+__device__ __forceinline__ uint4 codes_to_h8(uint32_t lo, uint32_t hi, uint32_t scale2) {
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint16_t pair = (uint16_t)((j < 2 ? lo : hi) >> (16 * (j & 1)));
+        asm("{\n\t.reg .b32 h;\n\tcvt.rn.f16x2.e4m3x2 h, %1;\n\tmul.rn.f16x2 %0, h, %2;\n\t}"
+            : "=r"(out[j])
+            : "h"(pair), "r"(scale2));
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+// Eight bf16 values times a power of two.
+__device__ __forceinline__ uint4 bf8_to_h8(uint4 v, float gain) {
+    auto pair = [&](uint32_t w) { return f2_to_h2(__uint_as_float(w << 16) * gain, __uint_as_float(w & 0xFFFF0000u) * gain); };
+    return make_uint4(pair(v.x), pair(v.y), pair(v.z), pair(v.w));
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
@@ -316,10 +354,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         mbar_init(&ctl->edge_full, 2 * kFillWarps);
         mbar_init(&ctl->drained, 1);
         if (KVFP8) {
-            for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->q_raw, 1);
+            mbar_init(&ctl->q_conv, 4 * kFillWarps);
+            for (int i = 0; i < 3; ++i) {
                 mbar_init(&ctl->k_raw[i], 1);
-                mbar_init(&ctl->v_raw[i], 1);
                 mbar_init(&ctl->k_conv[i], 2 * kFillWarps);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&ctl->v_raw[i], 1);
                 mbar_init(&ctl->v_conv[i], 2 * kFillWarps);
             }
         }
@@ -426,6 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(kAllLanes, mbar_wait(bar, parity, p.err, p.wait_ns)) != 0;
     };
+    const bool softmax_warp = warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4;
     bool ok = true;
 
     if (warp == 0) {
@@ -439,8 +482,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             int page0 = page_of(t, 0), page1 = page_of(t, 1), vpage0 = 0, vpage1 = 0;
             if (seg > 0 && !(ok = wait(&ctl->q_empty, (seg - 1) & 1u))) break;
             if (elect_one_sync()) {
-                if (rank == 0) mbar_arrive_expect_tx(&ctl->q_full, 2 * kQAtoms * kAtom);
-                tma_pair_load_3d(q_s, &qmap, q_full, 0, s.it.row0 + 64 * rank, 0);
+                if (KVFP8) {
+                    mbar_arrive_expect_tx(&ctl->q_raw, kQAtoms * kAtom);
+                    tma_load_3d(q_s, &qmap, &ctl->q_raw, 0, s.it.row0 + 64 * rank, 0);
+                } else {
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl->q_full, 2 * kQAtoms * kAtom);
+                    tma_pair_load_3d(q_s, &qmap, q_full, 0, s.it.row0 + 64 * rank, 0);
+                }
             }
             ++seg;
             for (int u = s.u0; ok && u <= s.u1; ++u) {
@@ -474,21 +522,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                             constexpr int kBytes = unit_atoms<KVFP8>(0) * kAtom;
                             uint8_t* dst = k_s + j * kBytes;
                             const uint32_t bar = k_full + 8 * j;
-                            if (KVFP8 && j < 2 && !t.copied) {
-                                // the codes of four atoms into the middle two (see the conversion below)
+                            if (KVFP8 && !t.copied) {
+                                // the codes of four atoms into the middle two, or the rotary part (see the conversion)
                                 if (rank == 0) mbar_arrive(&ctl->k_full[j]);
-                                mbar_arrive_expect_tx(&ctl->k_raw[j], 2 * kAtom);
-                                tma_load_4d(dst + kAtom, &codemap, &ctl->k_raw[j], 0, 0, 2 * j, page);
+                                mbar_arrive_expect_tx(&ctl->k_raw[j], (j < 2 ? 2 : 1) * kAtom);
+                                if (j < 2)
+                                    tma_load_4d(dst + kAtom, &codemap, &ctl->k_raw[j], 0, 0, 2 * j, page);
+                                else
+                                    tma_load_3d(dst, &rotmap, &ctl->k_raw[j], kKvFp8RopeOff, 0, page);
                             } else {
                                 if (rank == 0) mbar_arrive_expect_tx(&ctl->k_full[j], 2 * unit_atoms<KVFP8>(j) * kAtom);
-                                if (!KVFP8)
-                                    tma_pair_load_4d(dst, &kmap, bar, 0, 0, unit_atom<KVFP8>(j), page);
-                                else if (j < 2)
-                                    tma_pair_load_4d(dst, &vmap, bar, 0, 0, unit_atom<KVFP8>(j), page);
-                                else if (t.copied)
-                                    tma_pair_load_4d(dst, &kmap, bar, 0, 0, unit_atom<KVFP8>(j), page);
-                                else
-                                    tma_pair_load_3d(dst, &rotmap, bar, kKvFp8RopeOff, 0, page);
+                                tma_pair_load_4d(dst, KVFP8 && j < 2 ? &vmap : &kmap, bar, 0, 0, unit_atom<KVFP8>(j), page);
                             }
                         }
                     }
@@ -555,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             umma_pair_f16_ss(tmem + 128 * j, pa + (uint64_t)(2 * kk),
-                                             b + (uint64_t)(j * (2 * kAtom / 16) + 128 * kk), kIdescPV,
+                                             b + (uint64_t)(j * (2 * kAtom / 16) + 128 * kk), kIdescPV<KVFP8>,
                                              first && h == 0 && kk == 0 ? 0u : 1u);
                     umma_pair_commit(&ctl->v_empty[h], 3);
                     if (h == 1) umma_pair_commit(&ctl->pv_done, 3);
@@ -565,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             return true;
         };
         while (ok && next_segment(p, w, s)) {
-            if (!(ok = wait(&ctl->q_full, seg & 1u))) break;
+            if (!(ok = wait(KVFP8 ? &ctl->q_conv : &ctl->q_full, seg & 1u))) break;
             ++seg;
             bool edge = false, raw = false;
             for (int u = s.u0; ok && u < s.u1; ++u, ++tile) {
@@ -577,7 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 #pragma unroll
                 for (int j = 0; j < kKUnits; ++j) {
                     if (!(ok = wait(&ctl->k_full[j], tile & 1u))) break;
-                    if (KVFP8 && j < 2 && cur_raw && !(ok = wait(&ctl->k_conv[j], k_raws & 1u))) break;
+                    if (KVFP8 && cur_raw && !(ok = wait(&ctl->k_conv[j], k_raws & 1u))) break;
                     tc_fence_after();
                     if (elect_one_sync()) {
                         constexpr uint32_t kStep = kAtom / 16;
@@ -585,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 #pragma unroll
                         for (int kk = 0; kk < 4 * unit_atoms<KVFP8>(j); ++kk) {
                             const uint32_t at = (unit_atom<KVFP8>(j) + kk / 4) * kStep + 2 * (kk & 3);
-                            umma_pair_f16_ss(d, qd + at, kd + at, kIdescQK, j == 0 && kk == 0 ? 0u : 1u);
+                            umma_pair_f16_ss(d, qd + at, kd + at, kIdescQK<KVFP8>, j == 0 && kk == 0 ? 0u : 1u);
                         }
                         umma_pair_commit(&ctl->k_empty[j], 3);
                         if (j == kKUnits - 1) {
@@ -607,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             mbar_wait(&ctl->drained, 0, p.err);
         }
         __syncwarp();
-    } else if (warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4) {
+    } else if (softmax_warp) {
         // ---------------- softmax: thread (row, half of the positions) ----------------
         Walk w = start;
         Segment s = ctl->first;
@@ -693,15 +737,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 const float m_new = raise ? mt : m_used;
                 const float alpha = (raise && m_used != -INFINITY) ? exp2f(m_used - m_new) : 1.f;
                 const float mu = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf) = 0
-                // weights: the sum takes the fp32 values, the products their bf16 rounding (at most 2^-9 each
-                // way, unbiased), so that lse keeps fp32 accuracy
+                // weights: the sum takes the fp32 values, the products their rounding to bf16 or f16 (at most
+                // 2^-8 or 2^-11 of each, unbiased), so that lse keeps fp32 accuracy
                 uint32_t packed[32];
                 float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
                     const float e0 = exp2_fast(fmaf(sv[j], p.scale_log2, -mu));
                     const float e1 = exp2_fast(fmaf(sv[j + 1], p.scale_log2, -mu));
-                    packed[j / 2] = f2_to_bf2(e0, e1);
+                    packed[j / 2] = KVFP8 ? f2_to_h2(e0, e1) : f2_to_bf2(e0, e1);
                     ps[(j / 2) & 7] += e0 + e1;
                 }
                 const float rs = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
@@ -745,7 +789,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             const float l = half == 0 ? l_sum + other : other + l_sum;  // the same sum in both halves
             const bool whole = s.u0 == 0 && s.u1 == s.it.tiles_a + s.it.tiles_b && !p.packed;
             float* slot = p.partial + partial_slot(p, s.index, pair, s.u0 == 0) * kPartialFloats;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            constexpr float kTakeOut = KVFP8 ? 1.f / kF16Gain : 1.f;
+            const float inv = l == 0.f ? 0.f : kTakeOut / l;
             // A thread holds 256 values of its row.  They pass through this warp's part of the P memory, 128 bytes
             // a row at a time, so that a store instruction writes four whole 128-byte lines (row by row it touched
             // 32, and took 6400 cycles a segment).
@@ -805,8 +850,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     for (int k = 0; k < 8; ++k) {
                         const float* v = &o[k >> 2][4 * (k & 3)];
                         st_shared_v4(p_row + ((k ^ (r & 7)) << 4),
-                                     make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                                __float_as_uint(v[3])));
+                                     make_uint4(__float_as_uint(v[0] * kTakeOut), __float_as_uint(v[1] * kTakeOut),
+                                                __float_as_uint(v[2] * kTakeOut), __float_as_uint(v[3] * kTakeOut)));
                     }
                     if (c + 32 < 256) {  // the next ones come while these are written
                         tmem_ld16(trow + c + 32, o[0]);
@@ -883,32 +928,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         }
     }
     if constexpr (KVFP8) {
-        // ---------------- FP8 rows: codes times scales, rounded to bf16, into the K and V rings ----------------
+        // ---------------- FP8 rows: codes times scales, as f16, into the K and V rings ----------------
         // The codes of a row of two atoms (128 dims, one scale) come by TMA into that row's place in one of the two, so
         // that a row is expanded inside what it will fill: of four atoms, codes 0-127 lie in atom 1, 128-255 in atom
         // 2.  Eight lanes of a warp take a row, 16 codes each; they read, meet, and write.  Four warps expand K (this
-        // CTA's page), four V (both pages, this CTA's 256 dims), a row of every 16 each.  Tiles converted ahead pass by.
+        // CTA's page), four V (both pages, this CTA's 256 dims), a row of every 16 each; the rotary part and, at the
+        // start of a segment, q go from bf16 to f16 where they are.  Tiles converted ahead pass by.
         const int cw = warp < kSoftmaxWarp ? warp - 2 : warp - kFillWarp + 2;  // 0-3: K, 4-7: V
-        if (cw >= 0 && !(warp >= kSoftmaxWarp && warp < kSoftmaxWarp + 4)) {
+        if (cw >= 0 && !softmax_warp) {
             const bool v_side = cw >= kFillWarps;
-            const int row0 = 4 * (cw & 3) + (lane >> 3), c = lane & 7;  // rows row0 + 16 i
-            const uint32_t done = leader(v_side ? &ctl->v_conv[0] : &ctl->k_conv[0]);
+            const int row0 = 4 * (cw & 3) + (lane >> 3), c = lane & 7;  // rows row0 + 16 i; (row & 7) is row0 & 7
+            const uint32_t done = leader(v_side ? &ctl->v_conv[0] : &ctl->k_conv[0]), q_done = leader(&ctl->q_conv);
             uint64_t* raw = v_side ? ctl->v_raw : ctl->k_raw;
             const uint32_t ring = smem_u32(v_side ? v_s : k_s) + row0 * 128;
-            Walk w = start;
-            Segment s = ctl->first;
-            int u = 0, u1 = 0;
-            auto advance = [&](Tile& t) {  // the next tile that is to be converted
-                do {
-                    if (++u >= u1) {
-                        if (!next_segment(p, w, s)) return false;
-                        u = s.u0;
-                        u1 = s.u1;
-                    }
-                    t = tile_of(p, s.it, u);
-                } while (t.copied);
-                return true;
-            };
+            const uint32_t own16 = (c ^ (row0 & 7)) << 4;  // this lane's 16 bytes of a swizzled row
             // scales of this lane's rows in the order of use: K the four scale tiles of a row, V two of each page
             auto load_scales = [&](const Tile& t, float (&sc)[4][4]) {
 #pragma unroll
@@ -926,57 +959,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     }
                 }
             };
-            Tile t, tn;
-            float sc[4][4], next[4][4];
-            bool have = advance(t);
-            if (have) load_scales(t, sc);
-            uint32_t phase = 0;
-            while (ok && have) {
-                const bool have_next = advance(tn);
-                if (have_next) load_scales(tn, next);
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {  // two atoms each
-                    if (!(q & 1) && !(ok = wait(&raw[q >> 1], phase))) break;
-                    const uint32_t at = ring + (4 * (q >> 1)) * kAtom;
-                    const uint32_t from = at + ((q & 1) ? 2 : 1) * kAtom, to = at + ((q & 1) ? 2 : 0) * kAtom + (c >> 2) * kAtom;
-                    uint4 code[4];
+            Walk w = start;
+            Segment s = ctl->first;
+            uint32_t seg = 0, phase = 0;
+            while (ok && next_segment(p, w, s)) {
+                // the first tile that is to be converted, and its scales, while q is on its way
+                int u = p.ahead != nullptr ? max(s.u0, s.it.tiles_a) : s.u0;
+                Tile t = tile_of(p, s.it, min(u, s.u1 - 1));
+                float next[4][4];
+                if (u < s.u1) load_scales(t, next);
+                if (!(ok = wait(&ctl->q_raw, seg++ & 1u))) break;
+#pragma unroll 3
+                for (int i = 0; i < kQAtoms * 64 * 8 / (64 * kFillWarps); ++i) {  // 16-byte pieces, 256 lanes
+                    const uint32_t at = smem_u32(q_s) + 16 * (32 * cw + lane + 256 * i);
+                    st_shared_v4(at, bf8_to_h8(ld_shared_v4(at), 1.f / kF16Gain));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(q_done);
+                for (; ok && u < s.u1; ++u) {
+                    const Tile cur = t;
+                    uint32_t sc[4][4];  // f16 pairs
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(code[i].x), "=r"(code[i].y), "=r"(code[i].z), "=r"(code[i].w)
-                                     : "r"(from + 16 * i * 128 + ((c ^ (row0 & 7)) << 4))
-                                     : "memory");
-                    __syncwarp();
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 lo = e4m3x8_to_bf16x8(make_uint2(code[i].x, code[i].y), sc[0][i]);
-                        uint4 hi = e4m3x8_to_bf16x8(make_uint2(code[i].z, code[i].w), sc[0][i]);
-                        if (v_side && t.edge) {  // V of positions that do not exist is 0, and infinities and NaN are
-                            const int pos = t.base + 64 * (q >> 1) + row0 + 16 * i;
-                            const uint32_t keep = pos >= t.lo && pos < t.hi ? 0xFFFFFFFFu : 0u;
-                            lo = make_uint4(finite2(lo.x) & keep, finite2(lo.y) & keep, finite2(lo.z) & keep, finite2(lo.w) & keep);
-                            hi = make_uint4(finite2(hi.x) & keep, finite2(hi.y) & keep, finite2(hi.z) & keep, finite2(hi.w) & keep);
-                        }
-                        // (row & 7) is row0 & 7
-                        st_shared_v4(to + 16 * i * 128 + (((2 * (c & 3)) ^ (row0 & 7)) << 4), lo);
-                        st_shared_v4(to + 16 * i * 128 + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4), hi);
-                        sc[0][i] = sc[1][i];
-                        sc[1][i] = sc[2][i];
-                        sc[2][i] = sc[3][i];
+                        for (int i = 0; i < 4; ++i) sc[j][i] = f2_to_h2(next[j][i] * kF16Gain, next[j][i] * kF16Gain);
+                    if (u + 1 < s.u1) {
+                        t = tile_of(p, s.it, u + 1);
+                        load_scales(t, next);
                     }
-                    if (q & 1) {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {  // two atoms each
+                        if (!(q & 1) && !(ok = wait(&raw[q >> 1], phase))) break;
+                        const uint32_t at = ring + (4 * (q >> 1)) * kAtom;
+                        const uint32_t from = at + ((q & 1) ? 2 : 1) * kAtom;
+                        const uint32_t to = at + ((q & 1) ? 2 : 0) * kAtom + (c >> 2) * kAtom;
+                        uint4 code[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) code[i] = ld_shared_v4(from + 16 * i * 128 + own16);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint4 lo = codes_to_h8(code[i].x, code[i].y, sc[0][i]);
+                            uint4 hi = codes_to_h8(code[i].z, code[i].w, sc[0][i]);
+                            if (v_side && cur.edge) {  // V of positions that do not exist is 0, and infinities and NaN are
+                                const int pos = cur.base + 64 * (q >> 1) + row0 + 16 * i;
+                                const uint32_t keep = pos >= cur.lo && pos < cur.hi ? 0xFFFFFFFFu : 0u;
+                                auto clean = [&](uint32_t v) { return finite2<0x7C00u>(v) & keep; };
+                                lo = make_uint4(clean(lo.x), clean(lo.y), clean(lo.z), clean(lo.w));
+                                hi = make_uint4(clean(hi.x), clean(hi.y), clean(hi.z), clean(hi.w));
+                            }
+                            st_shared_v4(to + 16 * i * 128 + (((2 * (c & 3)) ^ (row0 & 7)) << 4), lo);
+                            st_shared_v4(to + 16 * i * 128 + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4), hi);
+                            sc[0][i] = sc[1][i];
+                            sc[1][i] = sc[2][i];
+                            sc[2][i] = sc[3][i];
+                        }
+                        if (q & 1) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(done + 8 * (q >> 1));
+                        }
+                    }
+                    if (ok && !v_side) {
+                        if (!(ok = wait(&raw[2], phase))) break;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t at = ring + 8 * kAtom + 16 * i * 128 + own16;
+                            st_shared_v4(at, bf8_to_h8(ld_shared_v4(at), kF16Gain));
+                        }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(done + 8 * (q >> 1));
+                        if (lane == 0) mbar_arrive_cluster(done + 16);
                     }
+                    phase ^= 1u;
                 }
-                phase ^= 1u;
-                have = have_next;
-                t = tn;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[j][i] = next[j][i];
             }
         }
     }
@@ -996,7 +1053,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// FP8 rows of the prefix to bf16, once for all the tiles of rows that attend to them: a warp per position, in the
+// FP8 rows of the prefix to f16 (times kF16Gain), once for all the tiles of rows that attend to them: a warp per position, in the
 // order of the positions (rows behind the prefix in its last page are zeros).  Bound by L2 and HBM: 656 bytes read,
 // 1152 written a row.
 // ---------------------------------------------------------------------------------------------------------
@@ -1020,9 +1077,10 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
         scale = __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (lane >> 3));
         if (lane < 8) rot = __ldg(reinterpret_cast<const uint4*>(src + kKvFp8RopeOff) + lane);
     }
-    dst[2 * lane] = e4m3x8_to_bf16x8(make_uint2(code.x, code.y), scale);
-    dst[2 * lane + 1] = e4m3x8_to_bf16x8(make_uint2(code.z, code.w), scale);
-    if (lane < 8) dst[64 + lane] = rot;
+    const uint32_t scale2 = f2_to_h2(scale * kF16Gain, scale * kF16Gain);
+    dst[2 * lane] = codes_to_h8(code.x, code.y, scale2);
+    dst[2 * lane + 1] = codes_to_h8(code.z, code.w, scale2);
+    if (lane < 8) dst[64 + lane] = bf8_to_h8(rot, kF16Gain);
 }
 
 // ---------------------------------------------------------------------------------------------------------

@@ -127,17 +127,18 @@ class Attention:
         * scores: products of bf16 are exact in fp32; 36 steps of 16 products are accumulated, each within
           (1 + 17) * 2^-23 of the magnitudes summed (fp32 alignment may truncate): dz <= 36 * 18 * 2^-23 * reach
           is the worst case, 2^-23 * 53 * reach that of one rounding a step and one group's alignment.
-        * FP8 rows are rounded to bf16 before the products: dz <= 2^-8 * reach.
-        * weights: exp2 within 2^-22 and bf16 rounding 2^-8 of each; partial sums in fp32;
-        * FP8 rows as values: 2^-8; the output's own rounding 2^-8 |out|."""
+        * FP8 rows are multiplied as f16 (11 bits): their scale and its product with a code are each rounded by
+          2^-11, so dz <= 2^-10 * reach.  (q, with 8 bits, is exact in f16.)
+        * weights: exp2 within 2^-22 and their rounding, bf16 2^-8, with FP8 rows f16 2^-11; partial sums in fp32;
+        * FP8 rows as values: 2^-10; the output's own rounding 2^-8 |out|."""
         t = slice(None) if tokens is None else tokens
-        dz = self.reach[t] * (53 * 2.0 ** -23 + (2.0 ** -8 if fp8 else 0.0))
-        rel = torch.expm1(2 * dz) + 2.0 ** -8 + (2.0 ** -8 if fp8 else 0.0) + 2.0 ** -16
+        dz = self.reach[t] * (53 * 2.0 ** -23 + (2.0 ** -10 if fp8 else 0.0))
+        rel = torch.expm1(2 * dz) + (2.0 ** -11 + 2.0 ** -10 if fp8 else 2.0 ** -8) + 2.0 ** -16
         tol = rel[..., None] * self.weighted[t] * (1 + 2.0 ** -7) + 2.0 ** -8 * self.out[t].abs() + 1e-30
         err = (out[t].double() - self.out[t]).abs()
         assert bool((err <= tol).all()), f"worst error {err.max().item():.3g}, {(err / tol).max().item():.3g} of its bound"
         norm = self.out[t].norm()
-        assert (err.norm() <= 6e-3 * norm) or norm == 0, f"relative error {(err.norm() / norm).item():.3g}"
+        assert (err.norm() <= (3e-3 if fp8 else 4e-3) * norm) or norm == 0, f"relative error {(err.norm() / norm).item():.3g}"
         if lse is not None:
             got = lse[t].double()
             finite = self.lse[t].isfinite()
