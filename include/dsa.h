@@ -391,11 +391,12 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  *   q, kv_cache, page_table, seq_lens, cu_q_lens, out, lse   as for dsa_sparse_attn
  *   workspace  dsa_prefix_attn_workspace_size(dims, prefix_len) bytes, first 256 zero-filled once
  * dims->idx_* and top_k are not looked at.  Positions beyond p_t and rows behind L_b are never part of the
- * result, whatever they hold.  A score of -inf has weight 0; a NaN in a visible row, or in q, makes
- * the rows that see it NaN; with every score -inf, out = 0 and lse = -inf.
- * A sequence with n_b > L_b - prefix_len or a context beyond its page table (DSA_DEVERR_SEQ) and a token that
- * no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were; rows of a page that is out of range
- * (DSA_DEVERR_PAGE) are skipped.
+ * result, whatever they hold.  A score of -inf has weight 0 (an infinite value of such a row makes NaN of it);
+ * a NaN in a visible row, or in q, makes the rows that see it NaN; with every score -inf, out = 0 and
+ * lse = -inf.
+ * A sequence with n_b > L_b - prefix_len, n_b > max_q_len or a context beyond its page table (DSA_DEVERR_SEQ) and
+ * a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were; rows of a page that is out of
+ * range (DSA_DEVERR_PAGE) are skipped.
  * FP8 rows are multiplied as f16, with q as f16: an element code * scale, or a rotary value, of more than
  * 16376, or a q of more than 262016, becomes infinite (and its row NaN); below 2^-16 elements lose
  * relative precision.

@@ -43,6 +43,13 @@ namespace {
 constexpr uint32_t kAllLanes = 0xFFFFFFFFu;
 constexpr float kLn2 = 0.69314718055994531f;
 
+// An ordinary load of an input.  These kernels may be resident before the kernel that writes their inputs has ended
+// (they wait for its end before they load): not a case for loads that take memory as constant for a kernel's duration.
+template <typename T>
+__device__ __forceinline__ T ld_input(const T* p) {
+    return *p;
+}
+
 // ---------------------------------------------------------------------------------------------------------
 // Items and their division among the CTA pairs (used by both kernels)
 // ---------------------------------------------------------------------------------------------------------
@@ -58,8 +65,8 @@ struct Item {
 
 // Offsets and length of sequence b; false when they are inconsistent.
 __device__ __forceinline__ bool sequence(const PrefixParams& p, int b, int* c0, int* n, int* L) {
-    const int a = __ldg(p.cu_q_lens + b), e = __ldg(p.cu_q_lens + b + 1);
-    *L = __ldg(p.seq_lens + b);
+    const int a = ld_input(p.cu_q_lens + b), e = ld_input(p.cu_q_lens + b + 1);
+    *L = ld_input(p.seq_lens + b);
     *c0 = a;
     *n = e - a;
     if (a < 0 || e < a || e > p.total_q || *n > p.max_q_len) return false;
@@ -257,7 +264,7 @@ __device__ __forceinline__ Tile tile_of(const PrefixParams& p, const Item& it, i
 constexpr int kNoPage = INT32_MIN;
 __device__ __forceinline__ int page_of(const Tile& t, int h) {
     const int first = t.base + 64 * h;
-    return first < t.hi ? __ldg(t.pages + (first >> 6)) : kNoPage;
+    return first < t.hi ? ld_input(t.pages + (first >> 6)) : kNoPage;
 }
 
 // Infinities and NaN of a pair (bf16, or f16) become 0.
@@ -386,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             int c0, n, L;
             if (!sequence(p, b, &c0, &n, &L)) raise_error(p.err, DSA_DEVERR_SEQ);
         }
-        if (tid == 0 && (__ldg(p.cu_q_lens) != 0 || __ldg(p.cu_q_lens + p.batch) != p.total_q))
+        if (tid == 0 && (ld_input(p.cu_q_lens) != 0 || ld_input(p.cu_q_lens + p.batch) != p.total_q))
             raise_error(p.err, DSA_DEVERR_SEQ);
     }
     Walk start;
@@ -894,7 +901,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     const uint8_t* src = p.kv_cache + ((int64_t)(in ? pg : 0) * 64 + row0) * 1152 + 512 * rank + 16 * lane;
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        v[h][k] = in && pos + k >= t.lo && pos + k < t.hi ? __ldg(reinterpret_cast<const uint4*>(src + 1152 * k))
+                        v[h][k] = in && pos + k >= t.lo && pos + k < t.hi ? ld_input(reinterpret_cast<const uint4*>(src + 1152 * k))
                                                                           : make_uint4(0, 0, 0, 0);
                 }
                 uint32_t found = 0;  // an exponent of all ones carries into the sign bit's place
@@ -952,7 +959,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                                          (v_side ? 8 * rank : 8 * h);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 v = in ? __ldg(reinterpret_cast<const float2*>(src + 16 * i * kKvFp8RowBytes))
+                        const float2 v = in ? ld_input(reinterpret_cast<const float2*>(src + 16 * i * kKvFp8RowBytes))
                                             : make_float2(0.f, 0.f);
                         sc[2 * h][i] = v.x;
                         sc[2 * h + 1][i] = v.y;
@@ -1066,16 +1073,16 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
     grid_dependency_wait();
     allow_dependent_launch();
     uint4* dst = reinterpret_cast<uint4*>(p.ahead + (int64_t)pos * 1152);
-    const int pg = pos < p.prefix_len ? __ldg(p.page_table + (pos >> 6)) : -1;
+    const int pg = pos < p.prefix_len ? ld_input(p.page_table + (pos >> 6)) : -1;
     const bool in = pg >= 0 && pg < p.num_pages;
     if (!in && pos < p.prefix_len && lane == 0) raise_error(p.err, DSA_DEVERR_PAGE);
     uint4 code = make_uint4(0, 0, 0, 0), rot = code;
     float scale = 0.f;
     if (in) {
         const uint8_t* src = p.kv_cache + ((int64_t)pg * 64 + (pos & 63)) * kKvFp8RowBytes;
-        code = __ldg(reinterpret_cast<const uint4*>(src) + lane);
-        scale = __ldg(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (lane >> 3));
-        if (lane < 8) rot = __ldg(reinterpret_cast<const uint4*>(src + kKvFp8RopeOff) + lane);
+        code = ld_input(reinterpret_cast<const uint4*>(src) + lane);
+        scale = ld_input(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (lane >> 3));
+        if (lane < 8) rot = ld_input(reinterpret_cast<const uint4*>(src + kKvFp8RopeOff) + lane);
     }
     const uint32_t scale2 = f2_to_h2(scale * kF16Gain, scale * kF16Gain);
     dst[2 * lane] = codes_to_h8(code.x, code.y, scale2);
@@ -1177,7 +1184,7 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(
     int b = -1, c0 = 0, n = 0, L = 0;
     for (int j0 = 0; j0 < p.batch && b < 0; j0 += 32) {
         const int j = j0 + lane;
-        const bool hit = j < p.batch && __ldg(p.cu_q_lens + j) <= t && t < __ldg(p.cu_q_lens + j + 1);
+        const bool hit = j < p.batch && ld_input(p.cu_q_lens + j) <= t && t < ld_input(p.cu_q_lens + j + 1);
         const uint32_t bal = __ballot_sync(kAllLanes, hit);
         if (bal) b = j0 + __ffs(bal) - 1;
     }

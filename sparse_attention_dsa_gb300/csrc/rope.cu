@@ -8,9 +8,9 @@
 // Quantisation: scale = absmax / 448 per group (1 for an all-zero group) and E4M3(x / scale), correctly
 // rounded divisions; MXFP8 groups of 32 take 2^(floor(log2(absmax)) - 8).
 //
-// What bounds it: HBM for long steps (every byte is read and written once), launch and a chain of four
-// dependent loads (query offsets -> length -> page and table row) for short ones.  So a row is held as
-// 16-byte pieces, one to three a lane, whose loads are issued before that chain starts, and a 64-dim rotary
+// What bounds it: HBM for long steps (every byte is read and written once), launch and a chain of three
+// dependent loads (query offsets and length -> page and table row -> stores) for short ones.  So a row is held
+// as 16-byte pieces, one to three a lane, whose loads are issued before that chain starts, and a 64-dim rotary
 // block is 8 neighbouring lanes: interleaved pairs lie inside a piece, the halves' partner is the piece four
 // further, fetched by a shuffle.
 #include <cuda_runtime.h>
@@ -23,6 +23,24 @@ namespace dsa {
 namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// Two fp32 products, two fp32 sums in one instruction each (rounded like the single ones).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
 // Two E4M3 codes (a in the low byte), nearest-even, saturating at +-448.
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
@@ -43,68 +61,107 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]), f2_to_bf2(x[4], x[5]), f2_to_bf2(x[6], x[7]));
 }
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+__device__ __forceinline__ uint2 pack_codes(const float (&y)[8]) {
     return make_uint2(codes2(y[0], y[1]) | (codes2(y[2], y[3]) << 16), codes2(y[4], y[5]) | (codes2(y[6], y[7]) << 16));
 }
-__device__ __forceinline__ float absmax8(const float (&x)[8]) {
-    float m = 0.f;
+// E4M3 codes of x / scale, the quotient correctly rounded to fp32 first (so that both appends make the same codes).
+// Eight divisions are most of a piece's instructions, and the product with 1 / scale differs from the quotient by a
+// few units in the last place: only where it lies that close to a value halfway between two codes (fp32 bits 19..0
+// near 0x80000; below 2^-6 the codes have another spacing) are the quotients themselves taken.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
+    const float inv = __fdiv_rn(1.f, scale);
+    float y[8];
+    bool near = !(inv < 3e38f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-    return m;
+    for (int i = 0; i < 8; ++i) {
+        y[i] = x[i] * inv;
+        const uint32_t low = __float_as_uint(y[i]) & 0xFFFFFu;
+        near |= low - 0x7FFF8u <= 16u || fabsf(y[i]) < 0.015626f;
+    }
+    if (near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+    }
+    return pack_codes(y);
+}
+// The same for a scale of 2^e, -127 <= e <= 120: the product with 2^-e, a normal number, is the quotient.
+__device__ __forceinline__ uint2 codes8_exp(const float (&x)[8], int e) {
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 v = mul2(make_float2(x[i], x[i + 1]), make_float2(inv, inv));
+        y[i] = v.x;
+        y[i + 1] = v.y;
+    }
+    return pack_codes(y);
+}
+__device__ __forceinline__ float absmax8(const float (&x)[8]) {
+    const float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fabsf(x[2]));
+    const float b = fmaxf(fmaxf(fabsf(x[3]), fabsf(x[4])), fabsf(x[5]));
+    return fmaxf(fmaxf(fmaxf(a, b), fmaxf(fabsf(x[6]), fabsf(x[7]))), 0.f);  // (the 0: a group of NaN alone)
 }
 // absmax / 448 in fp32 (1 for an all-zero group)
 __device__ __forceinline__ float group_scale(float amax) { return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f; }
 
-// Shared exponent of an MX group: floor(log2(absmax)) - 8 within the E8M0 range, 0 for an all-zero group.
-// (Subnormal maxima lie below the clamp either way; infinities and NaN take the top exponent.)
+// Shared exponent of an MX group: floor(log2(absmax)) - 8 within the E8M0 range, 0 for an all-zero group.  (Subnormal
+// maxima lie below the range either way; an infinity gives 120.)
 __device__ __forceinline__ int mx_exponent(float amax) {
-    if (!(amax > 0.f)) return 0;
-    const int e = (int)(__float_as_uint(amax) >> 23) - 127 - 8;
-    return max(-127, min(127, e));
-}
-// 2^e for e in [-127, 127] (2^-127 is subnormal)
-__device__ __forceinline__ float exp2_int(int e) {
-    return e > -127 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(0x00400000u);
+    const uint32_t bits = __float_as_uint(amax);
+    return bits == 0u ? 0 : max(-127, (int)(bits >> 23) - 127 - 8);
 }
 
-// Rotates piece j (0..7) of a 64-dim rotary block in place.  Every lane of the warp calls it; `partner` is
-// the lane that holds piece j ^ 4 of the same block (any lane when !on).
-__device__ __forceinline__ void rotate_piece(float (&x)[8], const uint4& own, int j, bool on, int partner,
-                                             bool interleaved, const float* row) {
-    uint4 o;
-    o.x = __shfl_sync(kAll, own.x, partner);
-    o.y = __shfl_sync(kAll, own.y, partner);
-    o.z = __shfl_sync(kAll, own.z, partner);
-    o.w = __shfl_sync(kAll, own.w, partner);
-    if (!on) return;
+// A 64-dim rotary block is 8 pieces of 8 values.  Value i of piece j becomes x_i c_i + o_i s_i, o_i its partner in the
+// pair and s_i the sine with the sign of its side: the same c and s for every row of a token, so they are loaded once.
+struct Turn {
+    float c[8], s[8];
+};
+__device__ __forceinline__ void load_turn(Turn& t, const float* row, int j, bool interleaved) {
     const float4* t4 = reinterpret_cast<const float4*>(row);
-    if (interleaved) {
+    if (interleaved) {  // pairs (2i, 2i + 1) of the piece, angles 4j ..
         const float4 c = __ldg(t4 + j), s = __ldg(t4 + 8 + j);
         const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, cc[i]), __fmul_rn(b, ss[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(a, ss[i]), __fmul_rn(b, cc[i]));
+            t.c[2 * i] = t.c[2 * i + 1] = cc[i];
+            t.s[2 * i] = -ss[i];
+            t.s[2 * i + 1] = ss[i];
         }
-    } else {
-        float y[8];
-        unpack8(o, y);
+    } else {  // partner in piece j ^ 4, angles 8 (j & 3) ..
         const int q = 2 * (j & 3);
         const float4 c0 = __ldg(t4 + q), c1 = __ldg(t4 + q + 1), s0 = __ldg(t4 + 8 + q), s1 = __ldg(t4 + 9 + q);
         const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
         const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            // first half: x1 cos - x2 sin; second half: x1 sin + x2 cos
-            if (j < 4)
-                x[i] = __fsub_rn(__fmul_rn(x[i], cc[i]), __fmul_rn(y[i], ss[i]));
-            else
-                x[i] = __fadd_rn(__fmul_rn(y[i], ss[i]), __fmul_rn(x[i], cc[i]));
+            t.c[i] = cc[i];
+            t.s[i] = j < 4 ? -ss[i] : ss[i];
         }
+    }
+}
+// x: piece `own`, rotated in place where `on`.  `partner`: the lane that holds piece j ^ 4 (halves; every lane of the
+// warp calls).
+__device__ __forceinline__ void rotate_piece(float (&x)[8], const uint4& own, bool on, int partner, bool interleaved,
+                                             const Turn& t) {
+    float o[8];
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
+    } else {
+        uint4 v;
+        v.x = __shfl_sync(kAll, own.x, partner);
+        v.y = __shfl_sync(kAll, own.y, partner);
+        v.z = __shfl_sync(kAll, own.z, partner);
+        v.w = __shfl_sync(kAll, own.w, partner);
+        unpack8(v, o);
+    }
+    if (!on) return;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 y = add2(mul2(make_float2(x[i], x[i + 1]), make_float2(t.c[i], t.c[i + 1])),
+                              mul2(make_float2(o[i], o[i + 1]), make_float2(t.s[i], t.s[i + 1])));
+        x[i] = y.x;
+        x[i + 1] = y.y;
     }
 }
 
@@ -143,11 +200,49 @@ __device__ __forceinline__ bool locate(const RopeParams& r, int t, int lane, int
     return true;
 }
 
+// Rotates piece j (0..7) of a 64-dim rotary block in place.  Every lane of the warp calls it; `partner` is
+// the lane that holds piece j ^ 4 of the same block (any lane when !on).
+__device__ __forceinline__ void turn_piece(float (&x)[8], const uint4& own, int j, bool on, int partner,
+                                             bool interleaved, const float* row) {
+    uint4 o;
+    o.x = __shfl_sync(kAll, own.x, partner);
+    o.y = __shfl_sync(kAll, own.y, partner);
+    o.z = __shfl_sync(kAll, own.z, partner);
+    o.w = __shfl_sync(kAll, own.w, partner);
+    if (!on) return;
+    const float4* t4 = reinterpret_cast<const float4*>(row);
+    if (interleaved) {
+        const float4 c = __ldg(t4 + j), s = __ldg(t4 + 8 + j);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(a, cc[i]), __fmul_rn(b, ss[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(a, ss[i]), __fmul_rn(b, cc[i]));
+        }
+    } else {
+        float y[8];
+        unpack8(o, y);
+        const int q = 2 * (j & 3);
+        const float4 c0 = __ldg(t4 + q), c1 = __ldg(t4 + q + 1), s0 = __ldg(t4 + 8 + q), s1 = __ldg(t4 + 9 + q);
+        const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // first half: x1 cos - x2 sin; second half: x1 sin + x2 cos
+            if (j < 4)
+                x[i] = __fsub_rn(__fmul_rn(x[i], cc[i]), __fmul_rn(y[i], ss[i]));
+            else
+                x[i] = __fadd_rn(__fmul_rn(y[i], ss[i]), __fmul_rn(x[i], cc[i]));
+        }
+    }
+}
+
 constexpr int kAppendWarps = 8;
 
 // One warp per token.  Lane pieces: kv pieces lane and lane + 32 (the latent part, 16 lanes a 128-dim tile);
 // a third piece is the rotary part in lanes 0-7 and the indexer key in lanes 16-31.
-__global__ void __launch_bounds__(32 * kAppendWarps) rope_append_kernel(const RopeAppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 6) rope_append_kernel(const RopeAppendParams p) {
     const RopeParams& r = p.r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kAppendWarps + warp;
@@ -181,7 +276,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) rope_append_kernel(const Ro
         const int j = lane < 8 ? lane : kp - b8;
         const bool on = rot_on || (k_on && r.idx_begin >= 0 && j >= 0 && j < 8);
         const int partner = on ? (lane < 8 ? lane ^ 4 : 16 + b8 + (j ^ 4)) : lane;
-        rotate_piece(x, v2, j, on, partner, lane < 8 ? r.kv_interleaved != 0 : r.idx_interleaved != 0,
+        turn_piece(x, v2, j, on, partner, lane < 8 ? r.kv_interleaved != 0 : r.idx_interleaved != 0,
                      r.table + (int64_t)pos * 64);
     }
     if (has_kv && !p.kv_fp8) {
@@ -213,7 +308,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) rope_append_kernel(const Ro
         if (r.idx_dtype == DSA_MXFP8_E4M3) {
             const int e = mx_exponent(m);
             if (k_on) {
-                reinterpret_cast<uint2*>(p.k_cache + row * Di)[kp] = codes8(x, exp2_int(e));
+                reinterpret_cast<uint2*>(p.k_cache + row * Di)[kp] = codes8_exp(x, e);
                 if ((kp & 3) == 0) static_cast<uint8_t*>(p.k_scale)[row * (Di / 32) + (kp >> 2)] = (uint8_t)(e + 127);
             }
         } else {
@@ -228,83 +323,106 @@ __global__ void __launch_bounds__(32 * kAppendWarps) rope_append_kernel(const Ro
     }
 }
 
-constexpr int kQueryWarps = 8;
-constexpr int kSteps = 4;  // pieces a lane has in flight
+constexpr int kQueryWarps = 4;
+constexpr int kSteps = 4;    // warp steps in flight
 
-// A token's work is a list of warp steps: step i < pe_steps rotates heads 4i..4i+3 (8 lanes a head), later
-// ones hold two indexer rows (16 lanes a row).  gridDim.y CTAs share a token's steps.
-__global__ void __launch_bounds__(32 * kQueryWarps) rope_queries_kernel(const RopeQueriesParams p) {
+// Position of token t, found by warp 0 for the CTA; -1 where it has none.
+__device__ __forceinline__ int cta_position(const RopeParams& r, int t, int warp, int lane) {
+    __shared__ int found;
+    if (warp == 0) {
+        int b, pos;
+        const bool ok = locate(r, t, lane, &b, &pos);
+        if (lane == 0) found = ok ? pos : -1;
+    }
+    __syncthreads();
+    return found;
+}
+
+// A token's work is two lists of warp steps, each shared by the warps of its CTAs (blockIdx.y): heads 4s .. 4s + 3 of
+// the attention's queries (8 lanes a head, `pe_parts` CTAs), and two indexer rows (16 lanes a row, the other CTAs); a
+// warp takes at most kSteps steps, all in flight at once.  IDX: dsa_dtype_t of the indexer's output.
+template <int IDX>
+__global__ void __launch_bounds__(32 * kQueryWarps, 8) rope_queries_kernel(const RopeQueriesParams p, int pe_parts) {
     const RopeParams& r = p.r;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = blockIdx.x;
-    const int Di = r.idx_dim;
-    const int pe_steps = p.q_pe ? (p.heads + 3) / 4 : 0;
-    const int steps = pe_steps + (p.q_idx_in ? (p.idx_heads + 1) / 2 : 0);
-    const int stride = (int)gridDim.y * kQueryWarps;
-    int b = 0, pos = 0;
-    bool located = false;
-    for (int s0 = (int)blockIdx.y * kQueryWarps + warp; s0 < steps; s0 += stride * kSteps) {
+    if ((int)blockIdx.y < pe_parts) {
+        const int stride = pe_parts * kQueryWarps, s0 = (int)blockIdx.y * kQueryWarps + warp;
+        const int j = lane & 7, h0 = lane >> 3;  // piece, head of the step
+        const uint16_t* src = p.q_pe + t * p.q_pe_token_stride + h0 * p.q_pe_head_stride + 8 * j;
         uint4 v[kSteps];
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            const int s = s0 + k * stride;
-            v[k] = make_uint4(0, 0, 0, 0);
-            if (s < pe_steps) {
-                const int h = 4 * s + (lane >> 3);
-                if (h < p.heads)
-                    v[k] = *reinterpret_cast<const uint4*>(p.q_pe + t * p.q_pe_token_stride + h * p.q_pe_head_stride +
-                                                           8 * (lane & 7));
-            } else if (s < steps) {
-                const int h = 2 * (s - pe_steps) + (lane >> 4);
-                if (h < p.idx_heads && 8 * (lane & 15) < Di)
-                    v[k] = *reinterpret_cast<const uint4*>(p.q_idx_in + t * p.q_idx_stride + (int64_t)h * Di +
-                                                           8 * (lane & 15));
-            }
+            const int h = 4 * (s0 + k * stride);
+            v[k] = h + h0 < p.heads ? *reinterpret_cast<const uint4*>(src + h * p.q_pe_head_stride) : make_uint4(0, 0, 0, 0);
         }
-        if (!located) {
-            if (!locate(r, (int)t, lane, &b, &pos)) return;  // uniform over the warp
-            located = true;
-        }
-        const float* row = r.table + (int64_t)pos * 64;
+        const int pos = cta_position(r, (int)t, warp, lane);
+        if (pos < 0) return;
+        const bool inter = r.kv_interleaved != 0;
+        Turn turn;
+        load_turn(turn, r.table + (int64_t)pos * 64, j, inter);
+        uint16_t* dst = p.q + (t * p.heads + h0) * 576 + 512 + 8 * j;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            const int s = s0 + k * stride;
-            if (s >= steps) break;  // uniform over the warp
+            const int h = 4 * (s0 + k * stride);
+            if (h >= p.heads) break;  // uniform over the warp
             float x[8];
             unpack8(v[k], x);
-            if (s < pe_steps) {
-                const int h = 4 * s + (lane >> 3);
-                rotate_piece(x, v[k], lane & 7, true, lane ^ 4, r.kv_interleaved != 0, row);
-                if (h < p.heads)
-                    reinterpret_cast<uint4*>(p.q + (t * p.heads + h) * 576 + 512)[lane & 7] = pack8(x);
-                continue;
-            }
-            const int h = 2 * (s - pe_steps) + (lane >> 4), kp = lane & 15;
-            const bool on = h < p.idx_heads && 8 * kp < Di;
-            const int b8 = r.idx_begin >> 3, j = kp - b8;
-            const bool rot = on && r.idx_begin >= 0 && j >= 0 && j < 8;
-            rotate_piece(x, v[k], j, rot, rot ? (lane & 16) + b8 + (j ^ 4) : lane, r.idx_interleaved != 0, row);
-            const int64_t out = t * p.idx_heads + h;
-            if (r.idx_dtype == DSA_BF16) {
-                if (on) reinterpret_cast<uint4*>(p.q_idx + out * Di * 2)[kp] = pack8(x);
-                continue;
-            }
-            float m = on ? absmax8(x) : 0.f;
+            rotate_piece(x, v[k], true, lane ^ 4, inter, turn);
+            if (h + h0 < p.heads) *reinterpret_cast<uint4*>(dst + h * 576) = pack8(x);
+        }
+        return;
+    }
+    const int Di = r.idx_dim, stride = ((int)gridDim.y - pe_parts) * kQueryWarps;
+    const int s0 = ((int)blockIdx.y - pe_parts) * kQueryWarps + warp;
+    const int kp = lane & 15, h0 = lane >> 4;  // piece, row of the step
+    const bool in = 8 * kp < Di;
+    const uint16_t* src = p.q_idx_in + t * p.q_idx_stride + h0 * Di + 8 * kp;
+    uint4 w[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        const int h = 2 * (s0 + k * stride);
+        w[k] = h + h0 < p.idx_heads && in ? *reinterpret_cast<const uint4*>(src + h * Di) : make_uint4(0, 0, 0, 0);
+    }
+    const int pos = cta_position(r, (int)t, warp, lane);
+    if (pos < 0) return;
+    const int b8 = r.idx_begin >> 3, j = kp - b8;
+    const bool inter = r.idx_interleaved != 0;
+    const bool turns = in && r.idx_begin >= 0 && j >= 0 && j < 8;
+    const int partner = turns ? (lane & 16) + b8 + (j ^ 4) : lane;
+    Turn turn;
+    if (turns) load_turn(turn, r.table + (int64_t)pos * 64, j, inter);
+    const int64_t row0 = t * p.idx_heads + h0;
+    uint8_t* dst = p.q_idx + row0 * Di * (IDX == DSA_BF16 ? 2 : 1) + kp * (IDX == DSA_BF16 ? 16 : 8);
+    const int row_bytes = IDX == DSA_BF16 ? 2 * Di : Di;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        const int h = 2 * (s0 + k * stride);
+        if (h >= p.idx_heads) break;  // uniform over the warp
+        const bool on = h + h0 < p.idx_heads && in;
+        float x[8];
+        unpack8(w[k], x);
+        if (r.idx_begin >= 0) rotate_piece(x, w[k], turns, partner, inter, turn);
+        if constexpr (IDX == DSA_BF16) {
+            if (on) *reinterpret_cast<uint4*>(dst + h * row_bytes) = pack8(x);
+        } else {
+            float m = absmax8(x);  // 0 where there is no piece
             m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
             m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
-            if (r.idx_dtype == DSA_MXFP8_E4M3) {
+            if constexpr (IDX == DSA_MXFP8_E4M3) {
                 const int e = mx_exponent(m);
                 if (on) {
-                    reinterpret_cast<uint2*>(p.q_idx + out * Di)[kp] = codes8(x, exp2_int(e));
-                    if ((kp & 3) == 0) static_cast<uint8_t*>(p.q_scale)[out * (Di / 32) + (kp >> 2)] = (uint8_t)(e + 127);
+                    *reinterpret_cast<uint2*>(dst + h * row_bytes) = codes8_exp(x, e);
+                    if ((kp & 3) == 0)
+                        static_cast<uint8_t*>(p.q_scale)[(row0 + h) * (Di / 32) + (kp >> 2)] = (uint8_t)(e + 127);
                 }
             } else {
                 m = fmaxf(m, __shfl_xor_sync(kAll, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(kAll, m, 8));
                 const float scale = group_scale(m);
                 if (on) {
-                    reinterpret_cast<uint2*>(p.q_idx + out * Di)[kp] = codes8(x, scale);
-                    if (kp == 0) static_cast<float*>(p.q_scale)[out] = scale;
+                    *reinterpret_cast<uint2*>(dst + h * row_bytes) = codes8(x, scale);
+                    if (kp == 0) static_cast<float*>(p.q_scale)[row0 + h] = scale;
                 }
             }
         }
@@ -320,11 +438,21 @@ cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_rope_queries(const RopeQueriesParams& p, cudaStream_t stream) {
-    // few tokens: each one's steps are spread over several CTAs, until the SMs have one each
-    const int steps = (p.q_pe ? (p.heads + 3) / 4 : 0) + (p.q_idx_in ? (p.idx_heads + 1) / 2 : 0);
-    int parts = 1;
-    while (parts * kQueryWarps < steps && (int64_t)p.r.total_q * parts < 2 * p.num_sms) ++parts;
-    rope_queries_kernel<<<dim3((unsigned)p.r.total_q, (unsigned)parts), 32 * kQueryWarps, 0, stream>>>(p);
+    // CTAs of each kind a token: enough for kSteps steps a warp; with few tokens more, until the SMs have two each
+    const int pe = p.q_pe ? (p.heads + 3) / 4 : 0, idx = p.q_idx_in ? (p.idx_heads + 1) / 2 : 0;
+    auto parts = [&](int steps) {
+        int n = steps > 0 ? 1 : 0;
+        while (n * kQueryWarps < steps && (n * kQueryWarps * kSteps < steps || (int64_t)p.r.total_q * n < p.num_sms)) ++n;
+        return n;
+    };
+    const int pe_parts = parts(pe);
+    const dim3 grid((unsigned)p.r.total_q, (unsigned)(pe_parts + parts(idx))), block(32 * kQueryWarps);
+    if (p.r.idx_dtype == DSA_MXFP8_E4M3)
+        rope_queries_kernel<DSA_MXFP8_E4M3><<<grid, block, 0, stream>>>(p, pe_parts);
+    else if (p.r.idx_dtype == DSA_FP8_E4M3)
+        rope_queries_kernel<DSA_FP8_E4M3><<<grid, block, 0, stream>>>(p, pe_parts);
+    else
+        rope_queries_kernel<DSA_BF16><<<grid, block, 0, stream>>>(p, pe_parts);
     return cudaGetLastError();
 }
 

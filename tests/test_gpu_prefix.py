@@ -70,6 +70,12 @@ SHAPES = {
     "full_heads_many": ([1100 + 7 * i for i in range(12)], [1] * 12, 1090, 128),
     "full_heads_chunk": ([600, 700], [100, 150], 450, 128),
     "heads_33": ([2100, 2300, 2048], [1, 9, 4], 2000, 33),
+    # enough tiles of rows over the prefix that FP8 rows are converted ahead: merged, then packed rows
+    "full_heads_long_prefix": ([1100 + 7 * i for i in range(20)], [1] * 20, 1090, 128),
+    "packed_long_prefix": ([2510 + 3 * i for i in range(64)], [1] * 64, 2500, 16),
+    # more items than are divided evenly: whole items in turn
+    "thousands_of_short_ones": ([1 + i % 70 for i in range(2100)], [1] * 2100, 0, 128),
+    "many_behind_one_page": ([64 + 1 + i % 5 for i in range(300)], [1] * 300, 64, 32),
 }
 
 
@@ -110,7 +116,7 @@ def test_without_lse():
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("name", ["own_page_copies", "no_prefix_ragged", "ragged_queries_and_none", "whole_prompt",
-                                  "whole_prompts_behind_a_prefix", "packed_many", "full_heads_chunk"])
+                                  "whole_prompts_behind_a_prefix", "packed_many", "full_heads_chunk", "full_heads_long_prefix", "packed_long_prefix"])
 def test_what_is_not_visible_does_not_matter(name, fp8):
     """NaN and infinities in rows behind each sequence's end, in spare pages, and in the copies of the prefix's
     last page that are not read, change no bit."""
@@ -239,6 +245,53 @@ def test_two_calls_at_once_with_their_own_workspaces():
     torch.cuda.synchronize()
     a.check()
     b.check()
+
+
+def test_two_graphs_of_one_workspace():
+    """Two captured calls of different shapes that share a workspace, replayed in turn."""
+    a, b = Call(*SHAPES["packed_long_prefix"], fp8=True, seed=18), Call(*SHAPES["full_heads_many"], seed=19)
+    size = max(a.workspace.numel(), b.workspace.numel())
+    a.workspace = b.workspace = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c in (a, b):
+        c.run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run()
+        graphs.append(g)
+        c.out.zero_(), c.lse.zero_()
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    a.check()
+    b.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("name", ["packed_many", "full_heads_chunk", "one_token_no_prefix"])
+def test_waits_give_up_at_their_limit(name, fp8):
+    """With a limit of a nanosecond some wait finds its phase incomplete and gives up: the call reports it and ends,
+    and the next call, at the default limit, is right."""
+    c = Call(*SHAPES[name], fp8=fp8, seed=20)
+    old = dsa.set_wait_limit_ns(1)
+    try:
+        c.run()
+        assert c.error() & dsa.DSA_DEVERR_TIMEOUT
+    finally:
+        dsa.set_wait_limit_ns(old)
+    dsa.clear_device_error(c.workspace)
+    c.run().check()
+
+
+def test_more_queries_than_announced_are_reported():
+    c = Call([300, 300], [1, 3], 200, 16, seed=21)
+    c.dims.max_q_len = 2
+    ref = Attention(c.b, c.q, c.cache, False)
+    c.run()
+    assert c.error() == dsa.DSA_DEVERR_SEQ
+    assert bool((c.out[1:] == 7).all())
+    ref.check(c.out, c.lse, False, tokens=slice(0, 1))
 
 
 def test_a_captured_call_replays_on_new_lengths():
