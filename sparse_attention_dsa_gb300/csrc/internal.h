@@ -254,8 +254,9 @@ struct PrefixParams {
 };
 constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs
 constexpr int kPlanItems = 2048;     // most items that are divided evenly
-constexpr int kPackCost = 5;         // what a partial result costs, in tiles
-constexpr int kWholeTiles = 6;       // contexts of no more tiles are not divided
+constexpr int kDivideCost = 11;      // what dividing costs each pair, in tiles
+constexpr int kPartCost = 1;         // what a partial result costs, in tiles
+constexpr int kWholeTiles = 16;      // longer own contexts are always divided
 constexpr int kAheadGain = 100;      // tiles that converting ahead must save
 // A partial result: O [128][512] fp32 (unnormalised), then (maximum in log2 units, sum) per row.
 constexpr int kPartialFloats = 128 * 512 + 2 * 128;

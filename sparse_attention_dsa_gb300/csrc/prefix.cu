@@ -120,6 +120,7 @@ __device__ __forceinline__ int64_t partial_slot(const PrefixParams& p, int item,
 
 // On the line an item is kItemCost places longer than its tiles, in front of them: what its queries' load, its
 // first tile's latency and its result cost in tiles.  Parts are no shorter than kMinPlaces on average.
+// (20 sequences of 4096 positions, 128 heads: 28.1, 26.7, 25.9, 26.6, 27.5 us with 1, 2, 3, 4, 6 places.)
 // A tile of FP8 rows that are converted in passing takes three places.  A cut gives the tiles that begin before it to
 // the part before it.
 constexpr int kItemCost = 3;
@@ -1098,6 +1099,7 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
 constexpr int kCombineThreads = 128;
 constexpr int kCombineBlocks = 1216;  // eight blocks on each of 152 SMs
 constexpr int kManyParts = 8;
+constexpr int kPartsInFlight = 4;
 
 // One row's parts: those of its own item, then of the packed item over the prefix.
 struct RowParts {
@@ -1125,39 +1127,35 @@ __device__ __forceinline__ float add_parts(const PrefixParams& p, const RowParts
     }
     float Ls = 0.f, mu = 0.f;
     bool first = true;
-    for (int i = sub; i < parts; i += 2 * step) {  // two parts in flight
-        const bool two = i + step < parts;
-        const float* slot0 = part_of_row(p, r, i, &tr);
-        const float2 s0 = __ldcg(reinterpret_cast<const float2*>(slot0 + 128 * 512) + tr);
-        const float4* o0 = reinterpret_cast<const float4*>(slot0 + tr * 512) + lane;
-        const float* slot1 = part_of_row(p, r, two ? i + step : i, &tr);
-        const float2 s1 = __ldcg(reinterpret_cast<const float2*>(slot1 + 128 * 512) + tr);
-        const float4* o1 = reinterpret_cast<const float4*>(slot1 + tr * 512) + lane;
-        float4 a[4], b[4];
+    for (int i = sub; i < parts; i += kPartsInFlight * step) {
+        float2 ml[kPartsInFlight];
+        float4 o[kPartsInFlight][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            a[k] = __ldcg(o0 + 32 * k);
-            b[k] = __ldcg(o1 + 32 * k);
+        for (int n = 0; n < kPartsInFlight; ++n) {
+            ml[n] = make_float2(-INFINITY, 0.f);
+            if (i + n * step >= parts) continue;
+            const float* slot = part_of_row(p, r, i + n * step, &tr);
+            ml[n] = __ldcg(reinterpret_cast<const float2*>(slot + 128 * 512) + tr);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[n][k] = __ldcg(reinterpret_cast<const float4*>(slot + tr * 512) + 32 * k + lane);
         }
-        if (first) {
+        if (first) {  // while they are on their way
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kAllLanes, M, off));
             mu = M == -INFINITY ? 0.f : M;
             first = false;
         }
-        const float w0 = exp2f(s0.x - mu), w1 = two ? exp2f(s1.x - mu) : 0.f;  // 0 for a part without a score
-        Ls += s0.y * w0 + (two ? s1.y * w1 : 0.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            acc[4 * k] += w0 * a[k].x;
-            acc[4 * k + 1] += w0 * a[k].y;
-            acc[4 * k + 2] += w0 * a[k].z;
-            acc[4 * k + 3] += w0 * a[k].w;
-            if (two) {
-                acc[4 * k] += w1 * b[k].x;
-                acc[4 * k + 1] += w1 * b[k].y;
-                acc[4 * k + 2] += w1 * b[k].z;
-                acc[4 * k + 3] += w1 * b[k].w;
+        for (int n = 0; n < kPartsInFlight; ++n) {
+            if (i + n * step >= parts) continue;
+            const float wgt = exp2f(ml[n].x - mu);  // 0 for a part without a score
+            Ls += ml[n].y * wgt;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[4 * k] += wgt * o[n][k].x;
+                acc[4 * k + 1] += wgt * o[n][k].y;
+                acc[4 * k + 2] += wgt * o[n][k].z;
+                acc[4 * k + 3] += wgt * o[n][k].w;
             }
         }
     }
@@ -1283,32 +1281,58 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(
 
 }  // namespace
 
-// Whether rows of different sequences share tiles over the prefix, and how many items there are.
+// Which items there are and how they are divided: of three ways the one whose time is the shortest by this estimate, in
+// tiles (an FP8 tile that is converted in passing counts as two) summed over the pairs.
+//   whole:   the pairs take whole merged items in turn; each round of them lasts as long as its longest item.
+//   divided: the line of merged items in equal parts, and kDivideCost for finding the parts and the second launch.
+//   packed:  the same with the prefix passed over by fewer tiles of rows, and all results written and read as partial
+//            ones: kPartCost each.
+// Measured, us (bf16 unless it says FP8; B sequences x heads, prefix + up to so many own positions):
+//                            whole   divided  packed
+//   38 x 128,    0 + 1024     17.5     24.5
+//   8 x 128,     0 + 2048     26.3     20.5
+//   100 x 128,   0 + 1024     32.9     35.8
+//   100 x 128,   0 + 2048     52.8     49.9
+//   64 x 16,   512 +  512     18.5     25.0     23.2
+//   64 x 16,  2048 +  512     33.1     37.9     25.3
+//   64 x 64,  1024 +  512     23.7     34.0     32.4
+//   16 x 64,  2048 +  512     31.1     23.3     23.0
+//   38 x 128,  512 +  512     27.3     30.8              FP8
+//   100 x 128,   0 +  896     52.9     46.5              FP8
+// The lengths are known to the device alone, so every own context counts as long as the table allows.  Whole items last
+// as long as the longest whatever the others are: they are taken up to kWholeTiles own tiles only, so that a batch with
+// one long sequence among short ones loses no more than about half of what an even one gains.
+//
+// FP8 rows of the prefix are converted ahead where that saves more than kAheadGain tiles' conversions in passing (less
+// two passes, for the launch, the rows' writing and reading): 8 x 128 behind 2048 positions 27.5 us ahead, 25.6 in
+// passing; behind 4096 28.6 and 32.6; 4 x 128 behind 4096 26.7 and 23.6, behind 8192 28.0 and 30.7.
 void plan_prefix(PrefixParams* p, int max_pages) {
     const int64_t rows = (int64_t)p->total_q * p->heads;
     p->prefix_tiles = (p->prefix_len + 127) / 128;
     p->packed_tiles = (int)((rows + 127) / 128);
     p->tiles_per_seq = (int)(((int64_t)p->max_q_len * p->heads + 127) / 128);
     const int64_t merged = (int64_t)p->batch * p->tiles_per_seq;
-    // Packing saves passes over the prefix and costs a second launch and the writing and reading of two results a
-    // row, of which one tile's takes about as long as kPackCost tiles of one pair's products.
     const int64_t most = p->packed_tiles + p->batch;  // tiles of the sequences' rows, whatever their lengths
     const int64_t alone = merged < most ? merged : most;
-    p->packed = merged + p->packed_tiles <= kPlanItems &&
-                (alone - p->packed_tiles) * p->prefix_tiles > kPackCost * (alone + p->packed_tiles);
-    const int64_t items = merged + (p->packed ? p->packed_tiles : 0);
-    // Many items, or none long enough to be worth a combination: each pair takes whole ones in turn.
-    const int64_t own = (int64_t)max_pages * 64 - (p->prefix_len & ~63);
-    const int64_t longest = p->prefix_tiles + (own + 127) / 128;
-    // (The places on the line are counted in 32 bits.)
-    const bool fits = items * (3 * longest + 3) <= INT32_MAX;
-    if (!fits) p->packed = 0;
+    const int64_t own_tiles = ((int64_t)max_pages * 64 - (p->prefix_len & ~63) + 127) / 128;
+    const int64_t longest = p->prefix_tiles + own_tiles;
+    const int64_t own = own_tiles * (p->kv_fp8 ? 2 : 1);
+    auto ahead = [&](int64_t row_tiles) { return p->kv_fp8 && (row_tiles - 2) * p->prefix_tiles > kAheadGain; };
+    auto prefix = [&](int64_t row_tiles) { return (int64_t)p->prefix_tiles * (p->kv_fp8 && !ahead(row_tiles) ? 2 : 1); };
+    const int64_t rounds = (alone + kPrefixPairs - 1) / kPrefixPairs;
+    const int64_t whole = own_tiles > kWholeTiles ? INT64_MAX : rounds * kPrefixPairs * (own + prefix(alone) + kItemCost);
+    const int64_t divided = alone * (own + prefix(alone) + kItemCost) + kPrefixPairs * kDivideCost;
+    const int64_t packed = alone * (own + kItemCost) + p->packed_tiles * (prefix(p->packed_tiles) + kItemCost) +
+                           (alone + p->packed_tiles) * kPartCost + kPrefixPairs * kDivideCost;
+    // Many items are even enough by themselves (1000 x 128 with up to 3000 positions: 368 us whole, 339 divided; two
+    // prompts of 4000 tokens, 16 heads, 1000 items: 482 and 508), and every CTA scans them all for a plan.  Places on the
+    // line are counted in 32 bits.
+    const bool fits = (merged + p->packed_tiles) * (3 * longest + kItemCost) <= INT32_MAX;
+    p->packed = fits && merged + p->packed_tiles <= kPlanItems && packed < divided && packed < whole;
+    p->planned = p->packed || (fits && merged <= kPlanItems && divided < whole);
     p->n_items = (int)(merged + (p->packed ? p->packed_tiles : 0));
-    // FP8: a tile converted in passing takes about half as long again as one of bf16 rows, for every tile of rows
-    // again; converting the prefix ahead takes a launch and about as long as a twentieth of a tile a tile.
     p->row_tiles = (int)(p->packed ? p->packed_tiles : alone);
-    p->convert_ahead = p->kv_fp8 && (int64_t)(p->row_tiles - 2) * p->prefix_tiles > kAheadGain;
-    p->planned = p->packed || (fits && items <= kPlanItems && longest > kWholeTiles);
+    p->convert_ahead = ahead(p->row_tiles);
 }
 
 size_t prefix_partial_bytes(const PrefixParams& p) {

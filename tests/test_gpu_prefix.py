@@ -19,10 +19,14 @@ def _built():
 
 
 class Call:
-    """A batch with its cache and queries, and one call."""
+    """A batch with its cache and queries, and one call.  wide: its page table has room for contexts so long that the
+    work is divided among the CTAs however short the sequences are."""
 
-    def __init__(self, seq_lens, q_lens, prefix, heads, fp8=False, seed=0, gain=1.0, **dims):
+    def __init__(self, seq_lens, q_lens, prefix, heads, fp8=False, seed=0, gain=1.0, wide=False, **dims):
         self.b = Batch(seq_lens, q_lens, prefix, seed)
+        if wide:
+            self.b.pt_host = torch.nn.functional.pad(self.b.pt_host, (0, 40), value=-1)
+            self.b.pt = self.b.pt_host.cuda()
         g = torch.Generator(device="cuda").manual_seed(seed + 1)
         rows = torch.randn((self.b.pages * PAGE, KV), generator=g, device="cuda").to(torch.bfloat16)
         if prefix % PAGE:  # every sequence's copy of the page in which the prefix ends
@@ -72,6 +76,7 @@ SHAPES = {
     "heads_33": ([2100, 2300, 2048], [1, 9, 4], 2000, 33),
     # enough tiles of rows over the prefix that FP8 rows are converted ahead: merged, then packed rows
     "full_heads_long_prefix": ([1100 + 7 * i for i in range(20)], [1] * 20, 1090, 128),
+    "packed_ragged": ([900 + 11 * i for i in range(24)], [i % 5 for i in range(24)], 800, 16),
     "packed_long_prefix": ([2510 + 3 * i for i in range(64)], [1] * 64, 2500, 16),
     # more items than are divided evenly: whole items in turn
     "thousands_of_short_ones": ([1 + i % 70 for i in range(2100)], [1] * 2100, 0, 128),
@@ -79,17 +84,17 @@ SHAPES = {
 }
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("name", list(SHAPES))
-def test_attention(name, fp8):
-    Call(*SHAPES[name], fp8=fp8, seed=len(name)).run().check()
+def test_attention(name, fp8, wide):
+    Call(*SHAPES[name], fp8=fp8, seed=len(name), wide=wide).run().check()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
 def test_peaked_scores(fp8):
     """Scores tens of units apart, so that the running maximum moves and most weights vanish."""
-    Call([1500, 1700], [1, 3], 1400, 64, fp8=fp8, seed=2, gain=12.0).run().check() if not fp8 else \
-        Call([1500, 1700], [1, 3], 1400, 64, fp8=True, seed=2, gain=4.0).run().check()
+    Call([1500, 1700], [1, 3], 1400, 64, fp8=fp8, seed=2, gain=4.0 if fp8 else 12.0, wide=True).run().check()
 
 
 def test_rising_and_falling_scores():
@@ -114,13 +119,15 @@ def test_without_lse():
     assert torch.equal(a.out, kept) and a.error() == 0
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("name", ["own_page_copies", "no_prefix_ragged", "ragged_queries_and_none", "whole_prompt",
-                                  "whole_prompts_behind_a_prefix", "packed_many", "full_heads_chunk", "full_heads_long_prefix", "packed_long_prefix"])
-def test_what_is_not_visible_does_not_matter(name, fp8):
+                                  "whole_prompts_behind_a_prefix", "packed_many", "full_heads_chunk",
+                                  "full_heads_long_prefix", "packed_long_prefix", "packed_ragged"])
+def test_what_is_not_visible_does_not_matter(name, fp8, wide):
     """NaN and infinities in rows behind each sequence's end, in spare pages, and in the copies of the prefix's
     last page that are not read, change no bit."""
-    c = Call(*SHAPES[name], fp8=fp8, seed=5).run()
+    c = Call(*SHAPES[name], fp8=fp8, seed=5, wide=wide).run()
     want = c.out.clone(), c.lse.clone()
     used = torch.zeros(c.b.pages * PAGE, dtype=torch.bool)
     for i in range(c.b.B):
@@ -139,11 +146,12 @@ def test_what_is_not_visible_does_not_matter(name, fp8):
     assert torch.equal(c.out, want[0]) and torch.equal(c.lse, want[1])
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("heads", [16, 128])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-def test_a_bad_new_row_reaches_only_the_queries_that_see_it(heads, value):
+def test_a_bad_new_row_reaches_only_the_queries_that_see_it(heads, value, wide):
     """Query j of a step must not notice what the later tokens of the step hold."""
-    c = Call([205, 100], [5, 5], 90, heads, seed=6).run()
+    c = Call([205, 100], [5, 5], 90, heads, seed=6, wide=wide).run()
     want = c.out.clone(), c.lse.clone()
     p = 203  # position of sequence 0's fourth query
     c.cache[int(c.b.pt_host[0, p // PAGE]), p % PAGE] = value
@@ -154,8 +162,9 @@ def test_a_bad_new_row_reaches_only_the_queries_that_see_it(heads, value):
     assert bool(c.out[3:5].isnan().all()) and bool(c.lse[3:5].isnan().all())
 
 
-def test_a_nan_query_row_stays_alone():
-    c = Call([205, 100, 170], [1, 1, 1], 90, 16, seed=7).run()
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_nan_query_row_stays_alone(wide):
+    c = Call([205, 100, 170], [1, 1, 1], 90, 16, seed=7, wide=wide).run()
     want = c.out.clone()
     c.q[1, 3, 10] = math.nan
     c.run()
@@ -164,23 +173,25 @@ def test_a_nan_query_row_stays_alone():
     assert torch.equal(c.out[keep], want[keep]) and bool(c.out[1, 3].isnan().all()) and bool(c.lse[1, 3].isnan())
 
 
-def test_scores_of_minus_infinity_have_no_weight():
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_of_minus_infinity_have_no_weight(wide):
     """Rows whose rotary part makes every score -inf: out 0, lse -inf; some of them: as if they were not there."""
-    c = Call([130, 70], [1, 1], 64, 16, seed=8)
+    c = Call([130, 70], [1, 1], 64, 16, seed=8, wide=wide)
     c.q[..., 575] = 1.0
     c.cache[..., 575] = -math.inf
     c.run()
     assert c.error() == 0
     assert not bool(c.out.any()) and bool((c.lse == -math.inf).all())
-    c = Call([130, 70], [1, 1], 64, 16, seed=8)
+    c = Call([130, 70], [1, 1], 64, 16, seed=8, wide=wide)
     c.q[..., 575] = 1.0
     page = int(c.b.pt_host[0, 0])
     c.cache[page, 5:60, 575] = -math.inf
     c.run().check()
 
 
-def test_inconsistent_sequences_are_reported_and_left_alone():
-    c = Call([300, 300, 300], [1, 1, 1], 200, 16, seed=9, total_q=5)
+@pytest.mark.parametrize("wide", [False, True])
+def test_inconsistent_sequences_are_reported_and_left_alone(wide):
+    c = Call([300, 300, 300], [1, 1, 1], 200, 16, seed=9, wide=wide, total_q=5)
     c.q = torch.cat([c.q, c.q[:2]])
     ref = Attention(c.b, c.q[:3], c.cache, False)
     c.b.lens[1] = 200  # its query would lie inside the prefix
@@ -196,11 +207,12 @@ def test_inconsistent_sequences_are_reported_and_left_alone():
     assert c.error() == dsa.DSA_DEVERR_SEQ and bool((c.out[1] == 7).all())
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("heads", [16, 128])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_bad_pages_are_reported_and_skipped(heads, fp8):
-    c = Call([400, 330], [1, 1], 256, heads, fp8=fp8, seed=10)
-    ref = Call([400, 330], [1, 1], 256, heads, fp8=fp8, seed=10).run()
+def test_bad_pages_are_reported_and_skipped(heads, fp8, wide):
+    c = Call([400, 330], [1, 1], 256, heads, fp8=fp8, seed=10, wide=wide)
+    ref = Call([400, 330], [1, 1], 256, heads, fp8=fp8, seed=10, wide=wide).run()
     c.b.pt[0, 5] = c.b.pages  # positions 320..383 of sequence 0
     c.run()
     assert c.error() == dsa.DSA_DEVERR_PAGE
@@ -223,8 +235,9 @@ def test_rows_behind_four_gigabytes():
     c.run().check()
 
 
-def test_the_same_twice_and_on_another_stream():
-    c = Call(*SHAPES["packed_many"], seed=12).run()
+@pytest.mark.parametrize("wide", [False, True])
+def test_the_same_twice_and_on_another_stream(wide):
+    c = Call(*SHAPES["packed_many"], seed=12, wide=wide).run()
     want = c.out.clone(), c.lse.clone()
     s = torch.cuda.Stream()
     for stream in (None, s):
@@ -236,7 +249,8 @@ def test_the_same_twice_and_on_another_stream():
 
 
 def test_two_calls_at_once_with_their_own_workspaces():
-    a, b = Call(*SHAPES["packed_many"], seed=13), Call(*SHAPES["full_heads_many"], seed=14)
+    a = Call(*SHAPES["packed_many"], seed=13, wide=True)
+    b = Call(*SHAPES["full_heads_many"], seed=14, wide=True)
     torch.cuda.synchronize()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     for _ in range(5):
@@ -249,7 +263,8 @@ def test_two_calls_at_once_with_their_own_workspaces():
 
 def test_two_graphs_of_one_workspace():
     """Two captured calls of different shapes that share a workspace, replayed in turn."""
-    a, b = Call(*SHAPES["packed_long_prefix"], fp8=True, seed=18), Call(*SHAPES["full_heads_many"], seed=19)
+    a = Call(*SHAPES["packed_long_prefix"], fp8=True, seed=18)
+    b = Call(*SHAPES["full_heads_many"], seed=19, wide=True)
     size = max(a.workspace.numel(), b.workspace.numel())
     a.workspace = b.workspace = torch.zeros(size, dtype=torch.uint8, device="cuda")
     graphs = []
@@ -269,11 +284,12 @@ def test_two_graphs_of_one_workspace():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("name", ["packed_many", "full_heads_chunk", "one_token_no_prefix"])
-def test_waits_give_up_at_their_limit(name, fp8):
+@pytest.mark.parametrize("name, wide", [("packed_many", True), ("full_heads_chunk", True), ("full_heads_chunk", False),
+                                        ("one_token_no_prefix", False)])
+def test_waits_give_up_at_their_limit(name, wide, fp8):
     """With a limit of a nanosecond some wait finds its phase incomplete and gives up: the call reports it and ends,
     and the next call, at the default limit, is right."""
-    c = Call(*SHAPES[name], fp8=fp8, seed=20)
+    c = Call(*SHAPES[name], fp8=fp8, seed=20, wide=wide)
     old = dsa.set_wait_limit_ns(1)
     try:
         c.run()
@@ -294,8 +310,9 @@ def test_more_queries_than_announced_are_reported():
     ref.check(c.out, c.lse, False, tokens=slice(0, 1))
 
 
-def test_a_captured_call_replays_on_new_lengths():
-    c = Call([700, 514, 600], [1, 1, 1], 512, 16, seed=15)
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_captured_call_replays_on_new_lengths(wide):
+    c = Call([700, 514, 600], [1, 1, 1], 512, 16, seed=15, wide=wide)
     c.b.lens -= 30
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
