@@ -170,7 +170,14 @@ template <bool KVFP8>
 constexpr uint32_t kIdescQK = make_idesc(128, 128, KVFP8 ? 0 : 1, KVFP8 ? 0 : 1, 0, 0);
 template <bool KVFP8>
 constexpr uint32_t kIdescPV = make_idesc(128, 256, KVFP8 ? 0 : 1, KVFP8 ? 0 : 1, 0, 1);
-constexpr float kRaise = 8.f;  // raise the running maximum (log2) only when it grows by more than this
+// Raise the running maximum (log2) only when it grows by more than this.
+template <bool KVFP8>
+constexpr float kRaise = KVFP8 ? 4.f : 8.f;
+// Weights are taken relative to 2^-kLift of the running maximum: f16 weights of up to 2^(kRaise + kLift) = 2^15 keep
+// their precision down to 2^-25 of the largest one's, so that a long context's many small weights beside a large
+// one are not lost (bf16 has fp32's range).
+template <bool KVFP8>
+constexpr float kLift = KVFP8 ? 11.f : 0.f;
 
 struct Segment {
     Item it;
@@ -741,10 +748,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 float other;
                 if (!(ok = swap(mx[0], &other))) break;
                 const float mt = fmaxf(mx[0], other) * p.scale_log2;
-                const bool raise = mt > m_used + kRaise;
+                const bool raise = mt > m_used + kRaise<KVFP8>;
                 const float m_new = raise ? mt : m_used;
                 const float alpha = (raise && m_used != -INFINITY) ? exp2f(m_used - m_new) : 1.f;
-                const float mu = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf) = 0
+                const float mu = m_new == -INFINITY ? 0.f : m_new - kLift<KVFP8>;  // nothing seen yet: exp2(-inf) = 0
                 // weights: the sum takes the fp32 values, the products their rounding to bf16 or f16 (at most
                 // 2^-8 or 2^-11 of each, unbiased), so that lse keeps fp32 accuracy
                 uint32_t packed[32];
@@ -795,6 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             float other;
             if (!(ok = swap(l_sum, &other))) break;
             const float l = half == 0 ? l_sum + other : other + l_sum;  // the same sum in both halves
+            const float m = m_used - kLift<KVFP8>;  // what O and l are relative to
             const bool whole = s.u0 == 0 && s.u1 == s.it.tiles_a + s.it.tiles_b && !p.packed;
             float* slot = p.partial + partial_slot(p, s.index, pair, s.u0 == 0) * kPartialFloats;
             constexpr float kTakeOut = KVFP8 ? 1.f / kF16Gain : 1.f;
@@ -843,7 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     write_lines(dst + 2 * c, 1024);
                 }
                 if (tr < s.it.nrows && half == 0 && p.lse)
-                    p.lse[(int64_t)s.it.row0 + tr] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+                    p.lse[(int64_t)s.it.row0 + tr] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             } else {
                 uint8_t* dst = reinterpret_cast<uint8_t*>(slot + row_first * 512 + 256 * half);
                 float o[2][16];
@@ -867,7 +875,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     }
                     write_lines(dst + 4 * c, 2048);
                 }
-                if (tr < s.it.nrows && half == 0) reinterpret_cast<float2*>(slot + 128 * 512)[tr] = make_float2(m_used, l);
+                if (tr < s.it.nrows && half == 0) reinterpret_cast<float2*>(slot + 128 * 512)[tr] = make_float2(m, l);
             }
             tc_fence_before();
             __syncwarp();

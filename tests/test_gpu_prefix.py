@@ -111,6 +111,21 @@ def test_rising_and_falling_scores():
         c.run().check()
 
 
+def test_many_small_weights_beside_a_large_one():
+    """FP8 rows: one score 24.5 powers of two above all the others, whose weights sum to a share that no rounding
+    of single ones may lose."""
+    c = Call([60000], [1], 0, 16, fp8=True, seed=22)
+    rows = torch.zeros((c.b.pages * PAGE, KV), device="cuda")
+    rows[:, :LATENT] = 1.0
+    sink = int(c.b.pt_host[0, 777 // PAGE]) * PAGE + 777 % PAGE
+    rows[sink] = 0.0
+    rows[sink, 575] = 17.0
+    c.cache = latent_fp8_rows(rows.to(torch.bfloat16)).view(c.b.pages, PAGE, -1)
+    c.q.zero_()
+    c.q[..., 575] = 24.0  # z = row's last value
+    c.run().check()
+
+
 def test_without_lse():
     a = Call(*SHAPES["two_queries"], seed=4).run()
     kept = a.out.clone()
