@@ -379,7 +379,7 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
 
 /*
  * Dense attention over the latent-KV cache for a batch whose sequences share a prefix ([A2] step 2 without
- * the selection; [A1] 3.2): for every query token t of sequence b and head h,
+ * the selection): for every query token t of sequence b and head h,
  *     z_s = softmax_scale * q[t,h,:] . kv[s,:]  for every visible position s = 0..p_t,
  *     out[t,h,:] = sum_s softmax(z)_s * kv[s, 0:v_dim],   lse[t,h] = log sum_s exp(z_s)
  * where positions below prefix_len are the same rows for every sequence: they are read through the page
@@ -398,8 +398,8 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  * a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were; rows of a page that is out of
  * range (DSA_DEVERR_PAGE) are skipped.
  * FP8 rows are multiplied as f16, with q as f16: an element code * scale, or a rotary value, of more than
- * 16376, or a q of more than 262016, becomes infinite (and its row NaN); below 2^-16 elements lose
- * relative precision.
+ * 16376, a scale of 64 or more, or a q of more than 262016 becomes infinite (and its row NaN); elements
+ * below 2^-16 and values of q below 2^-12 lose relative precision.
  * Supported: D = 576, Dv = 512, Hq <= 128.
  */
 dsa_status_t dsa_prefix_attn(const dsa_dims_t* dims, int32_t prefix_len, const void* q, const void* kv_cache,

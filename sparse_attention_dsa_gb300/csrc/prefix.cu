@@ -286,23 +286,26 @@ __device__ __forceinline__ uint32_t finite2(uint32_t v) {
 // FP8 rows are multiplied as f16, q and the weights with them: a code's four significant bits times a scale of eleven
 // lose three bits less than in bf16 (errors of 2^-11 against 2^-8), and a pair of codes takes two instructions rather
 // than six.  Rows are kept times kF16Gain, which cancels in the scores (q is divided by it) and is taken out of the
-// result, so that a row whose largest value is 0.007 still has a scale of full precision; the largest values are
-// 65504 / kF16Gain.
+// result; the largest values are 65504 / kF16Gain.  A row's scale is some 450 times smaller than its largest value: it is
+// kept 2^8 times larger, and the codes (whose range is small) as much smaller, so that both are exact down to
+// values of 2^-16.
 constexpr float kF16Gain = 4.f;
+constexpr float kScaleGain = 256.f * kF16Gain;
+constexpr uint32_t kCodeGain = 0x1C001C00u;  // 2^-8 twice
 __device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the low half
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-// Eight E4M3 codes times a scale given as a f16 pair.
+// Eight E4M3 codes times a scale, given as a f16 pair of scale * kScaleGain.
 __device__ __forceinline__ uint4 codes_to_h8(uint32_t lo, uint32_t hi, uint32_t scale2) {
     uint32_t out[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint16_t pair = (uint16_t)((j < 2 ? lo : hi) >> (16 * (j & 1)));
-        asm("{\n\t.reg .b32 h;\n\tcvt.rn.f16x2.e4m3x2 h, %1;\n\tmul.rn.f16x2 %0, h, %2;\n\t}"
+        asm("{\n\t.reg .b32 h;\n\tcvt.rn.f16x2.e4m3x2 h, %1;\n\tmul.rn.f16x2 h, h, %3;\n\tmul.rn.f16x2 %0, h, %2;\n\t}"
             : "=r"(out[j])
-            : "h"(pair), "r"(scale2));
+            : "h"(pair), "r"(scale2), "r"(kCodeGain));
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
@@ -999,7 +1002,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sc[j][i] = f2_to_h2(next[j][i] * kF16Gain, next[j][i] * kF16Gain);
+                        for (int i = 0; i < 4; ++i) sc[j][i] = f2_to_h2(next[j][i] * kScaleGain, next[j][i] * kScaleGain);
                     if (u + 1 < s.u1) {
                         t = tile_of(p, s.it, u + 1);
                         load_scales(t, next);
@@ -1093,7 +1096,7 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
         scale = ld_input(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + (lane >> 3));
         if (lane < 8) rot = ld_input(reinterpret_cast<const uint4*>(src + kKvFp8RopeOff) + lane);
     }
-    const uint32_t scale2 = f2_to_h2(scale * kF16Gain, scale * kF16Gain);
+    const uint32_t scale2 = f2_to_h2(scale * kScaleGain, scale * kScaleGain);
     dst[2 * lane] = codes_to_h8(code.x, code.y, scale2);
     dst[2 * lane + 1] = codes_to_h8(code.z, code.w, scale2);
     if (lane < 8) dst[64 + lane] = bf8_to_h8(rot, kF16Gain);

@@ -126,6 +126,19 @@ def test_many_small_weights_beside_a_large_one():
     c.run().check()
 
 
+@pytest.mark.parametrize("name", ["two_queries", "packed_long_prefix"])
+def test_small_fp8_rows(name):
+    """Rows of values about 2e-4: their scales are far below what f16 holds."""
+    c = Call(*SHAPES[name], fp8=True, seed=23)
+    g = torch.Generator(device="cuda").manual_seed(24)
+    rows = 2e-4 * torch.randn((c.b.pages * PAGE, KV), generator=g, device="cuda")
+    c.cache = latent_fp8_rows(rows.to(torch.bfloat16)).view(c.b.pages, PAGE, -1)
+    if c.prefix % PAGE:
+        page = c.b.pt[:, c.prefix // PAGE].long()
+        c.cache[page, :c.prefix % PAGE] = c.cache[page[0], :c.prefix % PAGE].clone()
+    c.run().check()
+
+
 def test_without_lse():
     a = Call(*SHAPES["two_queries"], seed=4).run()
     kept = a.out.clone()
