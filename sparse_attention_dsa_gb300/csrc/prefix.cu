@@ -11,11 +11,12 @@
 //   * merged: the tile's rows belong to one sequence and its positions are the prefix and then the sequence's
 //     own; with all its tiles in one place the result is written directly;
 //   * packed: an item of 128 rows of any sequences over the prefix, and for each sequence items over its own
-//     positions; the partial results of a row are combined by a second kernel.  Taken when the heads are so
-//     few that packing saves whole tiles (plan()).
+//     positions; the partial results of a row are combined by a second kernel.  Fewer tiles pass over the prefix
+//     where a sequence's rows do not fill one.
 // The tiles of all items form one line (each item with a few places for what it costs beside its tiles) that is
 // cut into equal parts, one for each CTA pair, so that the work is even whatever the lengths are; an item cut in
-// two or more is combined from its parts.
+// two or more is combined from its parts.  Short merged items are taken whole instead, in turn.  plan_prefix()
+// chooses, with the times of each way.
 //
 // One CTA pair (a cluster of two, cta_group::2) works on 128 rows, 64 in each CTA, because a 128 x 512 fp32
 // accumulator would fill the tensor memory of one: the pair's products of 128 rows put the first half of the
@@ -30,6 +31,15 @@
 // shared memory.  The running maximum is raised only when it grows by more than 2^8.
 //   Tiles that some row does not see whole (the prefix's or a context's end, the causal edge) take their V
 // through registers, where infinities and NaN become 0: 0 x inf would reach rows that do not see them.
+//   FP8 rows become f16 in the rings (eight warps), or, a prefix's that several tiles of rows attend to, once ahead.
+//
+// What bounds it, and measured (one GB300, warm).  A 128 x 128 tile costs 2 x 128 x 128 x (576 + 512) operations, 1.42 us on
+// a pair at the measured cuBLAS rate: prefix tiles, whose rows are in L2, take 1.30 us, bound by the tensor pipe and by
+// the shared-memory reads of Q K^T, which fill it.  Own bf16 rows are read once by one pair: 1.8 us a tile with all
+// pairs at it, 0.92 of the copy bandwidth.  Own FP8 rows: 2.97 us, bound by the chain of a ring's slot (free, codes
+// arrived, expanded in place under the products' reads, multiplied).  32 sequences of 1024 positions behind 16384, 128 heads:
+// 96 us, 1.56 PFLOP/s; 64 x 16 heads, 500 behind 32741: 62.5 us; 8 prompts of up to 257 queries x 32 heads behind 4096: 285 us,
+// 1.66 PFLOP/s; one short item: 12 us, all latency.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -1072,9 +1082,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// FP8 rows of the prefix to f16 (times kF16Gain), once for all the tiles of rows that attend to them: a warp per position, in the
-// order of the positions (rows behind the prefix in its last page are zeros).  Bound by L2 and HBM: 656 bytes read,
-// 1152 written a row.
+// FP8 rows of the prefix to f16 (times kF16Gain), once for all the tiles of rows that attend to them: a warp per
+// position, in the order of the positions (rows behind the prefix in its last page are zeros).  Bound by L2 and HBM:
+// 656 bytes read, 1152 written a row; 16000 rows take 6 to 8 us with the launch.
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kAheadWarps = 8;
 
@@ -1103,7 +1113,8 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Combination of partial results: one warp per row.
+// Combination of partial results: a warp per row, four parts' loads in flight (two: 1.5 us slower for rows of ten
+// parts).  Bound by latency (offsets, then parts) and L2: some 20 MB in about 7 us.
 //   M = max m_k, L = sum_k l_k 2^(m_k - M), out = sum_k 2^(m_k - M) O_k / L, lse = (M + log2 L) ln 2
 // ---------------------------------------------------------------------------------------------------------
 // The units of work are four rows, a warp each, or one row of an item in many parts, which the block's warps share.

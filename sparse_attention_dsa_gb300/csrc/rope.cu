@@ -13,6 +13,10 @@
 // as 16-byte pieces, one to three a lane, whose loads are issued before that chain starts, and a 64-dim rotary
 // block is 8 neighbouring lanes: interleaved pairs lie inside a piece, the halves' partner is the piece four
 // further, fetched by a shuffle.
+//
+// Measured (one GB300, warm).  rope_append: 4 tokens 2.5 us (latency), 512 tokens to FP8 5.4 us, eight ragged chunks of up to 4096
+// tokens, bf16, 17.2 us (75.8 MB in and out: 4.4 TB/s, 0.65 of the copy bandwidth).
+// rope_queries: 32 tokens 2.4 us, 4096 tokens of 128 + 64 heads to MXFP8 46.8 us (237 MB, 5.1 TB/s, 0.75).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
