@@ -188,7 +188,7 @@ __device__ __forceinline__ bool locate(const RopeParams& r, int t, int lane, int
             c1 = __shfl_sync(kAll, c1, src);
             L = __shfl_sync(kAll, L, src);
             const int64_t p = (int64_t)L - c1 + t;
-            if (c1 - c0 <= L && (int64_t)L <= (int64_t)r.max_pages * 64) {
+            if (c0 >= 0 && c1 - c0 <= L && (int64_t)L <= (int64_t)r.max_pages * 64) {
                 b = j0 + src;
                 pos = (int)p;
             }

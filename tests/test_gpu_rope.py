@@ -282,6 +282,21 @@ def test_queries_report_and_skip():
     assert not bool(q[0].any()) and not bool(q[2].any()) and bool(q[1].any())
 
 
+def test_offsets_out_of_range_are_reported():
+    """Offsets whose difference passes 32 bits own no token."""
+    b = Batch([300], [1], seed=12)
+    b.cu.copy_(torch.tensor([-2_000_000_000, 1_000_000_000], dtype=torch.int32))
+    table = rope_table(400, "cuda")
+    kvc = _caches(b, BF16, BF16, 128)[2]
+    old = kvc.clone()
+    dsa.rope_append(b.dims(), _rope(table), None, _normal((1, KV), 91), b.pt, b.lens, b.cu, None, None, kvc, b.workspace)
+    assert dsa.get_device_error(b.workspace) == dsa.DSA_DEVERR_SEQ and torch.equal(kvc, old)
+    dsa.clear_device_error(b.workspace)
+    q = torch.zeros((1, 128, KV), dtype=torch.bfloat16, device="cuda")
+    dsa.rope_queries(b.dims(), _rope(table), _normal((1, 128, 64), 92), q, None, None, None, b.lens, b.cu, b.workspace)
+    assert dsa.get_device_error(b.workspace) == dsa.DSA_DEVERR_SEQ and not bool(q.any())
+
+
 def test_infinities_and_nan_stay_in_their_groups():
     """A row with an infinity or a NaN leaves other rows and, in the latent part, other tiles as they would be."""
     b = Batch([10, 20], [2, 2], seed=12)
