@@ -394,9 +394,9 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  * result, whatever they hold.  A score of -inf has weight 0 (an infinite value of such a row makes NaN of it);
  * a NaN in a visible row, or in q, makes the rows that see it NaN; with every score -inf, out = 0 and
  * lse = -inf.
- * A sequence with n_b > L_b - prefix_len, n_b > max_q_len or a context beyond its page table (DSA_DEVERR_SEQ) and
- * a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were; rows of a page that is out of
- * range (DSA_DEVERR_PAGE) are skipped.
+ * A sequence with n_b > L_b - prefix_len, n_b > max_q_len or a context beyond its page table or of 2^31 - 255
+ * positions or more (DSA_DEVERR_SEQ) and a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left
+ * as they were; rows of a page that is out of range (DSA_DEVERR_PAGE) are skipped.
  * FP8 rows are multiplied as f16, with q as f16: an element code * scale, or a rotary value, of more than
  * 16376, a scale of 64 or more, or a q of more than 262016 becomes infinite (and its row NaN); elements
  * below 2^-16 and values of q below 2^-12 lose relative precision.

@@ -328,6 +328,17 @@ def test_waits_give_up_at_their_limit(name, wide, fp8):
     c.run().check()
 
 
+def test_a_context_whose_tiles_would_pass_32_bits_is_reported():
+    c = Call([300], [1], 0, 16, seed=25)
+    pages = (1 << 25) - 1  # the widest page table that a call takes
+    c.b.pt = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    c.dims.max_pages_per_seq = pages
+    c.workspace = torch.zeros(dsa.prefix_attn_workspace_size(c.dims, 0), dtype=torch.uint8, device="cuda")
+    c.b.lens.fill_(64 * pages)
+    c.run()
+    assert c.error() == dsa.DSA_DEVERR_SEQ and bool((c.out == 7).all())
+
+
 def test_more_queries_than_announced_are_reported():
     c = Call([300, 300], [1, 3], 200, 16, seed=21)
     c.dims.max_q_len = 2
