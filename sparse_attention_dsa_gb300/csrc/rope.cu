@@ -14,8 +14,9 @@
 // block is 8 neighbouring lanes: interleaved pairs lie inside a piece, the halves' partner is the piece four
 // further, fetched by a shuffle.
 //
-// Measured (one GB300, warm).  rope_append: 4 tokens 2.5 us (latency), 512 tokens to FP8 5.4 us, eight ragged chunks of up to 4096
-// tokens, bf16, 17.2 us (75.8 MB in and out: 4.4 TB/s, 0.65 of the copy bandwidth).
+// Measured (one GB300, warm).  rope_append: 4 tokens 2.4 us (latency), 380 tokens to FP8 4.7 us, 24693 to FP8 15.9 us
+// (20.9 with divisions beside ties); eight ragged chunks of up to 4096 tokens, bf16, 16.9 us (75.8 MB in and out: 4.5 TB/s,
+// 0.66 of the copy bandwidth; two tokens a warp, for half as many chains of loads, were no faster).
 // rope_queries: 32 tokens 2.4 us, 4096 tokens of 128 + 64 heads to MXFP8 46.8 us (237 MB, 5.1 TB/s, 0.75).
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -28,7 +29,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
-// Two fp32 products, two fp32 sums in one instruction each (rounded like the single ones).
+// Two fp32 products, sums or both in one instruction (rounded like the single ones).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
     asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
@@ -43,6 +44,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         "mov.b64 {%0, %1}, z;\n\t}"
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
 
@@ -68,21 +77,24 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 __device__ __forceinline__ uint2 pack_codes(const float (&y)[8]) {
     return make_uint2(codes2(y[0], y[1]) | (codes2(y[2], y[3]) << 16), codes2(y[4], y[5]) | (codes2(y[6], y[7]) << 16));
 }
-// E4M3 codes of x / scale, the quotient correctly rounded to fp32 first (so that both appends make the same codes).
-// Eight divisions are most of a piece's instructions, and the product with 1 / scale differs from the quotient by a
-// few units in the last place: only where it lies that close to a value halfway between two codes (fp32 bits 19..0
-// near 0x80000; below 2^-6 the codes have another spacing) are the quotients themselves taken.
+// E4M3 codes of x / scale, the quotient rounded to fp32 first (so that both appends make the same codes).  With the
+// correctly rounded reciprocal, y = x inv is within two units in the last place, y s - x is exact, and
+// y - (y s - x) inv differs from the quotient by 2^-23 units before its rounding (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990): three packed operations a pair where a division
+// takes ten a value.  (The signs are such that -0 stays -0.)  Scales whose products could leave fp32's range divide.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-    const float inv = __fdiv_rn(1.f, scale);
+    const float inv = __frcp_rn(scale);
     float y[8];
-    bool near = !(inv < 3e38f);
+    if (scale > 0x1p-80f && scale < 0x1p80f) {
+        const float2 inv2 = make_float2(inv, inv), minus2 = make_float2(-inv, -inv), scale2 = make_float2(scale, scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        y[i] = x[i] * inv;
-        const uint32_t low = __float_as_uint(y[i]) & 0xFFFFFu;
-        near |= low - 0x7FFF8u <= 16u || fabsf(y[i]) < 0.015626f;
-    }
-    if (near) {
+        for (int i = 0; i < 8; i += 2) {
+            const float2 v = mul2(make_float2(x[i], x[i + 1]), inv2);
+            const float2 q = fma2(fma2(v, scale2, make_float2(-x[i], -x[i + 1])), minus2, v);
+            y[i] = q.x;
+            y[i + 1] = q.y;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
     }
@@ -105,8 +117,13 @@ __device__ __forceinline__ float absmax8(const float (&x)[8]) {
     const float b = fmaxf(fmaxf(fabsf(x[3]), fabsf(x[4])), fabsf(x[5]));
     return fmaxf(fmaxf(fmaxf(a, b), fmaxf(fabsf(x[6]), fabsf(x[7]))), 0.f);  // (the 0: a group of NaN alone)
 }
-// absmax / 448 in fp32 (1 for an all-zero group)
-__device__ __forceinline__ float group_scale(float amax) { return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f; }
+// absmax / 448 in fp32 (1 for an all-zero group); the product with 1/448 and one correction, as above (no quotient by 448
+// comes closer to halfway between two fp32 numbers than a 14th of their distance)
+__device__ __forceinline__ float group_scale(float amax) {
+    if (!(amax > 0x1p-80f && amax < 0x1p120f)) return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    const float c = 1.f / 448.f, y = amax * c;
+    return __fmaf_rn(__fmaf_rn(-448.f, y, amax), c, y);
+}
 
 // Shared exponent of an MX group: floor(log2(absmax)) - 8 within the E8M0 range, 0 for an all-zero group.  (Subnormal
 // maxima lie below the range either way; an infinity gives 120.)

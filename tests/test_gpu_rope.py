@@ -4,6 +4,8 @@ Tolerances: a rotated value is two products and a sum in fp32, each within 2^-24
 rounding to the stored type (bf16 2^-8 relative, E4M3 2^-4 relative or half of its smallest step 2^-9); an fp32
 scale is one division, within 2^-24 of a maximum that is itself within 3 * 2^-24.
 """
+import math
+
 import pytest
 import torch
 
@@ -161,6 +163,32 @@ def test_without_a_rotation_it_is_the_plain_append(idx, kv):
     assert dsa.get_device_error(b.workspace) == 0
     for x, y in zip(a, c):
         assert x is None or torch.equal(x, y)
+
+
+def test_quantised_rows_of_every_magnitude_are_the_plain_append_s():
+    """Codes and scales are those of correctly rounded divisions, at magnitudes from subnormal to the largest, with
+    zeros of both signs, infinities and NaN: byte for byte what the plain append makes."""
+    b = Batch([4000], [4000], seed=16)
+    kv_new, k_new = _normal((b.T, KV), 93).float(), _normal((b.T, 128), 94).float()
+    power = torch.randint(-133, 125, (b.T, 1), generator=torch.Generator().manual_seed(95)).cuda().float()
+    power[:2000] = power[:2000] / 16
+    kv_new, k_new = kv_new * torch.exp2(power), k_new * torch.exp2(power)
+    for x in (kv_new, k_new):
+        x[:, 5::64] = 0.0
+        x[:, 7::64] = -0.0
+        x[100:110, 9] = math.inf
+        x[105:115, 300 % x.shape[1]] = math.nan
+    kv_new[:, LATENT:] = 0.0
+    kv_new, k_new = kv_new.to(torch.bfloat16), k_new.to(torch.bfloat16)
+    d = b.dims(idx_dim=128, idx_dtype=FP8, kv_dtype=FP8)
+    got, want = _caches(b, FP8, FP8, 128), _caches(b, FP8, FP8, 128)
+    dsa.rope_append(d, _rope(rope_table(4000, "cuda"), 0, 0, -1), k_new, kv_new, b.pt, b.lens, b.cu, *got, b.workspace)
+    dsa.append_rows(d, k_new, kv_new, b.pt, b.lens, b.cu, *want, b.workspace)
+    assert dsa.get_device_error(b.workspace) == 0
+    assert torch.equal(got[0], want[0])
+    assert torch.equal(got[1].view(torch.int32), want[1].view(torch.int32))
+    # (the rotary part, zeros, is left out: rotated by a negative cosine, 0 is -0)
+    assert torch.equal(got[2][..., :528], want[2][..., :528])
 
 
 @pytest.mark.parametrize("which", ["k", "kv"])
