@@ -344,8 +344,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6) rope_append_kernel(const
     }
 }
 
+// Warps of a CTA and warp steps in flight (4096 tokens to MXFP8: 47.0 us; with two steps 58.7, with six 53.6, with eight
+// 49.2; with two warps 46.7, with eight 51.1; 6 or 10 CTAs an SM instead of 8: 48.6, 52.8).
 constexpr int kQueryWarps = 4;
-constexpr int kSteps = 4;    // warp steps in flight
+constexpr int kSteps = 4;
 
 // Position of token t, found by warp 0 for the CTA; -1 where it has none.
 __device__ __forceinline__ int cta_position(const RopeParams& r, int t, int warp, int lane) {
