@@ -1122,9 +1122,14 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
 // ---------------------------------------------------------------------------------------------------------
 // The units of work are four rows, a warp each, or one row of an item in many parts, which the block's warps share.
 constexpr int kCombineThreads = 128;
+constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kCombineBlocks = 1216;  // eight blocks on each of 152 SMs
 constexpr int kManyParts = 8;
 constexpr int kPartsInFlight = 4;
+// Packed rows are combined by a block each up to so many tiles of them (1, 2, 4, 5, 6 tiles behind 16384 positions: 22.3,
+// 23.6, 27.9, 32.2, 35.0 us, with a warp each 27.9, 29.7, 31.8, 33.1, 35.1; 8 tiles behind 32768: 60.7 and 59.7): their
+// parts are the many that fewer tiles are cut in.
+constexpr int kSharedTiles = 5;
 
 // One row's parts: those of its own item, then of the packed item over the prefix.
 struct RowParts {
@@ -1197,27 +1202,65 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, int row, const 
     if (lane == 0 && p.lse) p.lse[row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
 }
 
-// Packed: every row has parts in two items.
+// The sums of a block's warps over the parts of one row, in the warps' order, in warp 0.
+struct WarpSums {
+    float4 acc[kCombineWarps][128];
+    float norm[kCombineWarps];
+};
+__device__ __forceinline__ void add_warps(WarpSums& sums, float (&acc)[16], float& Ls, int warp, int lane) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        sums.acc[warp][32 * k + lane] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+    if (lane == 0) sums.norm[warp] = Ls;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kCombineWarps; ++w) {
+        Ls += sums.norm[w];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = sums.acc[w][32 * k + lane];
+            acc[4 * k] += v.x;
+            acc[4 * k + 1] += v.y;
+            acc[4 * k + 2] += v.z;
+            acc[4 * k + 3] += v.w;
+        }
+    }
+}
+
+// Packed: every row has parts in two items.  SHARED: a block's warps share a row's parts.
+template <bool SHARED>
 __global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(const PrefixParams p) {
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5);
+    __shared__ WarpSums sums;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = SHARED ? blockIdx.x : blockIdx.x * kCombineWarps + warp;
     if (row >= p.total_q * p.heads) return;
     grid_dependency_wait();
+    const int2* parts = reinterpret_cast<const int2*>(p.plan + 4 * kPrefixPairs);
+    const int2 shared = __ldcg(parts + row / 128);
     const int t = row / p.heads;
     int b = -1, c0 = 0, n = 0, L = 0;
-    for (int j0 = 0; j0 < p.batch && b < 0; j0 += 32) {
-        const int j = j0 + lane;
-        const bool hit = j < p.batch && ld_input(p.cu_q_lens + j) <= t && t < ld_input(p.cu_q_lens + j + 1);
-        const uint32_t bal = __ballot_sync(kAllLanes, hit);
-        if (bal) b = j0 + __ffs(bal) - 1;
+    for (int j0 = 0; j0 < p.batch && b < 0; j0 += 128) {  // four loads on their way
+        int from[4], to[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int j = j0 + 32 * n + lane;
+            from[n] = j < p.batch ? ld_input(p.cu_q_lens + j) : INT32_MAX;
+            to[n] = j < p.batch ? ld_input(p.cu_q_lens + j + 1) : 0;
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const uint32_t hit = __ballot_sync(kAllLanes, from[n] <= t && t < to[n]);
+            if (hit && b < 0) b = j0 + 32 * n + __ffs(hit) - 1;
+        }
     }
     if (b < 0 || !sequence(p, b, &c0, &n, &L)) return;  // reported by the attention kernel
     const int local = row - c0 * p.heads;
-    const int2* parts = reinterpret_cast<const int2*>(p.plan + 4 * kPrefixPairs);
     RowParts r;
     r.item0 = p.packed_tiles + b * p.tiles_per_seq + local / 128;
     r.item1 = row / 128;
-    const int2 own = __ldcg(parts + r.item0), shared = __ldcg(parts + r.item1);
+    const int2 own = __ldcg(parts + r.item0);
     r.k0 = own.x;
     r.count0 = own.y;
     r.tr0 = local & 127;
@@ -1227,16 +1270,16 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(
     float acc[16], M;
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    const float Ls = add_parts(p, r, 0, 1, acc, &M, lane);
-    write_row(p, row, acc, M, Ls, lane);
+    float Ls = add_parts(p, r, SHARED ? warp : 0, SHARED ? kCombineWarps : 1, acc, &M, lane);
+    if (SHARED) add_warps(sums, acc, Ls, warp, lane);
+    if (!SHARED || warp == 0) write_row(p, row, acc, M, Ls, lane);
 }
 
 // Merged: only items in several parts, each described by the part that begins inside it first.
 __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(const PrefixParams p) {
     __shared__ int4 cut[kCombineThreads];
     __shared__ int first_unit[kCombineThreads + 1];
-    __shared__ __align__(16) float sums[kCombineThreads / 32][512];
-    __shared__ float norms[kCombineThreads / 32];
+    __shared__ WarpSums sums;
     static_assert(kPrefixPairs <= kCombineThreads, "one thread for each part");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
@@ -1249,9 +1292,9 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(
         const int o = __shfl_up_sync(kAllLanes, incl, off);
         if (lane >= off) incl += o;
     }
-    if (lane == 31) norms[warp] = __int_as_float(incl);
+    if (lane == 31) sums.norm[warp] = __int_as_float(incl);
     __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += __float_as_int(norms[w]);
+    for (int w = 0; w < warp; ++w) incl += __float_as_int(sums.norm[w]);
     first_unit[tid + 1] = incl;
     if (tid == 0) first_unit[0] = 0;
     __syncthreads();
@@ -1273,34 +1316,13 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(
         float acc[16], M;
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-        float Ls = add_parts(p, r, many ? warp : 0, many ? kCombineThreads / 32 : 1, acc, &M, lane);
+        float Ls = add_parts(p, r, many ? warp : 0, many ? kCombineWarps : 1, acc, &M, lane);
         if (!many) {
             if (tr < c.y) write_row(p, c.x + tr, acc, M, Ls, lane);
             continue;
         }
-        // the warps' sums, in their order
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            reinterpret_cast<float4*>(sums[warp])[32 * k + lane] =
-                make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
-        if (lane == 0) norms[warp] = Ls;
-        __syncthreads();
-        if (warp == 0) {
-#pragma unroll
-            for (int w = 1; w < kCombineThreads / 32; ++w) {
-                Ls += norms[w];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 v = reinterpret_cast<const float4*>(sums[w])[32 * k + lane];
-                    acc[4 * k] += v.x;
-                    acc[4 * k + 1] += v.y;
-                    acc[4 * k + 2] += v.z;
-                    acc[4 * k + 3] += v.w;
-                }
-            }
-            write_row(p, c.x + tr, acc, M, Ls, lane);
-        }
+        add_warps(sums, acc, Ls, warp, lane);
+        if (warp == 0) write_row(p, c.x + tr, acc, M, Ls, lane);
     }
 }
 
@@ -1396,10 +1418,14 @@ cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     if (e != cudaSuccess || !p.planned) return e;
     cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = 0;
-    constexpr int kRows = kCombineThreads / 32;
     if (p.packed) {
-        cfg.gridDim = dim3((unsigned)(((int64_t)p.total_q * p.heads + kRows - 1) / kRows));
-        return cudaLaunchKernelEx(&cfg, prefix_combine_packed_kernel, p);
+        const int rows = p.total_q * p.heads;
+        if (p.packed_tiles <= kSharedTiles) {
+            cfg.gridDim = dim3((unsigned)rows);
+            return cudaLaunchKernelEx(&cfg, prefix_combine_packed_kernel<true>, p);
+        }
+        cfg.gridDim = dim3((unsigned)(((int64_t)rows + kCombineWarps - 1) / kCombineWarps));
+        return cudaLaunchKernelEx(&cfg, prefix_combine_packed_kernel<false>, p);
     }
     cfg.gridDim = dim3(kCombineBlocks);
     return cudaLaunchKernelEx(&cfg, prefix_combine_merged_kernel, p);
