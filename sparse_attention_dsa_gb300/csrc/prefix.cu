@@ -1123,7 +1123,7 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
 // The units of work are four rows, a warp each, or one row of an item in many parts, which the block's warps share.
 constexpr int kCombineThreads = 128;
 constexpr int kCombineWarps = kCombineThreads / 32;
-constexpr int kCombineBlocks = 1216;  // eight blocks on each of 152 SMs
+constexpr int kCombineBlocks = 608;  // the four blocks that each of 152 SMs holds
 constexpr int kManyParts = 8;
 constexpr int kPartsInFlight = 4;
 // Packed rows are combined by a block each up to so many tiles of them (1, 2, 4, 5, 6 tiles behind 16384 positions: 22.3,
