@@ -390,7 +390,8 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  *   prefix_len >= 0, at most L_b - n_b for every sequence with queries (every query is behind the prefix)
  *   q, kv_cache, page_table, seq_lens, cu_q_lens, out, lse   as for dsa_sparse_attn
  *   workspace  dsa_prefix_attn_workspace_size(dims, prefix_len) bytes, first 256 zero-filled once
- * dims->idx_* and top_k are not looked at.  Positions beyond p_t and rows behind L_b are never part of the
+ * dims->idx_* and top_k are not looked at.  How the work is divided follows from dims and prefix_len alone: a page
+ * table about as wide as the longest context gives the shortest times.  Positions beyond p_t and rows behind L_b are never part of the
  * result, whatever they hold.  A score of -inf has weight 0 (an infinite value of such a row makes NaN of it);
  * a NaN in a visible row, or in q, makes the rows that see it NaN; with every score -inf, out = 0 and
  * lse = -inf.

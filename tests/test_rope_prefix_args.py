@@ -151,6 +151,17 @@ def test_prefix_workspace_size(L):
     assert dsa.prefix_attn_workspace_size(_dims(), -1) == 0
     assert dsa.prefix_attn_workspace_size(_dims(), 0) >= 256
     assert dsa.prefix_attn_workspace_size(_dims(), 100) >= 256
+    # partial results [128][512] and [128][2] fp32, two for each of 76 pairs, where the work is divided; one for each item
+    # and pair where rows are packed; converted rows of 1152 bytes for a long FP8 prefix
+    part = 4 * (128 * 512 + 2 * 128)
+    short = _dims(batch=8, total_q=8, max_pages_per_seq=8, num_pages=64)
+    long = _dims(batch=8, total_q=8, max_pages_per_seq=1000, num_pages=8000)
+    assert dsa.prefix_attn_workspace_size(short, 0) < part
+    assert 152 * part <= dsa.prefix_attn_workspace_size(long, 0) < 153 * part
+    packed = dict(batch=64, total_q=64, max_pages_per_seq=520, num_pages=2000, attn_heads=16)
+    assert (64 + 8 + 76) * part <= dsa.prefix_attn_workspace_size(_dims(**packed), 32768) < (64 + 8 + 77) * part
+    fp8 = dsa.prefix_attn_workspace_size(_dims(**packed, kv_dtype=dsa.DSA_FP8_E4M3), 32768)
+    assert fp8 == dsa.prefix_attn_workspace_size(_dims(**packed), 32768) + 32768 * 1152
 
 
 def test_wrappers_raise(L):
