@@ -1126,10 +1126,11 @@ constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kCombineBlocks = 608;  // the four blocks that each of 152 SMs holds
 constexpr int kManyParts = 8;
 constexpr int kPartsInFlight = 4;
-// Packed rows are combined by a block each up to so many tiles of them (1, 2, 4, 5, 6 tiles behind 16384 positions: 22.3,
-// 23.6, 27.9, 32.2, 35.0 us, with a warp each 27.9, 29.7, 31.8, 33.1, 35.1; 8 tiles behind 32768: 60.7 and 59.7): their
-// parts are the many that fewer tiles are cut in.
-constexpr int kSharedTiles = 5;
+// Packed rows' parts are shared by four or two warps up to so many tiles of rows: the fewer tiles, the more parts each is
+// cut in (16384 positions, 1, 4, 6, 12 tiles: a warp a row 28.4, 31.8, 35.2, 49.9 us; two 24.6, 29.8, 34.2, 52.2; four
+// 22.6, 28.4, 35.6, 54.1; 32741 positions, 8 tiles: 61.2, 60.3, 62.5).
+constexpr int kFourTiles = 5;
+constexpr int kTwoTiles = 8;
 
 // One row's parts: those of its own item, then of the packed item over the prefix.
 struct RowParts {
@@ -1202,11 +1203,12 @@ __device__ __forceinline__ void write_row(const PrefixParams& p, int row, const 
     if (lane == 0 && p.lse) p.lse[row] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
 }
 
-// The sums of a block's warps over the parts of one row, in the warps' order, in warp 0.
+// The sums of the `of` neighbouring warps that share a row's parts, in their order, in the first of them.
 struct WarpSums {
     float4 acc[kCombineWarps][128];
     float norm[kCombineWarps];
 };
+template <int OF>
 __device__ __forceinline__ void add_warps(WarpSums& sums, float (&acc)[16], float& Ls, int warp, int lane) {
     __syncthreads();
 #pragma unroll
@@ -1214,13 +1216,13 @@ __device__ __forceinline__ void add_warps(WarpSums& sums, float (&acc)[16], floa
         sums.acc[warp][32 * k + lane] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
     if (lane == 0) sums.norm[warp] = Ls;
     __syncthreads();
-    if (warp != 0) return;
+    if (warp % OF != 0) return;
 #pragma unroll
-    for (int w = 1; w < kCombineWarps; ++w) {
-        Ls += sums.norm[w];
+    for (int w = 1; w < OF; ++w) {
+        Ls += sums.norm[warp + w];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float4 v = sums.acc[w][32 * k + lane];
+            const float4 v = sums.acc[warp + w][32 * k + lane];
             acc[4 * k] += v.x;
             acc[4 * k + 1] += v.y;
             acc[4 * k + 2] += v.z;
@@ -1229,50 +1231,52 @@ __device__ __forceinline__ void add_warps(WarpSums& sums, float (&acc)[16], floa
     }
 }
 
-// Packed: every row has parts in two items.  SHARED: a block's warps share a row's parts.
-template <bool SHARED>
+// Packed: every row has parts in two items, which OF warps share.
+template <int OF>
 __global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(const PrefixParams p) {
     __shared__ WarpSums sums;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = SHARED ? blockIdx.x : blockIdx.x * kCombineWarps + warp;
-    if (row >= p.total_q * p.heads) return;
+    const int row = (int)blockIdx.x * (kCombineWarps / OF) + warp / OF;
+    const bool exists = row < p.total_q * p.heads;
     grid_dependency_wait();
     const int2* parts = reinterpret_cast<const int2*>(p.plan + 4 * kPrefixPairs);
-    const int2 shared = __ldcg(parts + row / 128);
-    const int t = row / p.heads;
+    const int2 shared = exists ? __ldcg(parts + row / 128) : make_int2(0, 0);
+    const int t = exists ? row / p.heads : -1;
     int b = -1, c0 = 0, n = 0, L = 0;
     for (int j0 = 0; j0 < p.batch && b < 0; j0 += 128) {  // four loads on their way
         int from[4], to[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int j = j0 + 32 * n + lane;
-            from[n] = j < p.batch ? ld_input(p.cu_q_lens + j) : INT32_MAX;
-            to[n] = j < p.batch ? ld_input(p.cu_q_lens + j + 1) : 0;
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + 32 * i + lane;
+            from[i] = j < p.batch ? ld_input(p.cu_q_lens + j) : INT32_MAX;
+            to[i] = j < p.batch ? ld_input(p.cu_q_lens + j + 1) : 0;
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const uint32_t hit = __ballot_sync(kAllLanes, from[n] <= t && t < to[n]);
-            if (hit && b < 0) b = j0 + 32 * n + __ffs(hit) - 1;
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t hit = __ballot_sync(kAllLanes, from[i] <= t && t < to[i]);
+            if (hit && b < 0) b = j0 + 32 * i + __ffs(hit) - 1;
         }
     }
-    if (b < 0 || !sequence(p, b, &c0, &n, &L)) return;  // reported by the attention kernel
-    const int local = row - c0 * p.heads;
-    RowParts r;
-    r.item0 = p.packed_tiles + b * p.tiles_per_seq + local / 128;
-    r.item1 = row / 128;
-    const int2 own = __ldcg(parts + r.item0);
-    r.k0 = own.x;
-    r.count0 = own.y;
-    r.tr0 = local & 127;
-    r.k1 = shared.x;
-    r.count1 = shared.y;
-    r.tr1 = row & 127;
-    float acc[16], M;
+    const bool ok = exists && b >= 0 && sequence(p, b, &c0, &n, &L);  // (if not: reported by the attention kernel)
+    float acc[16], M = -INFINITY, Ls = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    float Ls = add_parts(p, r, SHARED ? warp : 0, SHARED ? kCombineWarps : 1, acc, &M, lane);
-    if (SHARED) add_warps(sums, acc, Ls, warp, lane);
-    if (!SHARED || warp == 0) write_row(p, row, acc, M, Ls, lane);
+    if (ok) {
+        const int local = row - c0 * p.heads;
+        RowParts r;
+        r.item0 = p.packed_tiles + b * p.tiles_per_seq + local / 128;
+        r.item1 = row / 128;
+        const int2 own = __ldcg(parts + r.item0);
+        r.k0 = own.x;
+        r.count0 = own.y;
+        r.tr0 = local & 127;
+        r.k1 = shared.x;
+        r.count1 = shared.y;
+        r.tr1 = row & 127;
+        Ls = add_parts(p, r, warp % OF, OF, acc, &M, lane);
+    }
+    if (OF > 1) add_warps<OF>(sums, acc, Ls, warp, lane);
+    if (ok && warp % OF == 0) write_row(p, row, acc, M, Ls, lane);
 }
 
 // Merged: only items in several parts, each described by the part that begins inside it first.
@@ -1321,7 +1325,7 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(
             if (tr < c.y) write_row(p, c.x + tr, acc, M, Ls, lane);
             continue;
         }
-        add_warps(sums, acc, Ls, warp, lane);
+        add_warps<kCombineWarps>(sums, acc, Ls, warp, lane);
         if (warp == 0) write_row(p, c.x + tr, acc, M, Ls, lane);
     }
 }
@@ -1419,13 +1423,11 @@ cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     cfg.blockDim = dim3(kCombineThreads);
     cfg.dynamicSmemBytes = 0;
     if (p.packed) {
-        const int rows = p.total_q * p.heads;
-        if (p.packed_tiles <= kSharedTiles) {
-            cfg.gridDim = dim3((unsigned)rows);
-            return cudaLaunchKernelEx(&cfg, prefix_combine_packed_kernel<true>, p);
-        }
-        cfg.gridDim = dim3((unsigned)(((int64_t)rows + kCombineWarps - 1) / kCombineWarps));
-        return cudaLaunchKernelEx(&cfg, prefix_combine_packed_kernel<false>, p);
+        const int of = p.packed_tiles <= kFourTiles ? 4 : p.packed_tiles <= kTwoTiles ? 2 : 1, rows = kCombineWarps / of;
+        cfg.gridDim = dim3((unsigned)(((int64_t)p.total_q * p.heads + rows - 1) / rows));
+        return cudaLaunchKernelEx(&cfg, of == 4   ? prefix_combine_packed_kernel<4>
+                                        : of == 2 ? prefix_combine_packed_kernel<2>
+                                                  : prefix_combine_packed_kernel<1>, p);
     }
     cfg.gridDim = dim3(kCombineBlocks);
     return cudaLaunchKernelEx(&cfg, prefix_combine_merged_kernel, p);

@@ -78,6 +78,7 @@ SHAPES = {
     "full_heads_long_prefix": ([1100 + 7 * i for i in range(20)], [1] * 20, 1090, 128),
     "packed_ragged": ([900 + 11 * i for i in range(24)], [i % 5 for i in range(24)], 800, 16),
     "packed_long_prefix": ([2510 + 3 * i for i in range(64)], [1] * 64, 2500, 16),
+    "packed_thirteen_tiles": ([2510 + i % 90 for i in range(101)], [1] * 101, 2500, 16),
     # more items than are divided evenly: whole items in turn
     "thousands_of_short_ones": ([1 + i % 70 for i in range(2100)], [1] * 2100, 0, 128),
     "many_behind_one_page": ([64 + 1 + i % 5 for i in range(300)], [1] * 300, 64, 32),
