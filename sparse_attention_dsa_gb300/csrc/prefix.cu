@@ -202,6 +202,7 @@ struct Ctrl {
     uint64_t q_full, q_empty;
     uint64_t k_full[kKUnits], k_empty[kKUnits];
     uint64_t v_full[kVSlots], v_empty[kVSlots];
+    uint64_t v_turn[kVSlots];  // bf16: the slot is free for an edge tile's V (once for each edge tile)
     uint64_t s_full[2], s_empty[2];
     uint64_t p_full, pv_done, o_free, edge_full, drained, exchanged;
     // FP8: bf16 queries, codes and rotary parts are here; are converted
@@ -374,6 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         for (int i = 0; i < kVSlots; ++i) {
             mbar_init(&ctl->v_full[i], 1);
             mbar_init(&ctl->v_empty[i], 1);
+            mbar_init(&ctl->v_turn[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->s_full[i], 1);
@@ -583,6 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                             } else if (!KVFP8 && tv.edge) {
                                 // filled by the warps below, which have a barrier of their own
                                 if (rank == 0) mbar_arrive(&ctl->v_full[h]);
+                                mbar_arrive(&ctl->v_turn[h]);
                             } else {
                                 if (rank == 0) mbar_arrive_expect_tx(&ctl->v_full[h], 2 * kVSlot);
                                 tma_pair_load_4d(dst, &vmap, v_full + 8 * h, 0, 0, 4 * rank, page);
@@ -905,16 +908,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         const int fw = warp - kFillWarp;
         static_assert(kFillWarps == 4, "16 rows of a page each");
         const uint32_t edge_full = leader(&ctl->edge_full);
-        uint32_t vphase = 1;  // a tile takes every slot of the V ring once
+        // The ring does not wait for these warps at other tiles, so its own phases may pass them by (a parity names one
+        // of two phases).  v_turn has one phase for each edge tile, and the ring stays there until the tile is filled.
+        uint32_t turn = 0;
         static_assert(kVSlots == 2, "one slot for each page of a tile");
         while (ok && next_segment(p, w, s)) {
-            for (int u = s.u0; ok && u < s.u1; ++u, vphase ^= 1u) {
+            for (int u = s.u0; ok && u < s.u1; ++u) {
                 const Tile t = tile_of(p, s.it, u);
-                if (!t.edge) {
-                    // keep step with the ring (a parity names one of two phases: never run further ahead)
-                    ok = wait(&ctl->v_empty[0], vphase);
-                    continue;
-                }
+                if (!t.edge) continue;
                 // A row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's.  All is
                 // loaded and looked at before the slots are waited for: only the stores are on the way to the products.
                 const int row0 = 16 * fw;
@@ -947,12 +948,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (!(ok = wait(&ctl->v_empty[h], vphase))) break;
+                    if (!(ok = wait(&ctl->v_turn[h], turn & 1u))) break;
                     const uint32_t dst = smem_u32(v_s + h * kVSlot + (lane >> 3) * kAtom) + row0 * 128;
 #pragma unroll
                     for (int k = 0; k < 16; ++k) st_shared_v4(dst + k * 128 + (((lane & 7) ^ (k & 7)) << 4), v[h][k]);
                 }
                 if (!ok) break;
+                ++turn;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(edge_full);
