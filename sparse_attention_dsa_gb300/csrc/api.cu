@@ -207,11 +207,14 @@ bool prefix_sizes(const dsa_dims_t* d, int32_t prefix_len, dsa::PrefixParams* p)
     memset(p, 0, sizeof *p);
     if (d->batch < 1 || d->total_q < 1 || d->max_q_len < 1 || d->attn_heads < 1 || d->attn_heads > 128) return false;
     if ((int64_t)d->total_q * d->attn_heads > (int64_t)INT32_MAX - 128) return false;
-    const int64_t tiles = ((int64_t)d->max_q_len * d->attn_heads + 127) / 128;
+    // No sequence has more queries than the batch: whatever is announced, the rows of its tiles stay within total_q * heads
+    // (a last tile's within 32 bits).
+    const int32_t most_q = d->max_q_len < d->total_q ? d->max_q_len : d->total_q;
+    const int64_t tiles = ((int64_t)most_q * d->attn_heads + 127) / 128;
     if ((int64_t)d->batch * tiles > (int64_t)INT32_MAX / 2) return false;
     p->batch = d->batch;
     p->total_q = d->total_q;
-    p->max_q_len = d->max_q_len;
+    p->max_q_len = most_q;
     p->heads = d->attn_heads;
     p->prefix_len = prefix_len;
     p->kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;

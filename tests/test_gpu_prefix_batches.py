@@ -5,7 +5,7 @@ import torch
 import sparse_attention_dsa_gb300 as dsa  # noqa: F401
 
 from _gpu import ensure_built
-from test_gpu_prefix import Call
+from test_gpu_prefix import SHAPES, Call
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +23,9 @@ def test_a_long_chunk_among_single_queries(where):
     n = [1] * 64
     n[where] = 400
     Call([900 + (i % 9) * 31 for i in range(64)], n, 0, 128, seed=30).run().check()
+
+
+@pytest.mark.parametrize("name", ["one_row", "two_queries", "ragged_queries_and_none", "packed_many"])
+@pytest.mark.parametrize("most", [2**25, 2**31 - 1])
+def test_any_bound_on_the_query_counts_may_be_announced(name, most):
+    Call(*SHAPES[name], seed=31, max_q_len=most).run().check()
