@@ -387,7 +387,8 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  * maps all its positions (as a page pool with shared prefix pages leaves it); where prefix_len is not a
  * multiple of 64, the page in which it ends may be each sequence's own copy.  prefix_len = 0 is plain
  * attention of each sequence over its own context.
- *   prefix_len >= 0, at most L_b - n_b for every sequence with queries (every query is behind the prefix)
+ *   prefix_len >= 0, at most L_b - n_b for every sequence with queries (every query is behind the prefix), and below
+ *              2^31 - 256
  *   q, kv_cache, page_table, seq_lens, cu_q_lens, out, lse   as for dsa_sparse_attn
  *   workspace  dsa_prefix_attn_workspace_size(dims, prefix_len) bytes, first 256 zero-filled once
  * dims->idx_* and top_k are not looked at.  How the work is divided follows from dims and prefix_len alone: a page

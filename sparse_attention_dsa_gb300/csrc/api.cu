@@ -206,7 +206,7 @@ dsa::RopeParams rope_params(const dsa_dims_t* d, const dsa_rope_t* r, const int3
 bool prefix_sizes(const dsa_dims_t* d, int32_t prefix_len, dsa::PrefixParams* p) {
     memset(p, 0, sizeof *p);
     if (d->batch < 1 || d->total_q < 1 || d->max_q_len < 1 || d->attn_heads < 1 || d->attn_heads > 128) return false;
-    if ((int64_t)d->total_q * d->attn_heads > (int64_t)INT32_MAX - 128) return false;
+    if ((int64_t)d->total_q * d->attn_heads > (int64_t)INT32_MAX - 128 || prefix_len >= dsa::kLongestContext) return false;
     // No sequence has more queries than the batch: whatever is announced, the rows of its tiles stay within total_q * heads
     // (a last tile's within 32 bits).
     const int32_t most_q = d->max_q_len < d->total_q ? d->max_q_len : d->total_q;
@@ -794,6 +794,8 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
     if (prefix_len < 0) return fail(DSA_ERR_INVALID_ARG, "prefix_len must be >= 0 (got %d)", prefix_len);
     if ((int64_t)prefix_len > (int64_t)d->max_pages_per_seq * 64)
         return fail(DSA_ERR_INVALID_ARG, "prefix_len %d exceeds the page table's %d pages", prefix_len, d->max_pages_per_seq);
+    if (prefix_len >= dsa::kLongestContext)
+        return fail(DSA_ERR_UNSUPPORTED, "prefix_len must be below %d (got %d)", dsa::kLongestContext, prefix_len);
     if ((st = check_ptr(q, "q")) || (st = check_ptr(kv_cache, "kv_cache")) ||
         (st = check_ptr(page_table, "page_table")) || (st = check_ptr(seq_lens, "seq_lens")) ||
         (st = check_ptr(cu_q_lens, "cu_q_lens")) || (st = check_ptr(out, "out")) ||

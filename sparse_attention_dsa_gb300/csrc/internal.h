@@ -252,6 +252,7 @@ struct PrefixParams {
     int32_t convert_ahead;  // plan_prefix(): the prefix's FP8 rows are converted to f16 first
     uint8_t* ahead;         // those rows [ceil(prefix_len / 64) * 64][576] f16, or null
 };
+constexpr int kLongestContext = INT32_MAX - 255;  // the end of a context's last tile is a position, too
 constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs
 constexpr int kPlanItems = 2048;     // most items that are divided evenly
 constexpr int kDivideCost = 11;      // what dividing costs each pair, in tiles

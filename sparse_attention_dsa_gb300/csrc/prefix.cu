@@ -73,8 +73,6 @@ struct Item {
     int pos0, lrow0;    // position of the sequence's first query; first row within the sequence's rows
 };
 
-constexpr int kLongestContext = INT32_MAX - 255;  // the end of a context's last tile is a position, too
-
 // Offsets and length of sequence b; false when they are inconsistent.
 __device__ __forceinline__ bool sequence(const PrefixParams& p, int b, int* c0, int* n, int* L) {
     const int a = ld_input(p.cu_q_lens + b), e = ld_input(p.cu_q_lens + b + 1);

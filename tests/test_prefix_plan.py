@@ -31,3 +31,20 @@ def test_no_sequence_is_taken_to_have_more_queries_than_the_batch(batch, total, 
     for prefix in (0, 2000):
         small = _size(prefix, batch=batch, total_q=total, max_q_len=total, attn_heads=heads)
         assert _size(prefix, batch=batch, total_q=total, max_q_len=most, attn_heads=heads) == small
+
+
+FAKE = 0x10000  # an aligned non-null address; never dereferenced
+
+
+@pytest.mark.parametrize("prefix", [2**31 - 256, 2**31 - 128, 64 * (2**25 - 1)])
+@pytest.mark.parametrize("heads,dtype", [(16, dsa.DSA_BF16), (128, dsa.DSA_FP8_E4M3)])
+def test_a_prefix_that_no_context_can_hold_is_refused(prefix, heads, dtype):
+    """Contexts end before 2^31 - 255 positions and every query lies behind the prefix; tiles of a longer prefix would end
+    beyond 32 bits."""
+    d = _dims(batch=64, total_q=64, max_pages_per_seq=2**25 - 1, attn_heads=heads, kv_dtype=dtype)
+    with pytest.raises(dsa.DsaError, match="prefix_len") as e:
+        dsa.prefix_attn(d, prefix, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, stream=0)
+    assert e.value.status == dsa.DSA_ERR_UNSUPPORTED
+    assert dsa.prefix_attn_workspace_size(d, prefix) == 256
+    d.max_pages_per_seq = 1
+    assert dsa.prefix_attn_workspace_size(d, 2**31 - 1) == 256
