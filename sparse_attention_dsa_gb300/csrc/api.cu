@@ -211,7 +211,8 @@ bool prefix_sizes(const dsa_dims_t* d, int32_t prefix_len, dsa::PrefixParams* p)
     // (a last tile's within 32 bits).
     const int32_t most_q = d->max_q_len < d->total_q ? d->max_q_len : d->total_q;
     const int64_t tiles = ((int64_t)most_q * d->attn_heads + 127) / 128;
-    if ((int64_t)d->batch * tiles > (int64_t)INT32_MAX / 2) return false;
+    const int64_t most = ((int64_t)d->total_q * d->attn_heads + 127) / 128 + d->batch;  // tiles, whatever the lengths are
+    if ((d->batch * tiles < most ? d->batch * tiles : most) > (int64_t)INT32_MAX / 2) return false;
     p->batch = d->batch;
     p->total_q = d->total_q;
     p->max_q_len = most_q;
@@ -808,8 +809,7 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
     memset(&L, 0, sizeof L);
     dsa::PrefixParams& p = L.params;
     if (!prefix_sizes(d, prefix_len, &p))
-        return fail(DSA_ERR_UNSUPPORTED, "total_q * attn_heads (%d * %d) or batch * max_q_len (%d * %d) is too large",
-                    d->total_q, d->attn_heads, d->batch, d->max_q_len);
+        return fail(DSA_ERR_UNSUPPORTED, "total_q * attn_heads (%d * %d) or batch (%d) is too large", d->total_q, d->attn_heads, d->batch);
     p.q = static_cast<const uint16_t*>(q);
     p.kv_cache = static_cast<const uint8_t*>(kv_cache);
     p.page_table = page_table;

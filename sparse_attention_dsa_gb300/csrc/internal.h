@@ -241,7 +241,7 @@ struct PrefixParams {
     // filled in by plan_prefix()
     int32_t packed;         // rows of different sequences share tiles over the prefix
     int32_t packed_tiles;   // 128-row tiles of all the batch's rows
-    int32_t tiles_per_seq;  // 128-row tiles of the longest sequence's rows
+    int32_t tiles_per_seq;  // 128-row tiles of the longest sequence's rows, 0 where items are numbered by the rows in front
     int32_t prefix_tiles;   // 128-position tiles of the prefix
     int32_t row_tiles;      // 128-row tiles that attend to the prefix
     int32_t n_items;
@@ -255,6 +255,7 @@ struct PrefixParams {
 constexpr int kLongestContext = INT32_MAX - 255;  // the end of a context's last tile is a position, too
 constexpr int kPrefixPairs = 76;     // CTA pairs of the largest grid: one CTA on each of 152 SMs
 constexpr int kPlanItems = 2048;     // most items that are divided evenly
+constexpr int kPackItems = 4096;     // the same where rows are packed
 constexpr int kDivideCost = 11;      // what dividing costs each pair, in tiles
 constexpr int kPartCost = 1;         // what a partial result costs, in tiles
 constexpr int kWholeTiles = 16;      // longer own contexts are always divided

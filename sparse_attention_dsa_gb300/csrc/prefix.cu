@@ -85,6 +85,26 @@ __device__ __forceinline__ bool sequence(const PrefixParams& p, int b, int* c0, 
     return (int64_t)*n <= (int64_t)*L - p.prefix_len && (int64_t)*L <= (int64_t)p.max_pages * 64;
 }
 
+// Number of sequence b's first item among the sequences' items, c0 its first query.  Where one sequence has many queries
+// and most have few, tiles_per_seq numbers a sequence would be empty ones nearly all (tiles_per_seq is 0 then): b +
+// floor(c0 * heads / 128) is never less than the number of tiles in front of it.
+__device__ __forceinline__ int64_t first_item(const PrefixParams& p, int b, int c0) {
+    return p.tiles_per_seq > 0 ? (int64_t)b * p.tiles_per_seq : b + (int64_t)c0 * p.heads / 128;
+}
+// The sequence of item j then: the last one whose first item is not behind it.
+__device__ __forceinline__ int search_item(const PrefixParams& p, int j) {
+    int b = 0, hi = min(p.batch, j + 1);
+    while (hi - b > 1) {
+        const int mid = (b + hi) / 2;
+        if (first_item(p, mid, ld_input(p.cu_q_lens + mid)) <= j) b = mid;
+        else hi = mid;
+    }
+    return b;
+}
+
+// SEARCH: items are numbered by the rows in front of them (an instance of its own: with the choice in the code of every role
+// 32 x 64 heads of FP8 rows behind 16000 took 74.3 us instead of 71.2).
+template <bool SEARCH>
 __device__ __forceinline__ Item decode_item(const PrefixParams& p, int i) {
     Item it;
     it.b = -1;
@@ -98,11 +118,16 @@ __device__ __forceinline__ Item decode_item(const PrefixParams& p, int i) {
         return it;
     }
     const int j = i - nt;
-    it.b = j / p.tiles_per_seq;
-    const int r = j - it.b * p.tiles_per_seq;
+    it.b = SEARCH ? search_item(p, j) : j / p.tiles_per_seq;
     int c0, n, L;
-    const bool ok = sequence(p, it.b, &c0, &n, &L);
-    it.lrow0 = 128 * r;
+    bool ok = sequence(p, it.b, &c0, &n, &L);
+    if (SEARCH) {
+        const int64_t lrow0 = 128 * (j - first_item(p, it.b, c0));  // (a row that no sequence has: inconsistent offsets)
+        ok = ok && lrow0 >= 0 && lrow0 < (int64_t)n * p.heads;
+        it.lrow0 = ok ? (int)lrow0 : 0;
+    } else {
+        it.lrow0 = 128 * (j - it.b * p.tiles_per_seq);
+    }
     it.row0 = ok ? c0 * p.heads + it.lrow0 : 0;
     it.nrows = ok ? min(128, n * p.heads - it.lrow0) : 0;
     if (it.nrows <= 0) {
@@ -214,7 +239,7 @@ struct Ctrl {
 };
 constexpr int kSmem = 1024 + 2 * kQAtoms * kAtom + kVSlots * kVSlot + kPBytes + (int)sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
-static_assert(kPlanItems * 4 <= kQAtoms * kAtom, "the plan's scan is done in the K ring's memory");
+static_assert(kPackItems >= kPlanItems && kPackItems * 4 <= kQAtoms * kAtom, "the plan's scan is done in the K ring's memory");
 
 // Where a role stands in its pair's list of segments.
 struct Walk {
@@ -222,10 +247,11 @@ struct Walk {
     bool decoded;          // the segment passed in holds the next item already
 };
 
+template <bool SEARCH>
 __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Segment& s) {
     if (p.planned) {
         while (w.left > 0 && w.item < p.n_items) {
-            if (!w.decoded) s.it = decode_item(p, w.item);
+            if (!w.decoded) s.it = decode_item<SEARCH>(p, w.item);
             w.decoded = false;
             const int tiles = s.it.tiles_a + s.it.tiles_b;
             if (tiles > 0) {  // w.tile counts places
@@ -242,7 +268,7 @@ __device__ __forceinline__ bool next_segment(const PrefixParams& p, Walk& w, Seg
         return false;
     }
     while (w.item >= 0) {  // whole items, the ones with the most positions (the last of each sequence) first
-        if (!w.decoded) s.it = decode_item(p, w.item);
+        if (!w.decoded) s.it = decode_item<SEARCH>(p, w.item);
         w.decoded = false;
         s.index = w.item;
         s.u0 = 0;
@@ -338,7 +364,7 @@ __device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2
     return y;
 }
 
-template <bool KVFP8>
+template <bool KVFP8, bool SEARCH>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     prefix_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap codemap,
@@ -430,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         int sum = 0;
         Item mine;  // the last of the run, the only one as a rule
         for (int i = i0; i < i1; ++i) {
-            mine = decode_item(p, i);
+            mine = decode_item<SEARCH>(p, i);
             cum[i] = places(p, mine);
             sum += cum[i];
         }
@@ -453,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         if (idle && rank == 0 && tid == 0) reinterpret_cast<int4*>(p.plan)[pair] = make_int4(0, 0, 0, 0);
         for (int i = i0; i < i1; ++i) {
             const int tiles = cum[i];
-            if (run > 1) mine = decode_item(p, i);
+            if (run > 1) mine = decode_item<SEARCH>(p, i);
             // for the combining kernel: packed, the parts of every item; merged, for each part that begins inside an
             // item, as the second of that item's parts, the item's rows and parts
             const bool here = w0 >= before && w0 < before + tiles;
@@ -482,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     } else {
         if (tid == 0) {
             ctl->first.index = p.n_items - 1 - pair;
-            ctl->first.it = decode_item(p, p.n_items - 1 - pair);  // no more pairs than items
+            ctl->first.it = decode_item<SEARCH>(p, p.n_items - 1 - pair);  // no more pairs than items
             ctl->first_place = 0;
         }
         start.left = pairs;
@@ -508,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         Segment s = ctl->first;
         uint32_t seg = 0, kphase = 1, vphase = 1;  // a tile takes every slot of both rings once
         const uint32_t q_full = leader(&ctl->q_full), k_full = leader(&ctl->k_full[0]), v_full = leader(&ctl->v_full[0]);
-        while (ok && next_segment(p, w, s)) {
+        while (ok && next_segment<SEARCH>(p, w, s)) {
             Tile t = tile_of(p, s.it, s.u0), tv = t;
             int page0 = page_of(t, 0), page1 = page_of(t, 1), vpage0 = 0, vpage1 = 0;
             if (seg > 0 && !(ok = wait(&ctl->q_empty, (seg - 1) & 1u))) break;
@@ -640,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             if (raw) ++v_raws;
             return true;
         };
-        while (ok && next_segment(p, w, s)) {
+        while (ok && next_segment<SEARCH>(p, w, s)) {
             if (!(ok = wait(KVFP8 ? &ctl->q_conv : &ctl->q_full, seg & 1u))) break;
             ++seg;
             bool edge = false, raw = false;
@@ -704,7 +730,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             ++swaps;
             return true;
         };
-        bool have = next_segment(p, w, s);
+        bool have = next_segment<SEARCH>(p, w, s);
         int first_pg = have ? page_of(tile_of(p, s.it, s.u0), half) : kNoPage;
         while (have) {
             const int tr = 64 * rank + r;  // row of the tile
@@ -811,7 +837,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             if (!ok) break;
             // the next segment, looked up while this one's last products run
             Segment ahead = s;
-            have = next_segment(p, w, ahead);
+            have = next_segment<SEARCH>(p, w, ahead);
             if (have) first_pg = page_of(tile_of(p, ahead.it, ahead.u0), half);
             // ---- the segment's result: O / l and lse, or O, m and l for the combining kernel ----
             if (!(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
@@ -910,7 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         // of two phases).  v_turn has one phase for each edge tile, and the ring stays there until the tile is filled.
         uint32_t turn = 0;
         static_assert(kVSlots == 2, "one slot for each page of a tile");
-        while (ok && next_segment(p, w, s)) {
+        while (ok && next_segment<SEARCH>(p, w, s)) {
             for (int u = s.u0; ok && u < s.u1; ++u) {
                 const Tile t = tile_of(p, s.it, u);
                 if (!t.edge) continue;
@@ -994,7 +1020,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             Walk w = start;
             Segment s = ctl->first;
             uint32_t seg = 0, phase = 0;
-            while (ok && next_segment(p, w, s)) {
+            while (ok && next_segment<SEARCH>(p, w, s)) {
                 // the first tile that is to be converted, and its scales, while q is on its way
                 int u = p.ahead != nullptr ? max(s.u0, s.it.tiles_a) : s.u0;
                 Tile t = tile_of(p, s.it, min(u, s.u1 - 1));
@@ -1264,7 +1290,7 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(
     if (ok) {
         const int local = row - c0 * p.heads;
         RowParts r;
-        r.item0 = p.packed_tiles + b * p.tiles_per_seq + local / 128;
+        r.item0 = p.packed_tiles + (int)first_item(p, b, c0) + local / 128;
         r.item1 = row / 128;
         const int2 own = __ldcg(parts + r.item0);
         r.k0 = own.x;
@@ -1362,9 +1388,10 @@ void plan_prefix(PrefixParams* p, int max_pages) {
     p->prefix_tiles = (p->prefix_len + 127) / 128;
     p->packed_tiles = (int)((rows + 127) / 128);
     p->tiles_per_seq = (int)(((int64_t)p->max_q_len * p->heads + 127) / 128);
-    const int64_t merged = (int64_t)p->batch * p->tiles_per_seq;
-    const int64_t most = p->packed_tiles + p->batch;  // tiles of the sequences' rows, whatever their lengths
-    const int64_t alone = merged < most ? merged : most;
+    const int64_t each = (int64_t)p->batch * p->tiles_per_seq;
+    const int64_t most = (int64_t)p->packed_tiles + p->batch;  // tiles of the sequences' rows, whatever their lengths
+    const int64_t alone = each < most ? each : most;
+    if (most < each) p->tiles_per_seq = 0;  // (see first_item)
     const int64_t own_tiles = ((int64_t)max_pages * 64 - (p->prefix_len & ~63) + 127) / 128;
     const int64_t longest = p->prefix_tiles + own_tiles;
     const int64_t own = own_tiles * (p->kv_fp8 ? 2 : 1);
@@ -1375,13 +1402,17 @@ void plan_prefix(PrefixParams* p, int max_pages) {
     const int64_t divided = alone * (own + prefix(alone) + kItemCost) + kPrefixPairs * kDivideCost;
     const int64_t packed = alone * (own + kItemCost) + p->packed_tiles * (prefix(p->packed_tiles) + kItemCost) +
                            (alone + p->packed_tiles) * kPartCost + kPrefixPairs * kDivideCost;
-    // Many items are even enough by themselves (1000 x 128 with up to 3000 positions: 368 us whole, 339 divided; two
-    // prompts of 4000 tokens, 16 heads, 1000 items: 482 and 508), and every CTA scans them all for a plan.  Places on the
-    // line are counted in 32 bits.
-    const bool fits = (merged + p->packed_tiles) * (3 * longest + kItemCost) <= INT32_MAX;
-    p->packed = fits && merged + p->packed_tiles <= kPlanItems && packed < divided && packed < whole;
-    p->planned = p->packed || (fits && merged <= kPlanItems && divided < whole);
-    p->n_items = (int)(merged + (p->packed ? p->packed_tiles : 0));
+    // Many items are even enough by themselves where their contexts are alike (1000 x 128 with up to 3000 positions: 368 us
+    // whole, 339 divided; two prompts of 4000 tokens, 16 heads, 1000 items: 482 and 508; 4096 tokens x 128 heads at 65536,
+    // 4096 items: 42.3 ms and 43.5, as the whole ones read the same rows at a time), and every CTA scans them all for a
+    // plan.  Packing saves more (2048 x 16 heads behind 4096, 2304 items: 369 us, 1350 whole): its limit is the 1 GB that
+    // the partial results take.  Places on the line are counted in 32 bits.  Batches of few queries but for one sequence:
+    // 64 x 128 heads at 1000 positions and one of 131072, 33 queries for another: 77 us divided, 1265 whole; 64 x 16
+    // behind 32768, 512 queries for one: 408 us packed, 1580 whole.
+    const bool fits = (alone + p->packed_tiles) * (3 * longest + kItemCost) <= INT32_MAX;
+    p->packed = fits && alone + p->packed_tiles <= kPackItems && packed < divided && packed < whole;
+    p->planned = p->packed || (fits && alone <= kPlanItems && divided < whole);
+    p->n_items = (int)(alone + (p->packed ? p->packed_tiles : 0));
     p->row_tiles = (int)(p->packed ? p->packed_tiles : alone);
     p->convert_ahead = ahead(p->row_tiles);
 }
@@ -1398,7 +1429,9 @@ size_t prefix_plan_bytes(const PrefixParams& p) { return ((size_t)(2 * p.n_items
 
 cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     const PrefixParams& p = L.params;
-    auto kernel = p.kv_fp8 ? prefix_pair_kernel<true> : prefix_pair_kernel<false>;
+    const bool search = p.tiles_per_seq == 0;
+    auto kernel = p.kv_fp8 ? (search ? prefix_pair_kernel<true, true> : prefix_pair_kernel<true, false>)
+                           : (search ? prefix_pair_kernel<false, true> : prefix_pair_kernel<false, false>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)(p.planned ? kPrefixPairs : (p.n_items < kPrefixPairs ? p.n_items : kPrefixPairs));

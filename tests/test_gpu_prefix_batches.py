@@ -2,9 +2,10 @@
 import pytest
 import torch
 
-import sparse_attention_dsa_gb300 as dsa  # noqa: F401
+import sparse_attention_dsa_gb300 as dsa
 
 from _gpu import ensure_built
+from _rope_prefix import Attention
 from test_gpu_prefix import SHAPES, Call
 
 pytestmark = pytest.mark.gpu
@@ -29,3 +30,46 @@ def test_a_long_chunk_among_single_queries(where):
 @pytest.mark.parametrize("most", [2**25, 2**31 - 1])
 def test_any_bound_on_the_query_counts_may_be_announced(name, most):
     Call(*SHAPES[name], seed=31, max_q_len=most).run().check()
+
+
+MIXED = {
+    # name: (seq_lens, q_lens, prefix, heads)
+    "chunk_first": ([900 + 31 * (i % 9) for i in range(40)], [70] + [1] * 39, 0, 128),
+    "chunk_last": ([900 + 31 * (i % 9) for i in range(40)], [1] * 39 + [70], 0, 128),
+    "chunk_between_empty_ones": ([700, 600, 900, 650, 800], [0, 0, 90, 0, 1], 512, 24),
+    "few_heads_chunk": ([2600 + 31 * (i % 9) for i in range(30)], [1] * 11 + [45] + [2] * 18, 2500, 16),
+    "chunk_of_odd_rows": ([520 + 7 * i for i in range(20)], [1] * 7 + [61, 0, 2] + [1] * 10, 450, 7),
+    "thousands_behind_a_prefix": ([1100 + i % 70 for i in range(2100)], [1] * 2100, 1090, 16),
+    "one_long_context": ([9000] + [300] * 30, [20] + [1] * 30, 0, 64),
+}
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("name", list(MIXED))
+def test_chunks_among_single_queries(name, fp8, wide):
+    Call(*MIXED[name], fp8=fp8, seed=32, wide=wide).run().check()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("heads", [16, 128])
+def test_inconsistent_sequences_beside_a_chunk(heads, wide):
+    """Sequences whose items are found by the rows in front of them: one that is inconsistent, and offsets that do not
+    begin at 0, take nothing from the others."""
+    n, L = [1, 40, 1, 2, 1, 1, 1, 1], [300, 420, 300, 310, 333, 500, 301, 290]
+    c = Call(L, n, 200, heads, seed=33, wide=wide)
+    ref = Attention(c.b, c.q, c.cache, False)
+    c.b.lens[4] = 200  # its query (token 44) would lie inside the prefix
+    c.run()
+    assert c.error() == dsa.DSA_DEVERR_SEQ
+    assert bool((c.out[44] == 7).all()) and bool((c.lse[44] == 7).all())
+    for t in (slice(0, 44), slice(45, 48)):
+        ref.check(c.out, c.lse, False, tokens=t)
+    dsa.clear_device_error(c.workspace)
+    c.out.fill_(7), c.lse.fill_(7)
+    c.b.lens[4] = 333
+    c.b.cu[0] = 1  # token 0 is nobody's, and sequence 0 has no query
+    c.run()
+    assert c.error() == dsa.DSA_DEVERR_SEQ
+    assert bool((c.out[0] == 7).all()) and bool((c.lse[0] == 7).all())
+    ref.check(c.out, c.lse, False, tokens=slice(1, 48))

@@ -48,3 +48,18 @@ def test_a_prefix_that_no_context_can_hold_is_refused(prefix, heads, dtype):
     assert dsa.prefix_attn_workspace_size(d, prefix) == 256
     d.max_pages_per_seq = 1
     assert dsa.prefix_attn_workspace_size(d, 2**31 - 1) == 256
+
+
+PART = 4 * (128 * 512 + 2 * 128)  # bytes of a partial result
+
+
+@pytest.mark.parametrize("what,dims,prefix", [
+    # one sequence with a chunk of queries among single ones: as the same batch without it
+    ("one of 33 queries", dict(batch=64, total_q=96, max_q_len=33, max_pages_per_seq=2048), 0),
+    ("one of 512 queries", dict(batch=256, total_q=767, max_q_len=512, max_pages_per_seq=64), 0),
+    ("chunk behind a prefix", dict(batch=64, total_q=575, max_q_len=512, max_pages_per_seq=523, attn_heads=16), 32768),
+    ("many behind a prefix", dict(batch=2048, total_q=2048, max_pages_per_seq=66, attn_heads=16), 4096),
+])
+def test_empty_items_do_not_count_against_a_division(what, dims, prefix):
+    """A division of the work is seen by the room for its partial results."""
+    assert _size(prefix, **dims) > 76 * PART
