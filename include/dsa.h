@@ -409,8 +409,12 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* dims, int32_t prefix_len, const v
                              float* lse, void* workspace, void* stream);
 
 /*
- * Bytes of workspace dsa_prefix_attn needs: the 256-byte error word area, then partial results where the
- * context is split over several CTAs.  0 when dims is NULL or prefix_len negative.  Host-only.
+ * Bytes of workspace that dsa_prefix_attn needs for these sizes, and for every call of the same attn_heads and kv_dtype whose
+ * batch, total_q, max_q_len, max_pages_per_seq and prefix_len are no larger: one buffer for a program's largest step
+ * serves its smaller ones.  (256 bytes of error word area, then partial results where contexts are split over several
+ * CTAs: 40 MB as a rule, up to 1.1 GB where the rows of some thousand sequences are packed behind a prefix; and 1152
+ * bytes a position of a long prefix of FP8 rows.)  256 where dsa_prefix_attn refuses the sizes as too large, 0 when dims
+ * is NULL or prefix_len negative.  Host-only.
  */
 size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len);
 

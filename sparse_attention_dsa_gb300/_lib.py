@@ -315,7 +315,13 @@ def prefix_attn_workspace_size(dims: DsaDims, prefix_len: int) -> int:
 
 
 def prefix_attn(dims, prefix_len, q, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace, stream=None):
-    """dsa_prefix_attn: dense attention of a batch whose first prefix_len positions are the same rows."""
+    """dsa_prefix_attn: dense attention of a batch whose first prefix_len positions are the same rows.  A workspace tensor
+    of fewer than prefix_attn_workspace_size() bytes is refused."""
+    if hasattr(workspace, "numel"):
+        need = prefix_attn_workspace_size(dims, prefix_len)
+        have = workspace.numel() * workspace.element_size()
+        if have < need:
+            raise DsaError(DSA_ERR_INVALID_ARG, f"workspace of {have} bytes is too small: the call needs {need}")
     _check(lib().dsa_prefix_attn(ctypes.byref(dims), int(prefix_len), _ptr(q), _ptr(kv_cache), _ptr(page_table),
                                  _ptr(seq_lens), _ptr(cu_q_lens), _ptr(out), _ptr(lse), _ptr(workspace),
                                  _stream(stream)))

@@ -783,7 +783,7 @@ size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len
     if (!dims || prefix_len < 0) return 0;
     dsa::PrefixParams p;
     if (!prefix_sizes(dims, prefix_len, &p)) return dsa::kErrorWordArea;
-    return dsa::kErrorWordArea + dsa::prefix_plan_bytes(p) + dsa::prefix_partial_bytes(p) + dsa::prefix_ahead_bytes(p);
+    return dsa::kErrorWordArea + dsa::prefix_workspace_bound(p, dims->max_pages_per_seq);
 }
 
 dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void* q, const void* kv_cache,

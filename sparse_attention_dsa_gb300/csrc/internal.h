@@ -245,6 +245,7 @@ struct PrefixParams {
     int32_t prefix_tiles;   // 128-position tiles of the prefix
     int32_t row_tiles;      // 128-row tiles that attend to the prefix
     int32_t n_items;
+    int32_t slot_by_item;   // where partial results lie (partial_slot)
     int32_t planned;  // the items' tiles are divided evenly among the CTA pairs (else: whole items in turn)
     // workspace (planned)
     int32_t* plan;  // merged: an int4 for each part; packed: behind those, an int2 for each item (see the kernels)
@@ -266,6 +267,7 @@ void plan_prefix(PrefixParams* p, int max_pages);  // from the sizes alone
 size_t prefix_plan_bytes(const PrefixParams& p);
 size_t prefix_partial_bytes(const PrefixParams& p);
 size_t prefix_ahead_bytes(const PrefixParams& p);
+size_t prefix_workspace_bound(const PrefixParams& p, int max_pages);  // the three, of any call that is no larger
 struct PrefixLaunch {
     CUtensorMap qmap;  // 3-D view [9][T*Hq][64] of q: 64-dim atoms of 64 rows, nine at a time
     // 4-D views [pages][9][64][64] of 16-bit rows (the bf16 cache, or the prefix's FP8 rows converted ahead)

@@ -147,11 +147,11 @@ __device__ __forceinline__ Item decode_item(const PrefixParams& p, int i) {
 __device__ __forceinline__ int part_begin(int k, int W, int G) { return (int)((int64_t)k * W / G); }
 __device__ __forceinline__ int part_of(int w, int W, int G) { return (int)((((int64_t)w + 1) * G - 1) / W); }
 
-// Where pair k leaves its partial result of an item.  Merged: only a pair's first and last segment can be cut,
-// and a segment with the item's first tile is the last one.  Packed: every segment has a result to combine,
-// and there are at most item + pair of them before this one.
+// Where pair k leaves its partial result of an item.  By item: there are at most item + pair of them before this one (packed:
+// every segment has a result to combine).  By pair: of merged items only a pair's first and last segment can be cut, and a
+// segment with the item's first tile is the last one.
 __device__ __forceinline__ int64_t partial_slot(const PrefixParams& p, int item, int k, bool has_first_tile) {
-    return p.packed ? item + k : 2 * k + (has_first_tile ? 1 : 0);
+    return p.slot_by_item ? item + k : 2 * k + (has_first_tile ? 1 : 0);
 }
 
 // On the line an item is kItemCost places longer than its tiles, in front of them: what its queries' load, its
@@ -481,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             const int tiles = cum[i];
             if (run > 1) mine = decode_item<SEARCH>(p, i);
             // for the combining kernel: packed, the parts of every item; merged, for each part that begins inside an
-            // item, as the second of that item's parts, the item's rows and parts
+            // item, as the second of that item's parts, the item's rows, parts (first, and count << 8) and number
             const bool here = w0 >= before && w0 < before + tiles;
             if (rank == 0 && (p.packed ? pair == 0 : here && !idle)) {
                 int k0 = 0, count = 0;
@@ -494,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     reinterpret_cast<int2*>(p.plan + 4 * kPrefixPairs)[i] = make_int2(k0, count);
                 else
                     reinterpret_cast<int4*>(p.plan)[pair] =
-                        make_int4(mine.row0, count > 1 && k0 == pair - 1 ? mine.nrows : 0, k0, count);
+                        make_int4(mine.row0, count > 1 && k0 == pair - 1 ? mine.nrows : 0, k0 | (count << 8), i);
             }
             if (here) {
                 ctl->first.index = i;
@@ -1315,7 +1315,7 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(
     grid_dependency_wait();
     const int4 d = tid > 0 && tid < kPrefixPairs ? __ldcg(reinterpret_cast<const int4*>(p.plan) + tid) : make_int4(0, 0, 0, 0);
     cut[tid] = d;
-    const int units = d.w > kManyParts ? d.y : (d.y + 3) / 4;
+    const int units = (d.z >> 8) > kManyParts ? d.y : (d.y + 3) / 4;
     int incl = units;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -1337,11 +1337,12 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_merged_kernel(
             else hi = mid;
         }
         const int4 c = cut[lo];
-        const bool many = c.w > kManyParts;
+        const bool many = (c.z >> 8) > kManyParts;
         const int tr = many ? u - first_unit[lo] : 4 * (u - first_unit[lo]) + warp;
         RowParts r = {};
-        r.k0 = c.z;
-        r.count0 = tr < c.y ? c.w : 0;
+        r.item0 = c.w;
+        r.k0 = c.z & 255;
+        r.count0 = tr < c.y ? c.z >> 8 : 0;
         r.tr0 = tr;
         float acc[16], M;
 #pragma unroll
@@ -1390,7 +1391,8 @@ void plan_prefix(PrefixParams* p, int max_pages) {
     p->tiles_per_seq = (int)(((int64_t)p->max_q_len * p->heads + 127) / 128);
     const int64_t each = (int64_t)p->batch * p->tiles_per_seq;
     const int64_t most = (int64_t)p->packed_tiles + p->batch;  // tiles of the sequences' rows, whatever their lengths
-    const int64_t alone = each < most ? each : most;
+    const int64_t items = min(each, most);
+    const int64_t alone = min(items, (int64_t)p->total_q);  // (no token's heads take more than a tile)
     if (most < each) p->tiles_per_seq = 0;  // (see first_item)
     const int64_t own_tiles = ((int64_t)max_pages * 64 - (p->prefix_len & ~63) + 127) / 128;
     const int64_t longest = p->prefix_tiles + own_tiles;
@@ -1409,23 +1411,57 @@ void plan_prefix(PrefixParams* p, int max_pages) {
     // the partial results take.  Places on the line are counted in 32 bits.  Batches of few queries but for one sequence:
     // 64 x 128 heads at 1000 positions and one of 131072, 33 queries for another: 77 us divided, 1265 whole; 64 x 16
     // behind 32768, 512 queries for one: 408 us packed, 1580 whole.
-    const bool fits = (alone + p->packed_tiles) * (3 * longest + kItemCost) <= INT32_MAX;
-    p->packed = fits && alone + p->packed_tiles <= kPackItems && packed < divided && packed < whole;
-    p->planned = p->packed || (fits && alone <= kPlanItems && divided < whole);
-    p->n_items = (int)(alone + (p->packed ? p->packed_tiles : 0));
+    const bool fits = (items + p->packed_tiles) * (3 * longest + kItemCost) <= INT32_MAX;
+    p->packed = fits && p->packed_tiles < alone && items + p->packed_tiles <= kPackItems && packed < divided && packed < whole;
+    p->planned = p->packed || (fits && items <= kPlanItems && divided < whole);
+    p->n_items = (int)(items + (p->packed ? p->packed_tiles : 0));
+    p->slot_by_item = p->packed || (p->heads < 128 && p->n_items < kPrefixPairs);
     p->row_tiles = (int)(p->packed ? p->packed_tiles : alone);
     p->convert_ahead = ahead(p->row_tiles);
 }
 
+namespace {
+size_t plan_bytes(int64_t items) { return ((size_t)(2 * items + 4 * kPrefixPairs) * sizeof(int32_t) + 255) / 256 * 256; }
+size_t ahead_bytes(int prefix_len) { return ((size_t)prefix_len + 63) / 64 * 64 * 1152; }
+}  // namespace
+
+size_t prefix_plan_bytes(const PrefixParams& p) { return p.planned ? plan_bytes(p.n_items) : 0; }
 size_t prefix_partial_bytes(const PrefixParams& p) {
     if (!p.planned) return 0;
-    const int64_t slots = p.packed ? p.n_items + kPrefixPairs : 2 * kPrefixPairs;
-    return (size_t)slots * kPartialFloats * sizeof(float);
+    return (size_t)(p.slot_by_item ? p.n_items + kPrefixPairs : 2 * kPrefixPairs) * kPartialFloats * sizeof(float);
 }
-size_t prefix_ahead_bytes(const PrefixParams& p) {
-    return p.convert_ahead ? (size_t)((p.prefix_len + 63) / 64) * 64 * 1152 : 0;
+size_t prefix_ahead_bytes(const PrefixParams& p) { return p.convert_ahead ? ahead_bytes(p.prefix_len) : 0; }
+
+// Which way is taken jumps back and forth with the sizes (8 sequences of 2048 positions are divided, 38 are taken whole,
+// without any partial result), and a program keeps one workspace for its largest step.  So what is asked for is the
+// most that any call takes with no larger batch, total_q, max_q_len, prefix_len and max_pages: from the rules above,
+//   divided: one item is the likeliest case (it leaves 75 pairs idle), and no way of splitting the longest context
+//     into prefix and own positions has more than tiles + 1 tiles;
+//   packed: with 128 heads there are as many packed tiles as tiles of sequences, so never; else, y being the prefix
+//     tiles' cost, packed_tiles (y + 4) + alone < alone y and alone <= packed_tiles + batch leave fewer than
+//     batch (y - 1) / 5 packed tiles;
+//   converted ahead: for the longest prefix and the most row tiles, if at all.
+size_t prefix_workspace_bound(const PrefixParams& p, int max_pages) {
+    const int64_t each = (int64_t)p.batch * (((int64_t)p.max_q_len * p.heads + 127) / 128);
+    const int64_t items = min(each, (int64_t)p.packed_tiles + p.batch);
+    const int64_t tiles = ((int64_t)max_pages + 1) / 2, weight = p.kv_fp8 ? 2 : 1;
+    const int64_t longest = weight * (tiles + (p.prefix_len > 0 ? 1 : 0)) + kItemCost;
+    int64_t most_items = 0, slots = 0;
+    if (tiles > kWholeTiles || (kPrefixPairs - 1) * longest > kPrefixPairs * kDivideCost) {
+        most_items = min(items, (int64_t)kPlanItems);
+        slots = p.heads == 128 ? 2 * kPrefixPairs : min(items + kPrefixPairs, (int64_t)2 * kPrefixPairs);
+    }
+    const int64_t y = weight * p.prefix_tiles;
+    const int64_t packed = min((int64_t)p.packed_tiles, (p.batch * (y - 1) - 1) / 5);
+    if (p.heads < 128 && y > 1 && packed > 0) {
+        const int64_t n = min(packed + min(each, packed + p.batch), (int64_t)kPackItems);
+        most_items = max(most_items, n);
+        slots = max(slots, n + kPrefixPairs);
+    }
+    const bool ahead = p.kv_fp8 && (max(items, (int64_t)p.packed_tiles) - 2) * p.prefix_tiles > kAheadGain;
+    return (slots > 0 ? plan_bytes(most_items) : 0) + (size_t)slots * kPartialFloats * sizeof(float) +
+           (ahead ? ahead_bytes(p.prefix_len) : 0);
 }
-size_t prefix_plan_bytes(const PrefixParams& p) { return ((size_t)(2 * p.n_items + 4 * kPrefixPairs) * sizeof(int32_t) + 255) / 256 * 256; }
 
 cudaError_t launch_prefix(const PrefixLaunch& L, cudaStream_t stream) {
     const PrefixParams& p = L.params;

@@ -73,3 +73,24 @@ def test_inconsistent_sequences_beside_a_chunk(heads, wide):
     assert c.error() == dsa.DSA_DEVERR_SEQ
     assert bool((c.out[0] == 7).all()) and bool((c.lse[0] == 7).all())
     ref.check(c.out, c.lse, False, tokens=slice(1, 48))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,prefix", [(16, 0), (16, 2500), (128, 0), (128, 1090)])
+def test_one_workspace_for_a_batch_that_shrinks(heads, prefix, fp8):
+    """A workspace of the largest step's size, and nothing written behind it by that step or the smaller ones."""
+    steps = [([prefix + 1000 + 13 * (i % 40) for i in range(size)], [1] * size) for size in (128, 76, 40, 9, 2, 1)]
+    steps.append(([prefix + 700, prefix + 500], [60, 3]))
+    calls = [Call(L, n, prefix, heads, fp8=fp8, seed=34) for L, n in steps]
+    for c in calls:  # as wide a page table for every step, as a program has
+        c.b.pt = torch.nn.functional.pad(c.b.pt, (0, prefix // 64 + 33 - c.b.pt.shape[1]), value=-1)
+        c.dims.max_pages_per_seq = c.b.pt.shape[1]
+    d = calls[0].dims
+    largest = dsa.DsaDims(**{**{n: getattr(d, n) for n, _ in d._fields_}, "max_q_len": 60})
+    size = dsa.prefix_attn_workspace_size(largest, prefix)
+    room = torch.full((size + (64 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    room[:256] = 0
+    for c in calls:
+        c.workspace = room[:size]
+        c.run().check()
+    assert bool((room[size:] == 0xA5).all())
