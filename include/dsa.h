@@ -383,7 +383,8 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  *     z_s = softmax_scale * q[t,h,:] . kv[s,:]  for every visible position s = 0..p_t,
  *     out[t,h,:] = sum_s softmax(z)_s * kv[s, 0:v_dim],   lse[t,h] = log sum_s exp(z_s)
  * where positions below prefix_len are the same rows for every sequence: they are read through the page
- * table of sequence 0, once for all the sequences that share a matrix tile.  Every sequence's table still
+ * table of the first sequence whose context covers them (L_b >= prefix_len; a slot of a padded batch with no
+ * context needs no pages), once for all the sequences that share a matrix tile.  Every sequence's table still
  * maps all its positions (as a page pool with shared prefix pages leaves it); where prefix_len is not a
  * multiple of 64, the page in which it ends may be each sequence's own copy.  prefix_len = 0 is plain
  * attention of each sequence over its own context.

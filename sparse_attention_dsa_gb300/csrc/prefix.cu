@@ -85,6 +85,21 @@ __device__ __forceinline__ bool sequence(const PrefixParams& p, int b, int* c0, 
     return (int64_t)*n <= (int64_t)*L - p.prefix_len && (int64_t)*L <= (int64_t)p.max_pages * 64;
 }
 
+// The sequence through whose page table the prefix is read: the first whose context covers it (0 if there is none: no
+// sequence has a query behind the prefix then).  Called by a whole warp; mine: seq_lens[lane], -1 where there is none.
+__device__ __forceinline__ int prefix_source(const PrefixParams& p, int mine, int lane) {
+    for (int j0 = 0;;) {
+        const uint32_t hit = __ballot_sync(kAllLanes, mine >= p.prefix_len && (int64_t)mine <= (int64_t)p.max_pages * 64);
+        if (hit) return j0 + __ffs(hit) - 1;
+        j0 += 32;
+        if (j0 >= p.batch) return 0;
+        mine = j0 + lane < p.batch ? ld_input(p.seq_lens + j0 + lane) : -1;
+    }
+}
+__device__ __forceinline__ int first_length(const PrefixParams& p, int lane) {
+    return lane < p.batch ? ld_input(p.seq_lens + lane) : -1;
+}
+
 // Number of sequence b's first item among the sequences' items, c0 its first query.  Where one sequence has many queries
 // and most have few, tiles_per_seq numbers a sequence would be empty ones nearly all (tiles_per_seq is 0 then): b +
 // floor(c0 * heads / 128) is never less than the number of tiles in front of it.
@@ -232,6 +247,7 @@ struct Ctrl {
     uint64_t q_raw, q_conv, k_raw[3], k_conv[3], v_raw[2], v_conv[2];
     uint32_t tmem_base;
     int32_t failed;
+    int32_t prefix_source;
     int32_t first_place;  // this pair's first item (in `first`) and its place in it
     Segment first;
     int32_t scan[kMaxWarps];
@@ -286,13 +302,14 @@ struct Tile {
     bool edge;
     bool copied;  // FP8: its rows have been converted ahead
 };
-__device__ __forceinline__ Tile tile_of(const PrefixParams& p, const Item& it, int u) {
+// shared: the page-table row of the prefix.
+__device__ __forceinline__ Tile tile_of(const PrefixParams& p, const int32_t* shared, const Item& it, int u) {
     Tile t;
     if (u < it.tiles_a) {
         t.base = 128 * u;
         t.lo = 0;
         t.hi = p.prefix_len;
-        t.pages = p.page_table;
+        t.pages = shared;
         t.edge = t.base + 128 > t.hi;
         t.copied = p.ahead != nullptr;
     } else {
@@ -446,6 +463,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         if (tid == 0 && (ld_input(p.cu_q_lens) != 0 || ld_input(p.cu_q_lens + p.batch) != p.total_q))
             raise_error(p.err, DSA_DEVERR_SEQ);
     }
+    constexpr int kSourceWarp = 3;
+    const int first_L = warp == kSourceWarp ? first_length(p, lane) : 0;  // looked at behind the plan's own loads
     Walk start;
     bool idle = false;
     if (p.planned) {
@@ -513,6 +532,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         }
         start.left = pairs;
     }
+    if (warp == kSourceWarp) {
+        const int b = prefix_source(p, first_L, lane);
+        if (lane == 0) ctl->prefix_source = b;
+    }
     tc_fence_before();
     __syncthreads();
     start.item = ctl->first.index;
@@ -521,6 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
     cluster_wait();  // the peer's barriers exist before anything arrives on them
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+    const int32_t* shared = p.page_table + (int64_t)ctl->prefix_source * p.max_pages;
     auto leader = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(kAllLanes, mbar_wait(bar, parity, p.err, p.wait_ns)) != 0;
@@ -535,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         uint32_t seg = 0, kphase = 1, vphase = 1;  // a tile takes every slot of both rings once
         const uint32_t q_full = leader(&ctl->q_full), k_full = leader(&ctl->k_full[0]), v_full = leader(&ctl->v_full[0]);
         while (ok && next_segment<SEARCH>(p, w, s)) {
-            Tile t = tile_of(p, s.it, s.u0), tv = t;
+            Tile t = tile_of(p, shared, s.it, s.u0), tv = t;
             int page0 = page_of(t, 0), page1 = page_of(t, 1), vpage0 = 0, vpage1 = 0;
             if (seg > 0 && !(ok = wait(&ctl->q_empty, (seg - 1) & 1u))) break;
             if (elect_one_sync()) {
@@ -552,12 +576,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 Tile tn = t;
                 int next0 = kNoPage, next1 = kNoPage, later = kNoPage;
                 if (u + 1 < s.u1) {
-                    tn = tile_of(p, s.it, u + 1);
+                    tn = tile_of(p, shared, s.it, u + 1);
                     next0 = page_of(tn, 0);
                     next1 = page_of(tn, 1);
                 }
                 if (u + 2 < s.u1 && (u + 2 >= s.it.tiles_a || p.row_tiles <= 2)) {
-                    const Tile t2 = tile_of(p, s.it, u + 2);
+                    const Tile t2 = tile_of(p, shared, s.it, u + 2);
                     if (!t2.copied) later = page_of(t2, rank);
                 }
                 if (u < s.u1) {
@@ -673,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             for (int u = s.u0; ok && u < s.u1; ++u, ++tile) {
                 const uint32_t buf = tile & 1u;
                 const bool last = u == s.u1 - 1;
-                const Tile cur = tile_of(p, s.it, u);
+                const Tile cur = tile_of(p, shared, s.it, u);
                 const bool cur_raw = KVFP8 && !cur.copied;
                 if (!(ok = wait(&ctl->s_empty[buf], ((tile >> 1) & 1u) ^ 1u))) break;
 #pragma unroll
@@ -731,13 +755,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             return true;
         };
         bool have = next_segment<SEARCH>(p, w, s);
-        int first_pg = have ? page_of(tile_of(p, s.it, s.u0), half) : kNoPage;
+        int first_pg = have ? page_of(tile_of(p, shared, s.it, s.u0), half) : kNoPage;
         while (have) {
             const int tr = 64 * rank + r;  // row of the tile
             // positions this row sees: below `limit`
             const int limit = s.it.b < 0 ? p.prefix_len : s.it.pos0 + (s.it.lrow0 + tr) / p.heads + 1;
             float m_used = -INFINITY, l_sum = 0.f;
-            Tile t = tile_of(p, s.it, s.u0);
+            Tile t = tile_of(p, shared, s.it, s.u0);
             int pg = first_pg;
 #pragma unroll 1
             for (int u = s.u0; u < s.u1; ++u, ++tile) {
@@ -745,7 +769,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 const Tile cur = t;
                 const bool bad_page = pg < 0 || pg >= p.num_pages;
                 if (u + 1 < s.u1) {
-                    t = tile_of(p, s.it, u + 1);
+                    t = tile_of(p, shared, s.it, u + 1);
                     pg = page_of(t, half);
                 }
                 if (!(ok = wait(&ctl->s_full[buf], (tile >> 1) & 1u))) break;
@@ -838,7 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             // the next segment, looked up while this one's last products run
             Segment ahead = s;
             have = next_segment<SEARCH>(p, w, ahead);
-            if (have) first_pg = page_of(tile_of(p, ahead.it, ahead.u0), half);
+            if (have) first_pg = page_of(tile_of(p, shared, ahead.it, ahead.u0), half);
             // ---- the segment's result: O / l and lse, or O, m and l for the combining kernel ----
             if (!(ok = wait(&ctl->pv_done, (tile - 1) & 1u))) break;
             tc_fence_after();
@@ -938,7 +962,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         static_assert(kVSlots == 2, "one slot for each page of a tile");
         while (ok && next_segment<SEARCH>(p, w, s)) {
             for (int u = s.u0; ok && u < s.u1; ++u) {
-                const Tile t = tile_of(p, s.it, u);
+                const Tile t = tile_of(p, shared, s.it, u);
                 if (!t.edge) continue;
                 // A row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's.  All is
                 // loaded and looked at before the slots are waited for: only the stores are on the way to the products.
@@ -1023,7 +1047,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             while (ok && next_segment<SEARCH>(p, w, s)) {
                 // the first tile that is to be converted, and its scales, while q is on its way
                 int u = p.ahead != nullptr ? max(s.u0, s.it.tiles_a) : s.u0;
-                Tile t = tile_of(p, s.it, min(u, s.u1 - 1));
+                Tile t = tile_of(p, shared, s.it, min(u, s.u1 - 1));
                 float next[4][4];
                 if (u < s.u1) load_scales(t, next);
                 if (!(ok = wait(&ctl->q_raw, seg++ & 1u))) break;
@@ -1043,7 +1067,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sc[j][i] = f2_to_h2(next[j][i] * kScaleGain, next[j][i] * kScaleGain);
                     if (u + 1 < s.u1) {
-                        t = tile_of(p, s.it, u + 1);
+                        t = tile_of(p, shared, s.it, u + 1);
                         load_scales(t, next);
                     }
 #pragma unroll 1
@@ -1124,7 +1148,10 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
     grid_dependency_wait();
     allow_dependent_launch();
     uint4* dst = reinterpret_cast<uint4*>(p.ahead + (int64_t)pos * 1152);
-    const int pg = pos < p.prefix_len ? ld_input(p.page_table + (pos >> 6)) : -1;
+    // sequence 0's entry is the one as a rule: loaded beside the lengths that say so
+    int pg = pos < p.prefix_len ? ld_input(p.page_table + (pos >> 6)) : -1;
+    const int64_t b = prefix_source(p, first_length(p, lane), lane);
+    if (b > 0 && pos < p.prefix_len) pg = ld_input(p.page_table + b * p.max_pages + (pos >> 6));
     const bool in = pg >= 0 && pg < p.num_pages;
     if (!in && pos < p.prefix_len && lane == 0) raise_error(p.err, DSA_DEVERR_PAGE);
     uint4 code = make_uint4(0, 0, 0, 0), rot = code;
@@ -1266,7 +1293,7 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(
     const bool exists = row < p.total_q * p.heads;
     grid_dependency_wait();
     const int2* parts = reinterpret_cast<const int2*>(p.plan + 4 * kPrefixPairs);
-    const int2 shared = exists ? __ldcg(parts + row / 128) : make_int2(0, 0);
+    const int2 packed = exists ? __ldcg(parts + row / 128) : make_int2(0, 0);
     const int t = exists ? row / p.heads : -1;
     int b = -1, c0 = 0, n = 0, L = 0;
     for (int j0 = 0; j0 < p.batch && b < 0; j0 += 128) {  // four loads on their way
@@ -1296,8 +1323,8 @@ __global__ void __launch_bounds__(kCombineThreads) prefix_combine_packed_kernel(
         r.k0 = own.x;
         r.count0 = own.y;
         r.tr0 = local & 127;
-        r.k1 = shared.x;
-        r.count1 = shared.y;
+        r.k1 = packed.x;
+        r.count1 = packed.y;
         r.tr1 = row & 127;
         Ls = add_parts(p, r, warp % OF, OF, acc, &M, lane);
     }

@@ -94,3 +94,23 @@ def test_one_workspace_for_a_batch_that_shrinks(heads, prefix, fp8):
         c.workspace = room[:size]
         c.run().check()
     assert bool((room[size:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,slots,others", [(16, 1, 5), (16, 40, 30), (128, 2, 20), (128, 1, 2)])
+def test_padding_slots_in_front_need_no_pages(heads, slots, others, fp8, wide):
+    """Slots without a context, the first of the batch among them, and one whose context ends inside the prefix: their
+    page tables map nothing of the prefix."""
+    prefix = 1090
+    L, n = [prefix + 40 + 9 * i for i in range(others)], [1 + i % 2 for i in range(others)]
+    c = Call([0] * slots + [70] + L, [0] * (slots + 1) + n, prefix, heads, fp8=fp8, seed=35, wide=wide)
+    c.b.pt[:slots] = -1
+    c.b.pt[slots, 2:] = -1
+    c.run()
+    assert c.error() == 0
+    want = Call(L, n, prefix, heads, fp8=fp8, seed=35)  # the same batch without them, over the same cache
+    pt = c.b.pt[slots + 1:]
+    want.b.pt, want.b.pt_host = pt.contiguous(), pt.cpu()
+    want.cache, want.q = c.cache, c.q
+    Attention(want.b, want.q, want.cache, fp8).check(c.out, c.lse, fp8)
