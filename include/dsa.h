@@ -75,7 +75,7 @@ typedef enum {
  *   bytes   0..511  E4M3 codes of dims 0..511 (the latent part, also V), in 4 tiles of 128;
  *   bytes 512..527  4 fp32 scales, tile i covering dims 128*i .. 128*i+127;
  *   bytes 528..655  dims 512..575 (the rotary part) as bf16, unquantised (576 is not a multiple of 128).
- * Element d < 512 of the row is e4m3(code[d]) * scale[d / 128]; the kernels dequantise to bf16.
+ * Element d < 512 of the row is e4m3(code[d]) * scale[d / 128]; the kernels dequantise to bf16 (dsa_prefix_attn: to f16).
  */
 #define DSA_KV_FP8_ROW_BYTES 656
 
@@ -86,6 +86,7 @@ typedef enum {
 #define DSA_DEVERR_TIMEOUT 0x8 /* a pipeline wait exceeded its limit (one second unless
                                   dsa_set_wait_limit_ns() says otherwise) */
 #define DSA_DEVERR_ROPE 0x10   /* a position beyond the rotation table was needed */
+#define DSA_DEVERR_RANGE 0x20  /* a finite value beyond the range of dsa_prefix_attn's products with FP8 rows */
 
 typedef struct {
     int32_t batch;             /* B >= 1 sequences */
@@ -400,9 +401,10 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  * A sequence with n_b > L_b - prefix_len, n_b > max_q_len or a context beyond its page table or of 2^31 - 255
  * positions or more (DSA_DEVERR_SEQ) and a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left
  * as they were; rows of a page that is out of range (DSA_DEVERR_PAGE) are skipped.
- * FP8 rows are multiplied as f16, with q as f16: an element code * scale, or a rotary value, of more than
- * 16376, a scale of 64 or more, or a q of more than 262016 becomes infinite (and its row NaN); elements
- * below 2^-16 and values of q below 2^-12 lose relative precision.
+ * FP8 rows are multiplied as f16, with q as f16.  A visible element code * scale, or a rotary value, of a magnitude of more
+ * than 16376, a scale of 64 or more, and a q of more than 262016 are beyond that: reported (DSA_DEVERR_RANGE), and the rows
+ * that see them are NaN (dsa_sparse_attn, which multiplies as bf16, takes them).  Elements below 2^-16 and values of q
+ * below 2^-12 lose relative precision.
  * Supported: D = 576, Dv = 512, Hq <= 128.
  */
 dsa_status_t dsa_prefix_attn(const dsa_dims_t* dims, int32_t prefix_len, const void* q, const void* kv_cache,

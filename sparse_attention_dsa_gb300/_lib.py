@@ -18,6 +18,7 @@ DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_DEVICE, 
 DSA_BF16, DSA_FP8_E4M3, DSA_MXFP8_E4M3 = 0, 1, 2
 DSA_KV_FP8_ROW_BYTES = 656
 DSA_DEVERR_PAGE, DSA_DEVERR_SEQ, DSA_DEVERR_INDEX, DSA_DEVERR_TIMEOUT, DSA_DEVERR_ROPE = 0x1, 0x2, 0x4, 0x8, 0x10
+DSA_DEVERR_RANGE = 0x20
 DSA_ROPE_HALVES, DSA_ROPE_INTERLEAVED = 0, 1
 
 EXPORTED = (

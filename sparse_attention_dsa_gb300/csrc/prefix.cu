@@ -369,6 +369,42 @@ __device__ __forceinline__ uint4 bf8_to_h8(uint4 v, float gain) {
     auto pair = [&](uint32_t w) { return f2_to_h2(__uint_as_float(w << 16) * gain, __uint_as_float(w & 0xFFFF0000u) * gain); };
     return make_uint4(pair(v.x), pair(v.y), pair(v.z), pair(v.w));
 }
+// What lies beyond f16's range must not pass for an infinity: q of the other sign would make a score of -inf of it, and the
+// position would drop out of the result.  A row of K or q with such an element gets a NaN, so that every row of the result
+// that sees it does, and is reported.
+// Nonzero in the sign bits' places where a f16 value of the eight has an exponent of all ones (it carries into them).
+__device__ __forceinline__ uint32_t not_finite(const uint4& h) {
+    const uint32_t c = 0x7C007C00u, one = 0x04000400u;
+    return (((h.x & c) + one) | ((h.y & c) + one) | ((h.z & c) + one) | ((h.w & c) + one)) & 0x80008000u;
+}
+// Whether one of eight bf16 values is finite, and infinite as f16 times gain.
+__device__ __forceinline__ bool values_over(const uint4& v, float gain) {
+    const uint4 h = bf8_to_h8(v, gain);
+    if (not_finite(h) == 0) return false;
+    const uint32_t from[4] = {v.x, v.y, v.z, v.w}, to[4] = {h.x, h.y, h.z, h.w};
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int at = 16 * (j & 1);
+        found |= ((to[j >> 1] >> at) & 0x7FFFu) == 0x7C00u && ((from[j >> 1] >> at) & 0x7F80u) != 0x7F80u;
+    }
+    return found;
+}
+// Whether one of sixteen codes times their scale is infinite as f16, or the scale itself (64 and more); neither is a NaN.
+// No element of a smaller scale than kLargestScale is: 65520 / (448 * kF16Gain) = 36.56.
+constexpr float kLargestScale = 36.5f;
+__device__ __forceinline__ bool codes_over(const uint4& code, float scale) {
+    if (!(fabsf(scale) > kLargestScale)) return false;
+    const uint32_t scale2 = f2_to_h2(scale * kScaleGain, scale * kScaleGain);
+    if ((scale2 & 0x7FFFu) == 0x7C00u) return true;
+    const uint4 lo = codes_to_h8(code.x, code.y, scale2), hi = codes_to_h8(code.z, code.w, scale2);
+    const uint32_t to[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) found |= ((to[j >> 1] >> (16 * (j & 1))) & 0x7FFFu) == 0x7C00u;
+    return found;
+}
+constexpr uint32_t kNaN2 = 0x7E007E00u;  // f16 twice
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -1051,10 +1087,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 float next[4][4];
                 if (u < s.u1) load_scales(t, next);
                 if (!(ok = wait(&ctl->q_raw, seg++ & 1u))) break;
+                uint32_t odd = 0;
 #pragma unroll 3
                 for (int i = 0; i < kQAtoms * 64 * 8 / (64 * kFillWarps); ++i) {  // 16-byte pieces, 256 lanes
                     const uint32_t at = smem_u32(q_s) + 16 * (32 * cw + lane + 256 * i);
-                    st_shared_v4(at, bf8_to_h8(ld_shared_v4(at), 1.f / kF16Gain));
+                    const uint4 h = bf8_to_h8(ld_shared_v4(at), 1.f / kF16Gain);
+                    odd |= not_finite(h);
+                    st_shared_v4(at, h);
+                }
+                if (odd) {  // hardly ever: infinities and NaN, or values beyond the range
+#pragma unroll 1
+                    for (int i = 0; i < kQAtoms * 64 * 8 / (64 * kFillWarps); ++i) {
+                        const int n = 32 * cw + lane + 256 * i, row = (n >> 3) & 63, piece = 8 * (n >> 9) + ((n ^ row) & 7);
+                        const int tr = 64 * rank + row;
+                        if (tr >= s.it.nrows) continue;
+                        const uint16_t* src = p.q + ((int64_t)s.it.row0 + tr) * 576 + 8 * piece;
+                        if (!values_over(ld_input(reinterpret_cast<const uint4*>(src)), 1.f / kF16Gain)) continue;
+                        st_shared_v4(smem_u32(q_s) + 16 * n, make_uint4(kNaN2, kNaN2, kNaN2, kNaN2));
+                        // (items of the prefix hold tokens of no sequence, too; the others every row of one)
+                        if (s.it.b >= 0) raise_error(p.err, DSA_DEVERR_RANGE);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1062,10 +1114,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 for (; ok && u < s.u1; ++u) {
                     const Tile cur = t;
                     uint32_t sc[4][4];  // f16 pairs
+                    float largest = 0.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sc[j][i] = f2_to_h2(next[j][i] * kScaleGain, next[j][i] * kScaleGain);
+                        for (int i = 0; i < 4; ++i) {
+                            sc[j][i] = f2_to_h2(next[j][i] * kScaleGain, next[j][i] * kScaleGain);
+                            largest = fmaxf(largest, fabsf(next[j][i]));
+                        }
                     if (u + 1 < s.u1) {
                         t = tile_of(p, shared, s.it, u + 1);
                         load_scales(t, next);
@@ -1105,10 +1161,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                     }
                     if (ok && !v_side) {
                         if (!(ok = wait(&raw[2], phase))) break;
+                        uint32_t odd = largest > kLargestScale ? 1u : 0u;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t at = ring + 8 * kAtom + 16 * i * 128 + own16;
-                            st_shared_v4(at, bf8_to_h8(ld_shared_v4(at), kF16Gain));
+                            const uint4 h = bf8_to_h8(ld_shared_v4(at), kF16Gain);
+                            odd |= not_finite(h);
+                            st_shared_v4(at, h);
+                        }
+                        if (odd) {  // hardly ever: this lane's pieces of its rows that are beyond the range, if any (the NaN
+                                    // goes to the rotary part, which is handed over last)
+                            const int pg = page_of(cur, rank);
+#pragma unroll 1
+                            for (int i = 0; i < 4; ++i) {
+                                const int row = row0 + 16 * i, pos = cur.base + 64 * rank + row;
+                                if (pg < 0 || pg >= p.num_pages || pos < cur.lo || pos >= cur.hi) continue;
+                                const uint8_t* src = p.kv_cache + ((int64_t)pg * 64 + row) * kKvFp8RowBytes;
+                                bool over = values_over(ld_input(reinterpret_cast<const uint4*>(src + kKvFp8RopeOff) + c), kF16Gain);
+#pragma unroll 1
+                                for (int q = 0; q < 4; ++q)
+                                    over |= codes_over(ld_input(reinterpret_cast<const uint4*>(src) + 8 * q + c),
+                                                       ld_input(reinterpret_cast<const float*>(src + kKvFp8ScaleOff) + q));
+                                if (!over) continue;
+                                st_shared_v4(ring + 8 * kAtom + 16 * i * 128 + own16, make_uint4(kNaN2, kNaN2, kNaN2, kNaN2));
+                                raise_error(p.err, DSA_DEVERR_RANGE);
+                            }
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -1165,7 +1242,11 @@ __global__ void __launch_bounds__(32 * kAheadWarps) prefix_ahead_kernel(const Pr
     const uint32_t scale2 = f2_to_h2(scale * kScaleGain, scale * kScaleGain);
     dst[2 * lane] = codes_to_h8(code.x, code.y, scale2);
     dst[2 * lane + 1] = codes_to_h8(code.z, code.w, scale2);
-    if (lane < 8) dst[64 + lane] = bf8_to_h8(rot, kF16Gain);
+    uint4 turned = bf8_to_h8(rot, kF16Gain);
+    const bool over = codes_over(code, scale) || values_over(rot, kF16Gain);
+    if (over) raise_error(p.err, DSA_DEVERR_RANGE);
+    if (__any_sync(kAllLanes, over)) turned = make_uint4(kNaN2, kNaN2, kNaN2, kNaN2);
+    if (lane < 8) dst[64 + lane] = turned;
 }
 
 // ---------------------------------------------------------------------------------------------------------
