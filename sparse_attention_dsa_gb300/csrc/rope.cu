@@ -29,18 +29,10 @@ namespace {
 
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
-// Two fp32 products, sums or both in one instruction (rounded like the single ones).
+// Two fp32 products, or products and sums, in one instruction (rounded like the single ones).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
     asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
-        "mov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
         "mov.b64 {%0, %1}, z;\n\t}"
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
@@ -133,56 +125,82 @@ __device__ __forceinline__ int mx_exponent(float amax) {
 }
 
 // A 64-dim rotary block is 8 pieces of 8 values.  Value i of piece j becomes x_i c_i + o_i s_i, o_i its partner in the
-// pair and s_i the sine with the sign of its side: the same c and s for every row of a token, so they are loaded once.
-struct Turn {
-    float c[8], s[8];
+// pair and s_i the sine with the sign of its side.
+// The cosines and signed sines of values 4 h .. 4 h + 3 of a piece, from the position's table row.
+struct TableTurn {
+    const float* row;
+    int j;
+    __device__ __forceinline__ void get(int h, bool interleaved, float (&c)[4], float (&s)[4]) const {
+        if (interleaved) {  // pairs (2i, 2i + 1) of the piece, angles 4j ..
+            const float2 a = __ldg(reinterpret_cast<const float2*>(row) + 2 * j + h);
+            const float2 b = __ldg(reinterpret_cast<const float2*>(row) + 16 + 2 * j + h);
+            c[0] = c[1] = a.x;
+            c[2] = c[3] = a.y;
+            s[0] = -b.x;
+            s[1] = b.x;
+            s[2] = -b.y;
+            s[3] = b.y;
+        } else {  // partner in piece j ^ 4, angles 8 (j & 3) ..
+            const float4 a = __ldg(reinterpret_cast<const float4*>(row) + 2 * (j & 3) + h);
+            const float4 b = __ldg(reinterpret_cast<const float4*>(row) + 8 + 2 * (j & 3) + h);
+            const bool first = j < 4;
+            c[0] = a.x;
+            c[1] = a.y;
+            c[2] = a.z;
+            c[3] = a.w;
+            s[0] = first ? -b.x : b.x;
+            s[1] = first ? -b.y : b.y;
+            s[2] = first ? -b.z : b.z;
+            s[3] = first ? -b.w : b.w;
+        }
+    }
 };
-__device__ __forceinline__ void load_turn(Turn& t, const float* row, int j, bool interleaved) {
-    const float4* t4 = reinterpret_cast<const float4*>(row);
-    if (interleaved) {  // pairs (2i, 2i + 1) of the piece, angles 4j ..
-        const float4 c = __ldg(t4 + j), s = __ldg(t4 + 8 + j);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+// The same held in registers, for all the rows of a token.
+struct Turn {
+    float c[2][4], s[2][4];
+    __device__ __forceinline__ void load(const TableTurn& t, bool interleaved) {
+        t.get(0, interleaved, c[0], s[0]);
+        t.get(1, interleaved, c[1], s[1]);
+    }
+    __device__ __forceinline__ void get(int h, bool, float (&cc)[4], float (&ss)[4]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            t.c[2 * i] = t.c[2 * i + 1] = cc[i];
-            t.s[2 * i] = -ss[i];
-            t.s[2 * i + 1] = ss[i];
-        }
-    } else {  // partner in piece j ^ 4, angles 8 (j & 3) ..
-        const int q = 2 * (j & 3);
-        const float4 c0 = __ldg(t4 + q), c1 = __ldg(t4 + q + 1), s0 = __ldg(t4 + 8 + q), s1 = __ldg(t4 + 9 + q);
-        const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            t.c[i] = cc[i];
-            t.s[i] = j < 4 ? -ss[i] : ss[i];
+            cc[i] = c[h][i];
+            ss[i] = s[h][i];
         }
     }
-}
-// x: piece `own`, rotated in place where `on`.  `partner`: the lane that holds piece j ^ 4 (halves; every lane of the
-// warp calls).
+};
+// x: piece `own`, rotated in place where `on`.  `partner`: the lane that holds piece j ^ 4 (any lane where there is none);
+// `halves`: some lane of the warp pairs by halves (the same in every lane; every lane calls).  The sums are single
+// operations: a packed product and a packed sum were compiled to one fused operation, which does not round the product.
+template <typename T>
 __device__ __forceinline__ void rotate_piece(float (&x)[8], const uint4& own, bool on, int partner, bool interleaved,
-                                             const Turn& t) {
-    float o[8];
-    if (interleaved) {
+                                             bool halves, const T& turn) {
+    uint32_t w[4] = {own.x, own.y, own.z, own.w};
+    if (halves) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
-    } else {
-        uint4 v;
-        v.x = __shfl_sync(kAll, own.x, partner);
-        v.y = __shfl_sync(kAll, own.y, partner);
-        v.z = __shfl_sync(kAll, own.z, partner);
-        v.w = __shfl_sync(kAll, own.w, partner);
-        unpack8(v, o);
+        for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(kAll, w[i], partner);
     }
     if (!on) return;
+    auto half = [&](int h, const float2& o0, const float2& o1) {
+        float c[4], s[4];
+        turn.get(h, interleaved, c, s);
+        const float2 a0 = mul2(make_float2(x[4 * h], x[4 * h + 1]), make_float2(c[0], c[1]));
+        const float2 a1 = mul2(make_float2(x[4 * h + 2], x[4 * h + 3]), make_float2(c[2], c[3]));
+        const float2 b0 = mul2(o0, make_float2(s[0], s[1])), b1 = mul2(o1, make_float2(s[2], s[3]));
+        x[4 * h] = __fadd_rn(a0.x, b0.x);
+        x[4 * h + 1] = __fadd_rn(a0.y, b0.y);
+        x[4 * h + 2] = __fadd_rn(a1.x, b1.x);
+        x[4 * h + 3] = __fadd_rn(a1.y, b1.y);
+    };
+    auto pair = [](uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)); };
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float2 y = add2(mul2(make_float2(x[i], x[i + 1]), make_float2(t.c[i], t.c[i + 1])),
-                              mul2(make_float2(o[i], o[i + 1]), make_float2(t.s[i], t.s[i + 1])));
-        x[i] = y.x;
-        x[i + 1] = y.y;
+        for (int h = 0; h < 2; ++h)
+            half(h, make_float2(x[4 * h + 1], x[4 * h]), make_float2(x[4 * h + 3], x[4 * h + 2]));
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) half(h, pair(w[2 * h]), pair(w[2 * h + 1]));
     }
 }
 
@@ -219,44 +237,6 @@ __device__ __forceinline__ bool locate(const RopeParams& r, int t, int lane, int
     *b_out = b;
     *pos_out = pos;
     return true;
-}
-
-// Rotates piece j (0..7) of a 64-dim rotary block in place.  Every lane of the warp calls it; `partner` is
-// the lane that holds piece j ^ 4 of the same block (any lane when !on).
-__device__ __forceinline__ void turn_piece(float (&x)[8], const uint4& own, int j, bool on, int partner,
-                                             bool interleaved, const float* row) {
-    uint4 o;
-    o.x = __shfl_sync(kAll, own.x, partner);
-    o.y = __shfl_sync(kAll, own.y, partner);
-    o.z = __shfl_sync(kAll, own.z, partner);
-    o.w = __shfl_sync(kAll, own.w, partner);
-    if (!on) return;
-    const float4* t4 = reinterpret_cast<const float4*>(row);
-    if (interleaved) {
-        const float4 c = __ldg(t4 + j), s = __ldg(t4 + 8 + j);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, cc[i]), __fmul_rn(b, ss[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(a, ss[i]), __fmul_rn(b, cc[i]));
-        }
-    } else {
-        float y[8];
-        unpack8(o, y);
-        const int q = 2 * (j & 3);
-        const float4 c0 = __ldg(t4 + q), c1 = __ldg(t4 + q + 1), s0 = __ldg(t4 + 8 + q), s1 = __ldg(t4 + 9 + q);
-        const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // first half: x1 cos - x2 sin; second half: x1 sin + x2 cos
-            if (j < 4)
-                x[i] = __fsub_rn(__fmul_rn(x[i], cc[i]), __fmul_rn(y[i], ss[i]));
-            else
-                x[i] = __fadd_rn(__fmul_rn(y[i], ss[i]), __fmul_rn(x[i], cc[i]));
-        }
-    }
 }
 
 constexpr int kAppendWarps = 8;
@@ -297,8 +277,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6) rope_append_kernel(const
         const int j = lane < 8 ? lane : kp - b8;
         const bool on = rot_on || (k_on && r.idx_begin >= 0 && j >= 0 && j < 8);
         const int partner = on ? (lane < 8 ? lane ^ 4 : 16 + b8 + (j ^ 4)) : lane;
-        turn_piece(x, v2, j, on, partner, lane < 8 ? r.kv_interleaved != 0 : r.idx_interleaved != 0,
-                     r.table + (int64_t)pos * 64);
+        const bool inter = lane < 8 ? r.kv_interleaved != 0 : r.idx_interleaved != 0;
+        rotate_piece(x, v2, on, partner, inter, !r.kv_interleaved || !r.idx_interleaved,
+                     TableTurn{r.table + (int64_t)pos * 64, j});
     }
     if (has_kv && !p.kv_fp8) {
         uint4* dst = reinterpret_cast<uint4*>(p.kv_cache + row * 1152);
@@ -383,7 +364,7 @@ __global__ void __launch_bounds__(32 * kQueryWarps, 8) rope_queries_kernel(const
         if (pos < 0) return;
         const bool inter = r.kv_interleaved != 0;
         Turn turn;
-        load_turn(turn, r.table + (int64_t)pos * 64, j, inter);
+        turn.load({r.table + (int64_t)pos * 64, j}, inter);
         uint16_t* dst = p.q + (t * p.heads + h0) * 576 + 512 + 8 * j;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
@@ -391,7 +372,7 @@ __global__ void __launch_bounds__(32 * kQueryWarps, 8) rope_queries_kernel(const
             if (h >= p.heads) break;  // uniform over the warp
             float x[8];
             unpack8(v[k], x);
-            rotate_piece(x, v[k], true, lane ^ 4, inter, turn);
+            rotate_piece(x, v[k], true, lane ^ 4, inter, !inter, turn);
             if (h + h0 < p.heads) *reinterpret_cast<uint4*>(dst + h * 576) = pack8(x);
         }
         return;
@@ -414,7 +395,7 @@ __global__ void __launch_bounds__(32 * kQueryWarps, 8) rope_queries_kernel(const
     const bool turns = in && r.idx_begin >= 0 && j >= 0 && j < 8;
     const int partner = turns ? (lane & 16) + b8 + (j ^ 4) : lane;
     Turn turn;
-    if (turns) load_turn(turn, r.table + (int64_t)pos * 64, j, inter);
+    if (turns) turn.load({r.table + (int64_t)pos * 64, j}, inter);
     const int64_t row0 = t * p.idx_heads + h0;
     uint8_t* dst = p.q_idx + row0 * Di * (IDX == DSA_BF16 ? 2 : 1) + kp * (IDX == DSA_BF16 ? 16 : 8);
     const int row_bytes = IDX == DSA_BF16 ? 2 * Di : Di;
@@ -425,7 +406,7 @@ __global__ void __launch_bounds__(32 * kQueryWarps, 8) rope_queries_kernel(const
         const bool on = h + h0 < p.idx_heads && in;
         float x[8];
         unpack8(w[k], x);
-        if (r.idx_begin >= 0) rotate_piece(x, w[k], turns, partner, inter, turn);
+        if (r.idx_begin >= 0) rotate_piece(x, w[k], turns, partner, inter, !inter, turn);
         if constexpr (IDX == DSA_BF16) {
             if (on) *reinterpret_cast<uint4*>(dst + h * row_bytes) = pack8(x);
         } else {
