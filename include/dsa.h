@@ -365,7 +365,7 @@ dsa_status_t dsa_rope_append(const dsa_dims_t* dims, const dsa_rope_t* rope, con
  *   q          [T, Hq, D] bf16, written in dims 512..575
  *   q_idx_in   [T, Hi, Di] bf16, or NULL to leave the indexer's queries alone; token stride q_idx_stride
  *              elements (0: dense; else a multiple of 8, at least Hi * Di).  With bf16 output it may be
- *              q_idx itself (dense).
+ *              q_idx itself (dense; refused otherwise).
  *   q_idx      [T, Hi, Di] of dims->idx_dtype, output;  q_scale as for dsa_indexer_topk, output (NULL for bf16)
  *   workspace  as for dsa_rope_append
  * No page is looked up: num_pages and max_pages_per_seq play no part.  A token that no sequence owns or

@@ -755,6 +755,9 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* d, const dsa_rope_t* rope, const
         if ((st = check_stride(&q_idx_stride, (int64_t)d->idx_heads * d->idx_dim, "q_idx_stride")) ||
             (st = check_ptr(q_idx, "q_idx")) || (st = check_ptr(q_scale, "q_scale", d->idx_dtype != DSA_BF16)))
             return st;
+        // (a row of another place or width would be written over rows that other warps still have to read)
+        if (q_idx == q_idx_in && (d->idx_dtype != DSA_BF16 || q_idx_stride != (int64_t)d->idx_heads * d->idx_dim))
+            return fail(DSA_ERR_INVALID_ARG, "q_idx may be q_idx_in for dense bf16 rows only");
     }
     if (d->total_q == 0 || (!q_pe && !q_idx_in)) return DSA_OK;
     DeviceInfo dev;
