@@ -176,8 +176,10 @@ def _stream(stream):
             import torch
 
             _torch = torch
-        # the handle alone: building a Stream object for it takes 3 us, as long as the rest of a call
-        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
+        # the handle alone: building a Stream object for it takes 3 us, as long as the rest of a call (a private function,
+        # which a PyTorch may lack)
+        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(_torch.cuda.current_device()) if raw is not None else _torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
