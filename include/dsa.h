@@ -395,9 +395,9 @@ dsa_status_t dsa_rope_queries(const dsa_dims_t* dims, const dsa_rope_t* rope, co
  *   workspace  dsa_prefix_attn_workspace_size(dims, prefix_len) bytes, first 256 zero-filled once
  * dims->idx_* and top_k are not looked at.  How the work is divided follows from dims and prefix_len alone: a page
  * table about as wide as the longest context gives the shortest times.  Positions beyond p_t and rows behind L_b are never part of the
- * result, whatever they hold.  A score of -inf has weight 0 (an infinite value of such a row makes NaN of it);
- * a NaN in a visible row, or in q, makes the rows that see it NaN; with every score -inf, out = 0 and
- * lse = -inf.
+ * result, whatever they hold.  A score of -inf has weight 0 (an infinite value of such a row makes NaN of at least the
+ * dims of out that hold it); a NaN in a visible row, or in q, makes the rows that see it NaN; with every score -inf, out
+ * = 0 and lse = -inf.
  * A sequence with n_b > L_b - prefix_len, n_b > max_q_len or a context beyond its page table or of 2^31 - 255
  * positions or more (DSA_DEVERR_SEQ) and a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left
  * as they were; rows of a page that is out of range (DSA_DEVERR_PAGE) are skipped.

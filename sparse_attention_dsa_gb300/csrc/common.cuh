@@ -105,6 +105,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The larger of a value in any CTA of the cluster's shared memory and v stays there.
+__device__ __forceinline__ void red_max_cluster(uint32_t cluster_addr, unsigned long long v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u64 [%0], %1;" ::"r"(cluster_addr), "l"(v) : "memory");
+}
+
 // cp.async (16-byte, L2-only) into shared memory, completion tracked by an mbarrier arrive.
 __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");

@@ -252,6 +252,9 @@ struct Ctrl {
     Segment first;
     int32_t scan[kMaxWarps];
     float exchange[2][128];
+    // bf16: the first position whose V was cleaned in an edge tile of a segment (numbered from 1, one slot for each parity):
+    // segment << 32 | INT32_MAX - position
+    unsigned long long cleaned[2];
 };
 constexpr int kSmem = 1024 + 2 * kQAtoms * kAtom + kVSlots * kVSlot + kPBytes + (int)sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
@@ -477,6 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         }
         mbar_init(&ctl->exchanged, 4);
         ctl->failed = 0;
+        ctl->cleaned[0] = ctl->cleaned[1] = 0;
         fence_mbar_init();
     }
     __syncwarp();
@@ -778,7 +782,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         const uint32_t trow = tmem + ((uint32_t)(st & ~31) << 16);
         const uint32_t s_empty = leader(&ctl->s_empty[0]), p_full = leader(&ctl->p_full), o_free = leader(&ctl->o_free);
         const uint32_t p_row = smem_u32(p_s) + half * kAtom + r * 128;
-        uint32_t tile = 0, swaps = 0;
+        uint32_t tile = 0, swaps = 0, seg = 0;
         // A value of the row's other half (tensor-memory lane st ^ 64).  Two buffers, and a bounded wait instead
         // of a block barrier, so that a warp that has given up stops no other.
         auto swap = [&](float mine, float* other) {
@@ -904,7 +908,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
             tc_fence_after();
             float other;
             if (!(ok = swap(l_sum, &other))) break;
-            const float l = half == 0 ? l_sum + other : other + l_sum;  // the same sum in both halves
+            float l = half == 0 ? l_sum + other : other + l_sum;  // the same sum in both halves
+            if (!KVFP8) {
+                // An infinite value of weight 0 is NaN where V comes as it is; V of edge tiles had it cleaned, so that the rows
+                // that do not see it are not, and those that do become NaN here.
+                const unsigned long long bad = *const_cast<volatile unsigned long long*>(&ctl->cleaned[++seg & 1u]);
+                if ((uint32_t)(bad >> 32) == seg && limit > INT32_MAX - (int)(uint32_t)bad) l = NAN;
+            }
             const float m = m_used - kLift<KVFP8>;  // what O and l are relative to
             const bool whole = s.u0 == 0 && s.u1 == s.it.tiles_a + s.it.tiles_b && !p.packed;
             float* slot = p.partial + partial_slot(p, s.index, pair, s.u0 == 0) * kPartialFloats;
@@ -994,12 +1004,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
         const uint32_t edge_full = leader(&ctl->edge_full);
         // The ring does not wait for these warps at other tiles, so its own phases may pass them by (a parity names one
         // of two phases).  v_turn has one phase for each edge tile, and the ring stays there until the tile is filled.
-        uint32_t turn = 0;
+        uint32_t turn = 0, seg = 0;
         static_assert(kVSlots == 2, "one slot for each page of a tile");
         while (ok && next_segment<SEARCH>(p, w, s)) {
+            ++seg;
             for (int u = s.u0; ok && u < s.u1; ++u) {
                 const Tile t = tile_of(p, shared, s.it, u);
                 if (!t.edge) continue;
+                int bad = INT32_MAX;  // first position that this lane has to clean
                 // A row of 32 chunks (8 dims) at a time; rows 16 fw .. 16 fw + 15 of both pages are this warp's.  All is
                 // loaded and looked at before the slots are waited for: only the stores are on the way to the products.
                 const int row0 = 16 * fw;
@@ -1027,8 +1039,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            v[h][k] = make_uint4(finite2(v[h][k].x), finite2(v[h][k].y), finite2(v[h][k].z), finite2(v[h][k].w));
+                        for (int k = 0; k < 16; ++k) {
+                            const uint4 old = v[h][k];
+                            v[h][k] = make_uint4(finite2(old.x), finite2(old.y), finite2(old.z), finite2(old.w));
+                            if (((v[h][k].x ^ old.x) | (v[h][k].y ^ old.y) | (v[h][k].z ^ old.z) | (v[h][k].w ^ old.w)) != 0)
+                                bad = min(bad, t.base + 64 * h + row0 + k);
+                        }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -1039,6 +1055,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<KVFP8>, 1)
                 }
                 if (!ok) break;
                 ++turn;
+                if (bad != INT32_MAX) {  // for both CTAs' softmax; the slot's last segment has ended (its successor's weights
+                                         // are behind this tile)
+                    const unsigned long long mark = (unsigned long long)seg << 32 | (uint32_t)(INT32_MAX - bad);
+                    for (int r = 0; r < 2; ++r)
+                        red_max_cluster(mapa_shared(smem_u32(&ctl->cleaned[seg & 1u]), r), mark);
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(edge_full);
