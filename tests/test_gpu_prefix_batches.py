@@ -114,3 +114,31 @@ def test_padding_slots_in_front_need_no_pages(heads, slots, others, fp8, wide):
     want.b.pt, want.b.pt_host = pt.contiguous(), pt.cpu()
     want.cache, want.q = c.cache, c.q
     Attention(want.b, want.q, want.cache, fp8).check(c.out, c.lse, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_captured_between_other_work(fp8):
+    """Calls captured behind a memory fill and behind one another, with an input that the step itself writes."""
+    c = Call(*SHAPES["full_heads_long_prefix"], fp8=fp8, seed=36)
+    d = Call(*SHAPES["packed_many"], fp8=fp8, seed=37, wide=True)
+    q = c.q.clone()
+
+    def step():
+        c.q.zero_()
+        dsa.clear_device_error(c.workspace)
+        c.q.add_(q)
+        c.run()
+        dsa.clear_device_error(d.workspace)
+        d.run()
+        c.run()
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    c.out.zero_(), d.out.zero_()
+    for _ in range(3):
+        g.replay()
+    c.check()
+    d.check()

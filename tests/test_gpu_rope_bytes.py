@@ -86,3 +86,26 @@ def test_keys_and_queries_are_rotated_alike(kind, di, begin, pairing):
     if scale is not None:
         assert torch.equal(k_scale.flatten(0, 1)[b.rows], scale)
         assert torch.equal(q_scale, scale)
+
+
+def test_queries_of_every_magnitude_are_quantised_like_keys():
+    """From subnormal to the largest, with zeros of both signs, infinities and NaN (unrotated, so that they stay)."""
+    b = Batch([4000], [4000], seed=53)
+    x = torch.randn((b.T, 128), generator=torch.Generator(device="cuda").manual_seed(54), device="cuda")
+    power = torch.randint(-133, 125, (b.T, 1), generator=torch.Generator().manual_seed(55)).cuda().float()
+    power[:2000] = power[:2000] / 16
+    x = x * torch.exp2(power)
+    x[:, 5::64], x[:, 7::64] = 0.0, -0.0
+    x[100:110, 9], x[105:115, 44] = float("inf"), float("nan")
+    x = x.to(torch.bfloat16)
+    table = rope_table(4000, "cuda")
+    rope = dsa.DsaRope(table=table.data_ptr(), table_len=4000, kv_pairing=0, idx_pairing=0, idx_begin=-1)
+    for kind, shape, dtype in ((FP8, (), torch.float32), (MX, (4,), torch.uint8)):
+        d = b.dims(idx_heads=1, idx_dtype=kind)
+        k, q = (torch.zeros((n, 128), dtype=torch.uint8, device="cuda") for n in (b.pages * PAGE, b.T))
+        ks, qs = (torch.zeros((n, *shape), dtype=dtype, device="cuda") for n in (b.pages * PAGE, b.T))
+        dsa.rope_append(d, rope, x, None, b.pt, b.lens, b.cu, k, ks, None, b.workspace)
+        dsa.rope_queries(d, rope, None, None, x, q, qs, b.lens, b.cu, b.workspace)
+        assert dsa.get_device_error(b.workspace) == 0
+        assert torch.equal(k[b.rows], q)
+        assert torch.equal(ks[b.rows].view(torch.uint8), qs.view(torch.uint8))
