@@ -36,10 +36,10 @@
 // What bounds it, and measured (one GB300, warm).  A 128 x 128 tile costs 2 x 128 x 128 x (576 + 512) operations, 1.42 us on
 // a pair at the measured cuBLAS rate: prefix tiles, whose rows are in L2, take 1.30 us, bound by the tensor pipe and by
 // the shared-memory reads of Q K^T, which fill it.  Own bf16 rows are read once by one pair: 1.8 us a tile with all
-// pairs at it, 0.92 of the copy bandwidth.  Own FP8 rows: 2.97 us, bound by shared memory (245 KB of
+// pairs at it, 0.92 of the copy bandwidth.  Own FP8 rows: 3.1 us, bound by shared memory (245 KB of
 // operands, 280 KB for codes arriving, read and written back, a CTA and tile).  32 sequences of 1024 positions behind 16384, 128 heads:
-// 96 us, 1.56 PFLOP/s; 64 x 16 heads, 500 behind 32741: 62.5 us; 8 prompts of up to 257 queries x 32 heads behind 4096: 285 us,
-// 1.66 PFLOP/s; one short item: 12 us, all latency.
+// 91 to 93 us, 1.6 PFLOP/s; 64 x 16 heads, 500 behind 32741: 58 us; 8 prompts of up to 257 queries x 32 heads behind 4096: 277
+// to 304 us (the power limit), 1.6 to 1.7 PFLOP/s; one short item: 12 us, all latency.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -14,10 +14,13 @@
 // block is 8 neighbouring lanes: interleaved pairs lie inside a piece, the halves' partner is the piece four
 // further, fetched by a shuffle.
 //
-// Measured (one GB300, warm).  rope_append: 4 tokens 2.4 us (latency), 380 tokens to FP8 4.7 us, 24693 to FP8 15.9 us
-// (20.9 with divisions beside ties); eight ragged chunks of up to 4096 tokens, bf16, 16.9 us (75.8 MB in and out: 4.5 TB/s,
-// 0.66 of the copy bandwidth; two tokens a warp, for half as many chains of loads, were no faster).
-// rope_queries: 32 tokens 2.4 us, 4096 tokens of 128 + 64 heads to MXFP8 46.8 us (237 MB, 5.1 TB/s, 0.75).
+// Measured (one GB300; 20 calls in a graph, so that up to some 100 MB stay in L2; in brackets with L2 flushed before each).
+// rope_append: 4 tokens 2.5 us (3.3), latency; 380 tokens to FP8 4.7 us (7.4): every warp looks through the sequences, 32 a
+// round trip (one token of each of 32, 256, 1024 sequences: 3.4, 4.8, 10.2 us); 24693 tokens to FP8 15.1 us (20.5); eight
+// ragged chunks of up to 4096 tokens, bf16, 10.6 us (17.9: 75.8 MB in and out, 4.2 TB/s, 0.63 of the copy bandwidth: each
+// warp has three loads a lane on their way and then its own chain).  Two tokens a warp were no faster.
+// rope_queries: 32 tokens 2.5 us (3.7), 4096 tokens of 128 + 64 heads to MXFP8 46.2 us (50.1; 237 MB, 5.1 TB/s, 0.75),
+// to bf16 50.0 (49.3; 269 MB, 0.79), to FP8 52 to 59 (56.1: the quotients' reciprocals and corrections).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
