@@ -421,6 +421,93 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* dims, int32_t prefix_len, const v
  */
 size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len);
 
+/*
+ * Root-mean-square norm with the residual's addition, in front of a projection ([A4] 3.3), to bf16, to 8-bit codes with
+ * scales ([A3] 3.1, [A4] 4), or to both: for every row,
+ *     h = x + residual,   sum = bf16(h),   y = h / sqrt(mean(h^2) + eps) * weight
+ * in fp32 (from h before its rounding); out = bf16(y), codes and scales of y by the rules of dsa_rope_append.
+ *   x          [rows, dim] bf16, rows x_stride elements apart (0: dense; else a multiple of 8, at least dim)
+ *   residual   [rows, dim] bf16, or NULL (h = x);  sum [rows, dim] bf16 output, or NULL (without a residual: NULL)
+ *   weight     [dim] bf16
+ *   out        [rows, dim] bf16 output, rows out_stride elements apart (as x_stride), or NULL
+ *   codes      [rows, dim] E4M3 output, or NULL (codes_dtype, group and scale are not looked at then)
+ *   scale      codes_dtype DSA_FP8_E4M3: fp32, [rows] (group 0: a scale for the row) or [rows, dim / 128] (group 128);
+ *              DSA_MXFP8_E4M3: E8M0 bytes [rows, dim / 32] (group 32)
+ * sum may be residual or (dense) x; out may be x (of the same stride) or (dense) residual; otherwise outputs overlap nothing.
+ * An infinity or NaN in a row makes NaN as the formula does (a NaN code is 0x7F or 0xFF; scales are of the group's
+ * numbers); so do squares whose sum leaves fp32's range (magnitudes beyond 2^60): y is 0 there.  No workspace.
+ * Supported: dim a multiple of 8 (of the group) up to 16384.
+ */
+dsa_status_t dsa_rms_norm(int32_t rows, int32_t dim, const void* x, int64_t x_stride, const void* residual, void* sum,
+                          const void* weight, float eps, void* out, int64_t out_stride, int32_t codes_dtype, int32_t group,
+                          void* codes, void* scale, void* stream);
+
+/*
+ * Latent attention's weights, for the three calls below: w_kv [Hq, 256, 512] bf16; of head h, rows 0..127 are wk[h], which
+ * make the 128 unrotated dims of its keys from a latent row, and rows 128..255 wv[h], which make its 128 value dims.
+ */
+#define DSA_HEAD_NOPE 128
+#define DSA_HEAD_VALUE 128
+
+/*
+ * The queries' unrotated part in latent space (latent attention in absorbed form, [A2] step 2 works there): for every query
+ * token t and head h,
+ *     q[t,h,c] = sum_d q_nope[t,h,d] * wk[h,d,c]   for c = 0..511 (dims 512..575 are left as they are: dsa_rope_queries)
+ *   q_nope     [T, Hq, 128] bf16; head h of token t starts t * token_stride + h * head_stride elements in (both 0: dense;
+ *              else both multiples of 8, head_stride >= 128)
+ *   q          [T, Hq, D] bf16, written in dims 0..511
+ *   workspace  256 bytes, zero-filled once (only the error word is used, for a wait that gave up)
+ * Sums in fp32, rounded once.  Of dims, total_q, attn_heads, kv_dim and v_dim are looked at.  Supported: D = 576, Dv = 512,
+ * Hq <= 128.
+ */
+dsa_status_t dsa_absorb_queries(const dsa_dims_t* dims, const void* q_nope, int64_t token_stride, int64_t head_stride,
+                                const void* w_kv, void* q, void* workspace, void* stream);
+
+/*
+ * Attention over latent rows back to head values: for every query token t and head h,
+ *     out[t,h,d] = sum_c o_latent[t,h,c] * wv[h,d,c]
+ *   o_latent   [T, Hq, Dv] bf16, the out of dsa_sparse_attn, dsa_fused_decode or dsa_prefix_attn
+ *   out        [T, Hq, 128] bf16 output;  workspace and limits as for dsa_absorb_queries
+ */
+dsa_status_t dsa_value_heads(const dsa_dims_t* dims, const void* o_latent, const void* w_kv, void* out, void* workspace,
+                             void* stream);
+
+/*
+ * Causal attention with keys and values of every head (latent attention in expanded form; the dense attention of
+ * dsa_prefix_attn with 640 operations a query, position and head instead of 2176, and 2^18 a position and head for the keys
+ * and values: the form for prompts).  With c_s the latent part (dims 0..511) and r_s the rotary part of position s,
+ *     z_s = softmax_scale * (q_nope[t,h,:] . wk[h] c_s + q_pe[t,h,:] . r_s)   for every visible position s = 0..p_t,
+ *     out[t,h,:] = sum_s softmax(z)_s * wv[h] c_s,   lse[t,h] = log sum_s exp(z_s)
+ * Keys and values are rounded to bf16 (FP8 rows before that, too), the softmax's weights in the products as well.
+ *   total_pages  an upper bound of the pages in use: sum over the sequences with queries of ceil(L_b / 64)
+ *   q_nope     [T, Hq, 128] bf16, strides as for dsa_absorb_queries
+ *   q_pe       [T, Hq, 64] bf16, rotated (dsa_rope_queries; q + 512 with strides Hq * 576 and 576 is where that leaves it);
+ *              strides like q_nope's, head stride >= 64
+ *   w_kv       as above;  kv_cache, page_table, seq_lens, cu_q_lens as for dsa_sparse_attn
+ *   out        [T, Hq, 128] bf16 output;  lse [T, Hq] fp32 output, or NULL
+ *   workspace  dsa_expanded_attn_workspace_size(dims, total_pages) bytes, first 256 zero-filled once
+ * dims->idx_*, top_k and max_q_len are not looked at.  Positions beyond p_t and rows behind L_b are never part of the result,
+ * whatever they hold.  A score of -inf has weight 0; with every score -inf, out = 0 and lse = -inf.  A visible position
+ * with a value that is not finite, in its row or in its head values as bf16, makes NaN of the rows that see it (in
+ * out and lse; for all heads, where its values are those of one head); so does a page that is out of range, which is
+ * reported (DSA_DEVERR_PAGE).  A sequence with n_b > L_b, a context beyond its page table or pages beyond total_pages
+ * (DSA_DEVERR_SEQ) and a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were.
+ * Supported: D = 576, Dv = 512, Hq <= 128.
+ */
+dsa_status_t dsa_expanded_attn(const dsa_dims_t* dims, int32_t total_pages, const void* q_nope, int64_t q_nope_token_stride,
+                               int64_t q_nope_head_stride, const void* q_pe, int64_t q_pe_token_stride,
+                               int64_t q_pe_head_stride, const void* w_kv, const void* kv_cache, const int32_t* page_table,
+                               const int32_t* seq_lens, const int32_t* cu_q_lens, void* out, float* lse, void* workspace,
+                               void* stream);
+
+/*
+ * Bytes of workspace that dsa_expanded_attn needs for these sizes, and for every call of the same attn_heads whose batch,
+ * total_q and total_pages are no larger: mostly 512 bytes a position and head (64 KB for 128 heads) and 1152 bytes a
+ * position, positions counted in tiles of 128 a sequence.  256 where dsa_expanded_attn refuses the sizes as too large, 0 when
+ * dims is NULL or total_pages below 1.  Host-only.
+ */
+size_t dsa_expanded_attn_workspace_size(const dsa_dims_t* dims, int32_t total_pages);
+
 /* Zeroes the device error word (asynchronously on `stream`). */
 dsa_status_t dsa_clear_device_error(void* workspace, void* stream);
 

@@ -20,6 +20,7 @@ DSA_KV_FP8_ROW_BYTES = 656
 DSA_DEVERR_PAGE, DSA_DEVERR_SEQ, DSA_DEVERR_INDEX, DSA_DEVERR_TIMEOUT, DSA_DEVERR_ROPE = 0x1, 0x2, 0x4, 0x8, 0x10
 DSA_DEVERR_RANGE = 0x20
 DSA_ROPE_HALVES, DSA_ROPE_INTERLEAVED = 0, 1
+DSA_HEAD_NOPE, DSA_HEAD_VALUE = 128, 128
 
 EXPORTED = (
     "dsa_abi_version",
@@ -43,6 +44,11 @@ EXPORTED = (
     "dsa_rope_queries",
     "dsa_prefix_attn",
     "dsa_prefix_attn_workspace_size",
+    "dsa_rms_norm",
+    "dsa_absorb_queries",
+    "dsa_value_heads",
+    "dsa_expanded_attn",
+    "dsa_expanded_attn_workspace_size",
 )
 
 
@@ -154,6 +160,17 @@ def lib() -> ctypes.CDLL:
             L.dsa_prefix_attn.argtypes = [ctypes.POINTER(DsaDims), ctypes.c_int32] + [vp] * 9
             L.dsa_prefix_attn_workspace_size.restype = ctypes.c_size_t
             L.dsa_prefix_attn_workspace_size.argtypes = [ctypes.POINTER(DsaDims), ctypes.c_int32]
+            i32 = ctypes.c_int32
+            L.dsa_rms_norm.restype = st
+            L.dsa_rms_norm.argtypes = [i32, i32, vp, i64, vp, vp, vp, ctypes.c_float, vp, i64, i32, i32, vp, vp, vp]
+            L.dsa_absorb_queries.restype = st
+            L.dsa_absorb_queries.argtypes = [ctypes.POINTER(DsaDims), vp, i64, i64, vp, vp, vp, vp]
+            L.dsa_value_heads.restype = st
+            L.dsa_value_heads.argtypes = [ctypes.POINTER(DsaDims)] + [vp] * 5
+            L.dsa_expanded_attn.restype = st
+            L.dsa_expanded_attn.argtypes = [ctypes.POINTER(DsaDims), i32, vp, i64, i64, vp, i64, i64] + [vp] * 9
+            L.dsa_expanded_attn_workspace_size.restype = ctypes.c_size_t
+            L.dsa_expanded_attn_workspace_size.argtypes = [ctypes.POINTER(DsaDims), i32]
             _lib = L
     return _lib
 
@@ -328,3 +345,49 @@ def prefix_attn(dims, prefix_len, q, kv_cache, page_table, seq_lens, cu_q_lens, 
     _check(lib().dsa_prefix_attn(ctypes.byref(dims), int(prefix_len), _ptr(q), _ptr(kv_cache), _ptr(page_table),
                                  _ptr(seq_lens), _ptr(cu_q_lens), _ptr(out), _ptr(lse), _ptr(workspace),
                                  _stream(stream)))
+
+
+def rms_norm(x, weight, eps, out=None, codes=None, scale=None, codes_dtype=DSA_FP8_E4M3, group=0, residual=None, sum=None,
+             stream=None):
+    """dsa_rms_norm: x [rows, dim] (rows and the strides of x and out are those of the tensors) plus residual, normalised,
+    to bf16 (out) and codes with scales."""
+    rows, dim = x.shape
+    for name, t in (("x", x), ("out", out)):
+        if t is not None and (tuple(t.shape) != (rows, dim) or t.stride(1) != 1):
+            raise DsaError(DSA_ERR_INVALID_ARG, f"{name} must be [{rows}, {dim}] with dense rows (got {tuple(t.shape)}, "
+                                                f"strides {tuple(t.stride())})")
+    _check(lib().dsa_rms_norm(rows, dim, _ptr(x), x.stride(0) if rows > 1 else 0, _ptr(residual), _ptr(sum), _ptr(weight),
+                              float(eps), _ptr(out), out.stride(0) if out is not None and rows > 1 else 0, int(codes_dtype),
+                              int(group), _ptr(codes), _ptr(scale), _stream(stream)))
+
+
+def absorb_queries(dims, q_nope, w_kv, q, workspace, stream=None, q_nope_strides=(0, 0)):
+    """dsa_absorb_queries: the queries' unrotated part through each head's key weights, into dims 0..511 of q.
+    q_nope_strides: (token, head) in elements, (0, 0) = dense."""
+    _check(lib().dsa_absorb_queries(ctypes.byref(dims), _ptr(q_nope), int(q_nope_strides[0]), int(q_nope_strides[1]),
+                                    _ptr(w_kv), _ptr(q), _ptr(workspace), _stream(stream)))
+
+
+def value_heads(dims, o_latent, w_kv, out, workspace, stream=None):
+    """dsa_value_heads: attention over latent rows through each head's value weights."""
+    _check(lib().dsa_value_heads(ctypes.byref(dims), _ptr(o_latent), _ptr(w_kv), _ptr(out), _ptr(workspace),
+                                 _stream(stream)))
+
+
+def expanded_attn_workspace_size(dims: DsaDims, total_pages: int) -> int:
+    return int(lib().dsa_expanded_attn_workspace_size(ctypes.byref(dims), int(total_pages)))
+
+
+def expanded_attn(dims, total_pages, q_nope, q_pe, w_kv, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace,
+                  stream=None, q_nope_strides=(0, 0), q_pe_strides=(0, 0)):
+    """dsa_expanded_attn: causal attention of prompts with keys and values of every head, made of the latent rows.  A
+    workspace tensor of fewer than expanded_attn_workspace_size() bytes is refused.  Strides: (token, head) in elements."""
+    if hasattr(workspace, "numel"):
+        need = expanded_attn_workspace_size(dims, total_pages)
+        have = workspace.numel() * workspace.element_size()
+        if have < need:
+            raise DsaError(DSA_ERR_INVALID_ARG, f"workspace of {have} bytes is too small: the call needs {need}")
+    _check(lib().dsa_expanded_attn(ctypes.byref(dims), int(total_pages), _ptr(q_nope), int(q_nope_strides[0]),
+                                   int(q_nope_strides[1]), _ptr(q_pe), int(q_pe_strides[0]), int(q_pe_strides[1]),
+                                   _ptr(w_kv), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(cu_q_lens), _ptr(out),
+                                   _ptr(lse), _ptr(workspace), _stream(stream)))

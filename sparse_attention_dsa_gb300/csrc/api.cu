@@ -202,6 +202,95 @@ dsa::RopeParams rope_params(const dsa_dims_t* d, const dsa_rope_t* r, const int3
     return p;
 }
 
+// Token and head strides of a query array, in elements: both 0 stands for dense rows of `width`.
+dsa_status_t check_query_strides(int64_t* token, int64_t* head, int32_t width, int32_t heads, const char* name) {
+    if ((*token == 0) != (*head == 0) || *token < 0 || *token % 8 || *token >= (int64_t)1 << 38)
+        return fail(DSA_ERR_INVALID_ARG, "%s strides must both be 0 or both positive multiples of 8 (got %lld, %lld)", name,
+                    (long long)*token, (long long)*head);
+    if (*head == 0) {
+        *head = width;
+        *token = (int64_t)width * heads;
+    }
+    if (*head < width || *head % 8 || *head >= (int64_t)1 << 38)
+        return fail(DSA_ERR_INVALID_ARG, "%s strides: a head's rows must be at least %d elements apart, a multiple of 8 (got %lld)",
+                    name, width, (long long)*head);
+    return DSA_OK;
+}
+
+// The sizes that products of every head with its own weights go by.
+dsa_status_t check_heads(const dsa_dims_t* d) {
+    if (!d) return fail(DSA_ERR_INVALID_ARG, "dims is NULL");
+    if (d->total_q < 0) return fail(DSA_ERR_INVALID_ARG, "total_q must be >= 0 (got %d)", d->total_q);
+    if (d->attn_heads < 1) return fail(DSA_ERR_INVALID_ARG, "attn_heads must be >= 1 (got %d)", d->attn_heads);
+    if (d->attn_heads > 128) return fail(DSA_ERR_UNSUPPORTED, "attn_heads must be <= 128 (got %d)", d->attn_heads);
+    if (d->kv_dim != 576 || d->v_dim != 512)
+        return fail(DSA_ERR_UNSUPPORTED, "head products support kv_dim 576 / v_dim 512 (got %d / %d)", d->kv_dim, d->v_dim);
+    if (d->total_q > INT32_MAX - 256 || ((int64_t)d->total_q + 127) / 128 * 2 * d->attn_heads > INT32_MAX)
+        return fail(DSA_ERR_UNSUPPORTED, "total_q * attn_heads (%d * %d) is too large", d->total_q, d->attn_heads);
+    return DSA_OK;
+}
+
+// A 3-D view of 16-bit values, innermost first; strides in elements.
+dsa_status_t encode_rows(CUtensorMap* map, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                         const uint32_t (&box)[3], bool swizzle, const char* name) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t gdim[3] = {dims[0], dims[1], dims[2]}, gstride[2] = {strides[0] * 2, strides[1] * 2};
+    const cuuint32_t b[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, b, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DSA_OK : fail(DSA_ERR_CUDA, "tensor map for %s: CUresult %d", name, (int)r);
+}
+
+// Both products of every head with its weights w_kv [Hq, 256, 512].
+dsa_status_t run_heads(const dsa_dims_t* d, bool values, const void* in, int64_t token_stride, int64_t head_stride,
+                       const void* w_kv, void* out, void* workspace, void* stream) {
+    DeviceInfo dev;
+    dsa_status_t st = device_info(&dev);
+    if (st) return st;
+    dsa::HeadsLaunch L;
+    memset(&L, 0, sizeof L);
+    const uint64_t T = (uint64_t)d->total_q, H = (uint64_t)d->attn_heads;
+    const uint64_t inner = values ? 512 : dsa::kHeadNope, outer = values ? dsa::kHeadValue : 512;
+    const uint64_t row = values ? dsa::kHeadValue : (uint64_t)d->kv_dim;  // of the output
+    if ((st = encode_rows(&L.amap, in, {inner, H, T}, {(uint64_t)head_stride, (uint64_t)token_stride}, {64, 1, 128}, true,
+                          values ? "o_latent" : "q_nope")) ||
+        (st = encode_rows(&L.wmap, w_kv, {512, 256, H}, {512, 256 * 512}, {64, values ? 128u : 64u, 1}, true, "w_kv")) ||
+        (st = encode_rows(&L.omap, out, {outer, H, T}, {row, row * H}, {64, 1, 32}, true, "out")))
+        return st;
+    L.params.err = static_cast<int32_t*>(workspace);
+    L.params.total_q = d->total_q;
+    L.params.heads = d->attn_heads;
+    L.params.values = values ? 1 : 0;
+    L.params.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    L.num_sms = dev.num_sms;
+    cudaError_t e = dsa::launch_heads(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "head product launch");
+    return DSA_OK;
+}
+
+// The sizes of an expanded attention call and its workspace behind the error word area; false when they are too large.
+bool expand_sizes(const dsa_dims_t* d, int32_t total_pages, dsa::ExpandParams* p, size_t* bytes) {
+    memset(p, 0, sizeof *p);
+    *bytes = 0;
+    if (d->batch < 1 || d->total_q < 1 || d->attn_heads < 1 || d->attn_heads > 128 || total_pages < 1) return false;
+    if (d->total_q > INT32_MAX - 256) return false;
+    // a sequence takes half as many tiles as pages, or one more half; its blocks of queries likewise
+    const int64_t with = d->batch < d->total_q ? d->batch : d->total_q;
+    const int64_t tiles = ((int64_t)total_pages + with + 3) / 4 * 2;
+    const int64_t blocks = d->total_q / dsa::kExpandBlockRows + with;
+    if (tiles > INT32_MAX / 9 || blocks * d->attn_heads > INT32_MAX / 2) return false;
+    p->batch = d->batch;
+    p->total_q = d->total_q;
+    p->heads = d->attn_heads;
+    p->cap_tiles = (int32_t)tiles;
+    p->cap_blocks = (int32_t)blocks;
+    *bytes = dsa::expand_plan_bytes(*p) + (size_t)tiles * dsa::kExpandTileBytes +
+             (size_t)tiles * d->attn_heads * dsa::kExpandHeadTileBytes;
+    return true;
+}
+
 // The sizes of a shared-prefix attention call and their plan; false when they are empty or out of range.
 bool prefix_sizes(const dsa_dims_t* d, int32_t prefix_len, dsa::PrefixParams* p) {
     memset(p, 0, sizeof *p);
@@ -868,6 +957,150 @@ dsa_status_t dsa_prefix_attn(const dsa_dims_t* d, int32_t prefix_len, const void
     }
     cudaError_t e = dsa::launch_prefix(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
+    return DSA_OK;
+}
+
+dsa_status_t dsa_rms_norm(int32_t rows, int32_t dim, const void* x, int64_t x_stride, const void* residual, void* sum,
+                          const void* weight, float eps, void* out, int64_t out_stride, int32_t codes_dtype, int32_t group,
+                          void* codes, void* scale, void* stream) {
+    g_last_error.clear();
+    if (rows < 0 || dim < 1) return fail(DSA_ERR_INVALID_ARG, "need rows >= 0 and dim >= 1 (got %d, %d)", rows, dim);
+    if (dim % 8 || dim > 16384) return fail(DSA_ERR_UNSUPPORTED, "dim must be a multiple of 8 up to 16384 (got %d)", dim);
+    if (!(eps >= 0.f) || eps > 1e30f) return fail(DSA_ERR_INVALID_ARG, "eps must be a finite number >= 0");
+    if (rows == 0) return DSA_OK;  // (arrays without elements may have no address)
+    dsa_status_t st;
+    if ((st = check_ptr(x, "x")) || (st = check_stride(&x_stride, dim, "x_stride")) ||
+        (st = check_ptr(residual, "residual", false)) || (st = check_ptr(sum, "sum", false)) ||
+        (st = check_ptr(weight, "weight")) || (st = check_ptr(out, "out", false)) ||
+        (st = check_ptr(codes, "codes", false)))
+        return st;
+    if (!out && !codes) return fail(DSA_ERR_INVALID_ARG, "out and codes are both NULL");
+    if (out && (st = check_stride(&out_stride, dim, "out_stride"))) return st;
+    if (sum && !residual) return fail(DSA_ERR_INVALID_ARG, "sum without a residual");
+    // (a row of another place or width would be written over rows that other blocks still have to read)
+    if (out == x && out_stride != x_stride) return fail(DSA_ERR_INVALID_ARG, "out may be x with the same stride only");
+    if (sum && sum == x && x_stride != dim) return fail(DSA_ERR_INVALID_ARG, "sum may be x for dense rows only");
+    if (out && out == residual && out_stride != dim) return fail(DSA_ERR_INVALID_ARG, "out may be residual for dense rows only");
+    if (out && out == sum) return fail(DSA_ERR_INVALID_ARG, "out and sum are the same array");
+    if (codes) {
+        const bool mx = codes_dtype == DSA_MXFP8_E4M3;
+        if (codes_dtype != DSA_FP8_E4M3 && !mx)
+            return fail(DSA_ERR_INVALID_ARG, "codes_dtype %d is not a type of 8-bit codes", codes_dtype);
+        if (mx ? group != 32 : group != 0 && group != 128)
+            return fail(DSA_ERR_INVALID_ARG, "group must be 0 or 128 (FP8) or 32 (MXFP8) (got %d)", group);
+        if (group && dim % group) return fail(DSA_ERR_INVALID_ARG, "dim %d is not a multiple of the group of %d", dim, group);
+        if ((st = check_ptr(scale, "scale"))) return st;
+    }
+    DeviceInfo dev;
+    if ((st = device_info(&dev))) return st;
+    dsa::NormParams p;
+    memset(&p, 0, sizeof p);
+    p.x = static_cast<const uint16_t*>(x);
+    p.residual = static_cast<const uint16_t*>(residual);
+    p.sum = static_cast<uint16_t*>(sum);
+    p.weight = static_cast<const uint16_t*>(weight);
+    p.out = static_cast<uint16_t*>(out);
+    p.codes = static_cast<uint8_t*>(codes);
+    p.scale = scale;
+    p.x_stride = x_stride;
+    p.out_stride = out_stride;
+    p.rows = rows;
+    p.dim = dim;
+    p.group = group;
+    p.mx = codes_dtype == DSA_MXFP8_E4M3 ? 1 : 0;
+    p.eps = eps;
+    cudaError_t e = dsa::launch_norm(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm launch");
+    return DSA_OK;
+}
+
+dsa_status_t dsa_absorb_queries(const dsa_dims_t* d, const void* q_nope, int64_t token_stride, int64_t head_stride,
+                                const void* w_kv, void* q, void* workspace, void* stream) {
+    g_last_error.clear();
+    dsa_status_t st = check_heads(d);
+    if (st || (st = check_ptr(q_nope, "q_nope")) ||
+        (st = check_query_strides(&token_stride, &head_stride, dsa::kHeadNope, d->attn_heads, "q_nope")) ||
+        (st = check_ptr(w_kv, "w_kv")) || (st = check_ptr(q, "q")) || (st = check_ptr(workspace, "workspace")))
+        return st;
+    if (d->total_q == 0) return DSA_OK;
+    return run_heads(d, false, q_nope, token_stride, head_stride, w_kv, q, workspace, stream);
+}
+
+dsa_status_t dsa_value_heads(const dsa_dims_t* d, const void* o_latent, const void* w_kv, void* out, void* workspace,
+                             void* stream) {
+    g_last_error.clear();
+    dsa_status_t st = check_heads(d);
+    if (st || (st = check_ptr(o_latent, "o_latent")) || (st = check_ptr(w_kv, "w_kv")) || (st = check_ptr(out, "out")) ||
+        (st = check_ptr(workspace, "workspace")))
+        return st;
+    if (d->total_q == 0) return DSA_OK;
+    return run_heads(d, true, o_latent, (int64_t)d->attn_heads * d->v_dim, d->v_dim, w_kv, out, workspace, stream);
+}
+
+size_t dsa_expanded_attn_workspace_size(const dsa_dims_t* dims, int32_t total_pages) {
+    if (!dims || total_pages < 1) return 0;
+    dsa::ExpandParams p;
+    size_t bytes;
+    expand_sizes(dims, total_pages, &p, &bytes);
+    return dsa::kErrorWordArea + bytes;
+}
+
+dsa_status_t dsa_expanded_attn(const dsa_dims_t* d, int32_t total_pages, const void* q_nope, int64_t q_nope_token_stride,
+                               int64_t q_nope_head_stride, const void* q_pe, int64_t q_pe_token_stride,
+                               int64_t q_pe_head_stride, const void* w_kv, const void* kv_cache, const int32_t* page_table,
+                               const int32_t* seq_lens, const int32_t* cu_q_lens, void* out, float* lse, void* workspace,
+                               void* stream) {
+    g_last_error.clear();
+    dsa_status_t st = check_paging(d);
+    if (st || (st = check_latent_attention(d))) return st;
+    if (total_pages < 1) return fail(DSA_ERR_INVALID_ARG, "total_pages must be >= 1 (got %d)", total_pages);
+    if ((st = check_ptr(q_nope, "q_nope")) ||
+        (st = check_query_strides(&q_nope_token_stride, &q_nope_head_stride, dsa::kHeadNope, d->attn_heads, "q_nope")) ||
+        (st = check_ptr(q_pe, "q_pe")) ||
+        (st = check_query_strides(&q_pe_token_stride, &q_pe_head_stride, 64, d->attn_heads, "q_pe")) ||
+        (st = check_ptr(w_kv, "w_kv")) || (st = check_ptr(kv_cache, "kv_cache")) ||
+        (st = check_ptr(page_table, "page_table")) || (st = check_ptr(seq_lens, "seq_lens")) ||
+        (st = check_ptr(cu_q_lens, "cu_q_lens")) || (st = check_ptr(out, "out")) || (st = check_ptr(lse, "lse", false)) ||
+        (st = check_ptr(workspace, "workspace")))
+        return st;
+    if (d->total_q == 0) return DSA_OK;
+    dsa::ExpandLaunch L;
+    memset(&L, 0, sizeof L);
+    dsa::ExpandParams& p = L.params;
+    size_t bytes;
+    if (!expand_sizes(d, total_pages, &p, &bytes))
+        return fail(DSA_ERR_UNSUPPORTED, "total_q * attn_heads (%d * %d) or total_pages (%d) is too large", d->total_q,
+                    d->attn_heads, total_pages);
+    DeviceInfo dev;
+    if ((st = device_info(&dev))) return st;
+    p.kv_cache = static_cast<const uint8_t*>(kv_cache);
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.cu_q_lens = cu_q_lens;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.err = static_cast<int32_t*>(workspace);
+    p.num_pages = d->num_pages;
+    p.max_pages = d->max_pages_per_seq;
+    p.kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
+    p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
+    p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea;
+    p.plan = reinterpret_cast<int32_t*>(ws);
+    p.latents = ws + dsa::expand_plan_bytes(p);
+    p.kv = p.latents + (size_t)p.cap_tiles * dsa::kExpandTileBytes;
+    L.num_sms = dev.num_sms;
+    const uint64_t T = (uint64_t)d->total_q, H = (uint64_t)d->attn_heads;
+    if ((st = encode_rows(&L.nopemap, q_nope, {dsa::kHeadNope, H, T},
+                          {(uint64_t)q_nope_head_stride, (uint64_t)q_nope_token_stride}, {64, 1, 128}, true, "q_nope")) ||
+        (st = encode_rows(&L.pemap, q_pe, {64, H, T}, {(uint64_t)q_pe_head_stride, (uint64_t)q_pe_token_stride}, {64, 1, 128},
+                          true, "q_pe")) ||
+        (st = encode_rows(&L.cmap, p.latents, {64, 128, (uint64_t)p.cap_tiles * 9}, {64, 64 * 128}, {64, 128, 1}, false,
+                          "the gathered rows")) ||
+        (st = encode_rows(&L.wmap, w_kv, {512, 256, H}, {512, 256 * 512}, {64, 128, 1}, true, "w_kv")))
+        return st;
+    cudaError_t e = dsa::launch_expand(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "expanded attention launch");
     return DSA_OK;
 }
 

@@ -212,6 +212,22 @@ __device__ __forceinline__ void tma_pair_load_4d(void* dst, const CUtensorMap* m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
 }
+// Tiled store of a box from this CTA's shared memory (what lies outside the tensor is left out), tracked as a bulk
+// async-group of this thread; the groups' commit, and waits until all but the newest N groups have read their source, and
+// until all have been written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src_smem, int32_t c0, int32_t c1,
+                                             int32_t c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src_smem)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // L2 cache policy: evict first (all of the accessed lines).
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t pol;

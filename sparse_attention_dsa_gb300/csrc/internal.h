@@ -279,6 +279,88 @@ struct PrefixLaunch {
 };
 cudaError_t launch_prefix(const PrefixLaunch& launch, cudaStream_t stream);
 
+// ---- root-mean-square norm ------------------------------------------------------------------------------
+struct NormParams {
+    const uint16_t* x;         // [rows, dim] bf16 bits, rows x_stride elements apart; may be out or sum
+    const uint16_t* residual;  // [rows, dim] or null; may be sum
+    uint16_t* sum;             // [rows, dim] x + residual, or null
+    const uint16_t* weight;    // [dim]
+    uint16_t* out;             // [rows, dim], rows out_stride elements apart, or null
+    uint8_t* codes;            // [rows, dim] E4M3, or null
+    void* scale;               // fp32 [rows] or [rows, dim / 128], or E8M0 bytes [rows, dim / 32]
+    int64_t x_stride;
+    int64_t out_stride;
+    int32_t rows;
+    int32_t dim;
+    int32_t group;  // elements per scale, 0: the row
+    int32_t mx;     // E8M0 scales
+    float eps;
+};
+cudaError_t launch_norm(const NormParams& p, cudaStream_t stream);
+
+// ---- products of every head with its weights (latent attention, absorbed form) --------------------------
+constexpr int kHeadNope = 128;   // a head's unrotated key dims
+constexpr int kHeadValue = 128;  // a head's value dims
+struct HeadsParams {
+    int32_t* err;
+    int32_t total_q;
+    int32_t heads;
+    int32_t values;  // latent outputs to head values, or (0) queries to latent space
+    int32_t tiles;   // of 128 tokens (launch_heads)
+    int64_t units;   // tiles x slabs of weights (launch_heads)
+    uint64_t wait_ns;
+};
+struct HeadsLaunch {
+    CUtensorMap amap;  // 3-D view [T][Hq][inner dims] of the tokens' rows: 64 dims of 128 tokens of a head
+    CUtensorMap wmap;  // 3-D view [Hq][256][512] of the weights: 64 columns of 64 (absorb) or 128 rows
+    CUtensorMap omap;  // 3-D view [T][Hq][output dims]: 64 dims of 32 tokens of a head
+    HeadsParams params;
+    int num_sms;
+};
+cudaError_t launch_heads(const HeadsLaunch& launch, cudaStream_t stream);
+
+// ---- causal attention with expanded keys and values (latent attention, expanded form) --------------------
+constexpr int kExpandTileBytes = 9 * 128 * 128;      // latent and rotary parts of 128 positions
+constexpr int kExpandHeadTileBytes = 4 * 128 * 128;  // keys (without their rotary part) and values of 128 positions of a head
+constexpr int kExpandBlockRows = 256;                // queries of a block
+// int32 in front of the plan's list of blocks
+__host__ __device__ constexpr int64_t expand_plan_ints(int32_t batch) { return ((int64_t)2 * batch + 5 + 3) / 4 * 4; }
+struct ExpandParams {
+    const uint8_t* kv_cache;  // bf16 rows, or FP8 rows of kKvFp8RowBytes
+    const int32_t* page_table;
+    const int32_t* seq_lens;
+    const int32_t* cu_q_lens;
+    uint16_t* out;  // [T, Hq, 128] bf16 bits
+    float* lse;     // [T, Hq] or null
+    int32_t* err;
+    int32_t batch;
+    int32_t total_q;
+    int32_t num_pages;
+    int32_t max_pages;
+    int32_t heads;
+    int32_t kv_fp8;
+    float scale_log2;  // softmax_scale * log2(e)
+    uint64_t wait_ns;
+    // workspace
+    int32_t cap_tiles;   // even
+    int32_t cap_blocks;
+    int32_t* plan;
+    uint8_t* latents;  // [cap_tiles][9][128][64] bf16, 128-byte swizzle
+    uint8_t* kv;       // [cap_tiles][Hq][4] units of 16 KB
+};
+inline size_t expand_plan_bytes(const ExpandParams& p) {
+    return ((size_t)expand_plan_ints(p.batch) * 4 + (size_t)p.cap_blocks * 8 + 1023) / 1024 * 1024;
+}
+struct ExpandLaunch {
+    CUtensorMap nopemap;  // 3-D view [T][Hq][128] of the queries' unrotated part: 64 dims of 128 tokens of a head
+    CUtensorMap pemap;    // 3-D view [T][Hq][64] of their rotary part
+    CUtensorMap cmap;     // 3-D view [cap_tiles * 9][128][64] of the gathered tiles, as they lie
+    CUtensorMap wmap;     // 3-D view [Hq][256][512] of the weights: 64 columns of 128 rows
+    ExpandParams params;
+    int num_sms;
+};
+cudaError_t launch_expand(const ExpandLaunch& launch, cudaStream_t stream);
+
 // Sets the message returned by dsa_last_error_message() on this host thread.
 void set_last_error(const char* message);
 
