@@ -286,7 +286,7 @@ bool expand_sizes(const dsa_dims_t* d, int32_t total_pages, dsa::ExpandParams* p
     p->heads = d->attn_heads;
     p->cap_tiles = (int32_t)tiles;
     p->cap_blocks = (int32_t)blocks;
-    *bytes = dsa::expand_plan_bytes(*p) + (size_t)tiles * dsa::kExpandTileBytes +
+    *bytes = dsa::expand_plan_bytes(*p) + dsa::kExpandPartBytes + (size_t)tiles * dsa::kExpandTileBytes +
              (size_t)tiles * d->attn_heads * dsa::kExpandHeadTileBytes;
     return true;
 }
@@ -1087,7 +1087,9 @@ dsa_status_t dsa_expanded_attn(const dsa_dims_t* d, int32_t total_pages, const v
     p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     uint8_t* ws = static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea;
     p.plan = reinterpret_cast<int32_t*>(ws);
-    p.latents = ws + dsa::expand_plan_bytes(p);
+    p.ctas = dev.num_sms < dsa::kExpandCtas ? dev.num_sms : dsa::kExpandCtas;
+    p.partial = reinterpret_cast<float*>(ws + dsa::expand_plan_bytes(p));
+    p.latents = ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes;
     p.kv = p.latents + (size_t)p.cap_tiles * dsa::kExpandTileBytes;
     L.num_sms = dev.num_sms;
     const uint64_t T = (uint64_t)d->total_q, H = (uint64_t)d->attn_heads;

@@ -10,12 +10,14 @@
 // head) 2 x 256 x 512 for its keys and values, so this is the form for many queries a sequence.  Keys and values are
 // rounded to bf16, as a projection would leave them.
 //
-// Four kernels, chained by programmatic launches:
+// Five kernels, chained by programmatic launches:
 //   plan:    where each sequence's positions lie (tiles of 128, a sequence's own) and the list of blocks of 256 queries;
 //   gather:  the pages' rows as tiles of nine 16 KB pieces (64 dims of 128 positions, FP8 rows as bf16; zeros behind the
 //            last position), the layout that the tensor cores read (128-byte swizzle);
 //   keys:    K and V = W c: a matrix product of all tiles and heads, CTA pairs (256 positions x a head's 256 rows);
-//   attend:  a CTA takes 256 queries of a head as two tiles of 128 that share K and V.
+//   attend:  a CTA takes 256 queries of a head as two tiles of 128 that share K and V; all such items, each as long as its
+//            tiles of keys, are cut into equal parts, one for each CTA, or (where there are many) taken whole in turn;
+//   combine: the results of items that were cut.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -35,18 +37,31 @@ constexpr int kHeadTile = kExpandHeadTileBytes;  // keys (two units) and values 
 constexpr int kBlockRows = kExpandBlockRows;
 
 // What the plan kernel leaves, at the start of the plan area (int32), tile_begin [batch + 1], first_bad [batch], then
-// blocks, an int2 each.
+// blocks, an int2 each (sequence, first query), and cost, the places of the blocks before each (one more than blocks).
 struct PlanHead {
     int32_t tiles;    // in use
     int32_t blocks;   // in the list
-    int32_t counter;  // work items handed out
-    int32_t unused;
+    int32_t counter;  // whole items handed out
+    int32_t parts;    // the line of items is cut in so many parts; 0: whole items
+    int32_t group;    // whole items: heads that are worked on together
+    int32_t unused[3];
 };
 __device__ __forceinline__ PlanHead* plan_head(const ExpandParams& p) { return reinterpret_cast<PlanHead*>(p.plan); }
-__device__ __forceinline__ int32_t* tile_begin(const ExpandParams& p) { return p.plan + 4; }
+__device__ __forceinline__ int32_t* tile_begin(const ExpandParams& p) { return p.plan + sizeof(PlanHead) / 4; }
 // First position of a sequence that has no finite values or no page (INT32_MAX: none): rows that see it are NaN.
-__device__ __forceinline__ int32_t* first_bad(const ExpandParams& p) { return p.plan + 4 + p.batch + 1; }
+__device__ __forceinline__ int32_t* first_bad(const ExpandParams& p) { return tile_begin(p) + p.batch + 1; }
 __device__ __forceinline__ int2* blocks(const ExpandParams& p) { return reinterpret_cast<int2*>(p.plan + expand_plan_ints(p.batch)); }
+__device__ __forceinline__ int32_t* cost(const ExpandParams& p) { return reinterpret_cast<int32_t*>(blocks(p) + p.cap_blocks); }
+
+// A block's place on the line: kItemCost places for what it costs beside its tiles (its queries' load, its first scores'
+// latency, its result), then one for each tile of keys.  kMinPlaces: a part is no shorter on average.  kWholeItems: items
+// are taken whole where the longest is no more than that part of a CTA's share (whole items of a head meet its keys in
+// L2, and have nothing to combine).
+constexpr int kItemCost = 2;
+constexpr int kMinPlaces = 4;
+constexpr int kWholeItems = 8;
+constexpr int64_t kGroupBytes = 48 << 20;  // keys and values of heads that are worked on together
+__device__ __forceinline__ int tiles_before(int place, int n) { return min(n, max(0, place - kItemCost)); }
 
 __device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2^-22; exp2(-inf) = +0
     float y;
@@ -66,6 +81,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // plan: one block.  Every thread counts a run of sequences; a scan of the threads' sums numbers tiles and blocks.
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Queries and positions of sequence b; false when they are inconsistent.
 __device__ __forceinline__ bool sequence(const ExpandParams& p, int b, int* c0, int* n, int* L) {
@@ -79,70 +95,87 @@ __device__ __forceinline__ bool sequence(const ExpandParams& p, int b, int* c0, 
     return *n <= *L && (int64_t)*L <= (int64_t)p.max_pages * 64 && *L <= INT32_MAX - 255;
 }
 
+// Tiles of keys that a block of n queries from position pos0 sees.
+__device__ __forceinline__ int tiles_seen(int pos0, int n) { return (pos0 + n + 127) / 128; }
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpandParams p) {
-    __shared__ long long scan[2][kPlanThreads / 32];
+    __shared__ long long scan[3][kPlanWarps];
+    __shared__ int longest[kPlanWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_dependency_wait();
     allow_dependent_launch();
     const int run = (p.batch + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(p.batch, tid * run), b1 = min(p.batch, b0 + run);
-    long long tiles = 0, count = 0;
+    long long sum[3] = {0, 0, 0};  // tiles, blocks, places
+    int most = 0;
     for (int b = b0; b < b1; ++b) {
         int c0, n, L;
         if (!sequence(p, b, &c0, &n, &L)) {
             raise_error(p.err, DSA_DEVERR_SEQ);
             continue;
         }
-        if (n > 0) {
-            tiles += (L + 127) / 128;
-            count += (n + kBlockRows - 1) / kBlockRows;
-        }
+        if (n == 0) continue;
+        sum[0] += (L + 127) / 128;
+        sum[1] += (n + kBlockRows - 1) / kBlockRows;
+        for (int q = 0; q < n; q += kBlockRows) sum[2] += kItemCost + tiles_seen(L - n + q, min(kBlockRows, n - q));
+        most = max(most, kItemCost + (L + 127) / 128);
     }
-    long long ti = tiles, ci = count;
+    long long incl[3] = {sum[0], sum[1], sum[2]};
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long to = __shfl_up_sync(kAllLanes, ti, off), co = __shfl_up_sync(kAllLanes, ci, off);
-        if (lane >= off) {
-            ti += to;
-            ci += co;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const long long o = __shfl_up_sync(kAllLanes, incl[i], off);
+            if (lane >= off) incl[i] += o;
         }
+        most = max(most, __shfl_xor_sync(kAllLanes, most, off));
     }
     if (lane == 31) {
-        scan[0][warp] = ti;
-        scan[1][warp] = ci;
+        for (int i = 0; i < 3; ++i) scan[i][warp] = incl[i];
+        longest[warp] = most;
     }
     __syncthreads();
-    long long at = ti - tiles, block = ci - count, all_tiles = 0, all_blocks = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) {
-            at += scan[0][w];
-            block += scan[1][w];
+    long long before[3], all[3] = {0, 0, 0};
+    for (int i = 0; i < 3; ++i) {
+        before[i] = incl[i] - sum[i];
+        for (int w = 0; w < kPlanWarps; ++w) {
+            if (w < warp) before[i] += scan[i][w];
+            all[i] += scan[i][w];
         }
-        all_tiles += scan[0][w];
-        all_blocks += scan[1][w];
     }
+    for (int w = 0; w < kPlanWarps; ++w) most = max(most, longest[w]);
     for (int b = b0; b < b1; ++b) {
         int c0, n, L;
         const bool ok = sequence(p, b, &c0, &n, &L) && n > 0;
         const int mine = ok ? (L + 127) / 128 : 0, parts = ok ? (n + kBlockRows - 1) / kBlockRows : 0;
         // (more pages than were announced, or offsets that run backwards: left out)
-        const bool fits = at + mine <= p.cap_tiles && block + parts <= p.cap_blocks;
+        const bool fits = before[0] + mine <= p.cap_tiles && before[1] + parts <= p.cap_blocks;
         if (ok && !fits) raise_error(p.err, DSA_DEVERR_SEQ);
-        tile_begin(p)[b] = (int32_t)(at < p.cap_tiles ? at : p.cap_tiles);
+        tile_begin(p)[b] = (int32_t)(before[0] < p.cap_tiles ? before[0] : p.cap_tiles);
         first_bad(p)[b] = INT32_MAX;
-        for (int i = 0; i < parts && block + i < p.cap_blocks; ++i)
-            blocks(p)[block + i] = make_int2(fits ? b : -1, i * kBlockRows);
-        at += mine;
-        block += parts;
+        for (int i = 0; i < parts && before[1] + i < p.cap_blocks; ++i) {
+            const int q = i * kBlockRows;
+            blocks(p)[before[1] + i] = make_int2(fits ? b : -1, q);
+            cost(p)[before[1] + i] = (int32_t)before[2];
+            before[2] += kItemCost + tiles_seen(L - n + q, min(kBlockRows, n - q));
+        }
+        before[0] += mine;
+        before[1] += parts;
     }
     if (tid == 0) {
+        // (what does not fit leaves places that nobody works on)
         PlanHead h;
-        h.tiles = (int32_t)(all_tiles < p.cap_tiles ? all_tiles : p.cap_tiles);
-        h.blocks = (int32_t)(all_blocks < p.cap_blocks ? all_blocks : p.cap_blocks);
+        h.tiles = (int32_t)(all[0] < p.cap_tiles ? all[0] : p.cap_tiles);
+        h.blocks = (int32_t)(all[1] < p.cap_blocks ? all[1] : p.cap_blocks);
         h.counter = 0;
-        h.unused = 0;
+        const long long line = all[2] * p.heads;
+        h.parts = (int32_t)(line / kMinPlaces < p.ctas ? max(1LL, line / kMinPlaces) : p.ctas);
+        if (all[1] > p.cap_blocks || all[2] > INT32_MAX || line >= (long long)kWholeItems * p.ctas * most) h.parts = 0;
+        const long long head_bytes = max(1LL, (long long)h.tiles * kHeadTile);
+        h.group = (int32_t)max(1LL, min((long long)p.heads, kGroupBytes / head_bytes));
         *plan_head(p) = h;
         tile_begin(p)[p.batch] = h.tiles;
+        if (h.parts > 0) cost(p)[h.blocks] = (int32_t)all[2];
         if (p.cu_q_lens[0] != 0 || p.cu_q_lens[p.batch] != p.total_q) raise_error(p.err, DSA_DEVERR_SEQ);
     }
 }
@@ -416,23 +449,62 @@ constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
 constexpr uint32_t kIdescPV = make_idesc(128, 128, 1, 1, 0, 1);
 constexpr float kRaise = 8.f;  // the running maximum (log2) is raised only when it grows by more than this
 
-struct AttendItem {
-    int32_t row0, nrows;  // query tokens (none: no more items)
+// What a CTA works on at a time: a block of queries of a head, with the tiles of keys from j0 to j1 (all of them, or a part)
+struct Segment {
+    int32_t row0, nrows;  // query tokens (none: no more segments)
     int32_t head, seq;
     int32_t pos0;         // position of the first
     int32_t tile0;        // first tile of the sequence's keys
     int32_t n0, n1;       // tiles that queries 0-127, 128-255 see
+    int32_t j0, j1;
 };
+constexpr int kSegments = 4;  // in flight between the roles of a CTA
 struct AttendCtrl {
     uint64_t q_full[2], q_empty[2];
     uint64_t full[kRing], empty[kRing];
     uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
-    uint64_t item_full[2], item_empty[2];
+    uint64_t seg_full[kSegments], seg_empty[kSegments];
     uint64_t drained;
     uint32_t tmem_base;
     int32_t failed;
-    AttendItem items[2];
+    Segment segments[kSegments];
 };
+// Query tile w's tiles of a segment: from j0 to here.
+__device__ __forceinline__ int seg_end(const Segment& s, int w) { return min(s.j1, w == 0 ? s.n0 : s.n1); }
+
+// The block of a head at place x of its line (the last one that begins no later).  Called by a whole warp.
+__device__ __forceinline__ int block_at(const ExpandParams& p, int n_blocks, int x, int lane) {
+    const int32_t* c = cost(p);
+    int lo = 0, n = n_blocks;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + step * lane;
+        const uint32_t le = __ballot_sync(kAllLanes, step * lane < n && c[at] <= x);  // (lane 0's always)
+        const int k = 31 - __clz(le);
+        lo += step * k;
+        n = min(step, n - step * k);
+    }
+    return lo;
+}
+// Rows, keys and tiles of block i of a head; false for a block that is left out.
+__device__ __forceinline__ bool block_rows(const ExpandParams& p, int i, Segment* s) {
+    const int2 blk = blocks(p)[i];
+    if (blk.x < 0) return false;
+    const int c0 = p.cu_q_lens[blk.x], n = p.cu_q_lens[blk.x + 1] - c0;
+    s->seq = blk.x;
+    s->row0 = c0 + blk.y;
+    s->nrows = min(kBlockRows, n - blk.y);
+    s->pos0 = p.seq_lens[blk.x] - n + blk.y;
+    s->tile0 = tile_begin(p)[blk.x];
+    s->n0 = tiles_seen(s->pos0, min(s->nrows, 128));
+    s->n1 = s->nrows > 128 ? tiles_seen(s->pos0, s->nrows) : 0;
+    return true;
+}
+// Part k of a line of W places cut in G parts starts here.
+__device__ __forceinline__ int64_t part_begin(int64_t k, int64_t W, int64_t G) { return k * W / G; }
+// Where CTA c leaves a part of an item: at most its first and its last segment are parts, and the last begins its item.
+__device__ __forceinline__ float* part_slot(const ExpandParams& p, int c, bool first_tile) {
+    return p.partial + (int64_t)(2 * c + (first_tile ? 1 : 0)) * kExpandPartFloats;
+}
 constexpr int kAttendSmem = 1024 + 2 * kQTile + kRing * kUnit + (int)sizeof(AttendCtrl);
 static_assert(kAttendSmem <= 232448, "shared memory of one CTA");
 
@@ -453,8 +525,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             mbar_init(&ctl->p_full[i], 4);
             mbar_init(&ctl->o_full[i], 1);
             mbar_init(&ctl->o_free[i], 4);
-            mbar_init(&ctl->item_full[i], 1);
-            mbar_init(&ctl->item_empty[i], 9);  // the softmax warps and the products'
+        }
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(&ctl->seg_full[i], 1);
+            mbar_init(&ctl->seg_empty[i], 9);  // the softmax warps and the products'
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&ctl->full[i], 1);
@@ -477,151 +551,197 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(kAllLanes, mbar_wait(bar, parity, p.err, p.wait_ns)) != 0;
     };
-    // item number n of this CTA, once it is there; false: gave up
-    auto next_item = [&](uint32_t n, AttendItem* it) {
-        if (!wait(&ctl->item_full[n & 1u], (n >> 1) & 1u)) return false;
-        *it = ctl->items[n & 1u];
+    // segment number n of this CTA, once it is there; false: gave up.  With the last look at it, it is given back.
+    auto next_segment = [&](uint32_t n, Segment* s) {
+        if (!wait(&ctl->seg_full[n % kSegments], (n / kSegments) & 1u)) return false;
+        *s = ctl->segments[n % kSegments];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->item_empty[n & 1u]);
+        if (lane == 0) mbar_arrive(&ctl->seg_empty[n % kSegments]);
         return true;
     };
     bool ok = true;
 
     if (warp == kLoadWarp) {
-        // ---------------- items, and what each needs in the order of its use ----------------
-        const int n_blocks = plan_head(p)->blocks;
-        const int64_t n_items = (int64_t)n_blocks * p.heads;
-        uint32_t n = 0, u = 0, used[2] = {0, 0};  // items, units, items that used each query tile
-        while (ok) {
-            // heads one after another, so that a head's keys stay in L2 for its blocks; the last blocks (the most keys) first
-            AttendItem it;
-            it.nrows = 0;
-            int index = 0;
-            if (lane == 0) index = atomicAdd(&plan_head(p)->counter, 1);
-            index = __shfl_sync(kAllLanes, index, 0);
-            if (index < n_items) {
-                const int2 blk = blocks(p)[n_blocks - 1 - index % n_blocks];
-                if (blk.x < 0) continue;
-                const int c0 = p.cu_q_lens[blk.x], nq = p.cu_q_lens[blk.x + 1] - c0;
-                it.head = index / n_blocks;
-                it.seq = blk.x;
-                it.row0 = c0 + blk.y;
-                it.nrows = min(kBlockRows, nq - blk.y);
-                it.pos0 = p.seq_lens[blk.x] - nq + blk.y;
-                it.tile0 = tile_begin(p)[blk.x];
-                it.n0 = (it.pos0 + min(it.nrows, 128) + 127) / 128;
-                it.n1 = it.nrows > 128 ? (it.pos0 + it.nrows + 127) / 128 : 0;
-            }
-            if (!(ok = wait(&ctl->item_empty[n & 1u], ((n >> 1) & 1u) ^ 1u))) break;
+        // ---------------- segments, and what each needs in the order of its use ----------------
+        const PlanHead plan = *plan_head(p);
+        uint32_t n = 0, u = 0, used[2] = {0, 0};  // segments, units, segments that used each query tile
+        auto publish = [&](const Segment& s) {
+            if (!wait(&ctl->seg_empty[n % kSegments], ((n / kSegments) & 1u) ^ 1u)) return false;
             if (lane == 0) {
-                ctl->items[n & 1u] = it;
-                mbar_arrive(&ctl->item_full[n & 1u]);
+                ctl->segments[n % kSegments] = s;
+                mbar_arrive(&ctl->seg_full[n % kSegments]);
             }
             __syncwarp();
             ++n;
-            if (it.nrows == 0) break;
-            const uint8_t* kv = p.kv + ((int64_t)it.tile0 * p.heads + it.head) * kHeadTile;
-            const uint8_t* rotary = p.latents + (int64_t)it.tile0 * kTileBytes + 8 * kUnit;
-            const int tiles = max(it.n0, it.n1);
+            return true;
+        };
+        auto load = [&](const Segment& s) {
+            const uint8_t* kv = p.kv + ((int64_t)s.tile0 * p.heads + s.head) * kHeadTile;
+            const uint8_t* rotary = p.latents + (int64_t)s.tile0 * kTileBytes + 8 * kUnit;
             auto load_q = [&](int w) {
                 if (!wait(&ctl->q_empty[w], (used[w] & 1u) ^ 1u)) return false;
                 ++used[w];
                 if (elect_one_sync()) {
                     mbar_arrive_expect_tx(&ctl->q_full[w], kQTile);
                     uint8_t* dst = smem + w * kQTile;
-                    tma_load_3d(dst, &nopemap, &ctl->q_full[w], 0, it.head, it.row0 + 128 * w);
-                    tma_load_3d(dst + kUnit, &nopemap, &ctl->q_full[w], 64, it.head, it.row0 + 128 * w);
-                    tma_load_3d(dst + 2 * kUnit, &pemap, &ctl->q_full[w], 0, it.head, it.row0 + 128 * w);
+                    tma_load_3d(dst, &nopemap, &ctl->q_full[w], 0, s.head, s.row0 + 128 * w);
+                    tma_load_3d(dst + kUnit, &nopemap, &ctl->q_full[w], 64, s.head, s.row0 + 128 * w);
+                    tma_load_3d(dst + 2 * kUnit, &pemap, &ctl->q_full[w], 0, s.head, s.row0 + 128 * w);
                 }
                 return true;
             };
-            if (!(ok = load_q(0))) break;
-            for (int j = 0; ok && j < tiles; ++j) {
+            const bool have0 = s.j0 < s.n0, have1 = s.j0 < s.n1;
+            if (have0 && !load_q(0)) return false;
+            for (int j = s.j0; j < s.j1; ++j) {
                 const uint8_t* tile = kv + (int64_t)j * p.heads * kHeadTile;
 #pragma unroll 1
                 for (int k = 0; k < kTileUnits; ++k, ++u) {
                     const uint32_t slot = u % kRing;
-                    if (!(ok = wait(&ctl->empty[slot], ((u / kRing) & 1u) ^ 1u))) break;
+                    if (!wait(&ctl->empty[slot], ((u / kRing) & 1u) ^ 1u)) return false;
                     if (elect_one_sync()) {
                         const uint8_t* src = k == 2 ? rotary + (int64_t)j * kTileBytes : tile + (k < 2 ? k : k - 1) * kUnit;
                         mbar_arrive_expect_tx(&ctl->full[slot], kUnit);
                         bulk_copy_g2s(ring + slot * kUnit, src, kUnit, &ctl->full[slot]);
                     }
-                    if (j == 0 && k == 2 && it.n1 > 0 && !(ok = load_q(1))) break;
+                    if (j == s.j0 && k == 2 && have1 && !load_q(1)) return false;
                 }
             }
+            return true;
+        };
+        // A segment is looked up and published before the one in front of it is loaded for, so that nobody waits for that.
+        Segment s, published;
+        published.nrows = 0;
+        auto work = [&](const Segment& s) {
+            if (!publish(s) || (published.nrows > 0 && !load(published))) return false;
+            published = s;
+            return true;
+        };
+        if (plan.parts > 0) {
+            // this CTA's part of the line: the blocks of head 0, of head 1, ...
+            const int64_t head_line = cost(p)[plan.blocks], line = head_line * p.heads;
+            const int64_t x1 = part_begin(blockIdx.x + 1, line, plan.parts);
+            int64_t x = part_begin(blockIdx.x, line, plan.parts);
+            if ((int)blockIdx.x >= plan.parts) x = x1;
+            int block = -1;
+            while (ok && x < x1) {
+                s.head = (int)(x / head_line);
+                const int at = (int)(x - s.head * head_line);
+                if (block < 0) block = block_at(p, plan.blocks, at, lane);
+                const int begin = cost(p)[block], end = cost(p)[block + 1], n_tiles = end - begin - kItemCost;
+                const int64_t left = x1 - s.head * head_line;  // the part's end on this head's line
+                s.j0 = tiles_before(at - begin, n_tiles);
+                s.j1 = left >= end ? n_tiles : tiles_before((int)left - begin, n_tiles);
+                if (s.j1 > s.j0 && block_rows(p, block, &s)) ok = work(s);
+                x = s.head * head_line + end;
+                block = block + 1 < plan.blocks ? block + 1 : 0;
+            }
+        } else {
+            // Whole items, as CTAs become free.  Heads in groups whose keys fit L2; in a group the last blocks (of a sequence
+            // the ones with the most keys) first.
+            const int64_t n_items = (int64_t)plan.blocks * p.heads, group_items = (int64_t)plan.blocks * plan.group;
+            while (ok) {
+                int64_t index = 0;
+                if (lane == 0) index = atomicAdd(&plan_head(p)->counter, 1);
+                index = __shfl_sync(kAllLanes, index, 0);
+                if (index >= n_items) break;
+                const int group = (int)(index / group_items), rest = (int)(index - group * group_items);
+                const int heads = min(plan.group, p.heads - group * plan.group);
+                s.head = group * plan.group + rest % heads;
+                if (!block_rows(p, plan.blocks - 1 - rest / heads, &s)) continue;
+                s.j0 = 0;
+                s.j1 = max(s.n0, s.n1);
+                ok = work(s);
+            }
         }
+        s.nrows = 0;
+        if (ok) ok = work(s);
     } else if (warp == kProductWarp) {
         // ---------------- S_w(j) = Q_w K(j)^T and O_w += P_w(j) V(j), the two query tiles in turn ----------------
-        const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-        const uint64_t kd = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
-        const uint64_t vd = smem_desc(smem_u32(ring), kUnit / 2, 1024, kSwizzle128B);  // MN-major, dims 64.. half a unit on
-        uint32_t u = 0, used[2] = {0, 0}, tiles_done[2] = {0, 0};
-        for (uint32_t n = 0; ok; ++n) {
-            AttendItem it;
-            if (!(ok = next_item(n, &it)) || it.nrows == 0) break;
-            const int tiles = max(it.n0, it.n1);
-            auto count = [&](int w) { return w == 0 ? it.n0 : it.n1; };
-            // the ring's unit k of tile j (K: 0-2, V: 3, 4)
-            auto qk = [&](int w, int j) {
-                if (j >= count(w)) return true;
-                if (j == 0 && !wait(&ctl->q_full[w], used[w] & 1u)) return false;
-                const bool other = w == 0 && j < it.n1;  // the other query tile reads these keys, too
-#pragma unroll 1
-                for (int k = 0; k < 3; ++k) {
-                    const uint32_t at = u + kTileUnits * j + k, slot = at % kRing;
-                    if (!wait(&ctl->full[slot], (at / kRing) & 1u)) return false;
-                    tc_fence_after();
-                    if (elect_one_sync()) {
-                        const uint64_t a = qd + (uint64_t)((w * kQTile + k * kUnit) / 16), b = kd + (uint64_t)(slot * (kUnit / 16));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f16_ss(tmem + 128 * w, a + (uint64_t)(2 * kk), b + (uint64_t)(2 * kk), kIdescQK,
-                                        k == 0 && kk == 0 ? 0u : 1u);
-                        if (!other) umma_commit(&ctl->empty[slot]);
-                        if (k == 2) {
-                            umma_commit(&ctl->s_full[w]);
-                            if (j == count(w) - 1) umma_commit(&ctl->q_empty[w]);
-                        }
-                    }
-                }
-                return true;
-            };
-            auto pv = [&](int w, int j) {
-                if (j >= count(w)) return true;
-                if (!wait(&ctl->p_full[w], tiles_done[w] & 1u)) return false;
-                ++tiles_done[w];
-                if (j == 0 && !wait(&ctl->o_free[w], (used[w] & 1u) ^ 1u)) return false;
-                const bool other = w == 0 && j < it.n1, last = j == count(w) - 1;
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t at = u + kTileUnits * j + 3 + k, slot = at % kRing;
-                    if (!wait(&ctl->full[slot], (at / kRing) & 1u)) return false;
-                    tc_fence_after();
-                    if (elect_one_sync()) {
-                        const uint64_t b = vd + (uint64_t)(slot * (kUnit / 16));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f16_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 32 * k + 8 * kk, b + (uint64_t)(128 * kk),
-                                        kIdescPV, j == 0 && k == 0 && kk == 0 ? 0u : 1u);
-                        if (!other) umma_commit(&ctl->empty[slot]);
-                        if (k == 1 && last) umma_commit(&ctl->o_full[w]);
-                    }
-                }
-                return true;
-            };
-            ok = qk(0, 0) && qk(1, 0);
-            for (int j = 0; ok && j < tiles; ++j) ok = pv(0, j) && qk(0, j + 1) && pv(1, j) && qk(1, j + 1);
-            u += kTileUnits * tiles;
-            ++used[0];
-            if (it.n1 > 0) ++used[1];
-        }
-        // drain (default limit): every product is done before its memory is given back
+        // The steps of all segments form one row: a step's scores are asked for between the products of the weights of the
+        // step before it, also where that is the last of another segment.  One thread does it all: with waits and elections
+        // of the whole warp a unit's four products took 440 cycles to issue, and to be done 256.
         if (elect_one_sync()) {
+            auto wait_one = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, p.err, p.wait_ns); };
+            const uint64_t qd = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+            const uint64_t kd = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+            const uint64_t vd = smem_desc(smem_u32(ring), kUnit / 2, 1024, kSwizzle128B);  // MN-major, dims 64.. half a unit on
+            uint32_t segs[2] = {0, 0}, tiles_done[2] = {0, 0};
+            struct Step {
+                uint32_t u;              // its first unit
+                bool have[2];            // which query tiles have it
+                bool first[2], last[2];  // of its segment
+            };
+            auto qk = [&](int w, const Step& t) {
+                if (!t.have[w]) return true;
+                if (t.first[w] && !wait_one(&ctl->q_full[w], segs[w] & 1u)) return false;
+                const bool shared = t.have[w ^ 1];  // the other query tile reads these keys, too: the first waits, the second frees
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const uint32_t at = t.u + k, slot = at % kRing;
+                    if ((w == 0 || !shared) && !wait_one(&ctl->full[slot], (at / kRing) & 1u)) return false;
+                    if (k == 0) tc_fence_after();
+                    const uint64_t a = qd + (uint64_t)((w * kQTile + k * kUnit) / 16), b = kd + (uint64_t)(slot * (kUnit / 16));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ss(tmem + 128 * w, a + (uint64_t)(2 * kk), b + (uint64_t)(2 * kk), kIdescQK,
+                                    k == 0 && kk == 0 ? 0u : 1u);
+                    if (k == 2) umma_commit(&ctl->s_full[w]);
+                    if (w == 1 || !shared) umma_commit(&ctl->empty[slot]);
+                }
+                if (t.last[w]) umma_commit(&ctl->q_empty[w]);
+                return true;
+            };
+            auto pv = [&](int w, const Step& t) {
+                if (!t.have[w]) return true;
+                if (!wait_one(&ctl->p_full[w], tiles_done[w] & 1u)) return false;
+                ++tiles_done[w];
+                if (t.first[w] && !wait_one(&ctl->o_free[w], (segs[w] & 1u) ^ 1u)) return false;
+                const bool shared = t.have[w ^ 1];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t at = t.u + 3 + k, slot = at % kRing;
+                    if ((w == 0 || !shared) && !wait_one(&ctl->full[slot], (at / kRing) & 1u)) return false;
+                    if (k == 0) tc_fence_after();
+                    const uint64_t b = vd + (uint64_t)(slot * (kUnit / 16));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_f16_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 32 * k + 8 * kk, b + (uint64_t)(128 * kk), kIdescPV,
+                                    t.first[w] && k == 0 && kk == 0 ? 0u : 1u);
+                    if (w == 1 || !shared) umma_commit(&ctl->empty[slot]);
+                }
+                if (t.last[w]) {
+                    umma_commit(&ctl->o_full[w]);
+                    ++segs[w];
+                }
+                return true;
+            };
+            uint32_t u = 0;
+            Step before;
+            before.have[0] = before.have[1] = false;
+            for (uint32_t n = 0; ok; ++n) {
+                if (!(ok = wait_one(&ctl->seg_full[n % kSegments], (n / kSegments) & 1u))) break;
+                const Segment s = ctl->segments[n % kSegments];
+                mbar_arrive(&ctl->seg_empty[n % kSegments]);
+                if (s.nrows == 0) break;
+                for (int j = s.j0; ok && j < s.j1; ++j, u += kTileUnits) {
+                    Step now;
+                    now.u = u;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        now.have[w] = j < seg_end(s, w);
+                        now.first[w] = j == s.j0;
+                        now.last[w] = j == seg_end(s, w) - 1;
+                    }
+                    ok = pv(0, before) && qk(0, now) && pv(1, before) && qk(1, now);
+                    before = now;
+                }
+            }
+            ok = ok && pv(0, before) && pv(1, before);
+            // drain (default limit): every product is done before its memory is given back
             umma_commit(&ctl->drained);
             mbar_wait(&ctl->drained, 0, p.err);
         }
-        __syncwarp();
+        ok = __all_sync(kAllLanes, ok);
     } else {
         // ---------------- softmax: a thread has a query of its warp group's tile ----------------
         const int w = warp >> 2, r = tid & 127;
@@ -629,14 +749,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const uint32_t scol = trow + 128 * w, ocol = trow + kOCol + 128 * w;
         uint32_t tile = 0, used = 0;
         for (uint32_t n = 0; ok; ++n) {
-            AttendItem it;
-            if (!(ok = next_item(n, &it)) || it.nrows == 0) break;
-            const int tiles = w == 0 ? it.n0 : it.n1;
-            if (tiles == 0) continue;
+            Segment it;
+            if (!(ok = next_segment(n, &it)) || it.nrows == 0) break;
+            const int row = 128 * w + r, end = seg_end(it, w);
+            const bool part = it.j0 > 0 || it.j1 < max(it.n0, it.n1);
+            float* slot = part_slot(p, blockIdx.x, it.j0 == 0);
+            if (end <= it.j0) {  // nothing for this query tile
+                if (part && row < it.nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(-INFINITY, 0.f);
+                continue;
+            }
             const int first = it.pos0 + 128 * w, limit = first + r + 1;  // positions this query sees: below `limit`
             float m_used = -INFINITY, l_sum = 0.f;
 #pragma unroll 1
-            for (int j = 0; j < tiles; ++j, ++tile) {
+            for (int j = it.j0; j < end; ++j, ++tile) {
                 if (!(ok = wait(&ctl->s_full[w], tile & 1u))) break;
                 tc_fence_after();
                 float s[8][16];
@@ -709,29 +834,49 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             if (!(ok = wait(&ctl->o_full[w], used & 1u))) break;
             ++used;
             tc_fence_after();
-            if (*const_cast<volatile int32_t*>(first_bad(p) + it.seq) < limit) l_sum = NAN;
-            const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
-            const int row = 128 * w + r;
-            const int64_t at = (int64_t)(it.row0 + row) * p.heads + it.head;
-            uint4* dst = reinterpret_cast<uint4*>(p.out + at * 128);
+            if (part) {
+                float4* dst = reinterpret_cast<float4*>(slot + row * 128);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                float o[2][16];
-                tmem_ld16(ocol + c, o[0]);
-                tmem_ld16(ocol + c + 16, o[1]);
-                tmem_ld_wait();
-                tmem_regs_ready(o[0]);
-                tmem_regs_ready(o[1]);
-                if (row < it.nrows) {
+                for (int c = 0; c < 128; c += 32) {
+                    float o[2][16];
+                    tmem_ld16(ocol + c, o[0]);
+                    tmem_ld16(ocol + c + 16, o[1]);
+                    tmem_ld_wait();
+                    tmem_regs_ready(o[0]);
+                    tmem_regs_ready(o[1]);
+                    if (row < it.nrows) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float* f = &o[k >> 1][8 * (k & 1)];
-                        dst[c / 8 + k] = make_uint4(f2_to_bf2(f[0] * inv, f[1] * inv), f2_to_bf2(f[2] * inv, f[3] * inv),
-                                                    f2_to_bf2(f[4] * inv, f[5] * inv), f2_to_bf2(f[6] * inv, f[7] * inv));
+                        for (int k = 0; k < 8; ++k) {
+                            const float* f = &o[k >> 2][4 * (k & 3)];
+                            dst[c / 4 + k] = make_float4(f[0], f[1], f[2], f[3]);
+                        }
                     }
                 }
+                if (row < it.nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(m_used, l_sum);
+            } else {
+                if (first_bad(p)[it.seq] < limit) l_sum = NAN;
+                const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+                const int64_t at = (int64_t)(it.row0 + row) * p.heads + it.head;
+                uint4* dst = reinterpret_cast<uint4*>(p.out + at * 128);
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    float o[2][16];
+                    tmem_ld16(ocol + c, o[0]);
+                    tmem_ld16(ocol + c + 16, o[1]);
+                    tmem_ld_wait();
+                    tmem_regs_ready(o[0]);
+                    tmem_regs_ready(o[1]);
+                    if (row < it.nrows) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float* f = &o[k >> 1][8 * (k & 1)];
+                            dst[c / 8 + k] = make_uint4(f2_to_bf2(f[0] * inv, f[1] * inv), f2_to_bf2(f[2] * inv, f[3] * inv),
+                                                        f2_to_bf2(f[4] * inv, f[5] * inv), f2_to_bf2(f[6] * inv, f[7] * inv));
+                        }
+                    }
+                }
+                if (row < it.nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
             }
-            if (row < it.nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->o_free[w]);
@@ -750,6 +895,63 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == kProductWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// combine: items that were cut, 32 rows a block, four a warp; of a row's parts (m_k in log2 units, l_k, O_k)
+//   M = max m_k, L = sum_k l_k 2^(m_k - M), out = sum_k 2^(m_k - M) O_k / L, lse = (M + log2 L) ln 2
+// ---------------------------------------------------------------------------------------------------------
+constexpr int kCombineWarps = 8;
+constexpr int kCombineRows = 4 * kCombineWarps;
+
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const ExpandParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x + 1;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const PlanHead plan = *plan_head(p);
+    if (k >= plan.parts) return;
+    // the item in which part k begins; the first part that begins inside it takes care of it
+    const int64_t head_line = cost(p)[plan.blocks], line = head_line * p.heads, x = part_begin(k, line, plan.parts);
+    Segment s;
+    s.head = (int)(x / head_line);
+    const int block = block_at(p, plan.blocks, (int)(x - s.head * head_line), lane);
+    const int64_t begin = s.head * head_line + cost(p)[block];
+    const int n_tiles = cost(p)[block + 1] - cost(p)[block] - kItemCost;
+    auto cut = [&](int part) {  // its tiles in front of a part
+        const int64_t at = part_begin(part, line, plan.parts) - begin;
+        return at >= kItemCost + n_tiles ? n_tiles : at <= 0 ? 0 : tiles_before((int)at, n_tiles);
+    };
+    const int here = cut(k);
+    if (here <= 0 || here >= n_tiles || cut(k - 1) > 0 || !block_rows(p, block, &s)) return;
+    int last = k;
+    while (cut(last + 1) < n_tiles) ++last;
+    const int bad = first_bad(p)[s.seq];
+    for (int i = 0; i < 4; ++i) {
+        const int row = kCombineRows * blockIdx.y + 4 * warp + i;
+        if (row >= s.nrows) return;
+        auto stats = [&](int c) { return reinterpret_cast<const float2*>(part_slot(p, c, c == k - 1) + kBlockRows * 128)[row]; };
+        float M = -INFINITY, L = 0.f;
+        for (int c = k - 1; c <= last; ++c) M = fmaxf(M, stats(c).x);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = k - 1; c <= last; ++c) {
+            const float2 ml = stats(c);
+            const float4 o = reinterpret_cast<const float4*>(part_slot(p, c, c == k - 1) + row * 128)[lane];
+            // (no score above -inf: no weight, unless a NaN is among them; its O may never have been written)
+            const float w = ml.x > -INFINITY ? exp2f(ml.x - M) : ml.y == 0.f ? 0.f : NAN;
+            L += ml.y * w;
+            sum.x += w == 0.f ? 0.f : w * o.x;
+            sum.y += w == 0.f ? 0.f : w * o.y;
+            sum.z += w == 0.f ? 0.f : w * o.z;
+            sum.w += w == 0.f ? 0.f : w * o.w;
+        }
+        if (bad <= s.pos0 + row) L = NAN;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int64_t at = (int64_t)(s.row0 + row) * p.heads + s.head;
+        reinterpret_cast<uint2*>(p.out + at * 128)[lane] =
+            make_uint2(f2_to_bf2(sum.x * inv, sum.y * inv), f2_to_bf2(sum.z * inv, sum.w * inv));
+        if (lane == 0 && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
 }
 
 }  // namespace
@@ -780,11 +982,14 @@ cudaError_t launch_expand(const ExpandLaunch& L, cudaStream_t stream) {
     cfg.blockDim = dim3(kKeysThreads);
     cfg.dynamicSmemBytes = kKeysSmem;
     if ((e = cudaLaunchKernelEx(&cfg, keys_kernel, L.cmap, L.wmap, p)) != cudaSuccess) return e;
-    const int64_t items = (int64_t)p.cap_blocks * p.heads;
-    cfg.gridDim = dim3((unsigned)(items < L.num_sms ? items : L.num_sms));
+    cfg.gridDim = dim3((unsigned)p.ctas);
     cfg.blockDim = dim3(kAttendThreads);
     cfg.dynamicSmemBytes = kAttendSmem;
-    return cudaLaunchKernelEx(&cfg, attend_kernel, L.nopemap, L.pemap, p);
+    if ((e = cudaLaunchKernelEx(&cfg, attend_kernel, L.nopemap, L.pemap, p)) != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)p.ctas, kBlockRows / kCombineRows);
+    cfg.blockDim = dim3(32 * kCombineWarps);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, combine_kernel, p);
 }
 
 }  // namespace dsa

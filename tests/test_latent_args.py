@@ -151,7 +151,8 @@ def test_expanded_workspace_size(L):
     assert dsa.expanded_attn_workspace_size(_dims(), 2 ** 31 - 1) == 256
     size = lambda pages, **kw: dsa.expanded_attn_workspace_size(_dims(**kw), pages)
     tile = 128 * 1152 + 128 * 512 * 128  # 128 positions
-    assert 2 * tile <= size(1, total_q=1) < 3 * tile
+    parts = 2 * 152 * 4 * (256 * 128 + 2 * 256)  # two partial results for each SM
+    assert parts + 2 * tile <= size(1, total_q=1) < parts + 3 * tile
     # every smaller call fits
     largest = size(200, batch=7, total_q=900)
     for pages in (1, 2, 3, 100, 199, 200):
