@@ -60,6 +60,7 @@ __device__ __forceinline__ int32_t* cost(const ExpandParams& p) { return reinter
 constexpr int kItemCost = 2;
 constexpr int kMinPlaces = 4;
 constexpr int kWholeItems = 8;
+constexpr int kCutCost = 8;  // what cutting costs a CTA: writing parts, combining
 constexpr int64_t kGroupBytes = 48 << 20;  // keys and values of heads that are worked on together
 __device__ __forceinline__ int tiles_before(int place, int n) { return min(n, max(0, place - kItemCost)); }
 
@@ -170,7 +171,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpandParams p
         h.counter = 0;
         const long long line = all[2] * p.heads;
         h.parts = (int32_t)(line / kMinPlaces < p.ctas ? max(1LL, line / kMinPlaces) : p.ctas);
-        if (all[1] > p.cap_blocks || all[2] > INT32_MAX || line >= (long long)kWholeItems * p.ctas * most) h.parts = 0;
+        // how long the last CTA takes with whole items (its share and half an item; no more than one item each), and with parts
+        const long long whole = all[1] * p.heads <= p.ctas ? most : line / p.ctas + most / 2, cut = line / h.parts + kCutCost;
+        if (all[1] > p.cap_blocks || all[2] > INT32_MAX || whole <= cut || line >= (long long)kWholeItems * p.ctas * most)
+            h.parts = 0;
         const long long head_bytes = max(1LL, (long long)h.tiles * kHeadTile);
         h.group = (int32_t)max(1LL, min((long long)p.heads, kGroupBytes / head_bytes));
         *plan_head(p) = h;
@@ -902,55 +906,86 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 //   M = max m_k, L = sum_k l_k 2^(m_k - M), out = sum_k 2^(m_k - M) O_k / L, lse = (M + log2 L) ln 2
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kCombineWarps = 8;
-constexpr int kCombineRows = 4 * kCombineWarps;
+constexpr int kRowsPerWarp = 4;
+constexpr int kCombineRows = kRowsPerWarp * kCombineWarps;
+constexpr int kBatches = 2;  // of rows, one after another (all blocks are resident at once)
 
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const ExpandParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x + 1;
-    grid_dependency_wait();
-    allow_dependent_launch();
+    // The plan is older than the attention: its blocks, when they let this kernel start, had waited for the end of what
+    // made it.  So the item is looked up while the attention still runs.  (No block returns before its end, though: what is
+    // launched behind this kernel takes the end of all blocks for the end of the attention.)
     const PlanHead plan = *plan_head(p);
-    if (k >= plan.parts) return;
-    // the item in which part k begins; the first part that begins inside it takes care of it
-    const int64_t head_line = cost(p)[plan.blocks], line = head_line * p.heads, x = part_begin(k, line, plan.parts);
-    Segment s;
-    s.head = (int)(x / head_line);
-    const int block = block_at(p, plan.blocks, (int)(x - s.head * head_line), lane);
-    const int64_t begin = s.head * head_line + cost(p)[block];
-    const int n_tiles = cost(p)[block + 1] - cost(p)[block] - kItemCost;
-    auto cut = [&](int part) {  // its tiles in front of a part
+    const bool part_begins = k < plan.parts;
+    int64_t line = 1, begin = 0;
+    int n_tiles = 0, last = k;
+    auto cut = [&](int part) {  // the item's tiles in front of a part
         const int64_t at = part_begin(part, line, plan.parts) - begin;
         return at >= kItemCost + n_tiles ? n_tiles : at <= 0 ? 0 : tiles_before((int)at, n_tiles);
     };
-    const int here = cut(k);
-    if (here <= 0 || here >= n_tiles || cut(k - 1) > 0 || !block_rows(p, block, &s)) return;
-    int last = k;
-    while (cut(last + 1) < n_tiles) ++last;
+    Segment s;
+    s.nrows = 0;
+    if (part_begins) {
+        // the item in which part k begins; the first part that begins inside it takes care of it
+        const int64_t head_line = cost(p)[plan.blocks];
+        line = head_line * p.heads;
+        const int64_t x = part_begin(k, line, plan.parts);
+        s.head = (int)(x / head_line);
+        const int block = block_at(p, plan.blocks, (int)(x - s.head * head_line), lane);
+        begin = s.head * head_line + cost(p)[block];
+        n_tiles = cost(p)[block + 1] - cost(p)[block] - kItemCost;
+        const int here = cut(k);
+        if (here <= 0 || here >= n_tiles || cut(k - 1) > 0 || !block_rows(p, block, &s)) s.nrows = 0;
+        while (cut(last + 1) < n_tiles) ++last;
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (s.nrows == 0) return;
     const int bad = first_bad(p)[s.seq];
-    for (int i = 0; i < 4; ++i) {
-        const int row = kCombineRows * blockIdx.y + 4 * warp + i;
-        if (row >= s.nrows) return;
-        auto stats = [&](int c) { return reinterpret_cast<const float2*>(part_slot(p, c, c == k - 1) + kBlockRows * 128)[row]; };
-        float M = -INFINITY, L = 0.f;
-        for (int c = k - 1; c <= last; ++c) M = fmaxf(M, stats(c).x);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = k - 1; c <= last; ++c) {
-            const float2 ml = stats(c);
-            const float4 o = reinterpret_cast<const float4*>(part_slot(p, c, c == k - 1) + row * 128)[lane];
-            // (no score above -inf: no weight, unless a NaN is among them; its O may never have been written)
-            const float w = ml.x > -INFINITY ? exp2f(ml.x - M) : ml.y == 0.f ? 0.f : NAN;
-            L += ml.y * w;
-            sum.x += w == 0.f ? 0.f : w * o.x;
-            sum.y += w == 0.f ? 0.f : w * o.y;
-            sum.z += w == 0.f ? 0.f : w * o.z;
-            sum.w += w == 0.f ? 0.f : w * o.w;
+#pragma unroll 1
+    for (int batch = 0; batch < kBatches; ++batch) {
+        const int row0 = kCombineRows * (kBatches * blockIdx.y + batch) + kRowsPerWarp * warp;
+        if (row0 >= s.nrows) return;
+        // all rows' loads of a part are in flight together (rows behind the last are within the slot)
+        auto part = [&](int c) { return part_slot(p, c, c == k - 1); };
+        auto stats = [&](int c, int i) { return reinterpret_cast<const float2*>(part(c) + kBlockRows * 128)[row0 + i]; };
+        float M[kRowsPerWarp], L[kRowsPerWarp];
+        float4 sum[kRowsPerWarp];
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i) {
+            M[i] = -INFINITY;
+            L[i] = 0.f;
+            sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (bad <= s.pos0 + row) L = NAN;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int64_t at = (int64_t)(s.row0 + row) * p.heads + s.head;
-        reinterpret_cast<uint2*>(p.out + at * 128)[lane] =
-            make_uint2(f2_to_bf2(sum.x * inv, sum.y * inv), f2_to_bf2(sum.z * inv, sum.w * inv));
-        if (lane == 0 && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+#pragma unroll 2
+        for (int c = k - 1; c <= last; ++c)
+#pragma unroll
+            for (int i = 0; i < kRowsPerWarp; ++i) M[i] = fmaxf(M[i], stats(c, i).x);
+#pragma unroll 2
+        for (int c = k - 1; c <= last; ++c) {
+#pragma unroll
+            for (int i = 0; i < kRowsPerWarp; ++i) {
+                const float2 ml = stats(c, i);
+                const float4 o = reinterpret_cast<const float4*>(part(c) + (row0 + i) * 128)[lane];
+                // (no score above -inf: no weight, unless a NaN is among them; its O may never have been written)
+                const float w = ml.x > -INFINITY ? exp2f(ml.x - M[i]) : ml.y == 0.f ? 0.f : NAN;
+                L[i] += ml.y * w;
+                sum[i].x += w == 0.f ? 0.f : w * o.x;
+                sum[i].y += w == 0.f ? 0.f : w * o.y;
+                sum[i].z += w == 0.f ? 0.f : w * o.z;
+                sum[i].w += w == 0.f ? 0.f : w * o.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i) {
+            if (row0 + i >= s.nrows) break;
+            if (bad <= s.pos0 + row0 + i) L[i] = NAN;
+            const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
+            const int64_t at = (int64_t)(s.row0 + row0 + i) * p.heads + s.head;
+            reinterpret_cast<uint2*>(p.out + at * 128)[lane] =
+                make_uint2(f2_to_bf2(sum[i].x * inv, sum[i].y * inv), f2_to_bf2(sum[i].z * inv, sum[i].w * inv));
+            if (lane == 0 && p.lse) p.lse[at] = L[i] == 0.f ? -INFINITY : (M[i] + log2f(L[i])) * kLn2;
+        }
     }
 }
 
@@ -986,7 +1021,7 @@ cudaError_t launch_expand(const ExpandLaunch& L, cudaStream_t stream) {
     cfg.blockDim = dim3(kAttendThreads);
     cfg.dynamicSmemBytes = kAttendSmem;
     if ((e = cudaLaunchKernelEx(&cfg, attend_kernel, L.nopemap, L.pemap, p)) != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)p.ctas, kBlockRows / kCombineRows);
+    cfg.gridDim = dim3((unsigned)p.ctas, kBlockRows / (kBatches * kCombineRows));
     cfg.blockDim = dim3(32 * kCombineWarps);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, combine_kernel, p);
