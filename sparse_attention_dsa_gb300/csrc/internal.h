@@ -306,8 +306,7 @@ struct HeadsParams {
     int32_t total_q;
     int32_t heads;
     int32_t values;  // latent outputs to head values, or (0) queries to latent space
-    int32_t tiles;   // of 128 tokens (launch_heads)
-    int64_t units;   // tiles x slabs of weights (launch_heads)
+    int64_t units;   // tiles of 128 tokens x slabs of weights (launch_heads)
     uint64_t wait_ns;
 };
 struct HeadsLaunch {

@@ -9,6 +9,11 @@
 // What bounds it: HBM for long steps (every element is read and written once), launch and one round of loads and
 // reductions for short ones.  So a row is held in registers between its only load and its stores, as 16-byte pieces: a row
 // of up to 1024 values by a warp (no block barrier), a longer one by a block.
+//
+// Measured (one GB300; 20 calls in a graph; in brackets with L2 flushed before each): 32 rows of 4096 with the residual
+// 2.0 us (7.3), 1171 of 1536 to MXFP8 3.0 (9.3), latency; 4096 of 512 2.5 (9.3); 8192 rows of 8192 with the residual 78 us to
+// bf16 (85; 537 MB, 6.9 TB/s, 1.01 of the copy bandwidth), 80 to FP8 in tiles (85; 472 MB, 5.9 TB/s, 0.88: the codes' arithmetic
+// between a row's loads and its stores); 16384 of 4096 to FP8 rows 74 (81; 0.94).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,6 +27,7 @@ namespace {
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kRowsPerBlock = 4;  // rows of a warp each
 constexpr int kMaxWarps = 32;
+constexpr int kFewRows = 1216;    // eight blocks for each SM
 
 // Of all threads that share a row.  The block's result is in every thread; `slots` is used once a call.
 template <bool kWarpRow, typename F>
@@ -41,8 +47,10 @@ __device__ __forceinline__ float reduce_row(float v, float* slots, F op) {
 
 // Piece i of thread t is piece t + i * width of the row, so that a warp's loads are whole lines and a group of 32 or 128
 // values lies in neighbouring lanes.
-template <int P, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : 1024) norm_kernel(const NormParams p) {
+// (An instance for each kind of codes: with the choice inside, all paid for the registers of the largest, 101 us for 79.)
+enum Codes { kNone, kRow, kTile, kMx };
+template <int P, bool kWarpRow, Codes kCodes>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : 1024, kWarpRow ? 8 : 1) norm_kernel(const NormParams p) {
     __shared__ float sums[kMaxWarps], maxima[kMaxWarps];
     const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x, width = kWarpRow ? 32 : blockDim.x;
     const int64_t row = kWarpRow ? (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
@@ -87,11 +95,11 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : 1024) norm_ker
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] = at < pieces ? h[i][j] * r * w[j] : 0.f;
         if (p.out != nullptr && at < pieces) reinterpret_cast<uint4*>(p.out + row * p.out_stride)[at] = pack8(h[i]);
-        most = fmaxf(most, absmax8(h[i]));
+        if (kCodes == kRow) most = fmaxf(most, absmax8(h[i]));
     }
-    if (p.codes == nullptr) return;
+    if (kCodes == kNone) return;
     uint2* codes = reinterpret_cast<uint2*>(p.codes + row * p.dim);
-    if (p.group == 0) {
+    if (kCodes == kRow) {
         most = reduce_row<kWarpRow>(most, maxima, [](float a, float b) { return fmaxf(a, b); });
         const float scale = group_scale(most);
         if (t == 0) static_cast<float*>(p.scale)[row] = scale;
@@ -100,44 +108,73 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : 1024) norm_ker
             if (t + i * width < pieces) codes[t + i * width] = codes8(h[i], scale);
         return;
     }
-    const int lanes = p.group >> 3;  // 16 of a tile, 4 of an MX group
+    // groups of 16 lanes (a tile) or 4 (MX)
+    constexpr int lanes = kCodes == kTile ? 16 : 4;
+    float m[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) m[i] = absmax8(h[i]);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < P; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(kAll, m[i], off));
+    const int64_t first = row * (pieces / lanes);
+    if (kCodes == kMx) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int at = t + i * width, e = mx_exponent(m[i]);
+            const uint2 c = codes8_exp(h[i], e);
+            if (at < pieces) {
+                codes[at] = c;
+                if (at % 4 == 0) static_cast<uint8_t*>(p.scale)[first + at / 4] = (uint8_t)(e + 127);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int off = 4; off < 16; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < P; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(kAll, m[i], off));
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int at = t + i * width;
-        float m = absmax8(h[i]);
-        m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
-        if (lanes == 16) {
-            m = fmaxf(m, __shfl_xor_sync(kAll, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(kAll, m, 8));
-        }
-        if (at >= pieces) continue;
-        const int64_t group = row * (pieces / lanes) + at / lanes;
-        if (p.mx) {
-            const int e = mx_exponent(m);
-            if (at % lanes == 0) static_cast<uint8_t*>(p.scale)[group] = (uint8_t)(e + 127);
-            codes[at] = codes8_exp(h[i], e);
-        } else {
-            const float scale = group_scale(m);
-            if (at % lanes == 0) static_cast<float*>(p.scale)[group] = scale;
+        const float scale = group_scale(m[i]);
+        if (at < pieces) {
             codes[at] = codes8(h[i], scale);
+            if (at % 16 == 0) static_cast<float*>(p.scale)[first + at / 16] = scale;
         }
     }
+}
+
+template <Codes kCodes>
+void launch(const NormParams& p, cudaStream_t stream) {
+    const int pieces = p.dim / 8;
+    if (pieces <= 128) {
+        const dim3 grid((unsigned)((p.rows + kRowsPerBlock - 1) / kRowsPerBlock)), block(32 * kRowsPerBlock);
+        auto kernel = pieces <= 32 ? norm_kernel<1, true, kCodes> : pieces <= 64 ? norm_kernel<2, true, kCodes> : norm_kernel<4, true, kCodes>;
+        kernel<<<grid, block, 0, stream>>>(p);
+        return;
+    }
+    // A piece a thread for few rows (32 rows of 4096: 2.0 us, with four 2.3; 1171 of 1536 3.5 and 3.9), four for many, whose
+    // loads are in flight together and meet at a quarter of the barriers (8192 rows of 8192, bf16: 79 us, with one 92, with
+    // two 108; 16384 of 4096, row codes: 69, 89, 99), and for rows that are longer than a block's threads.
+    const int each = p.rows <= kFewRows && pieces <= 1024 ? 1 : 4;
+    auto kernel = each == 1 ? norm_kernel<1, false, kCodes> : norm_kernel<4, false, kCodes>;
+    const int threads = ((pieces + each - 1) / each + 31) / 32 * 32;
+    kernel<<<dim3((unsigned)p.rows), dim3((unsigned)threads), 0, stream>>>(p);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t stream) {
     if (p.rows <= 0) return cudaSuccess;
-    const int pieces = p.dim / 8;
-    if (pieces <= 128) {
-        const dim3 grid((unsigned)((p.rows + kRowsPerBlock - 1) / kRowsPerBlock)), block(32 * kRowsPerBlock);
-        auto kernel = pieces <= 32 ? norm_kernel<1, true> : pieces <= 64 ? norm_kernel<2, true> : norm_kernel<4, true>;
-        kernel<<<grid, block, 0, stream>>>(p);
-    } else {
-        const int threads = ((pieces + 1) / 2 + 31) / 32 * 32;
-        norm_kernel<2, false><<<dim3((unsigned)p.rows), dim3((unsigned)threads), 0, stream>>>(p);
-    }
+    if (p.codes == nullptr)
+        launch<kNone>(p, stream);
+    else if (p.mx)
+        launch<kMx>(p, stream);
+    else if (p.group == 0)
+        launch<kRow>(p, stream);
+    else
+        launch<kTile>(p, stream);
     return cudaGetLastError();
 }
 
