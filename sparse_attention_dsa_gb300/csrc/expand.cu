@@ -10,10 +10,10 @@
 // head) 2 x 256 x 512 for its keys and values, so this is the form for many queries a sequence.  Keys and values are
 // rounded to bf16, as a projection would leave them.
 //
-// Five kernels, chained by programmatic launches:
-//   plan:    where each sequence's positions lie (tiles of 128, a sequence's own) and the list of blocks of 256 queries;
-//   gather:  the pages' rows as tiles of nine 16 KB pieces (64 dims of 128 positions, FP8 rows as bf16; zeros behind the
-//            last position), the layout that the tensor cores read (128-byte swizzle);
+// Four kernels, chained by programmatic launches:
+//   gather:  the pages' rows as tiles (of 128 positions, a sequence's own) of nine 16 KB pieces (64 dims of 128 positions, FP8
+//            rows as bf16; zeros behind the last position), the layout that the tensor cores read (128-byte swizzle); and
+//            the plan: where each sequence's tiles and blocks of 256 queries are;
 //   keys:    K and V = W c: a matrix product of all tiles and heads, CTA pairs (256 positions x a head's 256 rows);
 //   attend:  a CTA takes 256 queries of a head as two tiles of 128 that share K and V; all such items, each as long as its
 //            tiles of keys, are cut into equal parts, one for each CTA, or (where there are many) taken whole in turn;
@@ -36,8 +36,8 @@ constexpr int kTileBytes = kExpandTileBytes;   // latent and rotary parts of 128
 constexpr int kHeadTile = kExpandHeadTileBytes;  // keys (two units) and values (two) of 128 positions of a head
 constexpr int kBlockRows = kExpandBlockRows;
 
-// What the plan kernel leaves, at the start of the plan area (int32), tile_begin [batch + 1], first_bad [batch], then
-// blocks, an int2 each (sequence, first query), and cost, the places of the blocks before each (one more than blocks).
+// What the gathering kernel leaves of its plan (int32): a PlanHead, then for each sequence its first tile, its first block
+// of queries and its first place on the line (one more of each than sequences; first tile -1: left out), and first_bad.
 struct PlanHead {
     int32_t tiles;    // in use
     int32_t blocks;   // in the list
@@ -48,10 +48,11 @@ struct PlanHead {
 };
 __device__ __forceinline__ PlanHead* plan_head(const ExpandParams& p) { return reinterpret_cast<PlanHead*>(p.plan); }
 __device__ __forceinline__ int32_t* tile_begin(const ExpandParams& p) { return p.plan + sizeof(PlanHead) / 4; }
+__device__ __forceinline__ int32_t* block_begin(const ExpandParams& p) { return tile_begin(p) + p.batch + 1; }
+__device__ __forceinline__ int32_t* place_begin(const ExpandParams& p) { return block_begin(p) + p.batch + 1; }
 // First position of a sequence that has no finite values or no page (INT32_MAX: none): rows that see it are NaN.
-__device__ __forceinline__ int32_t* first_bad(const ExpandParams& p) { return tile_begin(p) + p.batch + 1; }
-__device__ __forceinline__ int2* blocks(const ExpandParams& p) { return reinterpret_cast<int2*>(p.plan + expand_plan_ints(p.batch)); }
-__device__ __forceinline__ int32_t* cost(const ExpandParams& p) { return reinterpret_cast<int32_t*>(blocks(p) + p.cap_blocks); }
+__device__ __forceinline__ int32_t* first_bad(const ExpandParams& p) { return place_begin(p) + p.batch + 1; }
+static_assert(kExpandPlanHead == sizeof(PlanHead) / 4, "expand_plan_bytes()");
 
 // A block's place on the line: kItemCost places for what it costs beside its tiles (its queries' load, its first scores'
 // latency, its result), then one for each tile of keys.  kMinPlaces: a part is no shorter on average.  kWholeItems: items
@@ -63,6 +64,28 @@ constexpr int kWholeItems = 8;
 constexpr int kCutCost = 8;  // what cutting costs a CTA: writing parts, combining
 constexpr int64_t kGroupBytes = 48 << 20;  // keys and values of heads that are worked on together
 __device__ __forceinline__ int tiles_before(int place, int n) { return min(n, max(0, place - kItemCost)); }
+// Tiles of keys that n queries from position pos0 see.
+__device__ __forceinline__ int tiles_seen(int pos0, int n) { return (pos0 + n + 127) / 128; }
+// Places of a sequence's first i blocks, all of them whole, its first query at position pos0: block j takes kItemCost +
+// tiles_seen(pos0 + 256 j, 256) = kItemCost + tiles_seen(pos0, 0) + 2 (j + 1).
+static_assert(kBlockRows == 256, "two tiles more for each block");
+__device__ __forceinline__ int64_t places_before(int pos0, int64_t i) { return i * (kItemCost + tiles_seen(pos0, 0)) + i * (i + 1); }
+__device__ __forceinline__ int64_t places_of(int pos0, int n) {
+    const int64_t whole = places_before(pos0, n / kBlockRows);
+    return n % kBlockRows ? whole + kItemCost + tiles_seen(pos0, n) : whole;
+}
+// The last of a[0 .. n - 1] (ascending) that is not above x; a[0] is not.  Called by a whole warp.
+__device__ __forceinline__ int last_not_above(const int32_t* a, int n, int x, int lane) {
+    int lo = 0;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const uint32_t le = __ballot_sync(kAllLanes, step * lane < n && a[lo + step * lane] <= x);  // (lane 0's always)
+        const int k = 31 - __clz(le);
+        lo += step * k;
+        n = min(step, n - step * k);
+    }
+    return lo;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {  // relative error about 2^-22; exp2(-inf) = +0
     float y;
@@ -78,12 +101,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// ---------------------------------------------------------------------------------------------------------
-// plan: one block.  Every thread counts a run of sequences; a scan of the threads' sums numbers tiles and blocks.
-// ---------------------------------------------------------------------------------------------------------
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
-
 // Queries and positions of sequence b; false when they are inconsistent.
 __device__ __forceinline__ bool sequence(const ExpandParams& p, int b, int* c0, int* n, int* L) {
     const int a = p.cu_q_lens[b], e = p.cu_q_lens[b + 1];
@@ -96,29 +113,49 @@ __device__ __forceinline__ bool sequence(const ExpandParams& p, int b, int* c0, 
     return *n <= *L && (int64_t)*L <= (int64_t)p.max_pages * 64 && *L <= INT32_MAX - 255;
 }
 
-// Tiles of keys that a block of n queries from position pos0 sees.
-__device__ __forceinline__ int tiles_seen(int pos0, int n) { return (pos0 + n + 127) / 128; }
+// The sequence that a tile belongs to: the last one that begins no later and has tiles.
+__device__ __forceinline__ int sequence_of_tile(const ExpandParams& p, int tile) {
+    const int32_t* begin = tile_begin(p);
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (begin[mid] <= tile) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpandParams p) {
-    __shared__ long long scan[3][kPlanWarps];
-    __shared__ int longest[kPlanWarps];
+// ---------------------------------------------------------------------------------------------------------
+// gather: a block takes half tiles (64 positions, one page), a warp positions.  Every block numbers the sequences' tiles for
+// itself (each thread a run of sequences, then a scan of the threads' sums), which costs less than a kernel in front; the
+// first one leaves the plan.  Rows of a page that is out of range become NaN, and so the scores of whoever sees them.
+// Bound by HBM and L2: 1152 or 656 bytes read, 1152 written a position.
+// ---------------------------------------------------------------------------------------------------------
+constexpr int kGatherWarps = 8;
+constexpr int kGatherThreads = 32 * kGatherWarps;
+
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandParams p) {
+    __shared__ long long scan[3][kGatherWarps];
+    __shared__ int longest[kGatherWarps];
+    __shared__ int2 found[2];  // (sequence, first tile), one for each parity of the loop
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool plans = blockIdx.x == 0;
     grid_dependency_wait();
     allow_dependent_launch();
-    const int run = (p.batch + kPlanThreads - 1) / kPlanThreads;
+    const int run = (p.batch + kGatherThreads - 1) / kGatherThreads;
     const int b0 = min(p.batch, tid * run), b1 = min(p.batch, b0 + run);
     long long sum[3] = {0, 0, 0};  // tiles, blocks, places
     int most = 0;
     for (int b = b0; b < b1; ++b) {
         int c0, n, L;
         if (!sequence(p, b, &c0, &n, &L)) {
-            raise_error(p.err, DSA_DEVERR_SEQ);
+            if (plans) raise_error(p.err, DSA_DEVERR_SEQ);
             continue;
         }
         if (n == 0) continue;
         sum[0] += (L + 127) / 128;
         sum[1] += (n + kBlockRows - 1) / kBlockRows;
-        for (int q = 0; q < n; q += kBlockRows) sum[2] += kItemCost + tiles_seen(L - n + q, min(kBlockRows, n - q));
+        sum[2] += places_of(L - n, n);
         most = max(most, kItemCost + (L + 127) / 128);
     }
     long long incl[3] = {sum[0], sum[1], sum[2]};
@@ -139,105 +176,97 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ExpandParams p
     long long before[3], all[3] = {0, 0, 0};
     for (int i = 0; i < 3; ++i) {
         before[i] = incl[i] - sum[i];
-        for (int w = 0; w < kPlanWarps; ++w) {
+        for (int w = 0; w < kGatherWarps; ++w) {
             if (w < warp) before[i] += scan[i][w];
             all[i] += scan[i][w];
         }
     }
-    for (int w = 0; w < kPlanWarps; ++w) most = max(most, longest[w]);
-    for (int b = b0; b < b1; ++b) {
-        int c0, n, L;
-        const bool ok = sequence(p, b, &c0, &n, &L) && n > 0;
-        const int mine = ok ? (L + 127) / 128 : 0, parts = ok ? (n + kBlockRows - 1) / kBlockRows : 0;
-        // (more pages than were announced, or offsets that run backwards: left out)
-        const bool fits = before[0] + mine <= p.cap_tiles && before[1] + parts <= p.cap_blocks;
-        if (ok && !fits) raise_error(p.err, DSA_DEVERR_SEQ);
-        tile_begin(p)[b] = (int32_t)(before[0] < p.cap_tiles ? before[0] : p.cap_tiles);
-        first_bad(p)[b] = INT32_MAX;
-        for (int i = 0; i < parts && before[1] + i < p.cap_blocks; ++i) {
-            const int q = i * kBlockRows;
-            blocks(p)[before[1] + i] = make_int2(fits ? b : -1, q);
-            cost(p)[before[1] + i] = (int32_t)before[2];
-            before[2] += kItemCost + tiles_seen(L - n + q, min(kBlockRows, n - q));
+    const int tiles = (int)(all[0] < p.cap_tiles ? all[0] : p.cap_tiles);
+    if (plans) {
+        for (int w = 0; w < kGatherWarps; ++w) most = max(most, longest[w]);
+        long long at[3] = {before[0], before[1], before[2]};
+        for (int b = b0; b < b1; ++b) {
+            int c0, n, L;
+            const bool ok = sequence(p, b, &c0, &n, &L) && n > 0;
+            const int mine = ok ? (L + 127) / 128 : 0, parts = ok ? (n + kBlockRows - 1) / kBlockRows : 0;
+            // (more pages than were announced, or offsets that run backwards: left out)
+            const bool fits = at[0] + mine <= p.cap_tiles && at[1] + parts <= p.cap_blocks;
+            if (ok && !fits) raise_error(p.err, DSA_DEVERR_SEQ);
+            tile_begin(p)[b] = (int32_t)(at[0] < p.cap_tiles ? at[0] : p.cap_tiles);
+            block_begin(p)[b] = (int32_t)(at[1] < p.cap_blocks ? at[1] : p.cap_blocks);
+            place_begin(p)[b] = (int32_t)at[2];  // (looked at where all of it is within 32 bits)
+            first_bad(p)[b] = ok && !fits ? -1 : INT32_MAX;
+            at[0] += mine;
+            at[1] += parts;
+            if (ok) at[2] += places_of(L - n, n);
         }
-        before[0] += mine;
-        before[1] += parts;
+        if (tid == 0) {
+            // (what does not fit leaves places that nobody works on)
+            PlanHead h;
+            h.tiles = tiles;
+            h.blocks = (int32_t)(all[1] < p.cap_blocks ? all[1] : p.cap_blocks);
+            const long long line = all[2] * p.heads;
+            h.parts = (int32_t)(line / kMinPlaces < p.ctas ? max(1LL, line / kMinPlaces) : p.ctas);
+            // how long the last CTA takes with whole items (its share and half an item; no more than one item each), and with
+            // parts
+            const long long whole = all[1] * p.heads <= p.ctas ? most : line / p.ctas + most / 2, cut = line / h.parts + kCutCost;
+            if (all[1] > p.cap_blocks || all[2] > INT32_MAX || whole <= cut || line >= (long long)kWholeItems * p.ctas * most)
+                h.parts = 0;
+            h.counter = p.ctas;  // every CTA takes the item of its own number first
+            const long long head_bytes = max(1LL, (long long)h.tiles * kHeadTile);
+            h.group = (int32_t)max(1LL, min((long long)p.heads, kGroupBytes / head_bytes));
+            *plan_head(p) = h;
+            tile_begin(p)[p.batch] = h.tiles;
+            block_begin(p)[p.batch] = h.blocks;
+            place_begin(p)[p.batch] = (int32_t)all[2];
+            if (p.cu_q_lens[0] != 0 || p.cu_q_lens[p.batch] != p.total_q) raise_error(p.err, DSA_DEVERR_SEQ);
+        }
     }
-    if (tid == 0) {
-        // (what does not fit leaves places that nobody works on)
-        PlanHead h;
-        h.tiles = (int32_t)(all[0] < p.cap_tiles ? all[0] : p.cap_tiles);
-        h.blocks = (int32_t)(all[1] < p.cap_blocks ? all[1] : p.cap_blocks);
-        h.counter = 0;
-        const long long line = all[2] * p.heads;
-        h.parts = (int32_t)(line / kMinPlaces < p.ctas ? max(1LL, line / kMinPlaces) : p.ctas);
-        // how long the last CTA takes with whole items (its share and half an item; no more than one item each), and with parts
-        const long long whole = all[1] * p.heads <= p.ctas ? most : line / p.ctas + most / 2, cut = line / h.parts + kCutCost;
-        if (all[1] > p.cap_blocks || all[2] > INT32_MAX || whole <= cut || line >= (long long)kWholeItems * p.ctas * most)
-            h.parts = 0;
-        const long long head_bytes = max(1LL, (long long)h.tiles * kHeadTile);
-        h.group = (int32_t)max(1LL, min((long long)p.heads, kGroupBytes / head_bytes));
-        *plan_head(p) = h;
-        tile_begin(p)[p.batch] = h.tiles;
-        if (h.parts > 0) cost(p)[h.blocks] = (int32_t)all[2];
-        if (p.cu_q_lens[0] != 0 || p.cu_q_lens[p.batch] != p.total_q) raise_error(p.err, DSA_DEVERR_SEQ);
-    }
-}
-
-// The sequence that a tile belongs to: the last one that begins no later and has tiles.
-__device__ __forceinline__ int sequence_of_tile(const ExpandParams& p, int tile) {
-    const int32_t* begin = tile_begin(p);
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (begin[mid] <= tile) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-// ---------------------------------------------------------------------------------------------------------
-// gather: a block per half tile (64 positions, one page), a warp per position.  Bound by HBM and L2: 1152 or 656 bytes
-// read, 1152 written a position.
-// ---------------------------------------------------------------------------------------------------------
-constexpr int kGatherWarps = 8;
-
-__global__ void __launch_bounds__(32 * kGatherWarps) gather_kernel(const ExpandParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    grid_dependency_wait();
-    allow_dependent_launch();
-    const int halves = 2 * plan_head(p)->tiles;
-    for (int i = blockIdx.x; i < halves; i += gridDim.x) {
-        const int tile = i >> 1, b = sequence_of_tile(p, tile), base = 128 * (tile - tile_begin(p)[b]) + 64 * (i & 1);
+    const int halves = 2 * tiles;
+    uint32_t turn = 0;
+    for (int i = blockIdx.x; i < halves; i += gridDim.x, turn ^= 1u) {
+        const int tile = i >> 1;
+        if (tile >= before[0] && tile < before[0] + sum[0]) {  // a sequence of this thread's run
+            long long at = before[0];
+            for (int b = b0; b < b1; ++b) {
+                int c0, n, L;
+                if (!sequence(p, b, &c0, &n, &L) || n == 0) continue;
+                if (tile < at + (L + 127) / 128) {
+                    found[turn] = make_int2(b, (int)at);
+                    break;
+                }
+                at += (L + 127) / 128;
+            }
+        }
+        __syncthreads();
+        const int b = found[turn].x, base = 128 * (tile - found[turn].y) + 64 * (i & 1);
         const int L = p.seq_lens[b];
         const int pg = base < L ? p.page_table[(int64_t)b * p.max_pages + (base >> 6)] : 0;
         const bool in = pg >= 0 && pg < p.num_pages;
-        if (!in && threadIdx.x == 0) {
-            raise_error(p.err, DSA_DEVERR_PAGE);
-            atomicMin(first_bad(p) + b, base);
-        }
+        if (!in && tid == 0) raise_error(p.err, DSA_DEVERR_PAGE);
         uint8_t* dst = p.latents + (int64_t)tile * kTileBytes;
+        const uint4 zero = make_uint4(0, 0, 0, 0), nan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
 #pragma unroll 2
         for (int j = warp; j < 64; j += kGatherWarps) {
             const int row = 64 * (i & 1) + j;
             const bool have = in && base + j < L;
+            const uint4 none = in || base + j >= L ? zero : nan;
             auto put = [&](int chunk, uint4 v) {  // 16-byte chunk of the row's 72
                 *reinterpret_cast<uint4*>(dst + (chunk >> 3) * kUnit + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = v;
             };
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            if (!p.kv_fp8) {
+            if (!p.kv_fp8 || !have) {
                 const uint4* src = reinterpret_cast<const uint4*>(p.kv_cache + ((int64_t)pg * 64 + j) * 1152);
                 uint4 v[3];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) v[k] = have && lane + 32 * k < 72 ? src[lane + 32 * k] : zero;
+                for (int k = 0; k < 3; ++k) v[k] = have && lane + 32 * k < 72 ? src[lane + 32 * k] : none;
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
                     if (lane + 32 * k < 72) put(lane + 32 * k, v[k]);
             } else {
                 const uint8_t* src = p.kv_cache + ((int64_t)pg * 64 + j) * kKvFp8RowBytes;
-                const uint4 code = have ? reinterpret_cast<const uint4*>(src)[lane] : zero;
-                const float scale = have ? reinterpret_cast<const float*>(src + kKvFp8ScaleOff)[lane >> 3] : 0.f;
-                const uint4 rot = have && lane < 8 ? reinterpret_cast<const uint4*>(src + kKvFp8RopeOff)[lane] : zero;
+                const uint4 code = reinterpret_cast<const uint4*>(src)[lane];
+                const float scale = reinterpret_cast<const float*>(src + kKvFp8ScaleOff)[lane >> 3];
+                const uint4 rot = lane < 8 ? reinterpret_cast<const uint4*>(src + kKvFp8RopeOff)[lane] : zero;
                 put(2 * lane, e4m3x8_to_bf16x8(make_uint2(code.x, code.y), scale));
                 put(2 * lane + 1, e4m3x8_to_bf16x8(make_uint2(code.z, code.w), scale));
                 if (lane < 8) put(64 + lane, rot);
@@ -304,24 +333,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
     allow_dependent_launch();
     const uint32_t tmem = ctl->tmem_base;
     const int tiles = plan_head(p)->tiles;
-    const int64_t units = (int64_t)((tiles + 1) / 2) * p.heads;
-    const int64_t u0 = units * pair / pairs, u1 = units * (pair + 1) / pairs;  // unit: tiles u / heads, head u % heads
+    // unit u: tile pair u % tile_pairs of head u / tile_pairs, so that all pairs of CTAs are at the same few heads' weights
+    const int tile_pairs = (tiles + 1) / 2;
+    const int64_t units = (int64_t)tile_pairs * p.heads;
     auto leader = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(kAllLanes, mbar_wait(bar, parity, p.err, p.wait_ns)) != 0;
     };
     bool ok = true;
 
+    // (loads and products by one thread each: see the attention's products)
+    auto wait_one = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, p.err, p.wait_ns); };
     if (warp == 0) {
-        const uint32_t full = leader(&ctl->full[0]);
-        uint32_t n = 0;
-        for (int64_t u = u0; ok && u < u1; ++u) {
-            const int tile = 2 * (int)(u / p.heads) + rank, head = (int)(u % p.heads);
+        if (elect_one_sync()) {
+            const uint32_t full = leader(&ctl->full[0]);
+            uint32_t n = 0;
+            for (int64_t u = pair; ok && u < units; u += pairs) {
+                const int tile = 2 * (int)(u % tile_pairs) + rank, head = (int)(u / tile_pairs);
 #pragma unroll 1
-            for (int k = 0; k < 8; ++k, ++n) {
-                const uint32_t slot = n % kKeysStages;
-                if (!(ok = wait(&ctl->empty[slot], ((n / kKeysStages) & 1u) ^ 1u))) break;
-                if (elect_one_sync()) {
+                for (int k = 0; k < 8; ++k, ++n) {
+                    const uint32_t slot = n % kKeysStages;
+                    if (!(ok = wait_one(&ctl->empty[slot], ((n / kKeysStages) & 1u) ^ 1u))) break;
                     uint8_t* dst = smem + slot * 2 * kUnit;
                     if (rank == 0) mbar_arrive_expect_tx(&ctl->full[slot], 4 * kUnit);
                     // (the tile behind the last one, where their number is odd, has its place but no rows of its own)
@@ -330,34 +362,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                 }
             }
         }
+        ok = __all_sync(kAllLanes, ok);
     } else if (warp == 1 && rank == 0) {
-        const uint64_t ad = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-        uint32_t n = 0, t = 0;
-        for (int64_t u = u0; ok && u < u1; ++u, ++t) {
-            const uint32_t buf = t & 1u;
-            if (!(ok = wait(&ctl->d_empty[buf], ((t >> 1) & 1u) ^ 1u))) break;
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k, ++n) {
-                const uint32_t slot = n % kKeysStages;
-                if (!(ok = wait(&ctl->full[slot], (n / kKeysStages) & 1u))) break;
+        if (elect_one_sync()) {
+            const uint64_t ad = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+            uint32_t n = 0, t = 0;
+            for (int64_t u = pair; ok && u < units; u += pairs, ++t) {
+                const uint32_t buf = t & 1u;
+                if (!(ok = wait_one(&ctl->d_empty[buf], ((t >> 1) & 1u) ^ 1u))) break;
                 tc_fence_after();
-                if (elect_one_sync()) {
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k, ++n) {
+                    const uint32_t slot = n % kKeysStages;
+                    if (!(ok = wait_one(&ctl->full[slot], (n / kKeysStages) & 1u))) break;
                     const uint64_t a = ad + (uint64_t)(slot * (2 * kUnit / 16));
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma_pair_f16_ss(tmem + 256 * buf, a + (uint64_t)(2 * j), a + (uint64_t)(kUnit / 16 + 2 * j),
                                          kIdescKeys, k == 0 && j == 0 ? 0u : 1u);
                     umma_pair_commit(&ctl->empty[slot], 3);
-                    if (k == 7) umma_pair_commit(&ctl->d_full[buf], 3);
                 }
+                if (ok) umma_pair_commit(&ctl->d_full[buf], 3);
             }
-        }
-        // drain (default limit): every product of the pair is done before its memory is given back
-        if (elect_one_sync()) {
+            // drain (default limit): every product of the pair is done before its memory is given back
             umma_pair_commit(&ctl->drained, 1);
             mbar_wait(&ctl->drained, 0, p.err);
         }
-        __syncwarp();
+        ok = __all_sync(kAllLanes, ok);
     } else if (warp >= kKeysResultWarp) {
         // warp w has positions 32 w .. of its CTA's tile, a lane each: keys in columns 0-127, values behind them
         const int ew = warp - kKeysResultWarp;
@@ -365,8 +396,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
         const uint32_t d_empty = leader(&ctl->d_empty[0]);
         uint8_t* stage = o_s + ew * 2 * kPiece;
         uint32_t t = 0;
-        for (int64_t u = u0; ok && u < u1; ++u, ++t) {
-            const int tile = 2 * (int)(u / p.heads) + rank, head = (int)(u % p.heads);
+        for (int64_t u = pair; ok && u < units; u += pairs, ++t) {
+            const int tile = 2 * (int)(u % tile_pairs) + rank, head = (int)(u / tile_pairs);
             const uint32_t buf = t & 1u;
             if (!(ok = wait(&ctl->d_full[buf], (t >> 1) & 1u))) break;
             tc_fence_after();
@@ -476,32 +507,37 @@ struct AttendCtrl {
 // Query tile w's tiles of a segment: from j0 to here.
 __device__ __forceinline__ int seg_end(const Segment& s, int w) { return min(s.j1, w == 0 ? s.n0 : s.n1); }
 
-// The block of a head at place x of its line (the last one that begins no later).  Called by a whole warp.
-__device__ __forceinline__ int block_at(const ExpandParams& p, int n_blocks, int x, int lane) {
-    const int32_t* c = cost(p);
-    int lo = 0, n = n_blocks;  // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32, at = lo + step * lane;
-        const uint32_t le = __ballot_sync(kAllLanes, step * lane < n && c[at] <= x);  // (lane 0's always)
-        const int k = 31 - __clz(le);
-        lo += step * k;
-        n = min(step, n - step * k);
-    }
-    return lo;
-}
-// Rows, keys and tiles of block i of a head; false for a block that is left out.
-__device__ __forceinline__ bool block_rows(const ExpandParams& p, int i, Segment* s) {
-    const int2 blk = blocks(p)[i];
-    if (blk.x < 0) return false;
-    const int c0 = p.cu_q_lens[blk.x], n = p.cu_q_lens[blk.x + 1] - c0;
-    s->seq = blk.x;
-    s->row0 = c0 + blk.y;
-    s->nrows = min(kBlockRows, n - blk.y);
-    s->pos0 = p.seq_lens[blk.x] - n + blk.y;
-    s->tile0 = tile_begin(p)[blk.x];
+// Rows and keys of block i of sequence b; false where the sequence is left out.
+__device__ __forceinline__ bool block_rows(const ExpandParams& p, int b, int i, Segment* s) {
+    const int c0 = p.cu_q_lens[b], n = p.cu_q_lens[b + 1] - c0, q = i * kBlockRows;
+    s->seq = b;
+    s->row0 = c0 + q;
+    s->nrows = min(kBlockRows, n - q);
+    s->pos0 = p.seq_lens[b] - n + q;
+    s->tile0 = tile_begin(p)[b];
     s->n0 = tiles_seen(s->pos0, min(s->nrows, 128));
     s->n1 = s->nrows > 128 ? tiles_seen(s->pos0, s->nrows) : 0;
-    return true;
+    return first_bad(p)[b] >= 0;
+}
+// The block at place x of a head's line: its sequence and number there, its first place, and that of the next block.
+// Called by a whole warp.
+struct Place {
+    int b, i, begin, end;
+};
+__device__ __forceinline__ Place block_at(const ExpandParams& p, int x, int lane) {
+    Place w;
+    w.b = last_not_above(place_begin(p), p.batch, x, lane);
+    const int n = p.cu_q_lens[w.b + 1] - p.cu_q_lens[w.b], pos0 = p.seq_lens[w.b] - n, first = place_begin(p)[w.b];
+    int lo = 0, hi = (n + kBlockRows - 1) / kBlockRows;  // the last block that begins no later
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (places_before(pos0, mid) <= x - first) lo = mid;
+        else hi = mid;
+    }
+    w.i = lo;
+    w.begin = first + (int)places_before(pos0, lo);
+    w.end = first + (int)((lo + 1) * kBlockRows <= n ? places_before(pos0, lo + 1) : places_of(pos0, n));
+    return w;
 }
 // Part k of a line of W places cut in G parts starts here.
 __device__ __forceinline__ int64_t part_begin(int64_t k, int64_t W, int64_t G) { return k * W / G; }
@@ -622,39 +658,39 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         };
         if (plan.parts > 0) {
             // this CTA's part of the line: the blocks of head 0, of head 1, ...
-            const int64_t head_line = cost(p)[plan.blocks], line = head_line * p.heads;
+            const int64_t head_line = place_begin(p)[p.batch], line = head_line * p.heads;
             const int64_t x1 = part_begin(blockIdx.x + 1, line, plan.parts);
             int64_t x = part_begin(blockIdx.x, line, plan.parts);
             if ((int)blockIdx.x >= plan.parts) x = x1;
-            int block = -1;
             while (ok && x < x1) {
                 s.head = (int)(x / head_line);
                 const int at = (int)(x - s.head * head_line);
-                if (block < 0) block = block_at(p, plan.blocks, at, lane);
-                const int begin = cost(p)[block], end = cost(p)[block + 1], n_tiles = end - begin - kItemCost;
+                const Place w = block_at(p, at, lane);
+                const int n_tiles = w.end - w.begin - kItemCost;
                 const int64_t left = x1 - s.head * head_line;  // the part's end on this head's line
-                s.j0 = tiles_before(at - begin, n_tiles);
-                s.j1 = left >= end ? n_tiles : tiles_before((int)left - begin, n_tiles);
-                if (s.j1 > s.j0 && block_rows(p, block, &s)) ok = work(s);
-                x = s.head * head_line + end;
-                block = block + 1 < plan.blocks ? block + 1 : 0;
+                s.j0 = tiles_before(at - w.begin, n_tiles);
+                s.j1 = left >= w.end ? n_tiles : tiles_before((int)left - w.begin, n_tiles);
+                if (s.j1 > s.j0 && block_rows(p, w.b, w.i, &s)) ok = work(s);
+                x = s.head * head_line + w.end;
             }
         } else {
             // Whole items, as CTAs become free.  Heads in groups whose keys fit L2; in a group the last blocks (of a sequence
             // the ones with the most keys) first.
             const int64_t n_items = (int64_t)plan.blocks * p.heads, group_items = (int64_t)plan.blocks * plan.group;
-            while (ok) {
-                int64_t index = 0;
-                if (lane == 0) index = atomicAdd(&plan_head(p)->counter, 1);
-                index = __shfl_sync(kAllLanes, index, 0);
-                if (index >= n_items) break;
+            int64_t index = blockIdx.x;
+            while (ok && index < n_items) {
                 const int group = (int)(index / group_items), rest = (int)(index - group * group_items);
-                const int heads = min(plan.group, p.heads - group * plan.group);
+                const int heads = min(plan.group, p.heads - group * plan.group), block = plan.blocks - 1 - rest / heads;
                 s.head = group * plan.group + rest % heads;
-                if (!block_rows(p, plan.blocks - 1 - rest / heads, &s)) continue;
-                s.j0 = 0;
-                s.j1 = max(s.n0, s.n1);
-                ok = work(s);
+                const int b = last_not_above(block_begin(p), p.batch, block, lane);
+                if (block_rows(p, b, block - block_begin(p)[b], &s)) {
+                    s.j0 = 0;
+                    s.j1 = max(s.n0, s.n1);
+                    ok = work(s);
+                }
+                int next = 0;
+                if (lane == 0) next = atomicAdd(&plan_head(p)->counter, 1);
+                index = __shfl_sync(kAllLanes, next, 0);
             }
         }
         s.nrows = 0;
@@ -927,15 +963,15 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Expan
     s.nrows = 0;
     if (part_begins) {
         // the item in which part k begins; the first part that begins inside it takes care of it
-        const int64_t head_line = cost(p)[plan.blocks];
+        const int64_t head_line = place_begin(p)[p.batch];
         line = head_line * p.heads;
         const int64_t x = part_begin(k, line, plan.parts);
         s.head = (int)(x / head_line);
-        const int block = block_at(p, plan.blocks, (int)(x - s.head * head_line), lane);
-        begin = s.head * head_line + cost(p)[block];
-        n_tiles = cost(p)[block + 1] - cost(p)[block] - kItemCost;
+        const Place w = block_at(p, (int)(x - s.head * head_line), lane);
+        begin = s.head * head_line + w.begin;
+        n_tiles = w.end - w.begin - kItemCost;
         const int here = cut(k);
-        if (here <= 0 || here >= n_tiles || cut(k - 1) > 0 || !block_rows(p, block, &s)) s.nrows = 0;
+        if (here <= 0 || here >= n_tiles || cut(k - 1) > 0 || !block_rows(p, w.b, w.i, &s)) s.nrows = 0;
         while (cut(last + 1) < n_tiles) ++last;
     }
     grid_dependency_wait();
@@ -1004,12 +1040,9 @@ cudaError_t launch_expand(const ExpandLaunch& L, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(kPlanThreads);
-    if ((e = cudaLaunchKernelEx(&cfg, plan_kernel, p)) != cudaSuccess) return e;
     const int64_t halves = 2 * (int64_t)p.cap_tiles;
     cfg.gridDim = dim3((unsigned)(halves < 8 * L.num_sms ? halves : 8 * L.num_sms));
-    cfg.blockDim = dim3(32 * kGatherWarps);
+    cfg.blockDim = dim3(kGatherThreads);
     if ((e = cudaLaunchKernelEx(&cfg, gather_kernel, p)) != cudaSuccess) return e;
     const int64_t units = (int64_t)((p.cap_tiles + 1) / 2) * p.heads;
     const int pairs = L.num_sms / 2;

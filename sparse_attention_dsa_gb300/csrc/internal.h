@@ -326,8 +326,7 @@ constexpr int kExpandCtas = 152;                     // of the attention, at mos
 // A partial result: O [256][128] fp32 (unnormalised), then (maximum in log2 units, sum) per row.
 constexpr int kExpandPartFloats = 256 * 128 + 2 * 256;
 constexpr size_t kExpandPartBytes = (size_t)2 * kExpandCtas * kExpandPartFloats * 4;
-// int32 in front of the plan's list of blocks
-__host__ __device__ constexpr int64_t expand_plan_ints(int32_t batch) { return ((int64_t)2 * batch + 9 + 3) / 4 * 4; }
+constexpr int kExpandPlanHead = 8;  // int32 in front of the plan's arrays
 struct ExpandParams {
     const uint8_t* kv_cache;  // bf16 rows, or FP8 rows of kKvFp8RowBytes
     const int32_t* page_table;
@@ -347,14 +346,14 @@ struct ExpandParams {
     // workspace
     int32_t ctas;        // of the attention
     int32_t cap_tiles;   // even
-    int32_t cap_blocks;
+    int32_t cap_blocks;  // of queries, whatever the offsets say
     int32_t* plan;
     float* partial;    // two results of cut items for each CTA
     uint8_t* latents;  // [cap_tiles][9][128][64] bf16, 128-byte swizzle
     uint8_t* kv;       // [cap_tiles][Hq][4] units of 16 KB
 };
 inline size_t expand_plan_bytes(const ExpandParams& p) {
-    return ((size_t)expand_plan_ints(p.batch) * 4 + (size_t)p.cap_blocks * 12 + 4 + 1023) / 1024 * 1024;
+    return (((size_t)kExpandPlanHead + 4 * (size_t)p.batch + 3) * 4 + 1023) / 1024 * 1024;
 }
 struct ExpandLaunch {
     CUtensorMap nopemap;  // 3-D view [T][Hq][128] of the queries' unrotated part: 64 dims of 128 tokens of a head
