@@ -16,7 +16,7 @@
 //            the plan: where each sequence's tiles and blocks of 256 queries are;
 //   keys:    K and V = W c: a matrix product of all tiles and heads, CTA pairs (256 positions x a head's 256 rows);
 //   attend:  a CTA takes 256 queries of a head as two tiles of 128 that share K and V; all such items, each as long as its
-//            tiles of keys, are cut into equal parts, one for each CTA, or (where there are many) taken whole in turn;
+//            tiles of keys, are cut into equal parts, one for each CTA, or (where that does not pay) they are taken whole in turn;
 //   combine: the results of items that were cut.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -494,6 +494,13 @@ struct Segment {
     int32_t j0, j1;
 };
 constexpr int kSegments = 4;  // in flight between the roles of a CTA
+// 32 bytes, one whole sector (32-byte aligned)
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 struct AttendCtrl {
     uint64_t q_full[2], q_empty[2];
     uint64_t full[kRing], empty[kRing];
@@ -504,6 +511,7 @@ struct AttendCtrl {
     int32_t failed;
     Segment segments[kSegments];
 };
+__device__ __forceinline__ bool is_whole(const Segment& s) { return s.j0 == 0 && s.j1 == max(s.n0, s.n1); }
 // Query tile w's tiles of a segment: from j0 to here.
 __device__ __forceinline__ int seg_end(const Segment& s, int w) { return min(s.j1, w == 0 ? s.n0 : s.n1); }
 
@@ -545,6 +553,74 @@ __device__ __forceinline__ int64_t part_begin(int64_t k, int64_t W, int64_t G) {
 __device__ __forceinline__ float* part_slot(const ExpandParams& p, int c, bool first_tile) {
     return p.partial + (int64_t)(2 * c + (first_tile ? 1 : 0)) * kExpandPartFloats;
 }
+// The result of a query tile, or of its part of an item: behind the tile's last products, by the warps of its softmax.  (Parts
+// are combined by a kernel of their own: done here by an item's last part, the code for it cost the softmax's loop its
+// registers, called or not: 2250 us for an 8192-token prompt of 128 heads that takes 1735.)
+__device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* ctl, uint32_t seg, uint32_t ocol, bool have, float m_used,
+                                          float l_sum) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, w = warp >> 2, row = 128 * w + (tid & 127);
+    const Segment& it = ctl->segments[seg];
+    const int nrows = it.nrows;
+    const bool whole = is_whole(it), first_tile = it.j0 == 0;
+    const int64_t at = (int64_t)(it.row0 + row) * p.heads + it.head;
+    const bool poisoned = first_bad(p)[it.seq] <= it.pos0 + row;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->seg_empty[seg]);
+    auto free_o = [&] {  // in registers: the next products may have it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->o_free[w]);
+    };
+    auto read_o = [&](int c, float (&o)[2][16]) {
+        tmem_ld16(ocol + c, o[0]);
+        tmem_ld16(ocol + c + 16, o[1]);
+        tmem_ld_wait();
+        tmem_regs_ready(o[0]);
+        tmem_regs_ready(o[1]);
+    };
+    uint16_t* dst = p.out + at * 128;
+    if (whole) {
+        if (poisoned) l_sum = NAN;
+        const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+            float o[2][16];
+            read_o(c, o);
+            if (row < nrows) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = f2_to_bf2(o[k][2 * i] * inv, o[k][2 * i + 1] * inv);
+                    st_global_32(dst + c + 16 * k, v);
+                }
+            }
+        }
+        free_o();
+        if (row < nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
+        return;
+    }
+    float* slot = part_slot(p, blockIdx.x, first_tile);
+    if (have) {
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+            float o[2][16];
+            read_o(c, o);
+            if (row < nrows) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[k >> 1][8 * (k & 1) + i]);
+                    st_global_32(slot + row * 128 + c + 8 * k, v);
+                }
+            }
+        }
+        free_o();
+    }
+    if (row < nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(m_used, l_sum);
+}
+
 constexpr int kAttendSmem = 1024 + 2 * kQTile + kRing * kUnit + (int)sizeof(AttendCtrl);
 static_assert(kAttendSmem <= 232448, "shared memory of one CTA");
 
@@ -590,14 +666,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const uint32_t tmem = ctl->tmem_base;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(kAllLanes, mbar_wait(bar, parity, p.err, p.wait_ns)) != 0;
-    };
-    // segment number n of this CTA, once it is there; false: gave up.  With the last look at it, it is given back.
-    auto next_segment = [&](uint32_t n, Segment* s) {
-        if (!wait(&ctl->seg_full[n % kSegments], (n / kSegments) & 1u)) return false;
-        *s = ctl->segments[n % kSegments];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->seg_empty[n % kSegments]);
-        return true;
     };
     bool ok = true;
 
@@ -789,19 +857,21 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const uint32_t scol = trow + 128 * w, ocol = trow + kOCol + 128 * w;
         uint32_t tile = 0, used = 0;
         for (uint32_t n = 0; ok; ++n) {
-            Segment it;
-            if (!(ok = next_segment(n, &it)) || it.nrows == 0) break;
-            const int row = 128 * w + r, end = seg_end(it, w);
-            const bool part = it.j0 > 0 || it.j1 < max(it.n0, it.n1);
-            float* slot = part_slot(p, blockIdx.x, it.j0 == 0);
-            if (end <= it.j0) {  // nothing for this query tile
-                if (part && row < it.nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(-INFINITY, 0.f);
+            if (!(ok = wait(&ctl->seg_full[n % kSegments], (n / kSegments) & 1u))) break;
+            const Segment& it = ctl->segments[n % kSegments];  // read again behind the loop, to spare its registers
+            if (it.nrows == 0) break;
+            const int end = seg_end(it, w), begin = it.j0, first = it.pos0 + 128 * w;
+            auto give_back = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->seg_empty[n % kSegments]);
+            };
+            if (end <= begin && (is_whole(it) || 128 * w >= it.nrows)) {  // nothing for this query tile
+                give_back();
                 continue;
             }
-            const int first = it.pos0 + 128 * w, limit = first + r + 1;  // positions this query sees: below `limit`
             float m_used = -INFINITY, l_sum = 0.f;
 #pragma unroll 1
-            for (int j = it.j0; j < end; ++j, ++tile) {
+            for (int j = begin; j < end; ++j, ++tile) {
                 if (!(ok = wait(&ctl->s_full[w], tile & 1u))) break;
                 tc_fence_after();
                 float s[8][16];
@@ -811,7 +881,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k) tmem_regs_ready(s[k]);
                 if (128 * j + 128 > first + 1) {  // some query does not see all of it
-                    const int seen = limit - 128 * j;
+                    const int seen = first + r + 1 - 128 * j;
 #pragma unroll
                     for (int k = 0; k < 128; ++k)
                         if (k >= seen) s[k >> 4][k & 15] = -INFINITY;
@@ -870,56 +940,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 if (lane == 0) mbar_arrive(&ctl->p_full[w]);
             }
             if (!ok) break;
-            // ---- the result ----
-            if (!(ok = wait(&ctl->o_full[w], used & 1u))) break;
-            ++used;
-            tc_fence_after();
-            if (part) {
-                float4* dst = reinterpret_cast<float4*>(slot + row * 128);
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    float o[2][16];
-                    tmem_ld16(ocol + c, o[0]);
-                    tmem_ld16(ocol + c + 16, o[1]);
-                    tmem_ld_wait();
-                    tmem_regs_ready(o[0]);
-                    tmem_regs_ready(o[1]);
-                    if (row < it.nrows) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float* f = &o[k >> 2][4 * (k & 3)];
-                            dst[c / 4 + k] = make_float4(f[0], f[1], f[2], f[3]);
-                        }
-                    }
-                }
-                if (row < it.nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(m_used, l_sum);
-            } else {
-                if (first_bad(p)[it.seq] < limit) l_sum = NAN;
-                const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
-                const int64_t at = (int64_t)(it.row0 + row) * p.heads + it.head;
-                uint4* dst = reinterpret_cast<uint4*>(p.out + at * 128);
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    float o[2][16];
-                    tmem_ld16(ocol + c, o[0]);
-                    tmem_ld16(ocol + c + 16, o[1]);
-                    tmem_ld_wait();
-                    tmem_regs_ready(o[0]);
-                    tmem_regs_ready(o[1]);
-                    if (row < it.nrows) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float* f = &o[k >> 1][8 * (k & 1)];
-                            dst[c / 8 + k] = make_uint4(f2_to_bf2(f[0] * inv, f[1] * inv), f2_to_bf2(f[2] * inv, f[3] * inv),
-                                                        f2_to_bf2(f[4] * inv, f[5] * inv), f2_to_bf2(f[6] * inv, f[7] * inv));
-                        }
-                    }
-                }
-                if (row < it.nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
+            // ---- the result, or a part's ----
+            const bool have = end > begin;
+            if (have) {
+                if (!(ok = wait(&ctl->o_full[w], used & 1u))) break;
+                ++used;
+                tc_fence_after();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->o_free[w]);
+            write_result(p, ctl, n % kSegments, ocol, have, m_used, l_sum);
         }
     }
     if (!ok && lane == 0) ctl->failed = 1;
