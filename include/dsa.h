@@ -86,7 +86,8 @@ typedef enum {
 #define DSA_DEVERR_TIMEOUT 0x8 /* a pipeline wait exceeded its limit (one second unless
                                   dsa_set_wait_limit_ns() says otherwise) */
 #define DSA_DEVERR_ROPE 0x10   /* a position beyond the rotation table was needed */
-#define DSA_DEVERR_RANGE 0x20  /* a finite value beyond the range of dsa_prefix_attn's products with FP8 rows */
+#define DSA_DEVERR_RANGE 0x20  /* a finite value beyond the range of dsa_prefix_attn's products with FP8 rows, or of
+                                  dsa_expanded_attn's with head values */
 
 typedef struct {
     int32_t batch;             /* B >= 1 sequences */
@@ -478,7 +479,8 @@ dsa_status_t dsa_value_heads(const dsa_dims_t* dims, const void* o_latent, const
  * and values: the form for prompts).  With c_s the latent part (dims 0..511) and r_s the rotary part of position s,
  *     z_s = softmax_scale * (q_nope[t,h,:] . wk[h] c_s + q_pe[t,h,:] . r_s)   for every visible position s = 0..p_t,
  *     out[t,h,:] = sum_s softmax(z)_s * wv[h] c_s,   lse[t,h] = log sum_s exp(z_s)
- * Keys and values are rounded to bf16 (FP8 rows before that, too), the softmax's weights in the products as well.
+ * Keys are rounded to bf16 (FP8 rows before that, too), values and the softmax's weights in the products to f16: head values
+ * of a magnitude of more than 16376 are beyond that and reported (DSA_DEVERR_RANGE); those below 2^-16 lose relative precision.
  *   total_pages  an upper bound of the pages in use: sum over the sequences with queries of ceil(L_b / 64)
  *   q_nope     [T, Hq, 128] bf16, strides as for dsa_absorb_queries
  *   q_pe       [T, Hq, 64] bf16, rotated (dsa_rope_queries; q + 512 with strides Hq * 576 and 576 is where that leaves it);
@@ -488,8 +490,8 @@ dsa_status_t dsa_value_heads(const dsa_dims_t* dims, const void* o_latent, const
  *   workspace  dsa_expanded_attn_workspace_size(dims, total_pages) bytes, first 256 zero-filled once
  * dims->idx_*, top_k and max_q_len are not looked at.  Positions beyond p_t and rows behind L_b are never part of the result,
  * whatever they hold.  A score of -inf has weight 0; with every score -inf, out = 0 and lse = -inf.  A visible position
- * with a value that is not finite, in its row or in its head values as bf16, makes NaN of the rows that see it (in
- * out and lse; for all heads, where its values are those of one head); so does a page that is out of range, which is
+ * with a value that is not finite, in its row or in its head values as f16, makes NaN of the rows that see it (in
+ * out and lse; of all heads, also where the value is one head's); so does a page that is out of range, which is
  * reported (DSA_DEVERR_PAGE).  A sequence with n_b > L_b, a context beyond its page table or pages beyond total_pages
  * (DSA_DEVERR_SEQ) and a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were.
  * Supported: D = 576, Dv = 512, Hq <= 128.

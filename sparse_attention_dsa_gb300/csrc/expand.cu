@@ -7,8 +7,8 @@
 //   k[s, h] = [wk c_s | r_s] (192 dims),  v[s, h] = wv c_s (128 dims),
 //   z_s = scale * q[t, h] . k[s, h] for s = 0..p_t,  out[t, h] = softmax(z) . v,  lse[t, h] = logsumexp(z).
 // A (query, position, head) takes 2 (192 + 128) operations where the absorbed form takes 2 (576 + 512), and a (position,
-// head) 2 x 256 x 512 for its keys and values, so this is the form for many queries a sequence.  Keys and values are
-// rounded to bf16, as a projection would leave them.
+// head) 2 x 256 x 512 for its keys and values, so this is the form for many queries a sequence.  Keys are rounded to
+// bf16, as a projection would leave them (the queries they meet are bf16), values and weights to f16.
 //
 // Four kernels, chained by programmatic launches:
 //   gather:  the pages' rows as tiles (of 128 positions, a sequence's own) of nine 16 KB pieces (64 dims of 128 positions, FP8
@@ -275,6 +275,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
     }
 }
 
+// Values and weights are multiplied as f16 (11 bits, for bf16's 8: the output's error, 2 bf16 roundings less, fell from
+// 0.0030 to 0.0022 of its norm, of which 0.0017 are its own rounding).  Values are kept times kValueGain, which is taken out of
+// the result: exact down to 2^-16 and up to 65504 / kValueGain.
+constexpr float kValueGain = 4.f;
+__device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the low half
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
 // ---------------------------------------------------------------------------------------------------------
 // keys: D (256 positions x 256) = c W[h]^T for each pair of tiles and each head, cta_group::2: CTA c of the pair holds
 // tile 2 i + c and rows 128 c .. of the head's weights (c = 0: keys, 1: values), both in chunks of 64 inner dims; its
@@ -402,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
             if (!(ok = wait(&ctl->d_full[buf], (t >> 1) & 1u))) break;
             tc_fence_after();
             uint8_t* dst = p.kv + ((int64_t)tile * p.heads + head) * kHeadTile;
-            bool finite = true;
+            bool bad = false, beyond = false;  // a value is not finite as f16; and is finite itself
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {  // 64 columns each
                 float v[4][16];
@@ -417,20 +427,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                     if (lane == 0) mbar_arrive_cluster(d_empty + 8 * buf);
                 }
                 uint4 w[8];
-                uint32_t odd = 0;  // an exponent of all ones carries into the sign bit's place
+                if (c < 2) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float* f = &v[k >> 1][8 * (k & 1)];
-                    w[k] = make_uint4(f2_to_bf2(f[0], f[1]), f2_to_bf2(f[2], f[3]), f2_to_bf2(f[4], f[5]), f2_to_bf2(f[6], f[7]));
-                    const uint32_t e = 0x7F807F80u, one = 0x00800080u;
-                    odd |= ((w[k].x & e) + one) | ((w[k].y & e) + one) | ((w[k].z & e) + one) | ((w[k].w & e) + one);
-                }
-                // a weight of 0 times a value that is not finite is NaN, for rows that do not see the position too: its
-                // values become 0, and the rows that do see it NaN at the end
-                if (c >= 2 && (odd & 0x80008000u) != 0) {
-                    finite = false;
+                    for (int k = 0; k < 8; ++k) {
+                        const float* f = &v[k >> 1][8 * (k & 1)];
+                        w[k] = make_uint4(f2_to_bf2(f[0], f[1]), f2_to_bf2(f[2], f[3]), f2_to_bf2(f[4], f[5]), f2_to_bf2(f[6], f[7]));
+                    }
+                } else {
+                    uint32_t odd = 0;  // an exponent of all ones carries into the sign bit's place
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 8; ++k) {
+                        const float* f = &v[k >> 1][8 * (k & 1)];
+                        uint32_t* h = reinterpret_cast<uint32_t*>(&w[k]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            h[i] = f2_to_h2(f[2 * i] * kValueGain, f[2 * i + 1] * kValueGain);
+                            odd |= (h[i] & 0x7C007C00u) + 0x04000400u;
+                        }
+                    }
+                    // A weight of 0 times a value that is not finite is NaN, for rows that do not see the position too: its
+                    // values become 0, and the rows that do see it NaN at the end.
+                    if ((odd & 0x80008000u) != 0) {
+                        bad = true;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) beyond |= fabsf(v[k][i]) < INFINITY && fabsf(v[k][i]) * kValueGain >= 65520.f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 uint8_t* at = stage + (c & 1) * kPiece;
                 if (lane == 0) bulk_wait_read<1>();
@@ -447,8 +472,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                     bulk_commit();
                 }
             }
-            if (!finite && tile < tiles) {
+            if (bad && tile < tiles) {
                 const int b = sequence_of_tile(p, tile);
+                if (beyond) raise_error(p.err, DSA_DEVERR_RANGE);
                 atomicMin(first_bad(p) + b, 128 * (tile - tile_begin(p)[b]) + 32 * ew + lane);
             }
         }
@@ -481,8 +507,11 @@ constexpr int kQTile = 3 * kUnit;    // 128 queries x 192 dims
 constexpr int kTileUnits = 5;
 constexpr int kOCol = 256;           // tensor memory: S (and P in its first half) at 0 and 128, O at 256 and 384
 constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
-constexpr uint32_t kIdescPV = make_idesc(128, 128, 1, 1, 0, 1);
-constexpr float kRaise = 8.f;  // the running maximum (log2) is raised only when it grows by more than this
+constexpr uint32_t kIdescPV = make_idesc(128, 128, 0, 0, 0, 1);
+constexpr float kRaise = 4.f;  // the running maximum (log2) is raised only when it grows by more than this
+// Weights are taken relative to 2^-kLift of the running maximum: as f16, up to 2^(kRaise + kLift) = 2^15, they keep their
+// precision down to 2^-25 of the largest one's, so that a long context's many small weights beside a large one are not lost.
+constexpr float kLift = 11.f;
 
 // What a CTA works on at a time: a block of queries of a head, with the tiles of keys from j0 to j1 (all of them, or a part)
 struct Segment {
@@ -581,7 +610,7 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
     uint16_t* dst = p.out + at * 128;
     if (whole) {
         if (poisoned) l_sum = NAN;
-        const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+        const float inv = l_sum == 0.f ? 0.f : 1.f / (kValueGain * l_sum);
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
             float o[2][16];
@@ -597,7 +626,7 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
             }
         }
         free_o();
-        if (row < nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
+        if (row < nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used - kLift + log2f(l_sum)) * kLn2;
         return;
     }
     float* slot = part_slot(p, blockIdx.x, first_tile);
@@ -611,14 +640,14 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
                 for (int k = 0; k < 4; ++k) {
                     uint32_t v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[k >> 1][8 * (k & 1) + i]);
+                    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[k >> 1][8 * (k & 1) + i] * (1.f / kValueGain));
                     st_global_32(slot + row * 128 + c + 8 * k, v);
                 }
             }
         }
         free_o();
     }
-    if (row < nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(m_used, l_sum);
+    if (row < nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(m_used - kLift, l_sum);
 }
 
 constexpr int kAttendSmem = 1024 + 2 * kQTile + kRing * kUnit + (int)sizeof(AttendCtrl);
@@ -901,7 +930,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 const bool raise = mt > m_used + kRaise;
                 const float m_new = raise ? mt : m_used;
                 const float alpha = raise && m_used != -INFINITY ? exp2f(m_used - m_new) : 1.f;
-                const float mu = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf) = 0
+                const float mu = m_new == -INFINITY ? 0.f : m_new - kLift;  // nothing seen yet: exp2(-inf) = 0
                 if (__any_sync(kAllLanes, alpha != 1.f)) {  // (the products before this tile's scores are done)
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 16) {
@@ -914,7 +943,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         tmem_st16(ocol + c, o);
                     }
                 }
-                // weights: the sum takes the fp32 values, the products their rounding to bf16 (at most 2^-8 of each, unbiased)
+                // weights: the sum takes the fp32 values, the products their rounding to f16 (at most 2^-11 of each, unbiased)
                 float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
                 const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), mu2 = make_float2(-mu, -mu);
 #pragma unroll
@@ -926,7 +955,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         float2 e = fma2(make_float2(x[0], x[1]), scale2, mu2);
                         e.x = exp2_fast(e.x);
                         e.y = exp2_fast(e.y);
-                        packed[i / 2] = f2_to_bf2(e.x, e.y);
+                        packed[i / 2] = f2_to_h2(e.x, e.y);
                         sum[(i / 2) & 3] = add2(sum[(i / 2) & 3], e);
                     }
                     tmem_st16_u32(scol + 8 * k, packed);

@@ -85,7 +85,8 @@ class Expanded:
         self.weighted = torch.zeros_like(self.out)  # sum_s p_s |v_s|
         w = w_kv.double()
         acc = 2 * sum_rounding(LATENT)
-        # a key or value dim: the latent's rounding to bf16 (FP8 rows), the sum's, its own rounding to bf16
+        # a key or value dim: the latent's rounding to bf16 (FP8 rows), the sum's, its own rounding, a key's to bf16, a value's
+        # to f16 (half a step of 2^-26 of numbers below 2^-16)
         rows_off = (2.0 ** -8 if fp8 else 0.0) + acc
         for b in range(batch.B):
             t0, t1 = batch.cu_host[b], batch.cu_host[b + 1]
@@ -97,6 +98,7 @@ class Expanded:
             c, rot = r[:, :LATENT], r[:, LATENT:]
             k, size = torch.einsum("sc,hdc->shd", c, w), torch.einsum("sc,hdc->shd", c.abs(), w.abs())
             off = 2.0 ** -8 * k.abs() * (1 + 2.0 ** -8) + (1 + 2.0 ** -8) * rows_off * size
+            off[..., NOPE:] = 2.0 ** -11 * k[..., NOPE:].abs() + (1 + 2.0 ** -8) * rows_off * size[..., NOPE:] + 2.0 ** -27
             qn, qp = q_nope[t0:t1].double(), q_pe[t0:t1].double()
             z = (torch.einsum("thd,shd->ths", qn, k[..., :NOPE]) + torch.einsum("thd,sd->ths", qp, rot)) * scale
             dz = torch.einsum("thd,shd->ths", qn.abs(), off[..., :NOPE])
@@ -112,18 +114,19 @@ class Expanded:
             self.dv[t0:t1] = torch.einsum("ths,shd->thd", p, off[..., NOPE:])
             self.dz[t0:t1] = dz.masked_fill(hidden, 0).amax(-1)
 
-    def check(self, out, lse, tokens=None, norm=6e-3):
-        """Weights: e^(2 dz), exp2 within 2^-22, bf16 2^-8 and the sums' 2^-16; the output's own 2^-8.  norm: for standard normal
-        data, where each of up to six roundings to bf16 (0.0017 of a value, root mean square) enters the output's norm
-        by itself: latents, their keys' scores twice (1.4e-3 each), values, weights, output."""
+    def check(self, out, lse, tokens=None, norm=True):
+        """Weights: e^(2 dz), exp2 within 2^-22, f16 2^-11 and the sums' 2^-16; the output's own 2^-8.  norm: for standard normal
+        data, where a rounding to bf16 is 0.0017 of a value, root mean square, each enters the output's norm by itself: the
+        output's (0.0017), the keys' through the scores (0.0014), of FP8 rows the latents' through values (0.0017) and scores
+        (0.0014): 0.0022 and 0.0031, half as much again for a batch of few rows."""
         t = slice(None) if tokens is None else tokens
-        rel = torch.expm1(2 * self.dz[t])[..., None] + 2.0 ** -8 + 2.0 ** -16
+        rel = torch.expm1(2 * self.dz[t])[..., None] + 2.0 ** -11 + 2.0 ** -16
         tol = rel * (self.weighted[t] + self.dv[t]) + self.dv[t]
         tol = tol + 2.0 ** -8 * (self.out[t].abs() + tol) + 1e-30
         err = (out[t].double() - self.out[t]).abs()
         assert bool((err <= tol).all()), f"worst error {err.max().item():.3g}, {(err / tol).max().item():.3g} of its bound"
         size = self.out[t].norm()
-        assert norm is None or err.norm() <= norm * size, f"relative error {(err.norm() / size).item():.3g}"
+        assert not norm or err.norm() <= (4.7e-3 if self.fp8 else 3.3e-3) * size, f"relative error {(err.norm() / size).item():.3g}"
         if lse is not None:
             off = (lse[t].double() - self.lse[t]).abs()
             bound = self.dz[t] + 2.0 ** -18 + 2.0 ** -22 * self.lse[t].abs()

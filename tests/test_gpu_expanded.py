@@ -55,7 +55,7 @@ class Call:
                           self.out, self.lse, self.ws, **a)
         return self
 
-    def check(self, tokens=None, norm=6e-3, error=0):
+    def check(self, tokens=None, norm=True, error=0):
         assert dsa.get_device_error(self.ws) == error
         Expanded(self.b, self.q_nope, self.q_pe, self.w, self.kv, self.fp8).check(self.out, self.lse, tokens, norm)
 
@@ -150,7 +150,7 @@ def test_captured_calls_share_a_workspace():
 @pytest.mark.parametrize("std", [8.0, 0.01])
 def test_sharp_and_flat_weights(std):
     """Scores of a few hundred (one weight next to 1, the maximum rises again and again), and of next to nothing."""
-    Call([700], [400], 4, seed=81, std=std).run().check(norm=None)
+    Call([700], [400], 4, seed=81, std=std).run().check(norm=False)
 
 
 def test_rising_scores():
@@ -165,7 +165,7 @@ def test_rising_scores():
             lift = lift.flip(0)
         flat[row, LATENT] = lift.to(torch.bfloat16)
         c.q_pe[..., 0] = 8.0
-        c.run().check(norm=None)
+        c.run().check(norm=False)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -214,8 +214,35 @@ def test_a_row_that_is_not_finite(place, bad):
     ref = Expanded(c.b, c.q_nope, c.q_pe, c.w, c.kv, False)
     far = sign < -0.5
     err = (c.out[after][far].double() - ref.out[after][far]).norm()
-    assert err <= 6e-3 * ref.out[after][far].norm()
+    assert err <= 3.3e-3 * ref.out[after][far].norm()
     assert bool(((c.lse[after][far].double() - ref.lse[after][far]).abs() <= 0.05).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_values_beyond_range_are_reported(fp8):
+    """Head values beyond f16's range: reported, NaN for those who see them; the largest ones within it are exact enough."""
+    clean = Call([300], [260], 2, fp8, seed=115).run()
+    for size, fits in ((3.0e4, False), (1.2e4, True)):
+        c = Call([300], [260], 2, fp8, seed=115)
+        at = 180
+        page, place = int(c.b.pt_host[0, at // PAGE]), at % PAGE
+        row = torch.zeros(1, KV, dtype=torch.bfloat16, device="cuda")
+        row[0, 7] = size  # its head values are size times a column of the weights; those of one dim are made 1
+        c.w[:, NOPE:, 7] = 0
+        c.w[1, NOPE + 3, 7] = 1.0
+        c.w[:, :NOPE, 7] = 0
+        c.kv[page, place] = latent_fp8_rows(row)[0] if fp8 else row[0]
+        clean.w.copy_(c.w)
+        clean.run()
+        c.run()
+        pos = torch.tensor(c.b.pos, device="cuda")
+        before, after = pos < at, pos >= at
+        assert torch.equal(c.out[before], clean.out[before])
+        if fits:
+            c.check(norm=False)
+        else:
+            assert dsa.get_device_error(c.ws) == dsa.DSA_DEVERR_RANGE
+            assert bool(c.out[after].isnan().all())
 
 
 def test_queries_that_are_not_finite():
@@ -374,7 +401,6 @@ def test_a_layer_in_both_forms(fp8):
         assert dsa.get_device_error(w) == 0
     ref = Expanded(b, q_proj[..., :NOPE], queries[..., LATENT:], w_kv, cache, fp8)
     ref.check(expanded, lse2)
-    # the absorbed form: q, its output and the values are each rounded to bf16 (0.0017 each), weights too, scores as the
-    # keys' are
-    assert (absorbed.double() - ref.out).norm() <= 6e-3 * ref.out.norm()
+    # the absorbed form rounds to bf16 (0.0017 each): q, and so its scores, weights, its output and the values
+    assert (absorbed.double() - ref.out).norm() <= 5e-3 * ref.out.norm()
     assert (lse.double() - ref.lse).abs().max() <= ref.dz.max() + 2.0 ** -8 * 8
