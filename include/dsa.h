@@ -456,7 +456,7 @@ dsa_status_t dsa_rms_norm(int32_t rows, int32_t dim, const void* x, int64_t x_st
  *     q[t,h,c] = sum_d q_nope[t,h,d] * wk[h,d,c]   for c = 0..511 (dims 512..575 are left as they are: dsa_rope_queries)
  *   q_nope     [T, Hq, 128] bf16; head h of token t starts t * token_stride + h * head_stride elements in (both 0: dense;
  *              else both multiples of 8, head_stride >= 128)
- *   q          [T, Hq, D] bf16, written in dims 0..511
+ *   q          [T, Hq, D] bf16, written in dims 0..511; q_nope lies elsewhere
  *   workspace  256 bytes, zero-filled once (only the error word is used, for a wait that gave up)
  * Sums in fp32, rounded once.  Of dims, total_q, attn_heads, kv_dim and v_dim are looked at.  Supported: D = 576, Dv = 512,
  * Hq <= 128.

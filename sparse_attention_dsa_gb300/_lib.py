@@ -351,10 +351,10 @@ def rms_norm(x, weight, eps, out=None, codes=None, scale=None, codes_dtype=DSA_F
              stream=None):
     """dsa_rms_norm: x [rows, dim] (rows and the strides of x and out are those of the tensors) plus residual, normalised,
     to bf16 (out) and codes with scales."""
-    rows, dim = x.shape
+    rows, dim = x.shape if x.dim() == 2 else (-1, -1)
     for name, t in (("x", x), ("out", out)):
         if t is not None and (tuple(t.shape) != (rows, dim) or t.stride(1) != 1):
-            raise DsaError(DSA_ERR_INVALID_ARG, f"{name} must be [{rows}, {dim}] with dense rows (got {tuple(t.shape)}, "
+            raise DsaError(DSA_ERR_INVALID_ARG, f"{name} must be [rows, dim], the same for both, with dense rows (got {tuple(t.shape)}, "
                                                 f"strides {tuple(t.stride())})")
     _check(lib().dsa_rms_norm(rows, dim, _ptr(x), x.stride(0) if rows > 1 else 0, _ptr(residual), _ptr(sum), _ptr(weight),
                               float(eps), _ptr(out), out.stride(0) if out is not None and rows > 1 else 0, int(codes_dtype),

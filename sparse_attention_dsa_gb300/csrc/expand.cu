@@ -74,12 +74,14 @@ __device__ __forceinline__ int64_t places_of(int pos0, int n) {
     const int64_t whole = places_before(pos0, n / kBlockRows);
     return n % kBlockRows ? whole + kItemCost + tiles_seen(pos0, n) : whole;
 }
+// The plan and the lengths are read from L2: the combining kernel looks at them before it has waited for the kernel in front.
+__device__ __forceinline__ int ld_plan(const int32_t* a) { return __ldcg(a); }
 // The last of a[0 .. n - 1] (ascending) that is not above x; a[0] is not.  Called by a whole warp.
 __device__ __forceinline__ int last_not_above(const int32_t* a, int n, int x, int lane) {
     int lo = 0;  // the answer is in [lo, lo + n)
     while (n > 1) {
         const int step = (n + 31) / 32;
-        const uint32_t le = __ballot_sync(kAllLanes, step * lane < n && a[lo + step * lane] <= x);  // (lane 0's always)
+        const uint32_t le = __ballot_sync(kAllLanes, step * lane < n && ld_plan(a + lo + step * lane) <= x);  // (lane 0's always)
         const int k = 31 - __clz(le);
         lo += step * k;
         n = min(step, n - step * k);
@@ -126,13 +128,15 @@ __device__ __forceinline__ int sequence_of_tile(const ExpandParams& p, int tile)
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// gather: a block takes half tiles (64 positions, one page), a warp positions.  Every block numbers the sequences' tiles for
+// gather: a block takes 16 positions at a time, a warp two of them (with 64 a block, 4096 positions took 11.7 us).  Every block numbers the sequences' tiles for
 // itself (each thread a run of sequences, then a scan of the threads' sums), which costs less than a kernel in front; the
 // first one leaves the plan.  Rows of a page that is out of range become NaN, and so the scores of whoever sees them.
 // Bound by HBM and L2: 1152 or 656 bytes read, 1152 written a position.
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kGatherWarps = 8;
 constexpr int kGatherThreads = 32 * kGatherWarps;
+constexpr int kGatherRows = 2 * kGatherWarps;
+constexpr int kGatherUnits = 128 / kGatherRows;  // of a tile
 
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandParams p) {
     __shared__ long long scan[3][kGatherWarps];
@@ -222,10 +226,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
             if (p.cu_q_lens[0] != 0 || p.cu_q_lens[p.batch] != p.total_q) raise_error(p.err, DSA_DEVERR_SEQ);
         }
     }
-    const int halves = 2 * tiles;
+    const int64_t units = (int64_t)kGatherUnits * tiles;
     uint32_t turn = 0;
-    for (int i = blockIdx.x; i < halves; i += gridDim.x, turn ^= 1u) {
-        const int tile = i >> 1;
+    for (int64_t i = blockIdx.x; i < units; i += gridDim.x, turn ^= 1u) {
+        const int tile = (int)(i / kGatherUnits), row0 = kGatherRows * (int)(i % kGatherUnits);
         if (tile >= before[0] && tile < before[0] + sum[0]) {  // a sequence of this thread's run
             long long at = before[0];
             for (int b = b0; b < b1; ++b) {
@@ -239,23 +243,23 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
             }
         }
         __syncthreads();
-        const int b = found[turn].x, base = 128 * (tile - found[turn].y) + 64 * (i & 1);
+        const int b = found[turn].x, base = 128 * (tile - found[turn].y) + row0;
         const int L = p.seq_lens[b];
         const int pg = base < L ? p.page_table[(int64_t)b * p.max_pages + (base >> 6)] : 0;
         const bool in = pg >= 0 && pg < p.num_pages;
         if (!in && tid == 0) raise_error(p.err, DSA_DEVERR_PAGE);
         uint8_t* dst = p.latents + (int64_t)tile * kTileBytes;
         const uint4 zero = make_uint4(0, 0, 0, 0), nan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-#pragma unroll 2
-        for (int j = warp; j < 64; j += kGatherWarps) {
-            const int row = 64 * (i & 1) + j;
+#pragma unroll
+        for (int j = warp; j < kGatherRows; j += kGatherWarps) {
+            const int row = row0 + j, of_page = (base & 63) + j;
             const bool have = in && base + j < L;
             const uint4 none = in || base + j >= L ? zero : nan;
             auto put = [&](int chunk, uint4 v) {  // 16-byte chunk of the row's 72
                 *reinterpret_cast<uint4*>(dst + (chunk >> 3) * kUnit + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = v;
             };
             if (!p.kv_fp8 || !have) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.kv_cache + ((int64_t)pg * 64 + j) * 1152);
+                const uint4* src = reinterpret_cast<const uint4*>(p.kv_cache + ((int64_t)pg * 64 + of_page) * 1152);
                 uint4 v[3];
 #pragma unroll
                 for (int k = 0; k < 3; ++k) v[k] = have && lane + 32 * k < 72 ? src[lane + 32 * k] : none;
@@ -263,7 +267,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
                 for (int k = 0; k < 3; ++k)
                     if (lane + 32 * k < 72) put(lane + 32 * k, v[k]);
             } else {
-                const uint8_t* src = p.kv_cache + ((int64_t)pg * 64 + j) * kKvFp8RowBytes;
+                const uint8_t* src = p.kv_cache + ((int64_t)pg * 64 + of_page) * kKvFp8RowBytes;
                 const uint4 code = reinterpret_cast<const uint4*>(src)[lane];
                 const float scale = reinterpret_cast<const float*>(src + kKvFp8ScaleOff)[lane >> 3];
                 const uint4 rot = lane < 8 ? reinterpret_cast<const uint4*>(src + kKvFp8RopeOff)[lane] : zero;
@@ -546,15 +550,15 @@ __device__ __forceinline__ int seg_end(const Segment& s, int w) { return min(s.j
 
 // Rows and keys of block i of sequence b; false where the sequence is left out.
 __device__ __forceinline__ bool block_rows(const ExpandParams& p, int b, int i, Segment* s) {
-    const int c0 = p.cu_q_lens[b], n = p.cu_q_lens[b + 1] - c0, q = i * kBlockRows;
+    const int c0 = ld_plan(p.cu_q_lens + b), n = ld_plan(p.cu_q_lens + b + 1) - c0, q = i * kBlockRows;
     s->seq = b;
     s->row0 = c0 + q;
     s->nrows = min(kBlockRows, n - q);
-    s->pos0 = p.seq_lens[b] - n + q;
-    s->tile0 = tile_begin(p)[b];
+    s->pos0 = ld_plan(p.seq_lens + b) - n + q;
+    s->tile0 = ld_plan(tile_begin(p) + b);
     s->n0 = tiles_seen(s->pos0, min(s->nrows, 128));
     s->n1 = s->nrows > 128 ? tiles_seen(s->pos0, s->nrows) : 0;
-    return first_bad(p)[b] >= 0;
+    return ld_plan(first_bad(p) + b) >= 0;
 }
 // The block at place x of a head's line: its sequence and number there, its first place, and that of the next block.
 // Called by a whole warp.
@@ -564,7 +568,8 @@ struct Place {
 __device__ __forceinline__ Place block_at(const ExpandParams& p, int x, int lane) {
     Place w;
     w.b = last_not_above(place_begin(p), p.batch, x, lane);
-    const int n = p.cu_q_lens[w.b + 1] - p.cu_q_lens[w.b], pos0 = p.seq_lens[w.b] - n, first = place_begin(p)[w.b];
+    const int n = ld_plan(p.cu_q_lens + w.b + 1) - ld_plan(p.cu_q_lens + w.b), pos0 = ld_plan(p.seq_lens + w.b) - n;
+    const int first = ld_plan(place_begin(p) + w.b);
     int lo = 0, hi = (n + kBlockRows - 1) / kBlockRows;  // the last block that begins no later
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -853,8 +858,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 return true;
             };
             uint32_t u = 0;
-            Step before;
-            before.have[0] = before.have[1] = false;
+            Step before = {};
             for (uint32_t n = 0; ok; ++n) {
                 if (!(ok = wait_one(&ctl->seg_full[n % kSegments], (n / kSegments) & 1u))) break;
                 const Segment s = ctl->segments[n % kSegments];
@@ -1008,7 +1012,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Expan
     // The plan is older than the attention: its blocks, when they let this kernel start, had waited for the end of what
     // made it.  So the item is looked up while the attention still runs.  (No block returns before its end, though: what is
     // launched behind this kernel takes the end of all blocks for the end of the attention.)
-    const PlanHead plan = *plan_head(p);
+    PlanHead plan;
+    plan.parts = ld_plan(&plan_head(p)->parts);
     const bool part_begins = k < plan.parts;
     int64_t line = 1, begin = 0;
     int n_tiles = 0, last = k;
@@ -1020,7 +1025,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Expan
     s.nrows = 0;
     if (part_begins) {
         // the item in which part k begins; the first part that begins inside it takes care of it
-        const int64_t head_line = place_begin(p)[p.batch];
+        const int64_t head_line = ld_plan(place_begin(p) + p.batch);
         line = head_line * p.heads;
         const int64_t x = part_begin(k, line, plan.parts);
         s.head = (int)(x / head_line);
@@ -1097,8 +1102,8 @@ cudaError_t launch_expand(const ExpandLaunch& L, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int64_t halves = 2 * (int64_t)p.cap_tiles;
-    cfg.gridDim = dim3((unsigned)(halves < 8 * L.num_sms ? halves : 8 * L.num_sms));
+    const int64_t gathered = (int64_t)kGatherUnits * p.cap_tiles, blocks = 8 * L.num_sms;
+    cfg.gridDim = dim3((unsigned)(gathered < blocks ? gathered : blocks));
     cfg.blockDim = dim3(kGatherThreads);
     if ((e = cudaLaunchKernelEx(&cfg, gather_kernel, p)) != cudaSuccess) return e;
     const int64_t units = (int64_t)((p.cap_tiles + 1) / 2) * p.heads;

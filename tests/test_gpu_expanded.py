@@ -147,6 +147,34 @@ def test_captured_calls_share_a_workspace():
     small.check()
 
 
+def test_a_captured_call_with_other_lengths():
+    """What a graph's call plans by is read anew at each replay (items cut or whole, other tiles, other pages)."""
+    lens = [([1500, 40], [700, 40]), ([300, 300], [440, 300]), ([740, 1], [739, 1]), ([1500, 1500], [100, 640])]
+    c = Call([1500, 1500], [740, 0], 8, seed=77)
+    tokens, pt = 740, c.b.pt_host
+    c.pages = 48
+    c.ws = torch.zeros(dsa.expanded_attn_workspace_size(c.dims, c.pages), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run()
+    for seq, q in lens * 2:
+        q = [q[0], tokens - q[0]] if q[0] + q[1] > tokens else q
+        seq = [max(a, b) for a, b in zip(seq, q)]
+        b = Batch(seq, q, seed=78)
+        b.pt_host = pt
+        c.b.lens.copy_(b.lens)
+        c.b.cu.copy_(torch.tensor([0, q[0], q[0] + q[1]], dtype=torch.int32))
+        c.out.fill_(7)
+        c.lse.fill_(7)
+        graph.replay()
+        owned = q[0] + q[1]
+        assert dsa.get_device_error(c.ws) == (0 if owned == tokens else dsa.DSA_DEVERR_SEQ)
+        dsa.clear_device_error(c.ws)
+        ref = Expanded(b, c.q_nope[:owned], c.q_pe[:owned], c.w, c.kv, False)
+        ref.check(c.out[:owned], c.lse[:owned])
+        assert bool((c.out[owned:] == 7).all())
+
+
 @pytest.mark.parametrize("std", [8.0, 0.01])
 def test_sharp_and_flat_weights(std):
     """Scores of a few hundred (one weight next to 1, the maximum rises again and again), and of next to nothing."""

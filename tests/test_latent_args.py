@@ -169,6 +169,8 @@ def test_wrappers_raise():
         with pytest.raises(dsa.DsaError, match="out must be"):
             dsa.rms_norm(x, x[0], 1e-6, out=bad, stream=0)
     with pytest.raises(dsa.DsaError, match="x must be"):
+        dsa.rms_norm(x[0], x[0], 1e-6, out=x, stream=0)
+    with pytest.raises(dsa.DsaError, match="x must be"):
         dsa.rms_norm(torch.zeros((4, 128), dtype=torch.bfloat16)[:, ::2], x[0], 1e-6, out=x, stream=0)
     with pytest.raises(dsa.DsaError, match="eps"):
         dsa.rms_norm(x, x[0], -1.0, out=torch.zeros_like(x), stream=0)
