@@ -631,7 +631,7 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
             }
         }
         free_o();
-        if (row < nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used - kLift + log2f(l_sum)) * kLn2;
+        if (row < nrows && p.lse) p.lse[at] = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * kLn2;
         return;
     }
     float* slot = part_slot(p, blockIdx.x, first_tile);
@@ -652,7 +652,7 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
         }
         free_o();
     }
-    if (row < nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(m_used - kLift, l_sum);
+    if (row < nrows) reinterpret_cast<float2*>(slot + kBlockRows * 128)[row] = make_float2(m_used, l_sum);
 }
 
 constexpr int kAttendSmem = 1024 + 2 * kQTile + kRing * kUnit + (int)sizeof(AttendCtrl);
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 give_back();
                 continue;
             }
-            float m_used = -INFINITY, l_sum = 0.f;
+            float m_used = -INFINITY, l_sum = 0.f;  // what weights are relative to (log2): the maximum - kLift; their sum
 #pragma unroll 1
             for (int j = begin; j < end; ++j, ++tile) {
                 if (!(ok = wait(&ctl->s_full[w], tile & 1u))) break;
@@ -931,10 +931,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 #pragma unroll
                     for (int i = 0; i < h; ++i) mx[i] = fmaxf(mx[i], mx[i + h]);
                 const float mt = mx[0] * p.scale_log2;
-                const bool raise = mt > m_used + kRaise;
-                const float m_new = raise ? mt : m_used;
+                const bool raise = mt > m_used + (kRaise + kLift);
+                const float m_new = raise ? mt - kLift : m_used;
                 const float alpha = raise && m_used != -INFINITY ? exp2f(m_used - m_new) : 1.f;
-                const float mu = m_new == -INFINITY ? 0.f : m_new - kLift;  // nothing seen yet: exp2(-inf) = 0
+                const float mu = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet: exp2(-inf) = 0
                 if (__any_sync(kAllLanes, alpha != 1.f)) {  // (the products before this tile's scores are done)
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 16) {
