@@ -18,6 +18,15 @@
 //   attend:  a CTA takes 256 queries of a head as two tiles of 128 that share K and V; all such items, each as long as its
 //            tiles of keys, are cut into equal parts, one for each CTA, or (where that does not pay) they are taken whole in turn;
 //   combine: the results of items that were cut.
+//
+// What bounds it, and measured (one GB300; calls in a graph, in brackets with L2 flushed before).  The tensor pipe: a tile of 128 x
+// 128 is 1280 cycles of products, in which its softmax (about 1150) and its group's wait for the other tile's products pass.
+// An 8192-token prompt of 128 heads 1722 us (1805 to 1861), 3.02 TFLOP, 1.75 PFLOP/s, 0.93 of the measured cuBLAS rate, of
+// which gathering 8, keys 170 (275 GFLOP; their 537 MB are written at HBM's pace for writes), the rest attention at 1.8; in
+// a long loop the power limit takes up to 14% of the clock.  4096 queries behind 12288 of 16 heads 412 us (417), 0.87 of it:
+// the parts' results and their combination 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 177 us (183):
+// a quarter of the pairs in its tiles are masked, an item of some six tiles costs about two more, keys 48.  Three prompts of
+// up to 200 queries, 16 heads 23 us (32): three kernels' latency, one after another.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -37,10 +46,10 @@ constexpr int kHeadTile = kExpandHeadTileBytes;  // keys (two units) and values 
 constexpr int kBlockRows = kExpandBlockRows;
 
 // What the gathering kernel leaves of its plan (int32): a PlanHead, then for each sequence its first tile, its first block
-// of queries and its first place on the line (one more of each than sequences; first tile -1: left out), and first_bad.
+// of queries and its first place on the line (one more of each than sequences), and first_bad.
 struct PlanHead {
     int32_t tiles;    // in use
-    int32_t blocks;   // in the list
+    int32_t blocks;   // of queries, of a head
     int32_t counter;  // whole items handed out
     int32_t parts;    // the line of items is cut in so many parts; 0: whole items
     int32_t group;    // whole items: heads that are worked on together
@@ -50,19 +59,24 @@ __device__ __forceinline__ PlanHead* plan_head(const ExpandParams& p) { return r
 __device__ __forceinline__ int32_t* tile_begin(const ExpandParams& p) { return p.plan + sizeof(PlanHead) / 4; }
 __device__ __forceinline__ int32_t* block_begin(const ExpandParams& p) { return tile_begin(p) + p.batch + 1; }
 __device__ __forceinline__ int32_t* place_begin(const ExpandParams& p) { return block_begin(p) + p.batch + 1; }
-// First position of a sequence that has no finite values or no page (INT32_MAX: none): rows that see it are NaN.
+// First position of a sequence that has no finite values or no page (INT32_MAX: none): rows that see it are NaN.  -1: the
+// sequence is left out, as its tiles do not fit.
 __device__ __forceinline__ int32_t* first_bad(const ExpandParams& p) { return place_begin(p) + p.batch + 1; }
 static_assert(kExpandPlanHead == sizeof(PlanHead) / 4, "expand_plan_bytes()");
 
-// A block's place on the line: kItemCost places for what it costs beside its tiles (its queries' load, its first scores'
-// latency, its result), then one for each tile of keys.  kMinPlaces: a part is no shorter on average.  kWholeItems: items
-// are taken whole where the longest is no more than that part of a CTA's share (whole items of a head meet its keys in
-// L2, and have nothing to combine).
-constexpr int kItemCost = 2;
+// The line: the blocks of head 0, of head 1, ..., each kItemCost places for what it costs beside its tiles (its queries' load,
+// its first scores' latency, its result) and one for each tile of keys.  It is cut into equal parts, of kMinPlaces at least
+// on average, or its items are taken whole in turn:
+//   * whole, where the estimate of the last CTA's time is no longer than with parts (three short prompts 23.0 us, cut 30.9;
+//     eight ragged ones 176, cut 187; but 256 items of 112 tiles, for 152 CTAs, 455, cut 415);
+//   * whole, where the longest item is no more than 1 / kWholeItems of a CTA's share: heads go in groups whose keys and
+//     values (kGroupBytes) stay in L2 while all their blocks meet them (the 8192-token prompt of 128 heads 1722 us; head by head
+//     1753, all heads together 1881, cut 1939).
+constexpr int kItemCost = 2;  // (1 and 3: no difference beyond the runs')
 constexpr int kMinPlaces = 4;
 constexpr int kWholeItems = 8;
 constexpr int kCutCost = 8;  // what cutting costs a CTA: writing parts, combining
-constexpr int64_t kGroupBytes = 48 << 20;  // keys and values of heads that are worked on together
+constexpr int64_t kGroupBytes = 48 << 20;
 __device__ __forceinline__ int tiles_before(int place, int n) { return min(n, max(0, place - kItemCost)); }
 // Tiles of keys that n queries from position pos0 see.
 __device__ __forceinline__ int tiles_seen(int pos0, int n) { return (pos0 + n + 127) / 128; }
@@ -292,7 +306,9 @@ __device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the lo
 // ---------------------------------------------------------------------------------------------------------
 // keys: D (256 positions x 256) = c W[h]^T for each pair of tiles and each head, cta_group::2: CTA c of the pair holds
 // tile 2 i + c and rows 128 c .. of the head's weights (c = 0: keys, 1: values), both in chunks of 64 inner dims; its
-// tensor memory receives its tile's keys and values.
+// tensor memory receives its tile's keys and values.  A pair's tile takes half of what two single ones would from L2 (64 bytes
+// a cycle and SM), which would bound it otherwise.  8192 positions of 128 heads: 170 us, 1.6 PFLOP/s (head after head; tile
+// after tile 180; without its stores 137: 537 MB, which writes alone take 134 us for).
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kKeysThreads = 256;  // warp 0: TMA, 1: products, 2: tensor memory, 4-7: results
 constexpr int kKeysResultWarp = 4;
@@ -501,7 +517,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// attend
+// attend: S_w = Q_w K^T and O_w += P_w V for the two query tiles w = 0, 1 in turn, all in tensor memory (P over its own S as
+// 16-bit pairs), so that the softmax of one tile runs under the products of the other.  K and V come in 16 KB units (bulk
+// copies of what the keys kernel left in the tensor cores' layout) through a ring, each unit freed by the products that read it
+// last.  The running maximum is raised only when it grows by more than 2^kRaise.
+// Tried and not kept: results by warps of their own (the softmax's registers), one barrier for all units of a tile's keys or
+// values (the ring refills later: 440 us for 420 where keys come from HBM), both groups at the same queries' tiles of
+// keys in turn where there are no more than 128 (as long: it reads twice the keys a step), cut items joined by the last CTA
+// with a part (its code took registers from the softmax's loop: 1.3 times the time of all).
 // ---------------------------------------------------------------------------------------------------------
 constexpr int kAttendThreads = 320;  // warps 0-3 and 4-7: softmax of the two query tiles, 8: loads, 9: products
 constexpr int kLoadWarp = 8;

@@ -18,7 +18,7 @@
 // What bounds it: HBM.  Absorb writes 1024 bytes for 256 read, and writes alone run at 4.0 TB/s here (filling memory):
 // 4096 tokens of 128 heads 139 us for 537 MB written, 0.96 of that.  Values reads four times what it writes: 2111 tokens of
 // 128 heads 58 us for 363 MB, 6.3 TB/s, 0.93 of the copy bandwidth.  Few tokens: each head's weights once, and latency; 32
-// tokens of 128 heads 6.2 us (L2 flushed before each call 13.5), 130 tokens of 16 heads 6.1 (11.4).
+// tokens of 128 heads 6.0 to 7.0 us (L2 flushed before each call 13.5), 130 tokens of 16 heads 4.9 to 5.4 (11.4).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

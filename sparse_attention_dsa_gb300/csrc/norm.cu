@@ -11,9 +11,9 @@
 // of up to 1024 values by a warp (no block barrier), a longer one by a block.
 //
 // Measured (one GB300; 20 calls in a graph; in brackets with L2 flushed before each): 32 rows of 4096 with the residual
-// 2.0 us (7.3), 1171 of 1536 to MXFP8 3.0 (9.3), latency; 4096 of 512 2.5 (9.3); 8192 rows of 8192 with the residual 78 us to
-// bf16 (85; 537 MB, 6.9 TB/s, 1.01 of the copy bandwidth), 80 to FP8 in tiles (85; 472 MB, 5.9 TB/s, 0.88: the codes' arithmetic
-// between a row's loads and its stores); 16384 of 4096 to FP8 rows 74 (81; 0.94).
+// 2.0 us (7.3), 1171 of 1536 to MXFP8 3.0 to 3.7 (9.3), latency; 4096 of 512 2.5 to 3.2 (9.3); 8192 rows of 8192 with the
+// residual 78 us to bf16 (85; 537 MB, 6.9 TB/s, 1.01 of the copy bandwidth), 76 to 80 to FP8 in tiles (81 to 85; 472 MB, 6.1 TB/s,
+// 0.9: the codes' arithmetic between a row's loads and its stores); 16384 of 4096 to FP8 rows 74 (81; 0.94).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
