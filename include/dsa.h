@@ -87,7 +87,7 @@ typedef enum {
                                   dsa_set_wait_limit_ns() says otherwise) */
 #define DSA_DEVERR_ROPE 0x10   /* a position beyond the rotation table was needed */
 #define DSA_DEVERR_RANGE 0x20  /* a finite value beyond the range of dsa_prefix_attn's products with FP8 rows, or of
-                                  dsa_expanded_attn's with head values */
+                                  dsa_expanded_attn's products */
 
 typedef struct {
     int32_t batch;             /* B >= 1 sequences */
@@ -479,8 +479,9 @@ dsa_status_t dsa_value_heads(const dsa_dims_t* dims, const void* o_latent, const
  * and values: the form for prompts).  With c_s the latent part (dims 0..511) and r_s the rotary part of position s,
  *     z_s = softmax_scale * (q_nope[t,h,:] . wk[h] c_s + q_pe[t,h,:] . r_s)   for every visible position s = 0..p_t,
  *     out[t,h,:] = sum_s softmax(z)_s * wv[h] c_s,   lse[t,h] = log sum_s exp(z_s)
- * Keys are rounded to bf16 (FP8 rows before that, too), values and the softmax's weights in the products to f16: head values
- * of a magnitude of more than 16376 are beyond that and reported (DSA_DEVERR_RANGE); those below 2^-16 lose relative precision.
+ * Keys are rounded to bf16, values and the softmax's weights in the products to f16, and with FP8 rows their latent part and
+ * w_kv before that.  Head values and FP8 rows' elements of a magnitude of more than 16376 (w_kv with FP8 rows: 4094) are beyond
+ * that and reported (DSA_DEVERR_RANGE); those below 2^-16 (2^-18) lose relative precision.
  *   total_pages  an upper bound of the pages in use: sum over the sequences with queries of ceil(L_b / 64)
  *   q_nope     [T, Hq, 128] bf16, strides as for dsa_absorb_queries
  *   q_pe       [T, Hq, 64] bf16, rotated (dsa_rope_queries; q + 512 with strides Hq * 576 and 576 is where that leaves it);
@@ -503,8 +504,8 @@ dsa_status_t dsa_expanded_attn(const dsa_dims_t* dims, int32_t total_pages, cons
                                void* stream);
 
 /*
- * Bytes of workspace that dsa_expanded_attn needs for these sizes, and for every call of the same attn_heads whose batch,
- * total_q and total_pages are no larger: mostly 512 bytes a position and head (64 KB for 128 heads) and 1152 bytes a
+ * Bytes of workspace that dsa_expanded_attn needs for these sizes, and for every call of the same attn_heads and kv_dtype whose
+ * batch, total_q and total_pages are no larger: mostly 512 bytes a position and head (64 KB for 128 heads) and 1152 bytes a
  * position, positions counted in tiles of 128 a sequence.  256 where dsa_expanded_attn refuses the sizes as too large, 0 when
  * dims is NULL or total_pages below 1.  Host-only.
  */

@@ -284,9 +284,10 @@ bool expand_sizes(const dsa_dims_t* d, int32_t total_pages, dsa::ExpandParams* p
     p->batch = d->batch;
     p->total_q = d->total_q;
     p->heads = d->attn_heads;
+    p->kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
     p->cap_tiles = (int32_t)tiles;
     p->cap_blocks = (int32_t)blocks;
-    *bytes = dsa::expand_plan_bytes(*p) + dsa::kExpandPartBytes + (size_t)tiles * dsa::kExpandTileBytes +
+    *bytes = dsa::expand_plan_bytes(*p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(*p) + (size_t)tiles * dsa::kExpandTileBytes +
              (size_t)tiles * d->attn_heads * dsa::kExpandHeadTileBytes;
     return true;
 }
@@ -1082,14 +1083,15 @@ dsa_status_t dsa_expanded_attn(const dsa_dims_t* d, int32_t total_pages, const v
     p.err = static_cast<int32_t*>(workspace);
     p.num_pages = d->num_pages;
     p.max_pages = d->max_pages_per_seq;
-    p.kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
+    p.w_kv = static_cast<const uint16_t*>(w_kv);
     p.scale_log2 = d->softmax_scale * 1.4426950408889634f;
     p.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
     uint8_t* ws = static_cast<uint8_t*>(workspace) + dsa::kErrorWordArea;
     p.plan = reinterpret_cast<int32_t*>(ws);
     p.ctas = dev.num_sms < dsa::kExpandCtas ? dev.num_sms : dsa::kExpandCtas;
     p.partial = reinterpret_cast<float*>(ws + dsa::expand_plan_bytes(p));
-    p.latents = ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes;
+    p.weights16 = reinterpret_cast<uint16_t*>(ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes);
+    p.latents = ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(p);
     p.kv = p.latents + (size_t)p.cap_tiles * dsa::kExpandTileBytes;
     L.num_sms = dev.num_sms;
     const uint64_t T = (uint64_t)d->total_q, H = (uint64_t)d->attn_heads;
@@ -1099,7 +1101,7 @@ dsa_status_t dsa_expanded_attn(const dsa_dims_t* d, int32_t total_pages, const v
                           true, "q_pe")) ||
         (st = encode_rows(&L.cmap, p.latents, {64, 128, (uint64_t)p.cap_tiles * 9}, {64, 64 * 128}, {64, 128, 1}, false,
                           "the gathered rows")) ||
-        (st = encode_rows(&L.wmap, w_kv, {512, 256, H}, {512, 256 * 512}, {64, 128, 1}, true, "w_kv")))
+        (st = encode_rows(&L.wmap, p.kv_fp8 ? p.weights16 : w_kv, {512, 256, H}, {512, 256 * 512}, {64, 128, 1}, true, "w_kv")))
         return st;
     cudaError_t e = dsa::launch_expand(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "expanded attention launch");

@@ -11,9 +11,9 @@
 // bf16, as a projection would leave them (the queries they meet are bf16), values and weights to f16.
 //
 // Four kernels, chained by programmatic launches:
-//   gather:  the pages' rows as tiles (of 128 positions, a sequence's own) of nine 16 KB pieces (64 dims of 128 positions, FP8
-//            rows as bf16; zeros behind the last position), the layout that the tensor cores read (128-byte swizzle); and
-//            the plan: where each sequence's tiles and blocks of 256 queries are;
+//   gather:  the pages' rows as tiles (of 128 positions, a sequence's own) of nine 16 KB pieces (64 dims of 128 positions;
+//            zeros behind the last position; FP8 rows as f16, and then the weights, too), the layout that the tensor cores
+//            read (128-byte swizzle); and the plan: where each sequence's tiles and blocks of 256 queries are;
 //   keys:    K and V = W c: a matrix product of all tiles and heads, CTA pairs (256 positions x a head's 256 rows);
 //   attend:  a CTA takes 256 queries of a head as two tiles of 128 that share K and V; all such items, each as long as its
 //            tiles of keys, are cut into equal parts, one for each CTA, or (where that does not pay) they are taken whole in turn;
@@ -24,7 +24,7 @@
 // An 8192-token prompt of 128 heads 1722 us (1805 to 1861), 3.02 TFLOP, 1.75 PFLOP/s, 0.93 of the measured cuBLAS rate, of
 // which gathering 8, keys 170 (275 GFLOP; their 537 MB are written at HBM's pace for writes), the rest attention at 1.8; in
 // a long loop the power limit takes up to 14% of the clock.  4096 queries behind 12288 of 16 heads 412 us (417), 0.87 of it:
-// the parts' results and their combination 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 177 us (183):
+// the parts' results and their combination 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 181 us (188):
 // a quarter of the pairs in its tiles are masked, an item of some six tiles costs about two more, keys 48.  Three prompts of
 // up to 200 queries, 16 heads 23 us (32): three kernels' latency, one after another.
 #include <cuda_runtime.h>
@@ -141,6 +141,50 @@ __device__ __forceinline__ int sequence_of_tile(const ExpandParams& p, int tile)
     return lo;
 }
 
+// Values and weights are multiplied as f16 (11 bits, for bf16's 8: the output's error, 2 bf16 roundings less, fell from
+// 0.0030 to 0.0022 of its norm, of which 0.0017 are its own rounding).  Values are kept times kValueGain, which is taken out of
+// the result: exact down to 2^-16 and up to 65504 / kValueGain.
+constexpr float kValueGain = 4.f;
+__device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the low half
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// FP8 rows are multiplied as f16, too (a code's four bits times a scale lose 2^-11 of it, for bf16's 2^-8), times kRowGain, and
+// the weights with them, times kWeightGain (exact down to 2^-18): error 0.0022 instead of 0.0031.
+constexpr float kRowGain = 4.f;
+constexpr float kWeightGain = 16.f;
+// Eight E4M3 codes times a scale (in fp32), rounded to f16.
+__device__ __forceinline__ uint4 codes_to_h8(uint32_t lo, uint32_t hi, float scale) {
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint16_t pair = (uint16_t)((j < 2 ? lo : hi) >> (16 * (j & 1)));
+        float a, b;
+        asm("{\n\t.reg .b32 h2;\n\t.reg .f16 l, h;\n\tcvt.rn.f16x2.e4m3x2 h2, %2;\n\tmov.b32 {l, h}, h2;\n\t"
+            "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+            : "=f"(a), "=f"(b)
+            : "h"(pair));
+        out[j] = f2_to_h2(a * scale, b * scale);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+// Whether one of sixteen codes, none a NaN, times a finite scale is beyond f16's range (a rare path).
+__device__ __forceinline__ bool codes_beyond(const uint4& code, float scale) {
+    if (!(fabsf(scale) < INFINITY)) return false;
+    const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+    bool found = false;
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t c = (w[j >> 2] >> (8 * (j & 3))) & 0x7Fu;
+        const float v = c == 0x7Fu ? 0.f : (c >> 3) ? (8 + (c & 7)) * exp2f((float)(int)(c >> 3) - 10.f) : (c & 7) * 0x1p-9f;
+        found |= v * fabsf(scale) * kRowGain >= 65520.f;
+    }
+    return found;
+}
+// Nonzero in the sign bits' places where one of two f16 values has an exponent of all ones (it carries into them).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t h) { return ((h & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
+
 // ---------------------------------------------------------------------------------------------------------
 // gather: a block takes 16 positions at a time, a warp two of them (with 64 a block, 4096 positions took 11.7 us).  Every block numbers the sequences' tiles for
 // itself (each thread a run of sequences, then a scan of the threads' sums), which costs less than a kernel in front; the
@@ -240,6 +284,25 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
             if (p.cu_q_lens[0] != 0 || p.cu_q_lens[p.batch] != p.total_q) raise_error(p.err, DSA_DEVERR_SEQ);
         }
     }
+    if (p.kv_fp8) {  // the heads' weights as f16
+        const int64_t pieces = (int64_t)p.heads * (256 * 512 / 8);
+        bool beyond = false;
+        for (int64_t i = (int64_t)blockIdx.x * kGatherThreads + tid; i < pieces; i += (int64_t)gridDim.x * kGatherThreads) {
+            const uint4 v = reinterpret_cast<const uint4*>(p.w_kv)[i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xFFFF0000u);
+                h[j] = f2_to_h2(a * kWeightGain, b * kWeightGain);
+                if (not_finite2(h[j]) != 0)
+                    beyond |= (fabsf(a) < INFINITY && fabsf(a) * kWeightGain >= 65520.f) ||
+                              (fabsf(b) < INFINITY && fabsf(b) * kWeightGain >= 65520.f);
+            }
+            reinterpret_cast<uint4*>(p.weights16)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        if (beyond) raise_error(p.err, DSA_DEVERR_RANGE);
+    }
     const int64_t units = (int64_t)kGatherUnits * tiles;
     uint32_t turn = 0;
     for (int64_t i = blockIdx.x; i < units; i += gridDim.x, turn ^= 1u) {
@@ -263,7 +326,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
         const bool in = pg >= 0 && pg < p.num_pages;
         if (!in && tid == 0) raise_error(p.err, DSA_DEVERR_PAGE);
         uint8_t* dst = p.latents + (int64_t)tile * kTileBytes;
-        const uint4 zero = make_uint4(0, 0, 0, 0), nan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+        const uint4 zero = make_uint4(0, 0, 0, 0), nan = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);  // (as f16, too)
 #pragma unroll
         for (int j = warp; j < kGatherRows; j += kGatherWarps) {
             const int row = row0 + j, of_page = (base & 63) + j;
@@ -285,22 +348,17 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
                 const uint4 code = reinterpret_cast<const uint4*>(src)[lane];
                 const float scale = reinterpret_cast<const float*>(src + kKvFp8ScaleOff)[lane >> 3];
                 const uint4 rot = lane < 8 ? reinterpret_cast<const uint4*>(src + kKvFp8RopeOff)[lane] : zero;
-                put(2 * lane, e4m3x8_to_bf16x8(make_uint2(code.x, code.y), scale));
-                put(2 * lane + 1, e4m3x8_to_bf16x8(make_uint2(code.z, code.w), scale));
+                const uint4 lo = codes_to_h8(code.x, code.y, scale * kRowGain), hi = codes_to_h8(code.z, code.w, scale * kRowGain);
+                put(2 * lane, lo);
+                put(2 * lane + 1, hi);
                 if (lane < 8) put(64 + lane, rot);
+                // (an infinity makes what the keys kernel finds; here is known whether it was one before)
+                const uint32_t odd = not_finite2(lo.x) | not_finite2(lo.y) | not_finite2(lo.z) | not_finite2(lo.w) |
+                                     not_finite2(hi.x) | not_finite2(hi.y) | not_finite2(hi.z) | not_finite2(hi.w);
+                if (odd != 0 && codes_beyond(code, scale)) raise_error(p.err, DSA_DEVERR_RANGE);
             }
         }
     }
-}
-
-// Values and weights are multiplied as f16 (11 bits, for bf16's 8: the output's error, 2 bf16 roundings less, fell from
-// 0.0030 to 0.0022 of its norm, of which 0.0017 are its own rounding).  Values are kept times kValueGain, which is taken out of
-// the result: exact down to 2^-16 and up to 65504 / kValueGain.
-constexpr float kValueGain = 4.f;
-__device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the low half
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -314,7 +372,8 @@ constexpr int kKeysThreads = 256;  // warp 0: TMA, 1: products, 2: tensor memory
 constexpr int kKeysResultWarp = 4;
 constexpr int kKeysStages = 6;
 constexpr int kPiece = 32 * 128;  // 32 positions x 64 dims
-constexpr uint32_t kIdescKeys = make_idesc(256, 256, 1, 1, 0, 0);
+template <bool F16>  // FP8 rows
+constexpr uint32_t kIdescKeys = make_idesc(256, 256, F16 ? 0 : 1, F16 ? 0 : 1, 0, 0);
 
 struct KeysCtrl {
     uint64_t full[kKeysStages], empty[kKeysStages];
@@ -326,6 +385,7 @@ struct KeysCtrl {
 constexpr int kKeysSmem = 1024 + kKeysStages * 2 * kUnit + 4 * 2 * kPiece + (int)sizeof(KeysCtrl);
 static_assert(kKeysSmem <= 232448, "shared memory of one CTA");
 
+template <bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
     keys_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap wmap, const ExpandParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -409,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma_pair_f16_ss(tmem + 256 * buf, a + (uint64_t)(2 * j), a + (uint64_t)(kUnit / 16 + 2 * j),
-                                         kIdescKeys, k == 0 && j == 0 ? 0u : 1u);
+                                         kIdescKeys<F16>, k == 0 && j == 0 ? 0u : 1u);
                     umma_pair_commit(&ctl->empty[slot], 3);
                 }
                 if (ok) umma_pair_commit(&ctl->d_full[buf], 3);
@@ -441,6 +501,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                 tmem_ld_wait();
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_regs_ready(v[k]);
+                if (F16) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[k][i] *= 1.f / (kRowGain * kWeightGain);
+                }
                 if (c == 3) {
                     tc_fence_before();
                     __syncwarp();
@@ -454,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                         w[k] = make_uint4(f2_to_bf2(f[0], f[1]), f2_to_bf2(f[2], f[3]), f2_to_bf2(f[4], f[5]), f2_to_bf2(f[6], f[7]));
                     }
                 } else {
-                    uint32_t odd = 0;  // an exponent of all ones carries into the sign bit's place
+                    uint32_t odd = 0;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const float* f = &v[k >> 1][8 * (k & 1)];
@@ -462,12 +528,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             h[i] = f2_to_h2(f[2 * i] * kValueGain, f[2 * i + 1] * kValueGain);
-                            odd |= (h[i] & 0x7C007C00u) + 0x04000400u;
+                            odd |= not_finite2(h[i]);
                         }
                     }
                     // A weight of 0 times a value that is not finite is NaN, for rows that do not see the position too: its
                     // values become 0, and the rows that do see it NaN at the end.
-                    if ((odd & 0x80008000u) != 0) {
+                    if (odd != 0) {
                         bad = true;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -1115,7 +1181,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Expan
 cudaError_t launch_expand(const ExpandLaunch& L, cudaStream_t stream) {
     const ExpandParams& p = L.params;
     if (p.total_q <= 0) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(keys_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysSmem);
+    auto keys = p.kv_fp8 ? keys_kernel<true> : keys_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(keys, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1134,7 +1201,7 @@ cudaError_t launch_expand(const ExpandLaunch& L, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
     cfg.blockDim = dim3(kKeysThreads);
     cfg.dynamicSmemBytes = kKeysSmem;
-    if ((e = cudaLaunchKernelEx(&cfg, keys_kernel, L.cmap, L.wmap, p)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, keys, L.cmap, L.wmap, p)) != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)p.ctas);
     cfg.blockDim = dim3(kAttendThreads);
     cfg.dynamicSmemBytes = kAttendSmem;

@@ -329,6 +329,7 @@ constexpr size_t kExpandPartBytes = (size_t)2 * kExpandCtas * kExpandPartFloats 
 constexpr int kExpandPlanHead = 8;  // int32 in front of the plan's arrays
 struct ExpandParams {
     const uint8_t* kv_cache;  // bf16 rows, or FP8 rows of kKvFp8RowBytes
+    const uint16_t* w_kv;     // [Hq, 256, 512] bf16 bits
     const int32_t* page_table;
     const int32_t* seq_lens;
     const int32_t* cu_q_lens;
@@ -349,9 +350,11 @@ struct ExpandParams {
     int32_t cap_blocks;  // of queries, whatever the offsets say
     int32_t* plan;
     float* partial;    // two results of cut items for each CTA
-    uint8_t* latents;  // [cap_tiles][9][128][64] bf16, 128-byte swizzle
+    uint16_t* weights16;  // FP8 rows: w_kv as f16
+    uint8_t* latents;  // [cap_tiles][9][128][64] bf16 (FP8 rows' latent part: f16), 128-byte swizzle
     uint8_t* kv;       // [cap_tiles][Hq][4] units of 16 KB
 };
+inline size_t expand_weight_bytes(const ExpandParams& p) { return p.kv_fp8 ? (size_t)p.heads * 256 * 512 * 2 : 0; }
 inline size_t expand_plan_bytes(const ExpandParams& p) {
     return (((size_t)kExpandPlanHead + 4 * (size_t)p.batch + 3) * 4 + 1023) / 1024 * 1024;
 }

@@ -85,9 +85,10 @@ class Expanded:
         self.weighted = torch.zeros_like(self.out)  # sum_s p_s |v_s|
         w = w_kv.double()
         acc = 2 * sum_rounding(LATENT)
-        # a key or value dim: the latent's rounding to bf16 (FP8 rows), the sum's, its own rounding, a key's to bf16, a value's
-        # to f16 (half a step of 2^-26 of numbers below 2^-16)
-        rows_off = (2.0 ** -8 if fp8 else 0.0) + acc
+        # a key or value dim: the latent's rounding to f16 (FP8 rows; half a step of 2^-26 of numbers below 2^-16, which the
+        # weights, exact from 2^-18 on and half a step of 2^-28 off below, are covered by), the sum's, its own rounding, a
+        # key's to bf16, a value's to f16
+        rows_off = (2.0 ** -11 if fp8 else 0.0) + acc
         for b in range(batch.B):
             t0, t1 = batch.cu_host[b], batch.cu_host[b + 1]
             if t0 == t1:
@@ -97,8 +98,11 @@ class Expanded:
             r = latent_values(flat[(page * PAGE + at % PAGE).to(dev)], fp8)
             c, rot = r[:, :LATENT], r[:, LATENT:]
             k, size = torch.einsum("sc,hdc->shd", c, w), torch.einsum("sc,hdc->shd", c.abs(), w.abs())
-            off = 2.0 ** -8 * k.abs() * (1 + 2.0 ** -8) + (1 + 2.0 ** -8) * rows_off * size
-            off[..., NOPE:] = 2.0 ** -11 * k[..., NOPE:].abs() + (1 + 2.0 ** -8) * rows_off * size[..., NOPE:] + 2.0 ** -27
+            before = rows_off * size
+            if fp8:
+                before = before + 2.0 ** -27 * w.abs().sum(-1) + 2.0 ** -29 * c.abs().sum(-1)[:, None, None]
+            off = 2.0 ** -8 * k.abs() * (1 + 2.0 ** -8) + (1 + 2.0 ** -8) * before
+            off[..., NOPE:] = 2.0 ** -11 * k[..., NOPE:].abs() + (1 + 2.0 ** -8) * before[..., NOPE:] + 2.0 ** -27
             qn, qp = q_nope[t0:t1].double(), q_pe[t0:t1].double()
             z = (torch.einsum("thd,shd->ths", qn, k[..., :NOPE]) + torch.einsum("thd,sd->ths", qp, rot)) * scale
             dz = torch.einsum("thd,shd->ths", qn.abs(), off[..., :NOPE])
@@ -117,8 +121,7 @@ class Expanded:
     def check(self, out, lse, tokens=None, norm=True):
         """Weights: e^(2 dz), exp2 within 2^-22, f16 2^-11 and the sums' 2^-16; the output's own 2^-8.  norm: for standard normal
         data, where a rounding to bf16 is 0.0017 of a value, root mean square, each enters the output's norm by itself: the
-        output's (0.0017), the keys' through the scores (0.0014), of FP8 rows the latents' through values (0.0017) and scores
-        (0.0014): 0.0022 and 0.0031, half as much again for a batch of few rows."""
+        output's (0.0017) and the keys' through the scores (0.0014) make 0.0022, half as much again for a batch of few rows."""
         t = slice(None) if tokens is None else tokens
         rel = torch.expm1(2 * self.dz[t])[..., None] + 2.0 ** -11 + 2.0 ** -16
         tol = rel * (self.weighted[t] + self.dv[t]) + self.dv[t]
@@ -126,7 +129,7 @@ class Expanded:
         err = (out[t].double() - self.out[t]).abs()
         assert bool((err <= tol).all()), f"worst error {err.max().item():.3g}, {(err / tol).max().item():.3g} of its bound"
         size = self.out[t].norm()
-        assert not norm or err.norm() <= (4.7e-3 if self.fp8 else 3.3e-3) * size, f"relative error {(err.norm() / size).item():.3g}"
+        assert not norm or err.norm() <= 3.3e-3 * size, f"relative error {(err.norm() / size).item():.3g}"
         if lse is not None:
             off = (lse[t].double() - self.lse[t]).abs()
             bound = self.dz[t] + 2.0 ** -18 + 2.0 ** -22 * self.lse[t].abs()

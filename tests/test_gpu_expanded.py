@@ -94,6 +94,15 @@ def test_long_context():
     Call([20000], [40], 2, True, seed=32).run().check()
 
 
+def test_offsets_beyond_32_bits():
+    """Keys and values of 128 heads and 70000 positions take 4.6 GB of workspace: the first and the last head's results."""
+    c = Call([70000], [300], 128, seed=33, strided=True).run()
+    assert dsa.get_device_error(c.ws) == 0
+    for h in (0, 127):
+        one = slice(h, h + 1)
+        Expanded(c.b, c.q_nope[:, one], c.q_pe[:, one], c.w[one], c.kv, False).check(c.out[:, one], c.lse[:, one])
+
+
 def test_many_sequences():
     g = torch.Generator().manual_seed(5)
     lens = torch.randint(1, 400, (1500,), generator=g).tolist()
@@ -244,6 +253,28 @@ def test_a_row_that_is_not_finite(place, bad):
     err = (c.out[after][far].double() - ref.out[after][far]).norm()
     assert err <= 3.3e-3 * ref.out[after][far].norm()
     assert bool(((c.lse[after][far].double() - ref.lse[after][far]).abs() <= 0.05).all())
+
+
+def test_fp8_rows_and_weights_beyond_range_are_reported():
+    """An FP8 row's element, or a weight, beyond f16's range is reported and NaN for those who see it; a scale of infinity or
+    NaN is no finite value beyond range: NaN, and no report."""
+    clean = Call([300], [260], 2, True, seed=116).run()
+    clean.check()
+    pos = torch.tensor(clean.b.pos, device="cuda")
+    at = 180
+    page, place = int(clean.b.pt_host[0, at // PAGE]), at % PAGE
+    for scale, error in ((100.0, dsa.DSA_DEVERR_RANGE), (float("inf"), 0), (float("nan"), 0)):
+        c = Call([300], [260], 2, True, seed=116)
+        c.kv[page, place, :128] = 0x7E  # 448
+        c.kv[page, place, LATENT:LATENT + 4].view(torch.float32)[0] = scale
+        c.run()
+        assert dsa.get_device_error(c.ws) == error
+        assert torch.equal(c.out[pos < at], clean.out[pos < at])
+        assert bool(c.out[pos >= at].isnan().all() and c.lse[pos >= at].isnan().all())
+    c = Call([300], [260], 2, True, seed=116)
+    c.w[1, NOPE + 5, 9] = 5000.0
+    c.run()
+    assert dsa.get_device_error(c.ws) == dsa.DSA_DEVERR_RANGE and bool(c.out[:, 1].isnan().all())
 
 
 @pytest.mark.parametrize("fp8", [False, True])
