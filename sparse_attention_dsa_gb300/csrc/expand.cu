@@ -592,9 +592,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 // keys in turn where there are no more than 128 (as long: it reads twice the keys a step), cut items joined by the last CTA
 // with a part (its code took registers from the softmax's loop: 1.3 times the time of all).
 // ---------------------------------------------------------------------------------------------------------
-constexpr int kAttendThreads = 320;  // warps 0-3 and 4-7: softmax of the two query tiles, 8: loads, 9: products
+constexpr int kAttendThreads = 352;  // warps 0-3 and 4-7: softmax of the two query tiles, 8: loads, 9: products, 10: segments
 constexpr int kLoadWarp = 8;
 constexpr int kProductWarp = 9;
+constexpr int kPlanWarp = 10;
 constexpr int kRing = 8;             // units of K and V, in turn K K K V V
 constexpr int kQTile = 3 * kUnit;    // 128 queries x 192 dims
 constexpr int kTileUnits = 5;
@@ -614,8 +615,9 @@ struct Segment {
     int32_t tile0;        // first tile of the sequence's keys
     int32_t n0, n1;       // tiles that queries 0-127, 128-255 see
     int32_t j0, j1;
+    int32_t bad;          // first position without finite values (see first_bad())
 };
-constexpr int kSegments = 4;  // in flight between the roles of a CTA
+constexpr int kSegments = 3;  // in flight between the roles of a CTA
 // 32 bytes, one whole sector (32-byte aligned)
 __device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -647,7 +649,8 @@ __device__ __forceinline__ bool block_rows(const ExpandParams& p, int b, int i, 
     s->tile0 = ld_plan(tile_begin(p) + b);
     s->n0 = tiles_seen(s->pos0, min(s->nrows, 128));
     s->n1 = s->nrows > 128 ? tiles_seen(s->pos0, s->nrows) : 0;
-    return ld_plan(first_bad(p) + b) >= 0;
+    s->bad = ld_plan(first_bad(p) + b);
+    return s->bad >= 0;
 }
 // The block at place x of a head's line: its sequence and number there, its first place, and that of the next block.
 // Called by a whole warp.
@@ -686,7 +689,7 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
     const int nrows = it.nrows;
     const bool whole = is_whole(it), first_tile = it.j0 == 0;
     const int64_t at = (int64_t)(it.row0 + row) * p.heads + it.head;
-    const bool poisoned = first_bad(p)[it.seq] <= it.pos0 + row;
+    const bool poisoned = it.bad <= it.pos0 + row;
     __syncwarp();
     if (lane == 0) mbar_arrive(&ctl->seg_empty[seg]);
     auto free_o = [&] {  // in registers: the next products may have it
@@ -767,7 +770,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&ctl->seg_full[i], 1);
-            mbar_init(&ctl->seg_empty[i], 9);  // the softmax warps and the products'
+            mbar_init(&ctl->seg_empty[i], 10);  // the softmax warps, loads, products
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&ctl->full[i], 1);
@@ -793,10 +796,49 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     bool ok = true;
 
     if (warp == kLoadWarp) {
-        // ---------------- segments, and what each needs in the order of its use ----------------
+        // ---------------- what the segments need in the order of its use ----------------
+        if (elect_one_sync()) {
+            auto wait_one = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, p.err, p.wait_ns); };
+            uint32_t u = 0, used[2] = {0, 0};  // units, segments that used each query tile
+            for (uint32_t n = 0; ok; ++n) {
+                if (!(ok = wait_one(&ctl->seg_full[n % kSegments], (n / kSegments) & 1u))) break;
+                const Segment s = ctl->segments[n % kSegments];
+                mbar_arrive(&ctl->seg_empty[n % kSegments]);
+                if (s.nrows == 0) break;
+                const uint8_t* kv = p.kv + ((int64_t)s.tile0 * p.heads + s.head) * kHeadTile;
+                const uint8_t* rotary = p.latents + (int64_t)s.tile0 * kTileBytes + 8 * kUnit;
+                auto load_q = [&](int w) {
+                    if (!wait_one(&ctl->q_empty[w], (used[w] & 1u) ^ 1u)) return false;
+                    ++used[w];
+                    mbar_arrive_expect_tx(&ctl->q_full[w], kQTile);
+                    uint8_t* dst = smem + w * kQTile;
+                    tma_load_3d(dst, &nopemap, &ctl->q_full[w], 0, s.head, s.row0 + 128 * w);
+                    tma_load_3d(dst + kUnit, &nopemap, &ctl->q_full[w], 64, s.head, s.row0 + 128 * w);
+                    tma_load_3d(dst + 2 * kUnit, &pemap, &ctl->q_full[w], 0, s.head, s.row0 + 128 * w);
+                    return true;
+                };
+                if (s.j0 < s.n0) ok = load_q(0);
+                for (int j = s.j0; ok && j < s.j1; ++j) {
+                    const uint8_t* tile = kv + (int64_t)j * p.heads * kHeadTile;
+#pragma unroll 1
+                    for (int k = 0; ok && k < kTileUnits; ++k, ++u) {
+                        const uint32_t slot = u % kRing;
+                        if (!(ok = wait_one(&ctl->empty[slot], ((u / kRing) & 1u) ^ 1u))) break;
+                        const uint8_t* src = k == 2 ? rotary + (int64_t)j * kTileBytes : tile + (k < 2 ? k : k - 1) * kUnit;
+                        mbar_arrive_expect_tx(&ctl->full[slot], kUnit);
+                        bulk_copy_g2s(ring + slot * kUnit, src, kUnit, &ctl->full[slot]);
+                        if (j == s.j0 && k == 2 && s.j0 < s.n1) ok = load_q(1);
+                    }
+                }
+            }
+        }
+        ok = __all_sync(kAllLanes, ok);
+    } else if (warp == kPlanWarp) {
+        // ---------------- segments, looked up ahead of their use ----------------
         const PlanHead plan = *plan_head(p);
-        uint32_t n = 0, u = 0, used[2] = {0, 0};  // segments, units, segments that used each query tile
-        auto publish = [&](const Segment& s) {
+        uint32_t n = 0;
+        Segment s;
+        auto publish = [&] {
             if (!wait(&ctl->seg_empty[n % kSegments], ((n / kSegments) & 1u) ^ 1u)) return false;
             if (lane == 0) {
                 ctl->segments[n % kSegments] = s;
@@ -804,47 +846,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             }
             __syncwarp();
             ++n;
-            return true;
-        };
-        auto load = [&](const Segment& s) {
-            const uint8_t* kv = p.kv + ((int64_t)s.tile0 * p.heads + s.head) * kHeadTile;
-            const uint8_t* rotary = p.latents + (int64_t)s.tile0 * kTileBytes + 8 * kUnit;
-            auto load_q = [&](int w) {
-                if (!wait(&ctl->q_empty[w], (used[w] & 1u) ^ 1u)) return false;
-                ++used[w];
-                if (elect_one_sync()) {
-                    mbar_arrive_expect_tx(&ctl->q_full[w], kQTile);
-                    uint8_t* dst = smem + w * kQTile;
-                    tma_load_3d(dst, &nopemap, &ctl->q_full[w], 0, s.head, s.row0 + 128 * w);
-                    tma_load_3d(dst + kUnit, &nopemap, &ctl->q_full[w], 64, s.head, s.row0 + 128 * w);
-                    tma_load_3d(dst + 2 * kUnit, &pemap, &ctl->q_full[w], 0, s.head, s.row0 + 128 * w);
-                }
-                return true;
-            };
-            const bool have0 = s.j0 < s.n0, have1 = s.j0 < s.n1;
-            if (have0 && !load_q(0)) return false;
-            for (int j = s.j0; j < s.j1; ++j) {
-                const uint8_t* tile = kv + (int64_t)j * p.heads * kHeadTile;
-#pragma unroll 1
-                for (int k = 0; k < kTileUnits; ++k, ++u) {
-                    const uint32_t slot = u % kRing;
-                    if (!wait(&ctl->empty[slot], ((u / kRing) & 1u) ^ 1u)) return false;
-                    if (elect_one_sync()) {
-                        const uint8_t* src = k == 2 ? rotary + (int64_t)j * kTileBytes : tile + (k < 2 ? k : k - 1) * kUnit;
-                        mbar_arrive_expect_tx(&ctl->full[slot], kUnit);
-                        bulk_copy_g2s(ring + slot * kUnit, src, kUnit, &ctl->full[slot]);
-                    }
-                    if (j == s.j0 && k == 2 && have1 && !load_q(1)) return false;
-                }
-            }
-            return true;
-        };
-        // A segment is looked up and published before the one in front of it is loaded for, so that nobody waits for that.
-        Segment s, published;
-        published.nrows = 0;
-        auto work = [&](const Segment& s) {
-            if (!publish(s) || (published.nrows > 0 && !load(published))) return false;
-            published = s;
             return true;
         };
         if (plan.parts > 0) {
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 const int64_t left = x1 - s.head * head_line;  // the part's end on this head's line
                 s.j0 = tiles_before(at - w.begin, n_tiles);
                 s.j1 = left >= w.end ? n_tiles : tiles_before((int)left - w.begin, n_tiles);
-                if (s.j1 > s.j0 && block_rows(p, w.b, w.i, &s)) ok = work(s);
+                if (s.j1 > s.j0 && block_rows(p, w.b, w.i, &s)) ok = publish();
                 x = s.head * head_line + w.end;
             }
         } else {
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 if (block_rows(p, b, block - block_begin(p)[b], &s)) {
                     s.j0 = 0;
                     s.j1 = max(s.n0, s.n1);
-                    ok = work(s);
+                    ok = publish();
                 }
                 int next = 0;
                 if (lane == 0) next = atomicAdd(&plan_head(p)->counter, 1);
@@ -885,7 +886,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             }
         }
         s.nrows = 0;
-        if (ok) ok = work(s);
+        if (ok) ok = publish();
     } else if (warp == kProductWarp) {
         // ---------------- S_w(j) = Q_w K(j)^T and O_w += P_w(j) V(j), the two query tiles in turn ----------------
         // The steps of all segments form one row: a step's scores are asked for between the products of the weights of the
