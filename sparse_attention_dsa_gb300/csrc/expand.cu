@@ -617,7 +617,7 @@ struct Segment {
     int32_t j0, j1;
     int32_t bad;          // first position without finite values (see first_bad())
 };
-constexpr int kSegments = 3;  // in flight between the roles of a CTA
+constexpr int kSegments = 2;  // in flight between the roles of a CTA
 // 32 bytes, one whole sector (32-byte aligned)
 __device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
