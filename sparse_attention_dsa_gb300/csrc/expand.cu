@@ -46,29 +46,36 @@ constexpr int kHeadTile = kExpandHeadTileBytes;  // keys (two units) and values 
 constexpr int kBlockRows = kExpandBlockRows;
 
 // What the gathering kernel leaves of its plan (int32): a PlanHead, then for each sequence its first tile, its first block
-// of queries and its first place on the line (one more of each than sequences), and first_bad.
+// of queries and its first place on the line (one more of each than sequences), and first_bad.  Between the head and these,
+// with parts: the parts' first places on the line of all heads (int64).
 struct PlanHead {
     int32_t tiles;    // in use
     int32_t blocks;   // of queries, of a head
     int32_t counter;  // whole items handed out
     int32_t parts;    // the line of items is cut in so many parts; 0: whole items
     int32_t group;    // whole items: heads that are worked on together
-    int32_t unused[3];
+    int32_t whole;    // with parts: the last so many blocks of each head are whole items in front of them
+    int32_t head_line;  // with parts: places of a head's other blocks
+    int32_t unused;
 };
 __device__ __forceinline__ PlanHead* plan_head(const ExpandParams& p) { return reinterpret_cast<PlanHead*>(p.plan); }
-__device__ __forceinline__ int32_t* tile_begin(const ExpandParams& p) { return p.plan + sizeof(PlanHead) / 4; }
+__device__ __forceinline__ long long* part_begins(const ExpandParams& p) { return reinterpret_cast<long long*>(plan_head(p) + 1); }
+__device__ __forceinline__ int32_t* tile_begin(const ExpandParams& p) { return p.plan + kExpandPlanHead; }
 __device__ __forceinline__ int32_t* block_begin(const ExpandParams& p) { return tile_begin(p) + p.batch + 1; }
 __device__ __forceinline__ int32_t* place_begin(const ExpandParams& p) { return block_begin(p) + p.batch + 1; }
 // First position of a sequence that has no finite values or no page (INT32_MAX: none): rows that see it are NaN.  -1: the
 // sequence is left out, as its tiles do not fit.
 __device__ __forceinline__ int32_t* first_bad(const ExpandParams& p) { return place_begin(p) + p.batch + 1; }
-static_assert(kExpandPlanHead == sizeof(PlanHead) / 4, "expand_plan_bytes()");
+static_assert(kExpandPlanHead == sizeof(PlanHead) / 4 + 2 * (kExpandCtas + 1), "expand_plan_bytes()");
 
 // The line: the blocks of head 0, of head 1, ..., each kItemCost places for what it costs beside its tiles (its queries' load,
 // its first scores' latency, its result) and one for each tile of keys.  It is cut into equal parts, of kMinPlaces at least
 // on average, or its items are taken whole in turn:
 //   * whole, where the estimate of the last CTA's time is no longer than with parts (three short prompts 23.0 us, cut 30.9;
 //     eight ragged ones 176, cut 187; but 256 items of 112 tiles, for 152 CTAs, 455, cut 415);
+//     With parts, each CTA takes first one whole item (the last blocks of the heads, as many as all heads have CTAs for), where
+//     those leave every CTA a part: CTAs at the same head then meet its keys at about the same time, from L2
+//     instead of HBM, where parts alone begin anywhere.
 //   * whole, where the longest item is no more than 1 / kWholeItems of a CTA's share: heads go in groups whose keys and
 //     values (kGroupBytes) stay in L2 while all their blocks meet them (the 8192-token prompt of 128 heads 1722 us; head by head
 //     1753, all heads together 1881, cut 1939).
@@ -262,26 +269,68 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
             at[1] += parts;
             if (ok) at[2] += places_of(L - n, n);
         }
+        // (what does not fit leaves places that nobody works on)
+        const int blocks = (int)(all[1] < p.cap_blocks ? all[1] : p.cap_blocks);
+        const long long line = all[2] * p.heads;
+        int parts = (int)(line / kMinPlaces < p.ctas ? max(1LL, line / kMinPlaces) : p.ctas);
+        // how long the last CTA takes with whole items (its share and half an item; no more than one item each), and with parts
+        const long long alone = all[1] * p.heads <= p.ctas ? most : line / p.ctas + most / 2, cut = line / parts + kCutCost;
+        if (all[1] > p.cap_blocks || all[2] > INT32_MAX || alone <= cut || line >= (long long)kWholeItems * p.ctas * most) parts = 0;
+        const int whole = parts == p.ctas && (long long)(most + kMinPlaces) * p.ctas <= line ? min(p.ctas / p.heads, blocks - 1) : 0;
         if (tid == 0) {
-            // (what does not fit leaves places that nobody works on)
-            PlanHead h;
+            PlanHead h = {};
             h.tiles = tiles;
-            h.blocks = (int32_t)(all[1] < p.cap_blocks ? all[1] : p.cap_blocks);
-            const long long line = all[2] * p.heads;
-            h.parts = (int32_t)(line / kMinPlaces < p.ctas ? max(1LL, line / kMinPlaces) : p.ctas);
-            // how long the last CTA takes with whole items (its share and half an item; no more than one item each), and with
-            // parts
-            const long long whole = all[1] * p.heads <= p.ctas ? most : line / p.ctas + most / 2, cut = line / h.parts + kCutCost;
-            if (all[1] > p.cap_blocks || all[2] > INT32_MAX || whole <= cut || line >= (long long)kWholeItems * p.ctas * most)
-                h.parts = 0;
+            h.blocks = blocks;
+            h.parts = parts;
+            h.whole = whole;
             h.counter = p.ctas;  // every CTA takes the item of its own number first
-            const long long head_bytes = max(1LL, (long long)h.tiles * kHeadTile);
-            h.group = (int32_t)max(1LL, min((long long)p.heads, kGroupBytes / head_bytes));
+            h.group = max(1, min(p.heads, (int)(kGroupBytes / kHeadTile) / max(1, tiles)));
             *plan_head(p) = h;
-            tile_begin(p)[p.batch] = h.tiles;
-            block_begin(p)[p.batch] = h.blocks;
+            tile_begin(p)[p.batch] = tiles;
+            block_begin(p)[p.batch] = blocks;
             place_begin(p)[p.batch] = (int32_t)all[2];
             if (p.cu_q_lens[0] != 0 || p.cu_q_lens[p.batch] != p.total_q) raise_error(p.err, DSA_DEVERR_SEQ);
+        }
+        if (parts > 0) {
+            __syncthreads();  // the arrays are there
+            // Position of a block's first query, its sequence's first place, and its number in it.
+            auto look_up = [&](int block, int* n, int* pos0, int* first) {
+                int lo = 0, hi = p.batch;  // the last sequence that begins no later
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (ld_plan(block_begin(p) + mid) <= block) lo = mid;
+                    else hi = mid;
+                }
+                *n = p.cu_q_lens[lo + 1] - p.cu_q_lens[lo];
+                *pos0 = p.seq_lens[lo] - *n;
+                *first = ld_plan(place_begin(p) + lo);
+                return block - ld_plan(block_begin(p) + lo);
+            };
+            int n, pos0, first;
+            if (tid == 0) {
+                int32_t head_line = (int32_t)all[2];
+                if (whole > 0) {
+                    const int i = look_up(blocks - whole, &n, &pos0, &first);
+                    head_line = first + (int32_t)places_before(pos0, i);
+                }
+                plan_head(p)->head_line = head_line;
+                part_begins(p)[0] = 0;
+            }
+            // CTA c's part is its share of all places without its whole item (in 1 / parts of a place)
+            long long share = tid < parts ? line : 0;
+            if (tid < whole * p.heads) {
+                const int i = look_up(blocks - 1 - tid / p.heads, &n, &pos0, &first), q = i * kBlockRows;
+                share -= (long long)parts * (kItemCost + tiles_seen(pos0 + q, min(kBlockRows, n - q)));
+            }
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long o = __shfl_up_sync(kAllLanes, share, off);
+                if (lane >= off) share += o;
+            }
+            if (lane == 31) scan[0][warp] = share;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) share += scan[0][w];
+            if (tid < p.ctas) part_begins(p)[tid + 1] = share / parts;
         }
     }
     if (p.kv_fp8) {  // the heads' weights as f16
@@ -673,8 +722,8 @@ __device__ __forceinline__ Place block_at(const ExpandParams& p, int x, int lane
     w.end = first + (int)((lo + 1) * kBlockRows <= n ? places_before(pos0, lo + 1) : places_of(pos0, n));
     return w;
 }
-// Part k of a line of W places cut in G parts starts here.
-__device__ __forceinline__ int64_t part_begin(int64_t k, int64_t W, int64_t G) { return k * W / G; }
+// Part k of the line starts here.
+__device__ __forceinline__ int64_t part_begin(const ExpandParams& p, int k) { return __ldcg(part_begins(p) + k); }
 // Where CTA c leaves a part of an item: at most its first and its last segment are parts, and the last begins its item.
 __device__ __forceinline__ float* part_slot(const ExpandParams& p, int c, bool first_tile) {
     return p.partial + (int64_t)(2 * c + (first_tile ? 1 : 0)) * kExpandPartFloats;
@@ -849,11 +898,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             return true;
         };
         if (plan.parts > 0) {
-            // this CTA's part of the line: the blocks of head 0, of head 1, ...
-            const int64_t head_line = place_begin(p)[p.batch], line = head_line * p.heads;
-            const int64_t x1 = part_begin(blockIdx.x + 1, line, plan.parts);
-            int64_t x = part_begin(blockIdx.x, line, plan.parts);
-            if ((int)blockIdx.x >= plan.parts) x = x1;
+            // this CTA's whole item, if it has one, and its part of the line: the other blocks of head 0, of head 1, ...
+            if ((int)blockIdx.x < plan.whole * p.heads) {
+                const int block = plan.blocks - 1 - (int)blockIdx.x / p.heads;
+                const int b = last_not_above(block_begin(p), p.batch, block, lane);
+                s.head = (int)blockIdx.x % p.heads;
+                if (block_rows(p, b, block - block_begin(p)[b], &s)) {
+                    s.j0 = 0;
+                    s.j1 = max(s.n0, s.n1);
+                    ok = publish();
+                }
+            }
+            const int64_t head_line = plan.head_line, x1 = part_begin(p, blockIdx.x + 1);
+            int64_t x = part_begin(p, blockIdx.x);
             while (ok && x < x1) {
                 s.head = (int)(x / head_line);
                 const int at = (int)(x - s.head * head_line);
@@ -866,14 +923,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 x = s.head * head_line + w.end;
             }
         } else {
-            // Whole items, as CTAs become free.  Heads in groups whose keys fit L2; in a group the last blocks (of a sequence
-            // the ones with the most keys) first.
+            // Whole items, as CTAs become free.  Heads in groups whose keys fit L2, the last ones, whose keys were made last,
+            // first; in a group the last blocks (of a sequence the ones with the most keys) first.
             const int64_t n_items = (int64_t)plan.blocks * p.heads, group_items = (int64_t)plan.blocks * plan.group;
             int64_t index = blockIdx.x;
             while (ok && index < n_items) {
                 const int group = (int)(index / group_items), rest = (int)(index - group * group_items);
                 const int heads = min(plan.group, p.heads - group * plan.group), block = plan.blocks - 1 - rest / heads;
-                s.head = group * plan.group + rest % heads;
+                s.head = p.heads - 1 - (group * plan.group + rest % heads);
                 const int b = last_not_above(block_begin(p), p.batch, block, lane);
                 if (block_rows(p, b, block - block_begin(p)[b], &s)) {
                     s.j0 = 0;
@@ -1102,29 +1159,25 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Expan
     // The plan is older than the attention: its blocks, when they let this kernel start, had waited for the end of what
     // made it.  So the item is looked up while the attention still runs.  (No block returns before its end, though: what is
     // launched behind this kernel takes the end of all blocks for the end of the attention.)
-    PlanHead plan;
-    plan.parts = ld_plan(&plan_head(p)->parts);
-    const bool part_begins = k < plan.parts;
-    int64_t line = 1, begin = 0;
+    const bool begins = k < ld_plan(&plan_head(p)->parts);
+    int64_t begin = 0;
     int n_tiles = 0, last = k;
     auto cut = [&](int part) {  // the item's tiles in front of a part
-        const int64_t at = part_begin(part, line, plan.parts) - begin;
+        const int64_t at = part_begin(p, part) - begin;
         return at >= kItemCost + n_tiles ? n_tiles : at <= 0 ? 0 : tiles_before((int)at, n_tiles);
     };
     Segment s;
     s.nrows = 0;
-    if (part_begins) {
+    if (begins) {
         // the item in which part k begins; the first part that begins inside it takes care of it
-        const int64_t head_line = ld_plan(place_begin(p) + p.batch);
-        line = head_line * p.heads;
-        const int64_t x = part_begin(k, line, plan.parts);
+        const int64_t head_line = ld_plan(&plan_head(p)->head_line), x = part_begin(p, k);
         s.head = (int)(x / head_line);
         const Place w = block_at(p, (int)(x - s.head * head_line), lane);
         begin = s.head * head_line + w.begin;
         n_tiles = w.end - w.begin - kItemCost;
         const int here = cut(k);
         if (here <= 0 || here >= n_tiles || cut(k - 1) > 0 || !block_rows(p, w.b, w.i, &s)) s.nrows = 0;
-        while (cut(last + 1) < n_tiles) ++last;
+        while (last + 1 < p.ctas && cut(last + 1) < n_tiles) ++last;
     }
     grid_dependency_wait();
     allow_dependent_launch();

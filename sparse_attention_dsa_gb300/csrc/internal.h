@@ -326,7 +326,7 @@ constexpr int kExpandCtas = 152;                     // of the attention, at mos
 // A partial result: O [256][128] fp32 (unnormalised), then (maximum in log2 units, sum) per row.
 constexpr int kExpandPartFloats = 256 * 128 + 2 * 256;
 constexpr size_t kExpandPartBytes = (size_t)2 * kExpandCtas * kExpandPartFloats * 4;
-constexpr int kExpandPlanHead = 8;  // int32 in front of the plan's arrays
+constexpr int kExpandPlanHead = 8 + 2 * (kExpandCtas + 1);  // int32 in front of the plan's arrays
 struct ExpandParams {
     const uint8_t* kv_cache;  // bf16 rows, or FP8 rows of kKvFp8RowBytes
     const uint16_t* w_kv;     // [Hq, 256, 512] bf16 bits
