@@ -16,15 +16,16 @@
 //            read (128-byte swizzle); and the plan: where each sequence's tiles and blocks of 256 queries are;
 //   keys:    K and V = W c: a matrix product of all tiles and heads, CTA pairs (256 positions x a head's 256 rows);
 //   attend:  a CTA takes 256 queries of a head as two tiles of 128 that share K and V; all such items, each as long as its
-//            tiles of keys, are cut into equal parts, one for each CTA, or (where that does not pay) they are taken whole in turn;
+//            tiles of keys, are cut into equal parts, one for each CTA (long ones behind a whole item each), or (where that does not
+//            pay) they are taken whole in turn;
 //   combine: the results of items that were cut.
 //
-// What bounds it, and measured (one GB300; calls in a graph, in brackets with L2 flushed before).  The tensor pipe: a tile of 128 x
-// 128 is 1280 cycles of products, in which its softmax (about 1150) and its group's wait for the other tile's products pass.
-// An 8192-token prompt of 128 heads 1722 us (1805 to 1861), 3.02 TFLOP, 1.75 PFLOP/s, 0.93 of the measured cuBLAS rate, of
+// What bounds it, and measured (one GB300; calls in a graph, in brackets with L2 flushed before).  The tensor pipe: a tile of
+// 128 x 128 is 1280 cycles of products, in which its softmax (about 1150) and its group's wait for the other tile's products pass.
+// An 8192-token prompt of 128 heads 1722 to 1800 us (1805 to 1940), 3.02 TFLOP, 1.75 PFLOP/s, up to 0.93 of the measured cuBLAS rate, of
 // which gathering 8, keys 170 (275 GFLOP; their 537 MB are written at HBM's pace for writes), the rest attention at 1.8; in
-// a long loop the power limit takes up to 14% of the clock.  4096 queries behind 12288 of 16 heads 412 us (417), 0.87 of it:
-// the parts' results and their combination 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 181 us (188):
+// a long loop the power limit takes up to 14% of the clock.  4096 queries behind 12288 of 16 heads 395 to 406 us (400 to 410), 0.9 of it:
+// the parts' results and their combination 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 173 us (177):
 // a quarter of the pairs in its tiles are masked, an item of some six tiles costs about two more, keys 48.  Three prompts of
 // up to 200 queries, 16 heads 23 us (32): three kernels' latency, one after another.
 #include <cuda_runtime.h>
@@ -76,10 +77,11 @@ static_assert(kExpandPlanHead == sizeof(PlanHead) / 4 + 2 * (kExpandCtas + 1), "
 // its first scores' latency, its result) and one for each tile of keys.  It is cut into equal parts, of kMinPlaces at least
 // on average, or its items are taken whole in turn:
 //   * whole, where the estimate of the last CTA's time is no longer than with parts (three short prompts 23.0 us, cut 30.9;
-//     eight ragged ones 176, cut 187; but 256 items of 112 tiles, for 152 CTAs, 455, cut 415);
+//     eight ragged ones 176, cut 187; but 256 items of 112 tiles, for 152 CTAs, 455, cut into parts alone 415, now 399);
 //     With parts, each CTA takes first one whole item (the last blocks of the heads, as many as all heads have CTAs for), where
 //     those leave every CTA a part: CTAs at the same head then meet its keys at about the same time, from L2
-//     instead of HBM, where parts alone begin anywhere.
+//     instead of HBM, where parts alone begin anywhere (4096 queries behind 12288 of 16 heads 399 us for 409, two times 2048
+//     behind 28000 640 for 678).
 //   * whole, where the longest item is no more than 1 / kWholeItems of a CTA's share: heads go in groups whose keys and
 //     values (kGroupBytes) stay in L2 while all their blocks meet them (the 8192-token prompt of 128 heads 1722 us; head by head
 //     1753, all heads together 1881, cut 1939).
@@ -677,6 +679,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 constexpr int kAttendThreads = 352;  // warps 0-3 and 4-7: softmax of the two query tiles, 8: loads, 9: products, 10: segments
 constexpr int kLoadWarp = 8;
 constexpr int kProductWarp = 9;
+// (With segments looked up by the loads' warp, between its loads, three short prompts took 23.3 us, for 22.4; but an 8192-token
+// prompt of 128 heads in a long loop, at the power limit, 1.3% less than with this warp.)
 constexpr int kPlanWarp = 10;
 constexpr int kRing = 8;             // units of K and V, in turn K K K V V
 constexpr int kQTile = 3 * kUnit;    // 128 queries x 192 dims
@@ -699,7 +703,8 @@ struct Segment {
     int32_t j0, j1;
     int32_t bad;          // first position without finite values (see first_bad())
 };
-constexpr int kSegments = 2;  // in flight between the roles of a CTA
+// In flight between the roles of a CTA (with 3 it keeps items that another could begin: eight ragged prompts 180 us for 178).
+constexpr int kSegments = 2;
 // 32 bytes, one whole sector (32-byte aligned)
 __device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -757,7 +762,8 @@ __device__ __forceinline__ Place block_at(const ExpandParams& p, int x, int lane
 }
 // Part k of the line starts here.
 __device__ __forceinline__ int64_t part_begin(const ExpandParams& p, int k) { return __ldcg(part_begins(p) + k); }
-// Where CTA c leaves a part of an item: at most its first and its last segment are parts, and the last begins its item.
+// Where CTA c leaves a part of an item: at most the first and the last segment of its part of the line are parts of items, and
+// the last begins its item.
 __device__ __forceinline__ float* part_slot(const ExpandParams& p, int c, bool first_tile) {
     return p.partial + (int64_t)(2 * c + (first_tile ? 1 : 0)) * kExpandPartFloats;
 }

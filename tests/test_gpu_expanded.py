@@ -94,6 +94,26 @@ def test_long_context():
     Call([20000], [40], 2, True, seed=32).run().check()
 
 
+@pytest.mark.parametrize("seq_lens,q_lens,heads", [
+    ([600, 7, 512, 900, 333], [600, 0, 512, 300, 333], 24),           # more short items than CTAs, of several sequences
+    ([1 + 3 * i for i in range(256)], [1] * 256, 1),                  # 256 blocks of queries
+    ([1 + 3 * i for i in range(257)], [1 + i % 2 for i in range(257)], 1),
+    ([5000, 4700], [520, 500], 40),                                   # long items, fewer than two a CTA
+    ([40, 5000, 4000], [40, 1024, 0], 50),
+    ([6000], [768], 76),
+])
+def test_items_whole_and_cut(seq_lens, q_lens, heads):
+    c = Call(seq_lens, q_lens, heads, seed=35).run()
+    assert dsa.get_device_error(c.ws) == 0
+    for h in (0, heads // 2, heads - 1):
+        one = slice(h, h + 1)
+        Expanded(c.b, c.q_nope[:, one], c.q_pe[:, one], c.w[one], c.kv, False).check(c.out[:, one], c.lse[:, one])
+    want = c.out.clone(), c.lse.clone()
+    c.out.fill_(7.0)
+    c.run()
+    assert torch.equal(c.out, want[0]) and torch.equal(c.lse, want[1])
+
+
 def test_offsets_beyond_32_bits():
     """Keys and values of 128 heads and 70000 positions take 4.6 GB of workspace: the first and the last head's results."""
     c = Call([70000], [300], 128, seed=33, strided=True).run()
