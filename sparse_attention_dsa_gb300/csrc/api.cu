@@ -1090,6 +1090,7 @@ dsa_status_t dsa_expanded_attn(const dsa_dims_t* d, int32_t total_pages, const v
     p.plan = reinterpret_cast<int32_t*>(ws);
     p.ctas = dev.num_sms < dsa::kExpandCtas ? dev.num_sms : dsa::kExpandCtas;
     p.partial = reinterpret_cast<float*>(ws + dsa::expand_plan_bytes(p));
+    p.sectors = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.partial)) & 31) == 0;
     p.weights16 = reinterpret_cast<uint16_t*>(ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes);
     p.latents = ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(p);
     p.kv = p.latents + (size_t)p.cap_tiles * dsa::kExpandTileBytes;

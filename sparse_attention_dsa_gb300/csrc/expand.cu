@@ -705,11 +705,17 @@ struct Segment {
 };
 // In flight between the roles of a CTA (with 3 it keeps items that another could begin: eight ragged prompts 180 us for 178).
 constexpr int kSegments = 2;
-// 32 bytes, one whole sector (32-byte aligned)
-__device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// 32 bytes: one whole sector where `whole` says that dst is 32-byte aligned, as 16-byte pieces otherwise (arrays may begin at
+// any multiple of 16).
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t* v, bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
 }
 
 struct AttendCtrl {
@@ -806,7 +812,7 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
                     uint32_t v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = f2_to_bf2(o[k][2 * i] * inv, o[k][2 * i + 1] * inv);
-                    st_global_32(dst + c + 16 * k, v);
+                    st_global_32(dst + c + 16 * k, v, p.sectors);
                 }
             }
         }
@@ -826,7 +832,7 @@ __device__ __forceinline__ void write_result(const ExpandParams& p, AttendCtrl* 
                     uint32_t v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[k >> 1][8 * (k & 1) + i] * (1.f / kValueGain));
-                    st_global_32(slot + row * 128 + c + 8 * k, v);
+                    st_global_32(slot + row * 128 + c + 8 * k, v, p.sectors);
                 }
             }
         }

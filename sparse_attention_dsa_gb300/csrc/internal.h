@@ -342,6 +342,7 @@ struct ExpandParams {
     int32_t max_pages;
     int32_t heads;
     int32_t kv_fp8;
+    int32_t sectors;  // out and partial are 32-byte aligned
     float scale_log2;  // softmax_scale * log2(e)
     uint64_t wait_ns;
     // workspace
