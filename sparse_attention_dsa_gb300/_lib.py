@@ -347,18 +347,75 @@ def prefix_attn(dims, prefix_len, q, kv_cache, page_table, seq_lens, cu_q_lens, 
                                  _stream(stream)))
 
 
+_norm_types = None
+
+
+def _norm_rows(name, t, types, shape):
+    """The stride of an array of dense rows that may be a slice of wider ones (0 for a single row, whose stride says nothing).
+    Rows that overlap, as an expanded row's, are no array of rows."""
+    row, column = t.stride() if t.shape == shape else (0, 0)
+    if column == 1 and t.dtype in types:
+        if row >= shape[1]:
+            return row if shape[0] > 1 else 0
+        if shape[0] <= 1:
+            return 0
+    raise DsaError(DSA_ERR_INVALID_ARG, f"{name} must be [rows, dim], the same for x and out, with dense rows of bf16 (got {list(t.shape)} "
+                                        f"of {t.dtype}, strides {list(t.stride())})")
+
+
+def _norm_array(name, t, types, shape, flat=False):
+    """The address of a dense array of rms_norm of one of these types and this shape, or with more rows (flat: or [rows] for
+    [rows, 1]); None and a bare address are taken as they are."""
+    if t is None or isinstance(t, int):
+        return t
+    have = t.shape
+    if t.is_contiguous() and t.dtype in types and (
+            have == shape or (len(have) == len(shape) == 2 and have[0] >= shape[0] and have[1] == shape[1])
+            or (flat and len(have) == 1 and have[0] >= shape[0])):
+        return t.data_ptr()
+    raise DsaError(DSA_ERR_INVALID_ARG, f"{name} must be dense, {list(shape)} of {' or '.join(sorted(str(d) for d in types))} (got "
+                                        f"{list(have)} of {t.dtype}, strides {list(t.stride())})")
+
+
 def rms_norm(x, weight, eps, out=None, codes=None, scale=None, codes_dtype=DSA_FP8_E4M3, group=0, residual=None, sum=None,
              stream=None):
     """dsa_rms_norm: x [rows, dim] (rows and the strides of x and out are those of the tensors) plus residual, normalised,
-    to bf16 (out) and codes with scales."""
-    rows, dim = x.shape if x.dim() == 2 else (-1, -1)
-    for name, t in (("x", x), ("out", out)):
-        if t is not None and (tuple(t.shape) != (rows, dim) or t.stride(1) != 1):
-            raise DsaError(DSA_ERR_INVALID_ARG, f"{name} must be [rows, dim], the same for both, with dense rows (got {tuple(t.shape)}, "
-                                                f"strides {tuple(t.stride())})")
-    _check(lib().dsa_rms_norm(rows, dim, _ptr(x), x.stride(0) if rows > 1 else 0, _ptr(residual), _ptr(sum), _ptr(weight),
-                              float(eps), _ptr(out), out.stride(0) if out is not None and rows > 1 else 0, int(codes_dtype),
-                              int(group), _ptr(codes), _ptr(scale), _stream(stream)))
+    to bf16 (out) and codes with scales.  x and out may be slices of wider rows, the other arrays are dense: residual and sum
+    [rows, dim], weight [dim], codes [rows, dim] of one byte each, scale [rows] or [rows, 1], [rows, dim / 128], or bytes
+    [rows, dim / 32], all but weight of more rows, too; of other shapes, strides or types they are refused (16-bit integers stand
+    for bf16 bits)."""
+    global _norm_types
+    if _norm_types is None:
+        import torch
+
+        _norm_types = ({torch.bfloat16, torch.int16, torch.uint16}, {torch.uint8, torch.int8, torch.float8_e4m3fn},
+                       {torch.uint8, torch.int8, torch.float8_e8m0fnu}, {torch.float32})
+    bf16, e4m3, e8m0, fp32 = _norm_types
+    shape = x.shape
+    if len(shape) != 2:
+        raise DsaError(DSA_ERR_INVALID_ARG, f"x must be [rows, dim] (got {list(shape)})")
+    rows, dim = shape
+    x_stride = _norm_rows("x", x, bf16, shape)
+    out_stride = _norm_rows("out", out, bf16, shape) if out is not None else 0
+    weight = _norm_array("weight", weight, bf16, shape[1:])
+    if residual is not None:
+        residual = _norm_array("residual", residual, bf16, shape)
+    if sum is not None:
+        sum = _norm_array("sum", sum, bf16, shape)
+    if codes is not None:
+        codes = _norm_array("codes", codes, e4m3, shape)
+        if scale is None:
+            pass  # refused below
+        elif codes_dtype == DSA_MXFP8_E4M3:
+            scale = _norm_array("scale", scale, e8m0, (rows, dim // 32))
+        elif group:
+            scale = _norm_array("scale", scale, fp32, (rows, dim // 128))
+        else:
+            scale = _norm_array("scale", scale, fp32, (rows, 1), flat=True)
+    else:
+        scale = None
+    _check(lib().dsa_rms_norm(rows, dim, x.data_ptr(), x_stride, residual, sum, weight, float(eps), _ptr(out), out_stride,
+                              int(codes_dtype), int(group), codes, scale, _stream(stream)))
 
 
 def absorb_queries(dims, q_nope, w_kv, q, workspace, stream=None, q_nope_strides=(0, 0)):
