@@ -288,7 +288,7 @@ bool expand_sizes(const dsa_dims_t* d, int32_t total_pages, dsa::ExpandParams* p
     p->cap_tiles = (int32_t)tiles;
     p->cap_blocks = (int32_t)blocks;
     *bytes = dsa::expand_plan_bytes(*p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(*p) + (size_t)tiles * dsa::kExpandTileBytes +
-             (size_t)tiles * d->attn_heads * dsa::kExpandHeadTileBytes;
+             (size_t)tiles * d->attn_heads * (dsa::kExpandHeadTileBytes + 4);
     return true;
 }
 
@@ -1094,6 +1094,7 @@ dsa_status_t dsa_expanded_attn(const dsa_dims_t* d, int32_t total_pages, const v
     p.weights16 = reinterpret_cast<uint16_t*>(ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes);
     p.latents = ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(p);
     p.kv = p.latents + (size_t)p.cap_tiles * dsa::kExpandTileBytes;
+    p.forms = p.kv + (size_t)p.cap_tiles * p.heads * dsa::kExpandHeadTileBytes;
     L.num_sms = dev.num_sms;
     const uint64_t T = (uint64_t)d->total_q, H = (uint64_t)d->attn_heads;
     if ((st = encode_rows(&L.nopemap, q_nope, {dsa::kHeadNope, H, T},

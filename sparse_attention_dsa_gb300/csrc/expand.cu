@@ -28,6 +28,7 @@
 // the parts' results and their combination 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 173 us (177):
 // a quarter of the pairs in its tiles are masked, an item of some six tiles costs about two more, keys 48.  Three prompts of
 // up to 200 queries, 16 heads 23 us (32): three kernels' latency, one after another.
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -58,6 +59,8 @@ struct PlanHead {
     int32_t whole;    // with parts: the last so many blocks of each head are whole items in front of them
     int32_t head_line;  // with parts: places of a head's other blocks
     int32_t sorted;   // whole items: block_order() holds
+    int32_t wide;     // some values are kept as bf16 (see kSmall)
+    int32_t pad;
 };
 __device__ __forceinline__ PlanHead* plan_head(const ExpandParams& p) { return reinterpret_cast<PlanHead*>(p.plan); }
 __device__ __forceinline__ long long* part_begins(const ExpandParams& p) { return reinterpret_cast<long long*>(plan_head(p) + 1); }
@@ -158,6 +161,13 @@ __device__ __forceinline__ int sequence_of_tile(const ExpandParams& p, int tile)
 // 0.0030 to 0.0022 of its norm, of which 0.0017 are its own rounding).  Values are kept times kValueGain, which is taken out of
 // the result: exact down to 2^-16 and up to 65504 / kValueGain.
 constexpr float kValueGain = 4.f;
+constexpr float kValueLimit = 16380.f;  // times kValueGain it is 65520, which rounds to f16's infinity
+// Smaller ones lose bits (f16's steps end at 2^-24, that is 2^-26 of a value), so that a vector of small values alone would be
+// coarse or 0.  Where a position's largest value of a head, not 0, is below 2^-13 (as f16, times kValueGain: kSmall), the 32
+// positions that a warp of the keys kernel writes are kept, with their weights, as bf16: any magnitude, 8 bits.  Elsewhere a
+// value is off by 2^-27 at most, 2^-14 of its vector's largest.  The choice is a byte for each 32 positions of a head (`forms`),
+// which says how the weights are rounded and how the products of those positions are issued.
+constexpr uint32_t kSmall = 0x1000;  // 2^-11
 __device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the low half
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -576,7 +586,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
             if (!(ok = wait(&ctl->d_full[buf], (t >> 1) & 1u))) break;
             tc_fence_after();
             uint8_t* dst = p.kv + ((int64_t)tile * p.heads + head) * kHeadTile;
+            // dims 64 c .. of the values: unit 2 + position / 64
+            auto values_at = [&](int c) { return dst + (2 + (ew >> 1)) * kUnit + c * (kUnit / 2) + (ew & 1) * kPiece; };
+            auto give_back = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(d_empty + 8 * buf);
+            };
             bool bad = false, beyond = false;  // a value is not finite as f16; and is finite itself
+            uint32_t most = 0, any = 0;        // the position's largest value as f16, in either half; all values' bits
+            bool wide = false;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {  // 64 columns each
                 float v[4][16];
@@ -591,11 +610,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[k][i] *= 1.f / (kRowGain * kWeightGain);
                 }
-                if (c == 3) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(d_empty + 8 * buf);
-                }
                 uint4 w[8];
                 if (c < 2) {
 #pragma unroll
@@ -604,7 +618,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                         w[k] = make_uint4(f2_to_bf2(f[0], f[1]), f2_to_bf2(f[2], f[3]), f2_to_bf2(f[4], f[5]), f2_to_bf2(f[6], f[7]));
                     }
                 } else {
-                    uint32_t odd = 0;
+                    uint32_t here = 0;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const float* f = &v[k >> 1][8 * (k & 1)];
@@ -612,19 +626,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             h[i] = f2_to_h2(f[2 * i] * kValueGain, f[2 * i + 1] * kValueGain);
-                            odd |= not_finite2(h[i]);
+                            here = __vmaxu2(here, h[i] & 0x7FFF7FFFu);
+                            any |= __float_as_uint(f[2 * i]) | __float_as_uint(f[2 * i + 1]);
                         }
                     }
+                    most = __vmaxu2(most, here);
                     // A weight of 0 times a value that is not finite is NaN, for rows that do not see the position too: its
                     // values become 0, and the rows that do see it NaN at the end.
-                    if (odd != 0) {
+                    if (max(here & 0xFFFFu, here >> 16) >= 0x7C00u) {
                         bad = true;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) beyond |= fabsf(v[k][i]) < INFINITY && fabsf(v[k][i]) * kValueGain >= 65520.f;
+                            for (int i = 0; i < 16; ++i) beyond |= fabsf(v[k][i]) < INFINITY && fabsf(v[k][i]) >= kValueLimit;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = make_uint4(0, 0, 0, 0);
+                    }
+                    if (c == 3) {
+                        wide = __any_sync(kAllLanes, max(most & 0xFFFFu, most >> 16) < kSmall && (any << 1) != 0);
+                        if (!wide) give_back();
                     }
                 }
                 uint8_t* at = stage + (c & 1) * kPiece;
@@ -635,12 +655,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    // keys: unit c, positions in rows of 128 bytes; values: unit 2 + position / 64, of it dims 64 (c - 2) ..
-                    uint8_t* to = c < 2 ? dst + c * kUnit + ew * kPiece
-                                        : dst + (2 + (ew >> 1)) * kUnit + (c - 2) * (kUnit / 2) + (ew & 1) * kPiece;
-                    if (tile < tiles) bulk_copy_s2g(to, at, kPiece);
+                    // keys: unit c, positions in rows of 128 bytes
+                    if (tile < tiles) bulk_copy_s2g(c < 2 ? dst + c * kUnit + ew * kPiece : values_at(c - 2), at, kPiece);
                     bulk_commit();
                 }
+            }
+            if (__builtin_expect(wide, 0)) {
+                if (lane == 0) bulk_wait_all();  // the same places are written once more
+                __syncwarp();
+#pragma unroll 1
+                for (int c = 128; c < 256; c += 16) {
+                    float v[16];
+                    tmem_ld16(trow + 256 * buf + c, v);
+                    tmem_ld_wait();
+                    tmem_regs_ready(v);
+                    const float gain = kValueGain / (F16 ? kRowGain * kWeightGain : 1.f);
+                    uint32_t h[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = bad ? 0u : f2_to_bf2(v[2 * i] * gain, v[2 * i + 1] * gain);
+                    uint8_t* at = stage + ((c >> 6) & 1) * kPiece + lane * 128;
+                    const int chunk = (c >> 3) & 7;
+                    st_shared_v4(smem_u32(at) + ((chunk ^ (lane & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                    st_shared_v4(smem_u32(at) + (((chunk + 1) ^ (lane & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+                }
+                give_back();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    for (int c = 0; c < 2; ++c) {  // (a group for each piece, as above)
+                        if (tile < tiles) bulk_copy_s2g(values_at(c), stage + c * kPiece, kPiece);
+                        bulk_commit();
+                    }
+                }
+            }
+            if (lane == 0 && tile < tiles) {
+                p.forms[((int64_t)tile * p.heads + head) * 4 + ew] = wide;
+                if (wide) plan_head(p)->wide = 1;
             }
             if (bad && tile < tiles) {
                 const int b = sequence_of_tile(p, tile);
@@ -688,6 +738,7 @@ constexpr int kTileUnits = 5;
 constexpr int kOCol = 256;           // tensor memory: S (and P in its first half) at 0 and 128, O at 256 and 384
 constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
 constexpr uint32_t kIdescPV = make_idesc(128, 128, 0, 0, 0, 1);
+constexpr uint32_t kIdescWide = make_idesc(128, 128, 1, 1, 0, 1) - kIdescPV;  // what bf16 operands add to it
 constexpr float kRaise = 4.f;  // the running maximum (log2) is raised only when it grows by more than this
 // Weights are taken relative to 2^-kLift of the running maximum: as f16, up to 2^(kRaise + kLift) = 2^15, they keep their
 // precision down to 2^-25 of the largest one's, so that a long context's many small weights beside a large one are not lost.
@@ -702,6 +753,7 @@ struct Segment {
     int32_t n0, n1;       // tiles that queries 0-127, 128-255 see
     int32_t j0, j1;
     int32_t bad;          // first position without finite values (see first_bad())
+    int32_t wide;         // some values of the call are bf16 (see kSmall)
 };
 // In flight between the roles of a CTA (with 3 it keeps items that another could begin: eight ragged prompts 180 us for 178).
 constexpr int kSegments = 2;
@@ -768,6 +820,30 @@ __device__ __forceinline__ Place block_at(const ExpandParams& p, int x, int lane
 }
 // Part k of the line starts here.
 __device__ __forceinline__ int64_t part_begin(const ExpandParams& p, int k) { return __ldcg(part_begins(p) + k); }
+// How the values of a tile and head are kept: a byte for each 32 positions, 1 for bf16.
+__device__ __forceinline__ uint32_t forms_of(const ExpandParams& p, int tile, int head) {
+    return reinterpret_cast<const uint32_t*>(p.forms)[(int64_t)tile * p.heads + head];
+}
+// Weights of a tile's positions that are kept as bf16, from f16 in place.  (Rolled up: with a second conversion beside the first, in the
+// softmax's loop or in a loop of its own, calls without such values took 2 to 3% longer.)
+__device__ __forceinline__ void widen(uint32_t scol, uint32_t forms) {
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+        if (!((forms >> (8 * g)) & 1u)) continue;
+        float h[16];  // pairs
+        tmem_ld16(scol + 16 * g, h);
+        tmem_ld_wait();
+        tmem_regs_ready(h);
+        uint32_t packed[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+            packed[i] = f2_to_bf2(e.x, e.y);
+        }
+        tmem_st16_u32(scol + 16 * g, packed);
+    }
+    tmem_st_wait();
+}
 // Where CTA c leaves a part of an item: at most the first and the last segment of its part of the line are parts of items, and
 // the last begins its item.
 __device__ __forceinline__ float* part_slot(const ExpandParams& p, int c, bool first_tile) {
@@ -932,6 +1008,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const PlanHead plan = *plan_head(p);
         uint32_t n = 0;
         Segment s;
+        s.wide = plan.wide;
         auto publish = [&] {
             if (!wait(&ctl->seg_empty[n % kSegments], ((n / kSegments) & 1u) ^ 1u)) return false;
             if (lane == 0) {
@@ -1003,6 +1080,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             uint32_t segs[2] = {0, 0}, tiles_done[2] = {0, 0};
             struct Step {
                 uint32_t u;              // its first unit
+                uint32_t forms;          // of its values, a byte for each 32 positions
                 bool have[2];            // which query tiles have it
                 bool first[2], last[2];  // of its segment
             };
@@ -1028,6 +1106,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             };
             auto pv = [&](int w, const Step& t) {
                 if (!t.have[w]) return true;
+                uint32_t idesc[4];  // of 32 positions each
+#pragma unroll
+                for (int i = 0; i < 4; ++i) idesc[i] = kIdescPV + ((t.forms >> (8 * i)) & 1u) * kIdescWide;
                 if (!wait_one(&ctl->p_full[w], tiles_done[w] & 1u)) return false;
                 ++tiles_done[w];
                 if (t.first[w] && !wait_one(&ctl->o_free[w], (segs[w] & 1u) ^ 1u)) return false;
@@ -1040,8 +1121,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     const uint64_t b = vd + (uint64_t)(slot * (kUnit / 16));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_f16_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 32 * k + 8 * kk, b + (uint64_t)(128 * kk), kIdescPV,
-                                    t.first[w] && k == 0 && kk == 0 ? 0u : 1u);
+                        umma_f16_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 32 * k + 8 * kk, b + (uint64_t)(128 * kk),
+                                    idesc[2 * k + (kk >> 1)], t.first[w] && k == 0 && kk == 0 ? 0u : 1u);
                     if (w == 1 || !shared) umma_commit(&ctl->empty[slot]);
                 }
                 if (t.last[w]) {
@@ -1060,6 +1141,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 for (int j = s.j0; ok && j < s.j1; ++j, u += kTileUnits) {
                     Step now;
                     now.u = u;
+                    now.forms = s.wide ? forms_of(p, s.tile0 + j, s.head) : 0;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         now.have[w] = j < seg_end(s, w);
@@ -1098,6 +1180,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             float m_used = -INFINITY, l_sum = 0.f;  // what weights are relative to (log2): the maximum - kLift; their sum
 #pragma unroll 1
             for (int j = begin; j < end; ++j, ++tile) {
+                const bool wide = it.wide != 0;
                 if (!(ok = wait(&ctl->s_full[w], tile & 1u))) break;
                 tc_fence_after();
                 float s[8][16];
@@ -1140,7 +1223,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                         tmem_st16(ocol + c, o);
                     }
                 }
-                // weights: the sum takes the fp32 values, the products their rounding to f16 (at most 2^-11 of each, unbiased)
+                // weights: the sum takes the fp32 values, the products their rounding to f16 (at most 2^-11 of each, unbiased), and those
+                // once more to bf16 where the values are (see kSmall)
                 float2 sum[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
                 const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), mu2 = make_float2(-mu, -mu);
 #pragma unroll
@@ -1161,6 +1245,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 l_sum = l_sum * alpha + (half.x + half.y);
                 m_used = m_new;
                 tmem_st_wait();
+                if (__builtin_expect(wide, 0)) widen(scol, forms_of(p, it.tile0 + j, it.head));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->p_full[w]);

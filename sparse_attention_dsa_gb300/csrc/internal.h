@@ -326,7 +326,7 @@ constexpr int kExpandCtas = 152;                     // of the attention, at mos
 // A partial result: O [256][128] fp32 (unnormalised), then (maximum in log2 units, sum) per row.
 constexpr int kExpandPartFloats = 256 * 128 + 2 * 256;
 constexpr size_t kExpandPartBytes = (size_t)2 * kExpandCtas * kExpandPartFloats * 4;
-constexpr int kExpandPlanHead = 8 + 2 * (kExpandCtas + 1);  // int32 in front of the plan's arrays
+constexpr int kExpandPlanHead = 10 + 2 * (kExpandCtas + 1);  // int32 in front of the plan's arrays
 struct ExpandParams {
     const uint8_t* kv_cache;  // bf16 rows, or FP8 rows of kKvFp8RowBytes
     const uint16_t* w_kv;     // [Hq, 256, 512] bf16 bits
@@ -354,6 +354,7 @@ struct ExpandParams {
     uint16_t* weights16;  // FP8 rows: w_kv as f16
     uint8_t* latents;  // [cap_tiles][9][128][64] bf16 (FP8 rows' latent part: f16), 128-byte swizzle
     uint8_t* kv;       // [cap_tiles][Hq][4] units of 16 KB
+    uint8_t* forms;    // [cap_tiles][Hq][4] of the values of 32 positions: 1 for bf16, 0 for f16
 };
 inline size_t expand_weight_bytes(const ExpandParams& p) { return p.kv_fp8 ? (size_t)p.heads * 256 * 512 * 2 : 0; }
 inline size_t expand_plan_bytes(const ExpandParams& p) {
