@@ -481,9 +481,10 @@ dsa_status_t dsa_value_heads(const dsa_dims_t* dims, const void* o_latent, const
  *     out[t,h,:] = sum_s softmax(z)_s * wv[h] c_s,   lse[t,h] = log sum_s exp(z_s)
  * Keys are rounded to bf16, values and the softmax's weights in the products to f16 (to bf16 where the values that a position
  * has in a head are all below 2^-13, so that small ones keep their relative precision; beside larger ones of its own a value is
- * off by 2^-27 at most), and with FP8 rows their latent part and w_kv before that.  Head values and FP8 rows' elements of a
- * magnitude of more than 16376 (w_kv with FP8 rows: 4094) are beyond that and reported (DSA_DEVERR_RANGE); FP8 rows' elements
- * below 2^-16 and weights below 2^-18 lose relative precision.
+ * off by 2^-27 at most), and with FP8 rows their latent part and w_kv before that, each row, and each 16
+ * rows of w_kv from a multiple of 16 on, relative to their largest magnitude (11 bits down to 2^-28 of it, where it is 2^-48 or
+ * more).  Head values and FP8 rows' elements of a magnitude of more than
+ * 16376 (w_kv with FP8 rows: 4094) are beyond that and reported (DSA_DEVERR_RANGE).
  *   total_pages  an upper bound of the pages in use: sum over the sequences with queries of ceil(L_b / 64)
  *   q_nope     [T, Hq, 128] bf16, strides as for dsa_absorb_queries
  *   q_pe       [T, Hq, 64] bf16, rotated (dsa_rope_queries; q + 512 with strides Hq * 576 and 576 is where that leaves it);

@@ -287,7 +287,8 @@ bool expand_sizes(const dsa_dims_t* d, int32_t total_pages, dsa::ExpandParams* p
     p->kv_fp8 = d->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
     p->cap_tiles = (int32_t)tiles;
     p->cap_blocks = (int32_t)blocks;
-    *bytes = dsa::expand_plan_bytes(*p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(*p) + (size_t)tiles * dsa::kExpandTileBytes +
+    *bytes = dsa::expand_plan_bytes(*p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(*p) + dsa::expand_row_scale_bytes(*p) +
+             (size_t)tiles * dsa::kExpandTileBytes +
              (size_t)tiles * d->attn_heads * (dsa::kExpandHeadTileBytes + 4);
     return true;
 }
@@ -1092,7 +1093,9 @@ dsa_status_t dsa_expanded_attn(const dsa_dims_t* d, int32_t total_pages, const v
     p.partial = reinterpret_cast<float*>(ws + dsa::expand_plan_bytes(p));
     p.sectors = ((reinterpret_cast<uintptr_t>(p.out) | reinterpret_cast<uintptr_t>(p.partial)) & 31) == 0;
     p.weights16 = reinterpret_cast<uint16_t*>(ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes);
-    p.latents = ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(p);
+    p.weight_scale = reinterpret_cast<float*>(p.weights16 + (p.kv_fp8 ? (size_t)p.heads * 256 * 512 : 0));
+    p.row_scale = reinterpret_cast<float*>(ws + dsa::expand_plan_bytes(p) + dsa::kExpandPartBytes + dsa::expand_weight_bytes(p));
+    p.latents = reinterpret_cast<uint8_t*>(p.row_scale) + dsa::expand_row_scale_bytes(p);
     p.kv = p.latents + (size_t)p.cap_tiles * dsa::kExpandTileBytes;
     p.forms = p.kv + (size_t)p.cap_tiles * p.heads * dsa::kExpandHeadTileBytes;
     L.num_sms = dev.num_sms;

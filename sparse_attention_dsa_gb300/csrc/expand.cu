@@ -30,6 +30,7 @@
 // up to 200 queries, 16 heads 23 us (32): three kernels' latency, one after another.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -173,10 +174,17 @@ __device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the lo
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-// FP8 rows are multiplied as f16, too (a code's four bits times a scale lose 2^-11 of it, for bf16's 2^-8), times kRowGain, and
-// the weights with them, times kWeightGain (exact down to 2^-18): error 0.0022 instead of 0.0031.
+// FP8 rows are multiplied as f16, too (a code's four bits times a scale lose 2^-11 of it, for bf16's 2^-8: error 0.0022 instead of
+// 0.0031), and the weights with them.  A position's row, and kGainRows rows of
+// the weights together, are kept times a power of two that brings their largest magnitude to 2^14 or more, at least kRowGain or
+// kWeightGain: down to 2^-28 of the largest no bit is lost.  The keys kernel takes both out of its sums.
 constexpr float kRowGain = 4.f;
+constexpr int kRowGainLog2 = 2, kWeightGainLog2 = 4, kMostGainLog2 = 62;  // (the products of two stay within fp32)
 constexpr float kWeightGain = 16.f;
+constexpr int kGainRows = 16;  // (a factor for each column of a result instead: eight ragged prompts 193 us for 172)
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// The gain's exponent for a largest magnitude with this exponent of its own (128: not finite).
+__device__ __forceinline__ int gain_log2(int largest, int least) { return max(least, min(kMostGainLog2, 14 - largest)); }
 // Eight E4M3 codes times a scale (in fp32), rounded to f16.
 __device__ __forceinline__ uint4 codes_to_h8(uint32_t lo, uint32_t hi, float scale) {
     uint32_t out[4];
@@ -192,6 +200,10 @@ __device__ __forceinline__ uint4 codes_to_h8(uint32_t lo, uint32_t hi, float sca
     }
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
+// The magnitude of a code without its sign (0x7F: NaN, as 480).
+__device__ __forceinline__ float code_value(uint32_t c) {
+    return (c >> 3) ? (float)(8 + (c & 7)) * power_of_two((int)(c >> 3) - 10) : (float)(c & 7) * 0x1p-9f;
+}
 // Whether one of sixteen codes, none a NaN, times a finite scale is beyond f16's range (a rare path).
 __device__ __forceinline__ bool codes_beyond(const uint4& code, float scale) {
     if (!(fabsf(scale) < INFINITY)) return false;
@@ -200,8 +212,7 @@ __device__ __forceinline__ bool codes_beyond(const uint4& code, float scale) {
 #pragma unroll 1
     for (int j = 0; j < 16; ++j) {
         const uint32_t c = (w[j >> 2] >> (8 * (j & 3))) & 0x7Fu;
-        const float v = c == 0x7Fu ? 0.f : (c >> 3) ? (8 + (c & 7)) * exp2f((float)(int)(c >> 3) - 10.f) : (c & 7) * 0x1p-9f;
-        found |= v * fabsf(scale) * kRowGain >= 65520.f;
+        found |= c != 0x7Fu && code_value(c) * fabsf(scale) * kRowGain >= 65520.f;
     }
     return found;
 }
@@ -224,6 +235,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
     __shared__ int longest[kGatherWarps];
     __shared__ __align__(16) int block_tiles[kSortBlocks];
     __shared__ int2 found[2];  // (sequence, first tile), one for each parity of the loop
+    __shared__ uint32_t largest_weight[2][kGatherWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool plans = blockIdx.x == 0;
     grid_dependency_wait();
@@ -378,22 +390,42 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
             if (tid < p.ctas) part_begins(p)[tid + 1] = share / parts;
         }
     }
-    if (p.kv_fp8) {  // the heads' weights as f16
-        const int64_t pieces = (int64_t)p.heads * (256 * 512 / 8);
+    if (p.kv_fp8) {  // the heads' weights as f16 (by the last blocks first: the first ones have the plan and the first rows)
+        static_assert(kGainRows * 512 / 8 == 4 * kGatherThreads, "four pieces a thread");
         bool beyond = false;
-        for (int64_t i = (int64_t)blockIdx.x * kGatherThreads + tid; i < pieces; i += (int64_t)gridDim.x * kGatherThreads) {
-            const uint4 v = reinterpret_cast<const uint4*>(p.w_kv)[i];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[4];
+        uint32_t turn = 0;
+        for (int i = (int)gridDim.x - 1 - (int)blockIdx.x; i < p.heads * (256 / kGainRows); i += (int)gridDim.x, turn ^= 1u) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.w_kv) + (int64_t)i * 4 * kGatherThreads + tid;
+            uint4* dst = reinterpret_cast<uint4*>(p.weights16) + (int64_t)i * 4 * kGatherThreads + tid;
+            uint4 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xFFFF0000u);
-                h[j] = f2_to_h2(a * kWeightGain, b * kWeightGain);
-                if (not_finite2(h[j]) != 0)
-                    beyond |= (fabsf(a) < INFINITY && fabsf(a) * kWeightGain >= 65520.f) ||
-                              (fabsf(b) < INFINITY && fabsf(b) * kWeightGain >= 65520.f);
+            for (int k = 0; k < 4; ++k) v[k] = src[k * kGatherThreads];
+            uint32_t most = 0;  // as bf16 bits, in either half
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                most = __vmaxu2(__vmaxu2(most, __vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu)),
+                                __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu));
+            most = __reduce_max_sync(kAllLanes, max(most & 0xFFFFu, most >> 16));
+            if (lane == 0) largest_weight[turn][warp] = most;
+            __syncthreads();
+            most = __reduce_max_sync(kAllLanes, largest_weight[turn][lane % kGatherWarps]);
+            const int log2 = gain_log2((int)(most >> 7) - 127, kWeightGainLog2);
+            const float gain = power_of_two(log2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = __uint_as_float(w[j] << 16), b = __uint_as_float(w[j] & 0xFFFF0000u);
+                    h[j] = f2_to_h2(a * gain, b * gain);
+                    if (not_finite2(h[j]) != 0)
+                        beyond |= (fabsf(a) < INFINITY && fabsf(a) * kWeightGain >= 65520.f) ||
+                                  (fabsf(b) < INFINITY && fabsf(b) * kWeightGain >= 65520.f);
+                }
+                dst[k * kGatherThreads] = make_uint4(h[0], h[1], h[2], h[3]);
             }
-            reinterpret_cast<uint4*>(p.weights16)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+            if (tid == 0) p.weight_scale[i] = power_of_two(-log2);
         }
         if (beyond) raise_error(p.err, DSA_DEVERR_RANGE);
     }
@@ -430,6 +462,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
                 *reinterpret_cast<uint4*>(dst + (chunk >> 3) * kUnit + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = v;
             };
             if (!p.kv_fp8 || !have) {
+                if (p.kv_fp8 && lane == 0) p.row_scale[(int64_t)tile * 128 + row] = 1.f;
                 const uint4* src = reinterpret_cast<const uint4*>(p.kv_cache + ((int64_t)pg * 64 + of_page) * 1152);
                 uint4 v[3];
 #pragma unroll
@@ -442,7 +475,16 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
                 const uint4 code = reinterpret_cast<const uint4*>(src)[lane];
                 const float scale = reinterpret_cast<const float*>(src + kKvFp8ScaleOff)[lane >> 3];
                 const uint4 rot = lane < 8 ? reinterpret_cast<const uint4*>(src + kKvFp8RopeOff)[lane] : zero;
-                const uint4 lo = codes_to_h8(code.x, code.y, scale * kRowGain), hi = codes_to_h8(code.z, code.w, scale * kRowGain);
+                uint32_t most = __vmaxu4(__vmaxu4(code.x & 0x7F7F7F7Fu, code.y & 0x7F7F7F7Fu),
+                                         __vmaxu4(code.z & 0x7F7F7F7Fu, code.w & 0x7F7F7F7Fu));
+                most = __vmaxu2(most & 0x00FF00FFu, (most >> 8) & 0x00FF00FFu);
+                const float largest = fabsf(code_value(max(most & 0xFFFFu, most >> 16)) * scale);
+                const int log2 = gain_log2((int)(__reduce_max_sync(kAllLanes, __float_as_uint(largest)) >> 23) - 127, kRowGainLog2);
+                if (lane == 0) p.row_scale[(int64_t)tile * 128 + row] = power_of_two(-log2);
+                float gained = scale * power_of_two(log2);
+                // (codes of 0 beside a scale that the gain takes beyond fp32 are 0; others with such a scale are beyond range)
+                if (fabsf(gained) == INFINITY && fabsf(scale) < INFINITY) gained = copysignf(FLT_MAX, scale);
+                const uint4 lo = codes_to_h8(code.x, code.y, gained), hi = codes_to_h8(code.z, code.w, gained);
                 put(2 * lane, lo);
                 put(2 * lane + 1, hi);
                 if (lane < 8) put(64 + lane, rot);
@@ -583,6 +625,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
         for (int64_t u = pair; ok && u < units; u += pairs, ++t) {
             const int tile = 2 * (int)(u % tile_pairs) + rank, head = (int)(u / tile_pairs);
             const uint32_t buf = t & 1u;
+            // (FP8 rows: what the position and the weights' rows were multiplied by, taken out)
+            const float row_scale = F16 ? p.row_scale[(int64_t)tile * 128 + 32 * ew + lane] : 1.f;
+            const float4* weight_scale = reinterpret_cast<const float4*>(p.weight_scale + head * (256 / kGainRows));
             if (!(ok = wait(&ctl->d_full[buf], (t >> 1) & 1u))) break;
             tc_fence_after();
             uint8_t* dst = p.kv + ((int64_t)tile * p.heads + head) * kHeadTile;
@@ -605,10 +650,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tmem_regs_ready(v[k]);
                 if (F16) {
+                    static_assert(kGainRows == 16, "of a load of 16 columns");
+                    const float4 of = weight_scale[c];
+                    const float f[4] = {row_scale * of.x, row_scale * of.y, row_scale * of.z, row_scale * of.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[k][i] *= 1.f / (kRowGain * kWeightGain);
+                        for (int i = 0; i < 16; ++i) v[k][i] *= f[k];
                 }
                 uint4 w[8];
                 if (c < 2) {
@@ -669,10 +717,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kKeysThreads, 1)
                     tmem_ld16(trow + 256 * buf + c, v);
                     tmem_ld_wait();
                     tmem_regs_ready(v);
-                    const float gain = kValueGain / (F16 ? kRowGain * kWeightGain : 1.f);
+                    const float f = F16 ? row_scale * p.weight_scale[head * (256 / kGainRows) + c / kGainRows] : 1.f;
                     uint32_t h[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = bad ? 0u : f2_to_bf2(v[2 * i] * gain, v[2 * i + 1] * gain);
+                    for (int i = 0; i < 8; ++i) h[i] = bad ? 0u : f2_to_bf2(v[2 * i] * f * kValueGain, v[2 * i + 1] * f * kValueGain);
                     uint8_t* at = stage + ((c >> 6) & 1) * kPiece + lane * 128;
                     const int chunk = (c >> 3) & 7;
                     st_shared_v4(smem_u32(at) + ((chunk ^ (lane & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));

@@ -351,12 +351,15 @@ struct ExpandParams {
     int32_t cap_blocks;  // of queries, whatever the offsets say
     int32_t* plan;
     float* partial;    // two results of cut items for each CTA
-    uint16_t* weights16;  // FP8 rows: w_kv as f16
+    uint16_t* weights16;  // FP8 rows: w_kv as f16, 16 rows of 512 together times a power of two
+    float* weight_scale;  // [Hq * 16] that power's reciprocal
+    float* row_scale;     // [cap_tiles * 128] FP8 rows: the same of a position's latent part
     uint8_t* latents;  // [cap_tiles][9][128][64] bf16 (FP8 rows' latent part: f16), 128-byte swizzle
     uint8_t* kv;       // [cap_tiles][Hq][4] units of 16 KB
     uint8_t* forms;    // [cap_tiles][Hq][4] of the values of 32 positions: 1 for bf16, 0 for f16
 };
-inline size_t expand_weight_bytes(const ExpandParams& p) { return p.kv_fp8 ? (size_t)p.heads * 256 * 512 * 2 : 0; }
+inline size_t expand_weight_bytes(const ExpandParams& p) { return p.kv_fp8 ? ((size_t)p.heads * (256 * 512 * 2 + 16 * 4) + 1023) / 1024 * 1024 : 0; }
+inline size_t expand_row_scale_bytes(const ExpandParams& p) { return p.kv_fp8 ? (size_t)p.cap_tiles * 128 * 4 : 0; }
 inline size_t expand_plan_bytes(const ExpandParams& p) {
     return (((size_t)kExpandPlanHead + 4 * (size_t)p.batch + 3) * 4 + 1023) / 1024 * 1024;
 }
