@@ -34,6 +34,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "quant.cuh"
@@ -1425,8 +1427,11 @@ cudaError_t launch_expand(const ExpandLaunch& L, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int64_t gathered = (int64_t)kGatherUnits * p.cap_tiles, blocks = 8 * L.num_sms;
-    cfg.gridDim = dim3((unsigned)(gathered < blocks ? gathered : blocks));
+    // (FP8 rows: the weights are converted by the same blocks, many heads' also where there are few rows: 100 tokens of 128
+    // heads took 172 us with a block for each 16 rows alone)
+    const int64_t weights = p.kv_fp8 ? (int64_t)p.heads * (256 / kGainRows) : 0, blocks = 8 * L.num_sms;
+    const int64_t gathered = std::max(weights, (int64_t)kGatherUnits * p.cap_tiles);
+    cfg.gridDim = dim3((unsigned)std::min(gathered, blocks));
     cfg.blockDim = dim3(kGatherThreads);
     if ((e = cudaLaunchKernelEx(&cfg, gather_kernel, p)) != cudaSuccess) return e;
     const int64_t units = (int64_t)((p.cap_tiles + 1) / 2) * p.heads;
