@@ -435,8 +435,8 @@ size_t dsa_prefix_attn_workspace_size(const dsa_dims_t* dims, int32_t prefix_len
  *   scale      codes_dtype DSA_FP8_E4M3: fp32, [rows] (group 0: a scale for the row) or [rows, dim / 128] (group 128);
  *              DSA_MXFP8_E4M3: E8M0 bytes [rows, dim / 32] (group 32)
  * sum may be residual or (dense) x; out may be x (of the same stride) or (dense) residual; otherwise outputs overlap nothing.
- * An infinity or NaN in a row makes NaN as the formula does (a NaN code is 0x7F or 0xFF; scales are of the group's
- * numbers); so do squares whose sum leaves fp32's range (magnitudes beyond 2^60): y is 0 there.  No workspace.
+ * An infinity or NaN in a row, or an x + residual beyond fp32, makes NaN as the formula does (a NaN code is 0x7F or 0xFF; scales
+ * are of the group's numbers); finite rows of any magnitude have the formula's values.  No workspace.
  * Supported: dim a multiple of 8 (of the group) up to 16384.
  */
 dsa_status_t dsa_rms_norm(int32_t rows, int32_t dim, const void* x, int64_t x_stride, const void* residual, void* sum,

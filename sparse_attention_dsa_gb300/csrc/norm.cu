@@ -28,8 +28,9 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kRowsPerBlock = 4;  // rows of a warp each
 constexpr int kMaxWarps = 32;
 constexpr int kFewRows = 1216;    // eight blocks for each SM
+constexpr float kSmallMean = 0x1p-100f;  // of squares: below, some of a row's may be subnormal
 
-// Of all threads that share a row.  The block's result is in every thread; `slots` is used once a call.
+// Of all threads that share a row.  The block's result is in every thread; `slots` are its own until all have read it.
 template <bool kWarpRow, typename F>
 __device__ __forceinline__ float reduce_row(float v, float* slots, F op) {
 #pragma unroll
@@ -84,12 +85,33 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kRowsPerBlock : 1024, kWarpRow
         ss += (part[0] + part[1]) + (part[2] + part[3]);
     }
     ss = reduce_row<kWarpRow>(ss, sums, [](float a, float b) { return a + b; });
-    const float r = __frsqrt_rn(__fdiv_rn(ss, (float)p.dim) + p.eps);
+    const float mean = __fdiv_rn(ss, (float)p.dim) + p.eps;
+    float r = __frsqrt_rn(mean);
+    // Squares beyond fp32's range, or so small that they lose bits: the row times a power of two (its sum is stored before).  (In
+    // place and with the same slots: with others 8192 rows of 8192 took 78 us to FP8 tiles, not 72; as a function of its own 84.)
+    const bool scaled = ss == INFINITY || mean < kSmallMean;
+    if (__builtin_expect(scaled, 0)) {
+        const float f = ss == INFINITY ? 0x1p-72f : 0x1p80f;  // largest squares below 2^128 / 16384; the smallest numbers' normal
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int at = t + i * width;
+            if (p.sum != nullptr && at < pieces) reinterpret_cast<uint4*>(p.sum + row * p.dim)[at] = pack8(h[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[i][j] *= f;
+                ss = fmaf(h[i][j], h[i][j], ss);
+            }
+        }
+        if (!kWarpRow) __syncthreads();  // everyone has read the slots
+        ss = reduce_row<kWarpRow>(ss, sums, [](float a, float b) { return a + b; });
+        r = __frsqrt_rn(__fdiv_rn(ss, (float)p.dim) + p.eps * f * f);
+    }
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int at = t + i * width;
-        if (p.sum != nullptr && at < pieces) reinterpret_cast<uint4*>(p.sum + row * p.dim)[at] = pack8(h[i]);
+        if (p.sum != nullptr && !scaled && at < pieces) reinterpret_cast<uint4*>(p.sum + row * p.dim)[at] = pack8(h[i]);
         float w[8];
         unpack8(wv[i], w);
 #pragma unroll
