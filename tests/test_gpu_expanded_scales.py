@@ -117,3 +117,20 @@ def test_fp8_groups_of_zeros_with_any_scale():
     scales[:, 1] = torch.tensor([3.0e38, 1.0, -2.0e38, 1e-40], device="cuda")[torch.arange(len(flat), device="cuda") % 4]
     flat[:, LATENT:LATENT + 16] = scales.view(torch.uint8)
     check_call(c.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_captured_call_with_other_magnitudes(fp8):
+    """Which positions are kept in which form, and the rows' powers of two, are found anew at each replay."""
+    c = Call([700, 129], [400, 129], 3, fp8, seed=421)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run()
+    w = c.w.clone()
+    for power in (0, 24, 0, 12, 30):
+        c.w.copy_(w)
+        c.w[1:, NOPE:] *= 2.0 ** -power  # (one head keeps its values)
+        c.out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_call(c, half=BF16 if power else F16, heads=(0, 1, 2))
