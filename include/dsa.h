@@ -483,8 +483,8 @@ dsa_status_t dsa_value_heads(const dsa_dims_t* dims, const void* o_latent, const
  * has in a head are all below 2^-13, so that small ones keep their relative precision; beside larger ones of its own a value is
  * off by 2^-27 at most), and with FP8 rows their latent part and w_kv before that, each row, and each 16
  * rows of w_kv from a multiple of 16 on, relative to their largest magnitude (11 bits down to 2^-28 of it, where it is 2^-48 or
- * more).  Head values and FP8 rows' elements of a magnitude of more than
- * 16376 (w_kv with FP8 rows: 4094) are beyond that and reported (DSA_DEVERR_RANGE).
+ * more).  Head values and FP8 rows' elements of a magnitude of more than 16376 (w_kv with FP8 rows: 4094) are beyond that and
+ * reported (DSA_DEVERR_RANGE).
  *   total_pages  an upper bound of the pages in use: sum over the sequences with queries of ceil(L_b / 64)
  *   q_nope     [T, Hq, 128] bf16, strides as for dsa_absorb_queries
  *   q_pe       [T, Hq, 64] bf16, rotated (dsa_rope_queries; q + 512 with strides Hq * 576 and 576 is where that leaves it);
@@ -494,8 +494,9 @@ dsa_status_t dsa_value_heads(const dsa_dims_t* dims, const void* o_latent, const
  *   workspace  dsa_expanded_attn_workspace_size(dims, total_pages) bytes, first 256 zero-filled once
  * dims->idx_*, top_k and max_q_len are not looked at.  Positions beyond p_t and rows behind L_b are never part of the result,
  * whatever they hold.  A score of -inf has weight 0; with every score -inf, out = 0 and lse = -inf.  A visible position
- * with a value that is not finite, in its row or in its head values as f16, makes NaN of the rows that see it (in
- * out and lse; of all heads, also where the value is one head's); so does a page that is out of range, which is
+ * with a value that is not finite, in its row's latent part or in its head values as f16, makes NaN of the rows that see it (in
+ * out and lse; of all heads, also where the value is one head's), a NaN in its rotary part too, an infinity there by the score
+ * that it makes (NaN, or a weight of 0); so does a page that is out of range, which is
  * reported (DSA_DEVERR_PAGE).  A sequence with n_b > L_b, a context beyond its page table or pages beyond total_pages
  * (DSA_DEVERR_SEQ) and a token that no sequence owns (DSA_DEVERR_SEQ) have out and lse left as they were.
  * Supported: D = 576, Dv = 512, Hq <= 128.

@@ -8,7 +8,7 @@
 //   z_s = scale * q[t, h] . k[s, h] for s = 0..p_t,  out[t, h] = softmax(z) . v,  lse[t, h] = logsumexp(z).
 // A (query, position, head) takes 2 (192 + 128) operations where the absorbed form takes 2 (576 + 512), and a (position,
 // head) 2 x 256 x 512 for its keys and values, so this is the form for many queries a sequence.  Keys are rounded to
-// bf16, as a projection would leave them (the queries they meet are bf16), values and weights to f16.
+// bf16, as a projection would leave them (the queries they meet are bf16), values and weights to f16, small ones to bf16.
 //
 // Four kernels, chained by programmatic launches:
 //   gather:  the pages' rows as tiles (of 128 positions, a sequence's own) of nine 16 KB pieces (64 dims of 128 positions;
@@ -22,12 +22,13 @@
 //
 // What bounds it, and measured (one GB300; calls in a graph, in brackets with L2 flushed before).  The tensor pipe: a tile of
 // 128 x 128 is 1280 cycles of products, in which its softmax (about 1150) and its group's wait for the other tile's products pass.
-// An 8192-token prompt of 128 heads 1722 to 1800 us (1805 to 1940), 3.02 TFLOP, 1.75 PFLOP/s, up to 0.93 of the measured cuBLAS rate, of
-// which gathering 8, keys 170 (275 GFLOP; their 537 MB are written at HBM's pace for writes), the rest attention at 1.8; in
-// a long loop the power limit takes up to 14% of the clock.  4096 queries behind 12288 of 16 heads 395 to 406 us (400 to 410), 0.9 of it:
-// the parts' results and their combination 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 173 us (177):
-// a quarter of the pairs in its tiles are masked, an item of some six tiles costs about two more, keys 48.  Three prompts of
-// up to 200 queries, 16 heads 23 us (32): three kernels' latency, one after another.
+// An 8192-token prompt of 128 heads 1775 to 1960 us (1910 to 1970), by the card and its power limit, 3.02 TFLOP, up to 1.70 PFLOP/s,
+// 0.9 of the measured cuBLAS rate, of which gathering 8, keys 170 (275 GFLOP; their 537 MB are written at HBM's pace for
+// writes).  4096 queries behind 12288 of 16 heads 402 to 411 us (405 to 430), 0.88 of it: the parts' results and their combination
+// 15.  Eight ragged prompts of up to 1171 queries, 32 heads, FP8 rows 173 to 175 us (181 to 184): a quarter of the pairs in
+// its tiles are masked, an item of some six tiles costs about two more, keys 48.  Three prompts of up to 200 queries, 16 heads
+// 24 us (34): three kernels' latency, one after another.  With small values (kSmall) everywhere: 503 for the chunk, 217, 27 for the
+// short ones, 2295 for the long one.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -82,15 +83,15 @@ static_assert(kExpandPlanHead == sizeof(PlanHead) / 4 + 2 * (kExpandCtas + 1), "
 // The line: the blocks of head 0, of head 1, ..., each kItemCost places for what it costs beside its tiles (its queries' load,
 // its first scores' latency, its result) and one for each tile of keys.  It is cut into equal parts, of kMinPlaces at least
 // on average, or its items are taken whole in turn:
-//   * whole, where the estimate of the last CTA's time is no longer than with parts (three short prompts 23.0 us, cut 30.9;
-//     eight ragged ones 176, cut 187; but 256 items of 112 tiles, for 152 CTAs, 455, cut into parts alone 415, now 399);
+//   * whole, where the estimate of the last CTA's time is no longer than with parts (three short prompts 24.0 us, cut 31.4;
+//     eight ragged ones 174, cut 187; but 256 items of 112 tiles, for 152 CTAs, 465, cut 404);
 //     With parts, each CTA takes first one whole item (the last blocks of the heads, as many as all heads have CTAs for), where
 //     those leave every CTA a part: CTAs at the same head then meet its keys at about the same time, from L2
-//     instead of HBM, where parts alone begin anywhere (4096 queries behind 12288 of 16 heads 399 us for 409, two times 2048
-//     behind 28000 640 for 678).
+//     instead of HBM, where parts alone begin anywhere (4096 queries behind 12288 of 16 heads 401 us for 417, the last
+//     1569 and 2048 of 27359 and 28000 positions 803 for 863).
 //   * whole, where the longest item is no more than 1 / kWholeItems of a CTA's share: heads go in groups whose keys and
-//     values (kGroupBytes) stay in L2 while all their blocks meet them (the 8192-token prompt of 128 heads 1722 us; head by head
-//     1753, all heads together 1881, cut 1939).
+//     values (kGroupBytes) stay in L2 while all their blocks meet them (the 8192-token prompt of 128 heads 1912 us, at the power
+//     limit; head by head 1935, all heads together 2099, cut 2139).
 constexpr int kItemCost = 2;  // (1 and 3: no difference beyond the runs')
 constexpr int kMinPlaces = 4;
 constexpr int kWholeItems = 8;
@@ -177,13 +178,13 @@ __device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {  // a in the lo
     return r;
 }
 // FP8 rows are multiplied as f16, too (a code's four bits times a scale lose 2^-11 of it, for bf16's 2^-8: error 0.0022 instead of
-// 0.0031), and the weights with them.  A position's row, and kGainRows rows of
-// the weights together, are kept times a power of two that brings their largest magnitude to 2^14 or more, at least kRowGain or
-// kWeightGain: down to 2^-28 of the largest no bit is lost.  The keys kernel takes both out of its sums.
+// 0.0031), and the weights with them.  A position's row, and kGainRows rows of the weights together, are kept times a power of
+// two that brings their largest magnitude to 2^14 or more, at least kRowGain or kWeightGain: down to 2^-28 of the largest no bit
+// is lost.  The keys kernel takes both out of its sums.
 constexpr float kRowGain = 4.f;
 constexpr int kRowGainLog2 = 2, kWeightGainLog2 = 4, kMostGainLog2 = 62;  // (the products of two stay within fp32)
 constexpr float kWeightGain = 16.f;
-constexpr int kGainRows = 16;  // (a factor for each column of a result instead: eight ragged prompts 193 us for 172)
+constexpr int kGainRows = 16;  // (a factor for each column of a result instead: eight ragged prompts 193 us for 174)
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 // The gain's exponent for a largest magnitude with this exponent of its own (128: not finite).
 __device__ __forceinline__ int gain_log2(int largest, int least) { return max(least, min(kMostGainLog2, 14 - largest)); }
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const ExpandPara
         if (all[1] > p.cap_blocks || all[2] > INT32_MAX || alone <= cut || line >= (long long)kWholeItems * p.ctas * most) parts = 0;
         const int whole = parts == p.ctas && (long long)(most + kMinPlaces) * p.ctas <= line ? min(p.ctas / p.heads, blocks - 1) : 0;
         // Items of several sequences are taken in the order of their lengths, so that the CTAs end together (eight ragged prompts of
-        // 32 heads, FP8 rows: 173.6 us, sequence by sequence 177.9); of one they
+        // 32 heads, FP8 rows: 175 us, sequence by sequence 180); of one they
         // are in that order, and so many blocks that they are not sorted end together anyway.
         const bool sorted = parts == 0 && p.batch > 1 && blocks <= kSortBlocks && all[1] == blocks && blocks * p.heads > p.ctas;
         if (tid == 0) {
@@ -805,7 +806,7 @@ struct Segment {
     int32_t bad;          // first position without finite values (see first_bad())
     int32_t wide;         // some values of the call are bf16 (see kSmall)
 };
-// In flight between the roles of a CTA (with 3 it keeps items that another could begin: eight ragged prompts 180 us for 178).
+// In flight between the roles of a CTA (with 3 it keeps items that another could begin: eight ragged prompts 178 us for 174).
 constexpr int kSegments = 2;
 // 32 bytes: one whole sector where `whole` says that dst is 32-byte aligned, as 16-byte pieces otherwise (arrays may begin at
 // any multiple of 16).
@@ -874,8 +875,8 @@ __device__ __forceinline__ int64_t part_begin(const ExpandParams& p, int k) { re
 __device__ __forceinline__ uint32_t forms_of(const ExpandParams& p, int tile, int head) {
     return reinterpret_cast<const uint32_t*>(p.forms)[(int64_t)tile * p.heads + head];
 }
-// Weights of a tile's positions that are kept as bf16, from f16 in place.  (Rolled up: with a second conversion beside the first, in the
-// softmax's loop or in a loop of its own, calls without such values took 2 to 3% longer.)
+// Weights of a tile's positions that are kept as bf16, from f16 in place.  (Rolled up: with a second conversion beside the first, in
+// the softmax's loop or in a loop of its own, calls without such values took 2 to 3% longer instead of 1.)
 __device__ __forceinline__ void widen(uint32_t scol, uint32_t forms) {
 #pragma unroll 1
     for (int g = 0; g < 4; ++g) {

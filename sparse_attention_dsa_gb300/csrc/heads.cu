@@ -15,10 +15,12 @@
 // in tensor memory is double: four warps round a unit to bf16 and store it by TMA (32 tokens x 64 dims at a time, clipped at
 // the last token) while the next one is multiplied.
 //
-// What bounds it: HBM.  Absorb writes 1024 bytes for 256 read, and writes alone run at 4.0 TB/s here (filling memory):
-// 4096 tokens of 128 heads 139 us for 537 MB written, 0.96 of that.  Values reads four times what it writes: 2111 tokens of
-// 128 heads 58 us for 363 MB, 6.3 TB/s, 0.93 of the copy bandwidth.  Few tokens: each head's weights once, and latency; 32
-// tokens of 128 heads 6.0 to 7.0 us (L2 flushed before each call 13.5), 130 tokens of 16 heads 4.9 to 5.4 (11.4).
+// What bounds it: HBM.  Absorb writes 1024 bytes for 256 read, and writes alone run at 4.0 TB/s here (filling memory), 134 us for
+// the 537 MB of 4096 tokens of 128 heads.  These take 141 us, and read 248 MB where 151 are needed: 211 with dense rows (some
+// of a head's token rows come again for its second slab), 37 more where rows are 384 bytes apart (probably what fetches of 256 bytes
+// take along of their neighbours).  Values reads four times what it writes: 2111 tokens of 128 heads 58 us for 363 MB, 6.3 TB/s, 0.92 of
+// the copy bandwidth.  Few tokens: each head's weights once, and latency; 32 tokens of 128 heads 6.2 us (L2 flushed
+// before each call 13.5 to 15.5), 130 tokens of 16 heads 4.8 (11.4).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -7,13 +7,16 @@
 // (1 for a group of zeros) and E4M3(y / scale); per 32, scale = 2^(floor(log2(absmax)) - 8).
 //
 // What bounds it: HBM for long steps (every element is read and written once), launch and one round of loads and
-// reductions for short ones.  So a row is held in registers between its only load and its stores, as 16-byte pieces: a row
-// of up to 1024 values by a warp (no block barrier), a longer one by a block.
+// reductions for short ones.  So a row is held between its only load and its stores, as 16-byte pieces: a row of up to 1024
+// values by a warp (no block barrier), a longer one by a block.  It is in registers but for some values of a thread with four
+// pieces, whose 64 registers do not suffice (up to 72 bytes a thread are kept in local memory): with more registers fewer rows
+// are in flight (8192 rows of 8192 to FP8 tiles 135 us, for 72), and with the weights, which make the difference, loaded only behind the
+// reduction their latency stands in each row's way (96).
 //
 // Measured (one GB300; 20 calls in a graph; in brackets with L2 flushed before each): 32 rows of 4096 with the residual
-// 2.0 us (7.3), 1171 of 1536 to MXFP8 3.0 to 3.7 (9.3), latency; 4096 of 512 2.5 to 3.2 (9.3); 8192 rows of 8192 with the
-// residual 78 us to bf16 (85; 537 MB, 6.9 TB/s, 1.01 of the copy bandwidth), 76 to 80 to FP8 in tiles (81 to 85; 472 MB, 6.1 TB/s,
-// 0.9: the codes' arithmetic between a row's loads and its stores); 16384 of 4096 to FP8 rows 74 (81; 0.94).
+// 2.0 us (7.3), 1171 of 1536 to MXFP8 3.1 (9.3), latency; 4096 of 512 2.5 (9.3); 8192 rows of 8192 with the residual 78.5 us to
+// bf16 (85; 537 MB, 6.8 TB/s, 1.01 of the copy bandwidth), 72 to FP8 in tiles (79; 472 MB, 6.5 TB/s, 0.97), 69.5 to MXFP8 (77; 472 MB,
+// 6.8 TB/s); 16384 of 4096 with the residual to FP8 rows 75 (81; 470 MB, 0.93).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
